@@ -11,11 +11,13 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp4moe.so")
 
 c_i32, c_u32, c_f32, c_sz, c_vp = ctypes.c_int32, ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+c_i64 = ctypes.c_int64
 
 OK, INVALID_ARG, MISALIGNED, CAPACITY, UNSUPPORTED, CUDA_ERROR = range(6)
 ERR_TIMEOUT, ERR_EXPERT_ID, ERR_CAPACITY, ERR_NAN, ERR_SCALE_RANGE = 0x1, 0x2, 0x4, 0x8, 0x10
 SAT_L1, SAT_L2 = 0x1, 0x2
 W_NVFP4, W_MXFP4 = 0, 1
+BF16, FP16, FP32 = 0, 1, 2
 
 
 class Config(ctypes.Structure):
@@ -67,6 +69,13 @@ SIGNATURES = {
     "moe_shared_expert": (c_i32, [CP, c_i32, c_vp, SWP, c_vp, c_vp, c_vp]),
     "moe_combine_shared": (c_i32, [CP, c_i32] + [c_vp] * 6),
     "moe_forward_shared": (c_i32, [CP, c_i32] + [c_vp] * 11 + [SWP] + [c_vp] * 5),
+    "moe_shared_expert_fp8": (c_i32, [CP, c_i32, c_vp, c_vp, c_i64, SWP, c_vp, c_vp, c_vp]),
+    "moe_forward_shared_fp8": (c_i32, [CP, c_i32, c_vp, c_vp, c_vp, c_i64] + [c_vp] * 10 + [SWP] + [c_vp] * 5),
+    "fp4moe_add_rmsnorm": (c_i32, [c_i32] * 3 + [c_vp] * 3 + [c_f32] + [c_vp] * 4 + [c_i64, c_vp]),
+    "fp4moe_mx_bytes": (c_i32, [c_i32] * 3 + [ctypes.POINTER(c_sz)] * 2),
+    "fp4moe_mx_quantize": (c_i32, [c_i32] * 4 + [c_vp] * 5),
+    "fp4moe_mx_dequantize": (c_i32, [c_i32] * 4 + [c_vp] * 5),
+    "fp4moe_mx_gemm": (c_i32, [c_i32] * 5 + [c_vp] * 8),
 }
 
 _lib = None

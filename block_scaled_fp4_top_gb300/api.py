@@ -234,6 +234,145 @@ def fp4moe_refresh_gs2(cfg, ws, gw2, gs2_inout, alpha2_out, stream=None):
                                           _s(stream)), "fp4moe_refresh_gs2")
 
 
+def moe_shared_expert_fp8(cfg, T, x_codes, x_scales, se, o_shared, ws, stream=None):
+    """moe_shared_expert on the FP8 copy that fp4moe_add_rmsnorm writes (x_scales [H / 128, at least T])."""
+    _check_fp8(x_codes, x_scales, T, cfg.hidden)
+    _check(_lib.load().moe_shared_expert_fp8(ctypes.byref(cfg), T, _p(x_codes), _p(x_scales), x_scales.shape[1],
+                                             _sw(se), _p(o_shared), _p(ws), _s(stream)), "moe_shared_expert_fp8")
+
+
+def moe_forward_shared_fp8(cfg, T, x, x_codes, x_scales, router_w, router_bias, gs1, gs2, w1_fp4, w1_sf, alpha1,
+                           w2_fp4, w2_sf, alpha2, se, y, topk_ids_out, topk_w_out, ws, stream=None):
+    """moe_forward_shared with the shared expert fed from x's FP8 copy."""
+    _check_fp8(x_codes, x_scales, T, cfg.hidden)
+    _check(_lib.load().moe_forward_shared_fp8(ctypes.byref(cfg), T, _p(x), _p(x_codes), _p(x_scales),
+                                              x_scales.shape[1], _p(router_w), _p(router_bias), _p(gs1), _p(gs2),
+                                              _p(w1_fp4), _p(w1_sf), _p(alpha1), _p(w2_fp4), _p(w2_sf), _p(alpha2),
+                                              _sw(se), _p(y), _p(topk_ids_out), _p(topk_w_out), _p(ws), _s(stream)),
+           "moe_forward_shared_fp8")
+
+
+# ---------------------------------------------------------- dense operators
+# Their sizes and types come from the tensors, so the shapes are checked here: the library sees only pointers.
+_DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
+_BYTE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _dtype(t) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise Fp4MoeError(f"unsupported dtype {t.dtype}: bfloat16, float16 or float32")
+    return d
+
+
+def _want(name, t, shape, dtypes):
+    if t.shape != shape or t.dtype not in dtypes:
+        raise Fp4MoeError(f"{name}: expected {tuple(shape)} of {' or '.join(map(str, dtypes))}, got "
+                          f"{tuple(t.shape)} of {t.dtype}")
+
+
+def _want_bytes(name, t, nbytes):
+    if t.dtype != torch.uint8 or t.numel() != nbytes:
+        raise Fp4MoeError(f"{name}: expected {nbytes} bytes (uint8), got {t.numel()} of {t.dtype}")
+
+
+def _want_scalar(name, t):
+    if t.dtype != torch.float32 or t.numel() < 1:
+        raise Fp4MoeError(f"{name}: expected one float32")
+
+
+def _check_fp8(codes, scales, T, H):
+    _want("x_codes", codes, (T, H), _BYTE_TYPES)
+    if scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != (H + 127) // 128 \
+            or scales.shape[1] < T:
+        raise Fp4MoeError(f"x_scales: expected [{(H + 127) // 128}, at least {T}] of torch.float32, got "
+                          f"{tuple(scales.shape)} of {scales.dtype}")
+
+
+def fp4moe_add_rmsnorm(x, residual, gamma, eps, residual_out, y, y_codes=None, y_scales=None, stream=None):
+    """h = x + residual -> residual_out; y = h * rsqrt(mean(h^2) + eps) * gamma; y in E4M3 with a scale per 1 x 128
+    group -> y_codes [T, H] (uint8 or float8_e4m3fn), y_scales [ceil(H / 128), at least T] float32.
+
+    x [T, H] bfloat16, float16 or float32, and residual, residual_out, y, gamma [H] of its type. residual with
+    residual_out, and y_codes with y_scales, may be None; so may gamma (ones), and y where y_codes is given.
+    residual_out and y may each be x or residual."""
+    if x.dim() != 2:
+        raise Fp4MoeError(f"x: expected [T, H], got {tuple(x.shape)}")
+    T, H = x.shape
+    own = (x.dtype,)
+    d = _dtype(x)
+    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
+        if t is not None:
+            _want(name, t, (T, H), own)
+    if gamma is not None:
+        _want("gamma", gamma, (H,), own)
+    stride = 0
+    if y_codes is not None and y_scales is not None:
+        _check_fp8(y_codes, y_scales, T, H)
+        stride = y_scales.shape[1]
+    _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, _p(x), _p(residual), _p(gamma), eps, _p(residual_out), _p(y),
+                                          _p(y_codes), _p(y_scales), stride, _s(stream)), "fp4moe_add_rmsnorm")
+
+
+def mx_row_bytes(K: int) -> int:
+    """Bytes of one row of 4-bit codes: K rounded up to whole 32-element groups."""
+    return (K + 31) // 32 * 16
+
+
+def mx_sf_bytes(fmt: int, rows: int, K: int) -> int:
+    """Bytes of a microscaled matrix's scale tiles (128 rows x 4 scale columns, 512 bytes each)."""
+    block = 32 if fmt == _lib.W_MXFP4 else 16
+    return (rows + 127) // 128 * (((K + block - 1) // block + 3) // 4) * 512
+
+
+def fp4moe_mx_bytes(fmt: int, rows: int, K: int):
+    """(code bytes, scale bytes) of a [rows, K] matrix in the format W_MXFP4 or W_NVFP4."""
+    v = [ctypes.c_size_t() for _ in range(2)]
+    _check(_lib.load().fp4moe_mx_bytes(fmt, rows, K, *[ctypes.byref(x) for x in v]), "fp4moe_mx_bytes")
+    return tuple(x.value for x in v)
+
+
+def _check_mx(fmt, rows, K, codes, sf, gs):
+    _want_bytes("codes", codes, rows * mx_row_bytes(K))
+    _want_bytes("sf", sf, mx_sf_bytes(fmt, rows, K))
+    if gs is not None:
+        _want_scalar("gs", gs)
+
+
+def fp4moe_mx_quantize(fmt, x, gs, codes, sf, stream=None):
+    """x [rows, K] to E2M1 codes and block scales (fmt W_MXFP4, or W_NVFP4 under the global scale gs)."""
+    if x.dim() != 2:
+        raise Fp4MoeError(f"x: expected [rows, K], got {tuple(x.shape)}")
+    rows, K = x.shape
+    _check_mx(fmt, rows, K, codes, sf, gs)
+    _check(_lib.load().fp4moe_mx_quantize(fmt, _dtype(x), rows, K, _p(x), _p(gs), _p(codes), _p(sf), _s(stream)),
+           "fp4moe_mx_quantize")
+
+
+def fp4moe_mx_dequantize(fmt, codes, sf, gs, out, stream=None):
+    """The values of a microscaled matrix into out [rows, K]."""
+    if out.dim() != 2:
+        raise Fp4MoeError(f"out: expected [rows, K], got {tuple(out.shape)}")
+    rows, K = out.shape
+    _check_mx(fmt, rows, K, codes, sf, gs)
+    _check(_lib.load().fp4moe_mx_dequantize(fmt, _dtype(out), rows, K, _p(codes), _p(sf), _p(gs), _p(out),
+                                            _s(stream)), "fp4moe_mx_dequantize")
+
+
+def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream=None):
+    """out [M, N] = alpha * A B^T for microscaled A [M, K] and B [N, K]; alpha a device float32 or None (1); err a
+    zeroed device word (int32) that the caller keeps."""
+    if out.dim() != 2:
+        raise Fp4MoeError(f"out: expected [M, N], got {tuple(out.shape)}")
+    M, N = out.shape
+    _check_mx(fmt, M, K, a_codes, a_sf, alpha)
+    _check_mx(fmt, N, K, b_codes, b_sf, None)
+    if err.element_size() * err.numel() < 4:
+        raise Fp4MoeError("err: expected a device word of 4 bytes")
+    _check(_lib.load().fp4moe_mx_gemm(fmt, _dtype(out), M, N, K, _p(a_codes), _p(a_sf), _p(b_codes), _p(b_sf),
+                                      _p(alpha), _p(out), _p(err), _s(stream)), "fp4moe_mx_gemm")
+
+
 # --------------------------------------------------------------------------
 @dataclass
 class Weights:

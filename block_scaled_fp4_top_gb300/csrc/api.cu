@@ -9,10 +9,12 @@
 // step must not contain.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
 #include "common.cuh"
+#include "dense.cuh"
 #include "internal.h"
 
 namespace fp4moe {
@@ -209,12 +211,31 @@ fp4moe_status shared_launch(const fp4moe_config& cfg, int32_t T, const uint16_t*
                            err_word(ws), st);
 }
 
+// The shared expert from activations that are already in FP8.
+struct SharedInput {
+  const uint8_t* codes = nullptr;  // [T][H]; NULL: the shared expert quantises x itself
+  const float* scales = nullptr;   // [H / 128][stride]
+  int64_t stride = 0;
+};
+
+fp4moe_status check_shared_input(int32_t T, const SharedInput& in) {
+  FP4_TRY(check_ptrs(in.codes, in.scales));
+  return in.stride >= T ? FP4MOE_OK : FP4MOE_INVALID_ARG;
+}
+
+fp4moe_status shared_fp8_launch(const fp4moe_config& cfg, int32_t T, const SharedInput& in,
+                                const fp4moe_shared_weights& se, float* o_shared, void* ws, cudaStream_t st) {
+  const WsLayout L = ws_layout(cfg);
+  return se_forward_fp8_launch(cfg, T, in.codes, in.scales, in.stride, se.w1, se.w1_scales, se.w2, se.w2_scales,
+                               at<uint8_t>(ws, L.se_qh), at<float>(ws, L.se_sh), o_shared, err_word(ws), st);
+}
+
 // The routed layer, with the shared expert's output added in the combine when se is not NULL.
 fp4moe_status forward_impl(const fp4moe_config* cfg, int32_t T, const uint16_t* x, const uint16_t* router_w,
                            const float* router_bias, const float* gs1, const float* gs2, const uint8_t* w1_fp4,
                            const uint8_t* w1_sf, const float* alpha1, const uint8_t* w2_fp4, const uint8_t* w2_sf,
-                           const float* alpha2, const fp4moe_shared_weights* se, uint16_t* y, int32_t* topk_ids_out,
-                           float* topk_w_out, void* ws, fp4moe_stream_t stream) {
+                           const float* alpha2, const fp4moe_shared_weights* se, const SharedInput& se_in,
+                           uint16_t* y, int32_t* topk_ids_out, float* topk_w_out, void* ws, fp4moe_stream_t stream) {
   FP4_TRY(check_cfg(cfg));
   FP4_TRY(check_T(cfg, T));
   const bool mx = is_mx(cfg);  // MXFP4: gs1, gs2, alpha1 and alpha2 are unused and may be NULL
@@ -239,7 +260,8 @@ fp4moe_status forward_impl(const fp4moe_config* cfg, int32_t T, const uint16_t* 
     o_shared = at<float>(ws, L.se_o);
     if (cudaEventRecord(side->fork, st) != cudaSuccess || cudaStreamWaitEvent(side->s, side->fork, 0) != cudaSuccess)
       return FP4MOE_CUDA_ERROR;
-    rs = shared_launch(*cfg, T, x, *se, o_shared, ws, side->s);
+    rs = se_in.codes != nullptr ? shared_fp8_launch(*cfg, T, se_in, *se, o_shared, ws, side->s)
+                                : shared_launch(*cfg, T, x, *se, o_shared, ws, side->s);
     if (cudaEventRecord(side->join, side->s) != cudaSuccess && rs == FP4MOE_OK) rs = FP4MOE_CUDA_ERROR;
   }
   auto routed = [&]() -> fp4moe_status {
@@ -457,7 +479,7 @@ fp4moe_status moe_forward(const fp4moe_config* cfg, int32_t T, const uint16_t* x
                           const float* alpha2, uint16_t* y, int32_t* topk_ids_out, float* topk_w_out, void* ws,
                           fp4moe_stream_t stream) {
   return forward_impl(cfg, T, x, router_w, router_bias, gs1, gs2, w1_fp4, w1_sf, alpha1, w2_fp4, w2_sf, alpha2,
-                      nullptr, y, topk_ids_out, topk_w_out, ws, stream);
+                      nullptr, SharedInput(), y, topk_ids_out, topk_w_out, ws, stream);
 }
 
 fp4moe_status moe_forward_shared(const fp4moe_config* cfg, int32_t T, const uint16_t* x, const uint16_t* router_w,
@@ -469,7 +491,34 @@ fp4moe_status moe_forward_shared(const fp4moe_config* cfg, int32_t T, const uint
   FP4_TRY(check_cfg(cfg));
   FP4_TRY(check_shared(cfg, se));
   return forward_impl(cfg, T, x, router_w, router_bias, gs1, gs2, w1_fp4, w1_sf, alpha1, w2_fp4, w2_sf, alpha2, se,
-                      y, topk_ids_out, topk_w_out, ws, stream);
+                      SharedInput(), y, topk_ids_out, topk_w_out, ws, stream);
+}
+
+fp4moe_status moe_forward_shared_fp8(const fp4moe_config* cfg, int32_t T, const uint16_t* x, const uint8_t* x_codes,
+                                     const float* x_scales, int64_t scale_stride, const uint16_t* router_w,
+                                     const float* router_bias, const float* gs1, const float* gs2,
+                                     const uint8_t* w1_fp4, const uint8_t* w1_sf, const float* alpha1,
+                                     const uint8_t* w2_fp4, const uint8_t* w2_sf, const float* alpha2,
+                                     const fp4moe_shared_weights* se, uint16_t* y, int32_t* topk_ids_out,
+                                     float* topk_w_out, void* ws, fp4moe_stream_t stream) {
+  FP4_TRY(check_cfg(cfg));
+  FP4_TRY(check_shared(cfg, se));
+  const SharedInput in{x_codes, x_scales, scale_stride};
+  FP4_TRY(check_shared_input(T, in));
+  return forward_impl(cfg, T, x, router_w, router_bias, gs1, gs2, w1_fp4, w1_sf, alpha1, w2_fp4, w2_sf, alpha2, se,
+                      in, y, topk_ids_out, topk_w_out, ws, stream);
+}
+
+fp4moe_status moe_shared_expert_fp8(const fp4moe_config* cfg, int32_t T, const uint8_t* x_codes,
+                                    const float* x_scales, int64_t scale_stride, const fp4moe_shared_weights* se,
+                                    float* o_shared, void* ws, fp4moe_stream_t stream) {
+  FP4_TRY(check_cfg(cfg));
+  FP4_TRY(check_T(cfg, T));
+  FP4_TRY(check_shared(cfg, se));
+  const SharedInput in{x_codes, x_scales, scale_stride};
+  FP4_TRY(check_shared_input(T, in));
+  FP4_TRY(check_ptrs(o_shared, ws));
+  return shared_fp8_launch(*cfg, T, in, *se, o_shared, ws, (cudaStream_t)stream);
 }
 
 fp4moe_status moe_shared_expert(const fp4moe_config* cfg, int32_t T, const uint16_t* x,
@@ -696,6 +745,79 @@ fp4moe_status fp4moe_refresh_gs2(const fp4moe_config* cfg, void* ws, const float
   if (is_mx(cfg)) return FP4MOE_UNSUPPORTED;  // MXFP4 layers keep bf16 activations: no global scales
   FP4_TRY(check_ptrs(ws, gw2, gs2_inout, alpha2_out));
   return refresh_gs2_launch(local_experts(*cfg), amax_h_run(ws), gw2, gs2_inout, alpha2_out, (cudaStream_t)stream);
+}
+
+// ------------------------------------------------- the dense operators around the layer
+namespace {
+bool dtype_ok(int32_t d) { return d == FP4MOE_BF16 || d == FP4MOE_FP16 || d == FP4MOE_FP32; }
+bool format_ok(int32_t f) { return f == FP4MOE_W_NVFP4 || f == FP4MOE_W_MXFP4; }
+// A matrix of the dense operators: its scale tiles are addressed with 32-bit tile indices by TMA.
+fp4moe_status check_mx(int32_t format, int32_t rows, int32_t K) {
+  if (rows < 0 || K <= 0) return FP4MOE_INVALID_ARG;
+  if (!format_ok(format)) return FP4MOE_UNSUPPORTED;
+  if (mx_row_tiles(rows) * mx_col_tiles(format, K) > INT32_MAX) return FP4MOE_UNSUPPORTED;
+  return FP4MOE_OK;
+}
+}  // namespace
+
+fp4moe_status fp4moe_add_rmsnorm(int32_t dtype, int32_t T, int32_t H, const void* x, const void* residual,
+                                 const void* gamma, float eps, void* residual_out, void* y, uint8_t* y_codes,
+                                 float* y_scales, int64_t scale_stride, fp4moe_stream_t stream) {
+  if (T < 0 || H <= 0 || !(eps >= 0.0f) || std::isinf(eps)) return FP4MOE_INVALID_ARG;
+  if (!dtype_ok(dtype)) return FP4MOE_UNSUPPORTED;
+  if (T == 0) return FP4MOE_OK;  // an empty batch's buffers may be null
+  if ((residual == nullptr) != (residual_out == nullptr)) return FP4MOE_INVALID_ARG;
+  if ((y_codes == nullptr) != (y_scales == nullptr)) return FP4MOE_INVALID_ARG;
+  if (y == nullptr && y_codes == nullptr) return FP4MOE_INVALID_ARG;  // nothing to compute
+  if (y_codes != nullptr && scale_stride < T) return FP4MOE_INVALID_ARG;
+  FP4_TRY(check_ptrs(x));
+  for (const void* p : {residual, gamma, (const void*)residual_out, (const void*)y, (const void*)y_codes,
+                        (const void*)y_scales})
+    FP4_TRY(check_opt(p));
+  return add_rmsnorm_launch(dtype, T, H, x, residual, gamma, eps, residual_out, y, y_codes, y_scales, scale_stride,
+                            (cudaStream_t)stream);
+}
+
+fp4moe_status fp4moe_mx_bytes(int32_t format, int32_t rows, int32_t K, size_t* code_bytes, size_t* sf_bytes) {
+  FP4_TRY(check_mx(format, rows, K));
+  if (code_bytes) *code_bytes = (size_t)rows * (size_t)mx_row_bytes(K);
+  if (sf_bytes) *sf_bytes = (size_t)(mx_row_tiles(rows) * mx_col_tiles(format, K)) * 512;
+  return FP4MOE_OK;
+}
+
+fp4moe_status fp4moe_mx_quantize(int32_t format, int32_t dtype, int32_t rows, int32_t K, const void* x,
+                                 const float* gs, uint8_t* codes, uint8_t* sf, fp4moe_stream_t stream) {
+  FP4_TRY(check_mx(format, rows, K));
+  if (!dtype_ok(dtype)) return FP4MOE_UNSUPPORTED;
+  if (rows == 0) return FP4MOE_OK;
+  FP4_TRY(check_ptrs(x, codes, sf));
+  if (format == FP4MOE_W_NVFP4) FP4_TRY(check_ptrs(gs));
+  return mx_quantize_launch(format, dtype, rows, K, x, gs, codes, sf, (cudaStream_t)stream);
+}
+
+fp4moe_status fp4moe_mx_dequantize(int32_t format, int32_t dtype, int32_t rows, int32_t K, const uint8_t* codes,
+                                   const uint8_t* sf, const float* gs, void* out, fp4moe_stream_t stream) {
+  FP4_TRY(check_mx(format, rows, K));
+  if (!dtype_ok(dtype)) return FP4MOE_UNSUPPORTED;
+  if (rows == 0) return FP4MOE_OK;
+  FP4_TRY(check_ptrs(codes, sf, out));
+  if (format == FP4MOE_W_NVFP4) FP4_TRY(check_ptrs(gs));
+  return mx_dequantize_launch(format, dtype, rows, K, codes, sf, gs, out, (cudaStream_t)stream);
+}
+
+fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N, int32_t K, const uint8_t* a_codes,
+                             const uint8_t* a_sf, const uint8_t* b_codes, const uint8_t* b_sf, const float* alpha,
+                             void* out, uint32_t* err, fp4moe_stream_t stream) {
+  FP4_TRY(check_mx(format, M, K));
+  FP4_TRY(check_mx(format, N, K));
+  if (N == 0) return FP4MOE_INVALID_ARG;
+  if (!dtype_ok(dtype)) return FP4MOE_UNSUPPORTED;
+  if (mx_row_tiles(M) * mx_row_tiles(N) > INT32_MAX / 2) return FP4MOE_UNSUPPORTED;  // tile indices are 32-bit
+  if (M == 0) return FP4MOE_OK;
+  FP4_TRY(check_ptrs(a_codes, a_sf, b_codes, b_sf, out, err));
+  FP4_TRY(check_opt(alpha));
+  return mx_dense_launch(format, dtype, M, N, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err,
+                         (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,75 @@
+// Element types and 4-bit block formats of the dense operators (norm.cu, mxquant.cu, mxdense.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace fp4moe {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+// One rounding to nearest even into the storage type.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Two signed E4M3 codes (RNE, satfinite; NaN gives the NaN code): `lo` in the low byte.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The value of an E2M1 code: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+__device__ __forceinline__ float e2m1_to_f32(uint32_t q) {
+  const uint32_t e = (q >> 1) & 3u, m = q & 1u;
+  const float v = e ? __uint_as_float(((e + 126u) << 23) | (m << 22)) : 0.5f * (float)m;
+  return (q & 8u) ? -v : v;
+}
+
+// The microscaled 4-bit formats: elements per scale.
+template <int FMT>
+struct MxFormat;
+template <>
+struct MxFormat<FP4MOE_W_NVFP4> {
+  static constexpr int kBlock = 16;
+};
+template <>
+struct MxFormat<FP4MOE_W_MXFP4> {
+  static constexpr int kBlock = 32;
+};
+
+// The value of a scale byte: E8M0 is 2^(b - 127) with 0xFF for NaN; E4M3 has NaN at 0x7F.
+template <int FMT>
+__device__ __forceinline__ float mx_scale(uint32_t b) {
+  if constexpr (FMT == FP4MOE_W_MXFP4)
+    return b == 255u ? __uint_as_float(0x7FC00000u) : (b == 0u ? 0x1p-127f : __uint_as_float(b << 23));
+  else
+    return b == 0x7Fu ? __uint_as_float(0x7FC00000u) : e4m3_to_f32(b);
+}
+
+// sf_offset for matrices of any size: byte offset of scale (r, c), with col_tiles tiles across.
+__device__ __forceinline__ size_t mx_sf_offset(uint64_t r, uint32_t c, uint64_t col_tiles) {
+  return (size_t)(((r >> 7) * col_tiles + (c >> 2)) * 512u + (r & 31u) * 16u + ((r & 127u) >> 5) * 4u + (c & 3u));
+}
+
+inline int mx_block(int32_t format) { return format == FP4MOE_W_MXFP4 ? 32 : 16; }
+// Bytes of one row of codes: K rounded up to whole 32-element groups, so that every row starts 16-byte aligned.
+inline int64_t mx_row_bytes(int32_t K) { return ((int64_t)K + 31) / 32 * 16; }
+// 128 x 4 scale tiles of a matrix: row tiles and column tiles.
+inline int64_t mx_row_tiles(int32_t rows) { return ((int64_t)rows + 127) / 128; }
+inline int64_t mx_col_tiles(int32_t format, int32_t K) {
+  const int64_t b = mx_block(format);
+  return (((int64_t)K + b - 1) / b + 3) / 4;
+}
+
+}  // namespace fp4moe

@@ -504,6 +504,19 @@ bool encode_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner_bytes, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles (512 bytes each) as a 2-D tensor [tiles][128 words], boxes of box_tiles whole tiles, unswizzled.
+bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {128, tiles};
+  cuuint64_t strides[1] = {512};
+  cuuint32_t box[2] = {128, box_tiles};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 template <int MODE>
 bool configure_once() {

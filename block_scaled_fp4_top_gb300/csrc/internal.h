@@ -132,5 +132,25 @@ fp4moe_status se_quant_weights_launch(const fp4moe_config& cfg, int32_t which, c
 fp4moe_status se_forward_launch(const fp4moe_config& cfg, int32_t T, const uint16_t* x, const uint8_t* w1,
                                 const float* s1, const uint8_t* w2, const float* s2, uint8_t* qx, float* sx,
                                 uint8_t* qh, float* sh, float* out, uint32_t* err, cudaStream_t st);
+// The same from activations that are already quantised: qx [T][H], sx [H / 128][sx_stride].
+fp4moe_status se_forward_fp8_launch(const fp4moe_config& cfg, int32_t T, const uint8_t* qx, const float* sx,
+                                    int64_t sx_stride, const uint8_t* w1, const float* s1, const uint8_t* w2,
+                                    const float* s2, uint8_t* qh, float* sh, float* out, uint32_t* err,
+                                    cudaStream_t st);
+
+// The dense operators around the layer; dtype is an fp4moe_dtype, format an FP4MOE_W_* value.
+// norm.cu: residual addition, RMS norm, FP8 copy (codes and scales may be null)
+fp4moe_status add_rmsnorm_launch(int32_t dtype, int32_t T, int32_t H, const void* x, const void* residual,
+                                 const void* gamma, float eps, void* h_out, void* y, uint8_t* codes, float* scales,
+                                 int64_t scale_stride, cudaStream_t st);
+// mxquant.cu: microscaled 4-bit codes and scale tiles of a plain matrix, and back
+fp4moe_status mx_quantize_launch(int32_t format, int32_t dtype, int32_t rows, int32_t K, const void* x,
+                                 const float* gs, uint8_t* codes, uint8_t* sf, cudaStream_t st);
+fp4moe_status mx_dequantize_launch(int32_t format, int32_t dtype, int32_t rows, int32_t K, const uint8_t* codes,
+                                   const uint8_t* sf, const float* gs, void* out, cudaStream_t st);
+// mxdense.cu: out [M][N] = alpha * A B^T
+fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t N, int32_t K, const uint8_t* a,
+                              const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
+                              void* out, uint32_t* err, cudaStream_t st);
 
 }  // namespace fp4moe

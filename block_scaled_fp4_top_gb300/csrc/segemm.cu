@@ -73,7 +73,8 @@ struct SeMaps {
 struct SeParams {
   int T, KB, tcap;
   float limit;
-  const float* a_scale;  // [KB][tcap]
+  const float* a_scale;  // [KB][a_stride]
+  int64_t a_stride;      // at least T
   const float* w_scale;  // [N / 128][KB], logical block order (W1: gate blocks, then up blocks)
   int up_blk;            // W1: index of the first up block (Is / 128)
   uint8_t* h_codes;      // W1: [tcap][I] E4M3
@@ -82,6 +83,7 @@ struct SeParams {
   float* out;            // W2: [T][H] fp32
   int H;
   uint32_t* err;
+  int wait_first;        // the previous kernel may have written the weights: wait for it before anything else
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T, E4M3 x E4M3 with fp32 accumulation (kind::f8f6f4, K = 32).
@@ -146,8 +148,9 @@ __global__ void __launch_bounds__(SE_THREADS, 1)
   __shared__ float s_sw[2][SE_MAX_KB];      // weight scales: W1 gate and up block, W2 the tile's block
   __shared__ float s_amax[3][SE_BM];        // W1: amax of each half of a row's 64 h features; [2]: both
 
+  if (prm.wait_first) pdl_wait();
   pdl_trigger();
-  // The weights depend on no earlier kernel, so the producer starts streaming them before it waits
+  // The weights depend on no earlier kernel (or the wait above covers them), so the producer starts streaming them before it waits
   // for the previous kernel (programmatic dependent launch); every other read of a predecessor's
   // output waits first. Every CTA runs to the end (cluster peers read its shared memory), so an
   // abort raised elsewhere only skips work.
@@ -244,8 +247,8 @@ __global__ void __launch_bounds__(SE_THREADS, 1)
     pdl_wait();  // the activation scales come from the previous kernel
     for (int i = threadIdx.x; i < nk * SE_BM; i += 256) {
       const int kk = i / SE_BM, rr = i % SE_BM;
-      const int srow = min(mt * SE_BM + rr, prm.tcap - 1);  // scale rows past T exist but hold no token
-      s_sa[kk][rr] = __ldcg(prm.a_scale + (size_t)(kb0 + kk) * prm.tcap + srow);
+      const int srow = min(mt * SE_BM + rr, prm.T - 1);  // tile rows past T hold no token
+      s_sa[kk][rr] = __ldcg(prm.a_scale + (size_t)(kb0 + kk) * prm.a_stride + srow);
     }
     // W1 tile nt holds gate and up features 64 nt .. 64 nt + 63: gate block nt / 2 and up block
     // up_blk + nt / 2. W2 tile nt is block nt.
@@ -547,16 +550,15 @@ fp4moe_status se_quant_weights_launch(const fp4moe_config& cfg, int32_t which, c
   return cudaGetLastError() == cudaSuccess ? FP4MOE_OK : FP4MOE_CUDA_ERROR;
 }
 
-fp4moe_status se_forward_launch(const fp4moe_config& cfg, int32_t T, const uint16_t* x, const uint8_t* w1,
-                                const float* s1, const uint8_t* w2, const float* s2, uint8_t* qx, float* sx,
-                                uint8_t* qh, float* sh, float* out, uint32_t* err, cudaStream_t st) {
-  if (T == 0) return FP4MOE_OK;
+namespace {
+// W1 with the SwiGLU and the requantisation, then W2. wait_first: the kernel before W1 may have written the
+// weights (no quantisation of x stands between).
+fp4moe_status gemms_launch(const fp4moe_config& cfg, int32_t T, const uint8_t* qx, const float* sx,
+                           int64_t sx_stride, const uint8_t* w1, const float* s1, const uint8_t* w2,
+                           const float* s2, uint8_t* qh, float* sh, float* out, uint32_t* err,
+                           bool wait_first, cudaStream_t st) {
   const int H = cfg.hidden, Is = cfg.shared_inter;
   const int tcap = (int)se_tcap(cfg);
-  const int64_t groups = (int64_t)T * (H / 128);
-  if (launch_pdl(se_quant_x_kernel, dim3((unsigned)((groups + 7) / 8)), dim3(256), 0, st, T, H, tcap, x, qx, sx) !=
-      cudaSuccess)
-    return FP4MOE_CUDA_ERROR;
   if (!configure_se<0>() || !configure_se<1>()) return FP4MOE_CUDA_ERROR;
   const int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
@@ -579,8 +581,10 @@ fp4moe_status se_forward_launch(const fp4moe_config& cfg, int32_t T, const uint1
   p.I = Is;
   p.H = H;
   p.err = err;
+  p.wait_first = wait_first ? 1 : 0;  // W2 follows W1, which has waited
   p.KB = H / 128;
   p.a_scale = sx;
+  p.a_stride = sx_stride;
   p.w_scale = s1;
   p.up_blk = Is / 128;
   p.h_codes = qh;
@@ -589,13 +593,37 @@ fp4moe_status se_forward_launch(const fp4moe_config& cfg, int32_t T, const uint1
   if (launch_se_gemm<0>(g1, k_slices<0>((int)g1.x, (int)mt, p.KB, se_sms), st, m1, p) != cudaSuccess)
     return FP4MOE_CUDA_ERROR;
   p.KB = Is / 128;
+  p.wait_first = 0;
   p.a_scale = sh;
+  p.a_stride = tcap;
   p.w_scale = s2;
   p.out = out;
   const dim3 g2((unsigned)(H / SE_BN), mt);
   return launch_se_gemm<1>(g2, k_slices<1>((int)g2.x, (int)mt, p.KB, se_sms), st, m2, p) == cudaSuccess
              ? FP4MOE_OK
              : FP4MOE_CUDA_ERROR;
+}
+}  // namespace
+
+fp4moe_status se_forward_launch(const fp4moe_config& cfg, int32_t T, const uint16_t* x, const uint8_t* w1,
+                                const float* s1, const uint8_t* w2, const float* s2, uint8_t* qx, float* sx,
+                                uint8_t* qh, float* sh, float* out, uint32_t* err, cudaStream_t st) {
+  if (T == 0) return FP4MOE_OK;
+  const int H = cfg.hidden;
+  const int tcap = (int)se_tcap(cfg);
+  const int64_t groups = (int64_t)T * (H / 128);
+  if (launch_pdl(se_quant_x_kernel, dim3((unsigned)((groups + 7) / 8)), dim3(256), 0, st, T, H, tcap, x, qx, sx) !=
+      cudaSuccess)
+    return FP4MOE_CUDA_ERROR;
+  return gemms_launch(cfg, T, qx, sx, tcap, w1, s1, w2, s2, qh, sh, out, err, false, st);
+}
+
+fp4moe_status se_forward_fp8_launch(const fp4moe_config& cfg, int32_t T, const uint8_t* qx, const float* sx,
+                                    int64_t sx_stride, const uint8_t* w1, const float* s1, const uint8_t* w2,
+                                    const float* s2, uint8_t* qh, float* sh, float* out, uint32_t* err,
+                                    cudaStream_t st) {
+  if (T == 0) return FP4MOE_OK;
+  return gemms_launch(cfg, T, qx, sx, sx_stride, w1, s1, w2, s2, qh, sh, out, err, true, st);
 }
 
 }  // namespace fp4moe

@@ -464,6 +464,125 @@ fp4moe_status moe_forward_shared(const fp4moe_config* cfg, int32_t T, const uint
                                  uint16_t* y, int32_t* topk_ids_out, float* topk_w_out, void* ws,
                                  fp4moe_stream_t stream);
 
+/*
+ * moe_shared_expert_fp8: moe_shared_expert from activations that are already
+ * in block-FP8 (fp4moe_add_rmsnorm writes them), so its quantisation kernel is
+ * left out.
+ *   x_codes  [T][H] E4M3 bytes; x_scales [H / 128][scale_stride] fp32, the
+ *            scale of token t and group g at g * scale_stride + t,
+ *            scale_stride >= T (else FP4MOE_INVALID_ARG).
+ * Results and the other arguments are those of moe_shared_expert on the x whose
+ * quantisation these are.
+ */
+fp4moe_status moe_shared_expert_fp8(const fp4moe_config* cfg, int32_t T, const uint8_t* x_codes,
+                                    const float* x_scales, int64_t scale_stride, const fp4moe_shared_weights* se,
+                                    float* o_shared, void* ws, fp4moe_stream_t stream);
+
+/*
+ * moe_forward_shared_fp8: moe_forward_shared with the shared expert fed from
+ * x_codes and x_scales (as moe_shared_expert_fp8); the router and the routed
+ * experts read x.
+ */
+fp4moe_status moe_forward_shared_fp8(const fp4moe_config* cfg, int32_t T, const uint16_t* x, const uint8_t* x_codes,
+                                     const float* x_scales, int64_t scale_stride, const uint16_t* router_w,
+                                     const float* router_bias, const float* gs1, const float* gs2,
+                                     const uint8_t* w1_fp4, const uint8_t* w1_sf, const float* alpha1,
+                                     const uint8_t* w2_fp4, const uint8_t* w2_sf, const float* alpha2,
+                                     const fp4moe_shared_weights* se, uint16_t* y, int32_t* topk_ids_out,
+                                     float* topk_w_out, void* ws, fp4moe_stream_t stream);
+
+/* ------------------------------------------------------- dense operators --
+ * What runs right beside the MoE layer in a decoder block: a projection with
+ * microscaled 4-bit weights in front of it (fp4moe_mx_quantize of the
+ * activations, fp4moe_mx_gemm), and the residual addition with the norm whose
+ * output the router, the routed experts (y) and the shared expert (its FP8
+ * copy) read. They need no fp4moe_config and no workspace. The layer's
+ * conventions hold: device pointers 16-byte aligned, work enqueued on
+ * `stream`, no allocation, no synchronisation, capturable after a first call
+ * outside capture. Matrices are contiguous and row-major. Inference only: no
+ * call computes gradients.
+ */
+typedef enum fp4moe_dtype { FP4MOE_BF16 = 0, FP4MOE_FP16 = 1, FP4MOE_FP32 = 2 } fp4moe_dtype;
+
+/*
+ * fp4moe_add_rmsnorm: for every row t of T rows of H elements,
+ *   h    = RN(x + residual)                    -> residual_out
+ *   n    = h * rsqrt(mean(h^2) + eps) * gamma  (fp32)
+ *   y    = RN(n)
+ *   and per 1 x 128 group g of n (the last one may be short):
+ *   s    = RN(amax / 448)                      -> y_scales[g * scale_stride + t]
+ *   code = E4M3_satfinite(RN(n / s)), 0 where s == 0   -> y_codes[t][:]
+ * RN rounds once to the storage type `dtype` of x, residual, gamma,
+ * residual_out and y (an fp4moe_dtype). The norm is that of the rounded h, the
+ * stream that residual_out holds; the codes are taken from n before its
+ * rounding to y's type. Sums and statistics are fp32 (a sum of squares past
+ * fp32's range gives y = 0).
+ *   residual and residual_out are both given or both NULL (then h = x).
+ *   gamma [H] may be NULL (all ones). y may be NULL if y_codes is given.
+ *   y_codes [T][H] and y_scales (ceil(H / 128) rows of scale_stride floats,
+ *   scale_stride >= T) are both given or both NULL.
+ *   residual_out and y may each be the same buffer as x or residual (exactly,
+ *   not shifted), but not the same buffer as each other.
+ * A NaN or an infinity in a row reaches y as the formula has it. A group of n
+ * that holds a NaN has a NaN scale and NaN codes (0x7F or 0xFF).
+ * Any T >= 0, H >= 1, finite eps >= 0; else FP4MOE_INVALID_ARG.
+ */
+fp4moe_status fp4moe_add_rmsnorm(int32_t dtype, int32_t T, int32_t H, const void* x, const void* residual,
+                                 const void* gamma, float eps, void* residual_out, void* y, uint8_t* y_codes,
+                                 float* y_scales, int64_t scale_stride, fp4moe_stream_t stream);
+
+/*
+ * Microscaled 4-bit matrices: [rows][K] E2M1 codes with block scales along K.
+ * format FP4MOE_W_MXFP4: one E8M0 scale per 32 elements (OCP Microscaling
+ * v1.0); format FP4MOE_W_NVFP4: one E4M3 scale per 16 elements under a global
+ * scale g (quant direction: value = e2m1 * e4m3 / g).
+ *   codes: row r at r * ceil(K / 32) * 16 bytes, element 2c in the low nibble
+ *     of byte c, zero past K;
+ *   scales: the 128x4 tile layout above with C = ceil(K / 32) or ceil(K / 16)
+ *     columns, rows padded to a multiple of 128 and columns to a multiple of
+ *     4; bytes past the matrix must be zero (fp4moe_mx_quantize writes them).
+ * fp4moe_mx_bytes gives both sizes (host arithmetic; any output may be NULL).
+ * Any rows >= 0 and K >= 1 (else FP4MOE_INVALID_ARG); fewer than 2^31 scale
+ * tiles (else FP4MOE_UNSUPPORTED).
+ */
+fp4moe_status fp4moe_mx_bytes(int32_t format, int32_t rows, int32_t K, size_t* code_bytes, size_t* sf_bytes);
+
+/*
+ * fp4moe_mx_quantize: x [rows][K] of type dtype into that form. Per block,
+ * a = max|v| (a short last block counts as if zeros followed):
+ *   MXFP4: X = floor(log2 a) - 2 clamped to [-127, 127], -127 if a == 0;
+ *          scale byte X + 127, code E2M1_satfinite(v * 2^-X);
+ *   NVFP4: the arithmetic of moe_quantize_scatter under *gs.
+ * A block that holds an infinity or a NaN gets the NaN scale (0xFF or 0x7F)
+ * and zero codes: its values, and every product with it, are NaN.
+ *   gs: one fp32, NVFP4 only (ignored for MXFP4).
+ */
+fp4moe_status fp4moe_mx_quantize(int32_t format, int32_t dtype, int32_t rows, int32_t K, const void* x,
+                                 const float* gs, uint8_t* codes, uint8_t* sf, fp4moe_stream_t stream);
+
+/*
+ * fp4moe_mx_dequantize: the values, out [rows][K] of type dtype:
+ *   MXFP4: RN(e2m1 * 2^X); NVFP4: RN(RN_f32(e2m1 * e4m3 / g)), g = *gs.
+ */
+fp4moe_status fp4moe_mx_dequantize(int32_t format, int32_t dtype, int32_t rows, int32_t K, const uint8_t* codes,
+                                   const uint8_t* sf, const float* gs, void* out, fp4moe_stream_t stream);
+
+/*
+ * fp4moe_mx_gemm: out [M][N] = RN(alpha * A B^T) of two microscaled 4-bit
+ * matrices of one format, A [M][K] and B [N][K]: a block-scaled FP4 MMA with
+ * fp32 accumulation, multiplied by alpha in fp32 and rounded once to dtype.
+ *   alpha: one fp32, or NULL for 1. For NVFP4 pass 1 / (ga * gb)
+ *     (fp4moe_make_alpha).
+ *   err: device uint32, zeroed once by the caller: a bounded wait that runs
+ *     out sets FP4MOE_ERR_TIMEOUT in it, and calls that find the bit set skip
+ *     their work, as with a workspace's error word (fp4moe_read_error reads
+ *     and clears either).
+ * Deterministic: equal inputs give equal bits. Any M >= 0, N >= 1, K >= 1.
+ */
+fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N, int32_t K, const uint8_t* a_codes,
+                             const uint8_t* a_sf, const uint8_t* b_codes, const uint8_t* b_sf, const float* alpha,
+                             void* out, uint32_t* err, fp4moe_stream_t stream);
+
 /* ------------------------------------------------------------------ prep --
  * Load-time helpers. They run outside the timed hot path and may use
  * cudaMemsetAsync. They still never synchronise.
