@@ -44,8 +44,10 @@ def _p(t):
 
 
 def _s(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle of the current stream, without building a torch.cuda.Stream (0.2 against 3 us a call)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(rc: int, what: str):

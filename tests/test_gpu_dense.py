@@ -90,9 +90,17 @@ def test_norm_widths(dtype, H):
     check_norm(3, H, dtype, seed=H)
 
 
-@pytest.mark.parametrize("T", [1, 2, 64, 65, 700])
-def test_norm_rows(T):
-    check_norm(T, 4096, "bfloat16", seed=T)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,H", [(1, 4096), (2, 4096), (64, 4096), (65, 4090), (700, 4096), (700, 4090), (701, 129),
+                                 (703, 1001), (900, 8191), (153, 20001)])
+def test_norm_rows(dtype, T, H):
+    check_norm(T, H, dtype, seed=T)
+
+
+@pytest.mark.parametrize("H", [4090, 1001])
+@pytest.mark.parametrize("alias", ["h=x", "h=r,y=x"])
+def test_norm_many_rows_in_place(H, alias):
+    check_norm(400, H, "bfloat16", alias=alias)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
