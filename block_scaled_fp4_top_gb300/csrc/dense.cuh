@@ -60,6 +60,31 @@ __device__ __forceinline__ uint4 pack(const float (&v)[16 / sizeof(T)]) {
     return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
 
+// The OUT words from byte `drop` on of the IN words w, in place: drop is even and less than 16.
+template <int IN, int OUT>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[IN], int drop) {
+  static_assert(IN >= OUT + 4, "16 - 2 bytes can be dropped");
+#pragma unroll
+  for (int i = 0; i < OUT + 2; ++i) w[i] = (drop & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < OUT + 1; ++i) w[i] = (drop & 4) ? w[i + 1] : w[i];
+  const uint32_t sel = (drop & 2) ? 0x5432u : 0x3210u;
+#pragma unroll
+  for (int i = 0; i < OUT; ++i) w[i] = __byte_perm(w[i], w[i + 1], sel);
+}
+
+// 32 bytes at a 32-byte-aligned address in one access (256-bit, sm_100 and later): a thread fills whole sectors.
+__device__ __forceinline__ void ld_global_32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void st_global_32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Two signed E4M3 codes (RNE, satfinite; NaN gives the NaN code): `lo` in the low byte.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   uint16_t r;

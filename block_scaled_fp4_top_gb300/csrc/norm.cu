@@ -121,16 +121,10 @@ __device__ __forceinline__ uint4 ld_vec(const void* p) {
 
 // 16 bytes from byte 16 - back of the 32 bytes (prev, cur); back is the same in the whole CTA, 0 .. 14 and even.
 __device__ __forceinline__ uint4 shifted(uint4 prev, uint4 cur, int back) {
+  if (back == 0) return cur;
   uint32_t w[8] = {prev.x, prev.y, prev.z, prev.w, cur.x, cur.y, cur.z, cur.w};
-  const int sh = 16 - back;
-  if (sh & 16) return cur;
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = (sh & 8) ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = (sh & 4) ? w[i + 1] : w[i];
-  const uint32_t sel = (sh & 2) ? 0x5432u : 0x3210u;
-  return make_uint4(__byte_perm(w[0], w[1], sel), __byte_perm(w[1], w[2], sel), __byte_perm(w[2], w[3], sel),
-                    __byte_perm(w[3], w[4], sel));
+  shift_words<8, 4>(w, 16 - back);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Vector q of a row, in a thread's slot i, is q = i * blockDim + threadIdx.

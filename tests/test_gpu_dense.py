@@ -198,7 +198,8 @@ def check_quantize(fmt, x, g=1.0):
 @pytest.mark.parametrize("fmt", [NV, MX])
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,K", [(1, 1), (1, 16), (2, 31), (3, 32), (5, 33), (1, 64), (7, 100), (127, 128), (128, 96),
-                                    (129, 160), (130, 4096), (64, 1000), (300, 520), (1, 8191)])
+                                    (129, 160), (130, 4096), (64, 1000), (300, 520), (1, 8191), (700, 1023),
+                                    (40, 700), (400, 5000)])
 def test_quantize_bits(fmt, dtype, rows, K):
     check_quantize(fmt, rnd((rows, K), dtype, rows * 10007 + K, 1.5), 37.5)
 
