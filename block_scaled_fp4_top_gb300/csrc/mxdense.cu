@@ -6,76 +6,83 @@
 // epilogue multiplies by alpha and rounds once to the output type. Bytes: (M + N) K (1/2 + 1/32 or 1/16) in,
 // M N out; 2 M N K flops.
 //
-// A CTA owns one 128 x BN output tile at a time (BN weight rows), walking the tiles with a static stride.
-//   warps 0-7   epilogue (warp w: TMEM lanes 32 (w % 4) .., columns BN / 2 * (w / 4) ..).
-//   warp 8      producer: a ring stage is 256 K elements of A and B by TMA (128-byte swizzle) and their scale
-//               tiles, which a second pair of tensor maps views as rows of 512 bytes. Rows and columns past the
-//               matrices arrive as zeros.
-//   warp 9      MMA issuer, one thread.
-//   warps 10-11 scale copiers: tcgen05.cp of the stage's scale tiles into the stage's TMEM slot.
-// The accumulator takes BN TMEM columns; the epilogue moves it whole to registers and frees it before it
-// computes, so the next tile's MMAs wait only for that move.
+// This file holds the kernel for the small sizes, tiles of 128 x 64 or 128 x 128 on single CTAs, and the choice between
+// them and the large tiles of mxpair.cu.
+//   warps 0-7   epilogue (warp w: TMEM lanes 32 (w % 4) .., half of the columns).
+//   warps 8, 9  producers, of A and of B: a ring stage is 256 K elements of both by TMA (128-byte swizzle; of A only
+//               the leading 16, 32, 64 or 128 rows that hold M; rows and columns past the matrices arrive as
+//               zeros) and their scale tiles by bulk copies.
+//   warp 10     per stage, tcgen05.cp of the scale tiles into the stage's TMEM slot, then the MMAs.
+// A stage takes about 280 ns whatever its width (four MMAs of at least 65 cycles, the scale copies and the barriers
+// around them), so a product with fewer tiles than SMs splits K over a cluster of S CTAs. The CTAs of ranks 1 .. send
+// their fp32 partial tiles into buffers of rank 0's shared memory (st.async, counted in bytes on a barrier there),
+// and rank 0 adds them to its own in rank order: deterministic, and one trip between SMs instead of a barrier of the
+// cluster, a trip there and back and another barrier (1.8 us for one row).
+// With more tiles than SMs the grid walks them with a static stride, and the epilogue moves the accumulator to
+// registers before the next tile's MMAs need it.
 //
 // A 128 x 4 scale tile spans 64 K elements in NVFP4, one MMA, and 128 in MXFP4, two MMAs: there the instruction
 // descriptor's scale-factor ids pick bytes 0-1 or 2-3 of each row's four. The last stage of a K that is no
-// multiple of 256 issues only the MMAs that hold elements; TMA may load scale tiles of the next row tile behind
-// it, which no MMA reads. Elements past K inside an MMA have zero codes and a zero scale byte.
+// multiple of 256 issues only the MMAs that hold elements, and loads the scale tiles that exist. Elements past K
+// inside an MMA have zero codes and a zero scale byte. Rows of A that were
+// not loaded, and their scales, are whatever shared memory held: rows of an MMA are independent, and these are
+// dropped.
 //
 // Every wait is bounded (common.cuh): one that runs out sets FP4MOE_ERR_TIMEOUT in the caller's error word,
 // copies and MMAs in flight are drained, and the CTA frees its TMEM and returns.
+#include <algorithm>
+#include <climits>
 #include <mutex>
 
-#include "common.cuh"
-#include "dense.cuh"
 #include "internal.h"
+#include "mxdense.cuh"
 
 namespace fp4moe {
-
-bool encode_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint32_t box_rows);
-bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles);
-
 namespace {
 
-constexpr int DBM = 128;       // rows of A per tile (MMA M)
-constexpr int DK = 256;        // K elements per ring stage: 128 bytes of codes, 4 MMAs of K = 64
-constexpr int DEPI = 8;        // epilogue warps
-constexpr int DNCOPY = 2;      // scale copier warps
-constexpr int DTHREADS = 32 * (DEPI + 2 + DNCOPY);
-constexpr int DPRODUCER = DEPI, DMMA = DEPI + 1, DCOPY0 = DEPI + 2;
-constexpr uint32_t DTMEM_COLS = 512;
+constexpr int DBM = 128;          // rows of A per tile (MMA M); BN rows of B (MMA N)
+constexpr int DEPI = 8;           // epilogue warps
+constexpr int DPRODUCER = DEPI, DMMA = DEPI + 2;  // two producer warps
+constexpr int DTHREADS = 32 * (DEPI + 3);
+constexpr int kSmemMax = 232448;  // shared memory of a CTA
 
-// Sizes of one kernel instance.
+struct TileMaps {
+  CUtensorMap a, b;
+};
+
 template <int FMT, int BN>
 struct DenseCfg {
   static constexpr int kSfTiles = FMT == FP4MOE_W_MXFP4 ? 2 : 4;  // scale tiles per 128 rows of a stage
-  static constexpr int kHalves = BN / 128;
-  static constexpr int kA = DBM * 128, kB = BN * 128;
-  static constexpr int kSfa = kSfTiles * 512, kSfb = kHalves * kSfTiles * 512;
-  static constexpr int kBytes = kA + kB + kSfa + kSfb;
-  static constexpr int kStage = (kBytes + 1023) / 1024 * 1024;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kBarOff = kStages * kStage;
-  static constexpr int kSmem = kBarOff + 256 + 1024;  // barriers + 1024-byte alignment slack
-  static constexpr uint32_t kSlotCols = 4 * kSfTiles * (1 + kHalves);  // TMEM columns of one stage's scales
-  static constexpr int kCopies = kSfTiles * (1 + kHalves);
-  static_assert(BN + kSlotCols * kStages <= DTMEM_COLS, "accumulator and scale slots fit TMEM");
-  static_assert(kSmem <= 232448 - 64, "shared memory budget");
-  static_assert(8 * (3 * kStages + 4) <= 256, "barriers fit their area");
-};
-
-struct DenseMaps {
-  CUtensorMap a, b, sfa, sfb;
-};
-
-struct DenseParams {
-  int M, N, K;
-  int KB;            // ring stages per tile
-  int mt, nt;        // output tiles along M and N
-  int ct;            // scale tiles across K
-  const float* alpha;
-  void* out;
-  int vec;           // rows of out start 16-byte aligned
-  uint32_t* err;
+  static_assert(BN % 64 == 0, "scale addresses are even");
+  static constexpr int kB = BN * 128;
+  static constexpr int kSf = kSfTiles * 512;
+  // Bytes of a stage: A's rows that are loaded (16, 32, 64 or 128 of 128 bytes), B, the scales. The MMA reads 128
+  // rows of A all the same; what follows the loaded ones gives rows that are dropped.
+  __host__ __device__ static constexpr int stage(int a_rows) { return a_rows * 128 + kB + 2 * kSf; }
+  static constexpr int kMaxStages = 8;
+  static constexpr uint32_t kSlotCols = 4 * kSfTiles * 2;  // TMEM columns of one stage's scales
+  // Shared memory: a ring of n stages, the rows of A that the last stage's MMAs read past it, S - 1 partial tiles of
+  // `a_rows` rows, staging, barriers.
+  __host__ __device__ static constexpr int tail(int a_rows) {
+    const int past = (DBM - a_rows) * 128 - kB - 2 * kSf;
+    return past > 0 ? past : 0;
+  }
+  __host__ __device__ static constexpr int parts(int S, int a_rows) { return (S - 1) * a_rows * BN * 4; }
+  static constexpr int smem(int n, int a_rows, int S) {
+    return n * stage(a_rows) + tail(a_rows) + parts(S, a_rows) + DEPI * kEpiStage + 256;
+  }
+  static constexpr uint32_t tmem(int n) {
+    const uint32_t cols = BN + kSlotCols * (uint32_t)n;
+    return cols <= 128 ? 128u : cols <= 256 ? 256u : 512u;
+  }
+  // stages that fit, 0 if none does
+  static int fit(int a_rows, int S) {
+    int n = kMaxStages;
+    while (n > 0 && (smem(n, a_rows, S) > kSmemMax || BN + kSlotCols * (uint32_t)n > 512u)) --n;
+    return n;
+  }
+  static_assert(stage(16) % 1024 == 0, "stage must keep 1024-byte alignment");
+  static_assert(8 * (2 * kMaxStages + 4) <= 240, "barriers fit their area");
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T with block scales in TMEM (K = 64).
@@ -93,221 +100,281 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t adesc, uint64_t b
     tc_mma_nvf4(d, adesc, bdesc, idesc, sfa, sfb, accumulate);
 }
 
-// Instruction descriptor: idesc_nvf4, with E8M0 scales and the scale-factor ids of the MMA's half for MXFP4.
-template <int FMT>
-__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t sf_id) {
-  return idesc_nvf4(M, N) | (FMT == FP4MOE_W_MXFP4 ? (1u << 23) | (sf_id << 4) | (sf_id << 29) : 0u);
-}
-
-// Columns [0, n) of v into row pointer p (n <= 32): 16-byte stores where the row allows them.
-template <typename T>
-__device__ __forceinline__ void store_row(T* p, const float* v, int n, bool vec) {
-  constexpr int V = 16 / (int)sizeof(T);
-  if (vec) {  // n is a multiple of V, or at least 32
-#pragma unroll
-    for (int i = 0; i < 32; i += V) {
-      if (i < n) {
-        alignas(16) T t[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) t[j] = from_f32<T>(v[i + j]);
-        *reinterpret_cast<uint4*>(p + i) = *reinterpret_cast<const uint4*>(t);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) p[i] = from_f32<T>(v[i]);
-  }
-}
-
+// Grid (tiles or persistent CTAs, 1, S), cluster (1, 1, S). stages: ring depth; tmem_cols: a power of two that holds the accumulator and the stages' scales.
 template <int FMT, int BN, typename T>
 __global__ void __launch_bounds__(DTHREADS, 1)
-    mx_dense_kernel(const __grid_constant__ DenseMaps maps, const DenseParams prm) {
+    mx_dense_kernel(const __grid_constant__ TileMaps maps, const DenseParams prm, int stages, int a_rows,
+                    uint32_t tmem_cols) {
   using C = DenseCfg<FMT, BN>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bar_full = smem + C::kBarOff;
-  const uint32_t bar_empty = bar_full + 8 * C::kStages;
-  const uint32_t bar_sready = bar_empty + 8 * C::kStages;
-  const uint32_t bar_tfull = bar_sready + 8 * C::kStages;
+  constexpr int W = BN / 2;  // columns of one epilogue warp
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of the CTA's shared memory: no static part shifts it
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t smem = smem_u32(smem_raw);
+  const int a_bytes = a_rows * 128, stage_bytes = a_bytes + C::kB + 2 * C::kSf;
+  const int S = gridDim.z, z = blockIdx.z;
+  const int ring = stages * stage_bytes + C::tail(a_rows), parts = C::parts(S, a_rows);
+  uint8_t* const epi_stage = smem_raw + ring + parts;
+  const int bar_off = ring + parts + DEPI * kEpiStage;
+  const uint32_t bar_full = smem + bar_off;
+  const uint32_t bar_empty = bar_full + 8 * C::kMaxStages;
+  const uint32_t bar_tfull = bar_empty + 8 * C::kMaxStages;
   const uint32_t bar_tempty = bar_tfull + 8;
   const uint32_t bar_drain = bar_tempty + 8;
-  const uint32_t bar_cdrain = bar_drain + 8;
+  const uint32_t bar_parts = bar_drain + 8;  // rank 0: the partial tiles of the others have arrived
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 240);
+  uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 244);
 
   if (warp == 0) {
-    tmem_alloc(smem_u32(&s_tmem), DTMEM_COLS);
+    tmem_alloc(smem_u32(&s_tmem), tmem_cols);
     tmem_relinquish();
   }
   if (threadIdx.x == 32 * DPRODUCER) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(bar_full + 8 * s, 2);  // the producers
       mbar_init(bar_empty + 8 * s, 1);
-      mbar_init(bar_sready + 8 * s, DNCOPY);
     }
     mbar_init(bar_tfull, 1);
     mbar_init(bar_tempty, DEPI);
     mbar_init(bar_drain, 1);
-    mbar_init(bar_cdrain, DNCOPY);
+    mbar_init(bar_parts, 1);
     fence_mbar_init();
+    prefetch_map(&maps.a);
+    prefetch_map(&maps.b);
   }
+  __syncwarp();
+  if (S > 1) cluster_sync();  // rank 0's barrier is ready (before the wait for the previous kernel, which hides it)
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) s_abort = (*(volatile uint32_t*)prm.err & kAbortMask) != 0;
+  if (threadIdx.x == 0) {
+    s_abort = (*(volatile uint32_t*)prm.err & kAbortMask) != 0 ? 1u : 0u;
+    if ((smem & 1023u) != 0) {  // the swizzle needs it, and the compiler grants it
+      raise_error(prm.err, FP4MOE_ERR_CAPACITY);
+      s_abort = 1u;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
   // an earlier timeout poisons the call: no role takes a tile
   const int tiles = s_abort ? 0 : prm.mt * prm.nt;
-  const int KB = prm.KB;
+  const int kb0 = prm.KB * z / S, kb1 = prm.KB * (z + 1) / S;  // this slice's stages, one at least
 
-  if (warp == DPRODUCER && lane == 0) {
+  if (S > 1 && z == 0 && threadIdx.x == 32 * DMMA) {
+    // bytes that the others send: their columns in N by halves of the tile, rows in M
+    const int n = (int)blockIdx.x / prm.mt * BN, m = (int)blockIdx.x % prm.mt * DBM;
+    const int halves = prm.N - n > W ? 2 : 1;
+    mbar_arrive_expect_tx(bar_parts, (uint32_t)((S - 1) * min(prm.M - m, DBM) * halves * W * 4));
+  }
+  __syncwarp();
+  if ((warp == DPRODUCER || warp == DPRODUCER + 1) && lane == 0) {
+    const bool is_b = warp != DPRODUCER;
     const uint64_t pol = policy_evict_normal();
-    int it = 0;
+    const uint32_t code_bytes = is_b ? (uint32_t)C::kB : (uint32_t)a_bytes;
+    const uint32_t dst = is_b ? (uint32_t)a_bytes : 0u, sf_dst = (uint32_t)(a_bytes + C::kB) + (is_b ? C::kSf : 0u);
+    const CUtensorMap* map = is_b ? &maps.b : &maps.a;
+    int it = 0, s = 0;
+    uint32_t ph = 1;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const int m = t % prm.mt, n = t / prm.mt;
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int s = it % C::kStages;
-        if (!mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / C::kStages) & 1u) ^ 1u, prm.err)) {
+      const int row = is_b ? t / prm.mt * BN : t % prm.mt * DBM;
+      const uint8_t* sf = (is_b ? prm.b_sf : prm.a_sf) + 512 * (size_t)(row / 128) * prm.ct;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        if (!mbar_wait(bar_empty + 8 * s, ph, prm.err)) {
           ok = false;
           break;
         }
-        const uint32_t st = smem + s * C::kStage, full = bar_full + 8 * s;
-        mbar_arrive_expect_tx(full, C::kBytes);
-        tma_load_2d(st, &maps.a, full, kb * 128, m * DBM, pol);
-        tma_load_2d(st + C::kA, &maps.b, full, kb * 128, n * BN, pol);
-        tma_load_2d(st + C::kA + C::kB, &maps.sfa, full, 0, m * prm.ct + kb * C::kSfTiles, pol);
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h)
-          tma_load_2d(st + C::kA + C::kB + C::kSfa * (1 + h), &maps.sfb, full, 0,
-                      (n * C::kHalves + h) * prm.ct + kb * C::kSfTiles, pol);
+        const uint32_t st = smem + s * stage_bytes, full = bar_full + 8 * s;
+        const uint32_t sf_bytes = 512u * (uint32_t)min(C::kSfTiles, prm.ct - kb * C::kSfTiles);
+        mbar_arrive_expect_tx(full, code_bytes + sf_bytes);
+        tma_load_2d(st + dst, map, full, kb * 128, row, pol);
+        bulk_load(st + sf_dst, sf + 512 * (size_t)(kb * C::kSfTiles), sf_bytes, full, pol);
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
     }
     // on every path, let the copies already issued land before the CTA exits
-    for (int j = max(0, it - C::kStages); j < it; ++j)
-      drain_wait(bar_full + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
-  } else if (warp == DMMA && lane == 0) {
+    for (int j = max(0, it - stages); j < it; ++j)
+      drain_wait(bar_full + 8 * (j % stages), (uint32_t)(j / stages) & 1u);
+  } else if (warp == DMMA) {
+    const bool leader = elect_one();
     int tl = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
+    // A scale tile has one TMEM column for 32 rows, and a scale address is even (an odd one raises "misaligned
+    // address"), so an output tile begins at row 0 or 64 of a scale tile and none is narrower than 64.
+    uint32_t sfb_col = 0;
+    auto mma = [&](uint32_t st, uint32_t slot, int a, uint32_t acc) {
+      constexpr bool mx = FMT == FP4MOE_W_MXFP4;
+      const int tile = mx ? a >> 1 : a;
+      tc_mma_mx<FMT>(tmem, desc_sw128(st + 32 * a), desc_sw128(st + a_bytes + 32 * a),
+                     idesc_mx<FMT>(DBM, BN, mx ? 2 * (a & 1) : 0), slot + 4 * tile,
+                     slot + 4 * C::kSfTiles + 4 * tile + sfb_col, acc);
+    };
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tl) {
       // the epilogue has moved the previous tile's accumulator out of TMEM
-      if (!mbar_wait(bar_tempty, ((uint32_t)tl & 1u) ^ 1u, prm.err)) break;
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait(bar_full + 8 * s, ph, prm.err) || !mbar_wait(bar_sready + 8 * s, ph, prm.err)) {
+      if (!mbar_wait_warp(bar_tempty, ((uint32_t)tl & 1u) ^ 1u, prm.err)) break;
+      if constexpr (BN < 128) sfb_col = (uint32_t)(t / prm.mt % (128 / BN) * (BN / 32));
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_warp(bar_full + 8 * s, ph, prm.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t st = smem + (uint32_t)s * C::kStage;
-        const uint32_t sfa = tmem + BN + C::kSlotCols * s, sfb = sfa + 4 * C::kSfTiles;
-        const int atoms = min(4, (prm.K - kb * DK + 63) / 64);
+        const uint32_t st = smem + (uint32_t)(s * stage_bytes), slot = tmem + BN + C::kSlotCols * s;
+        const int atoms = (prm.K - kb * DK + 63) / 64;  // of this stage and those behind it
+        if (leader) {
+          // Copies and MMAs of one thread execute in order, and slot s is free: its last MMAs committed bar_empty.
+          const uint32_t sf = st + a_bytes + C::kB;
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          if (a < atoms) {
-            constexpr bool mx = FMT == FP4MOE_W_MXFP4;
-            const int tile = mx ? a >> 1 : a;
-            tc_mma_mx<FMT>(tmem, desc_sw128(st + 32 * a), desc_sw128(st + C::kA + 32 * a),
-                           idesc_mx<FMT>(DBM, BN, mx ? 2 * (a & 1) : 0), sfa + 4 * tile, sfb + 4 * C::kHalves * tile,
-                           (kb > 0 || a > 0) ? 1u : 0u);
-          }
-        }
-        tc_commit(bar_empty + 8 * s);
-        if (++s == C::kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      if (ok) tc_commit(bar_tfull);
-    }
-    tc_commit(bar_drain);
-    drain_wait(bar_drain, 0);  // no MMA may still write TMEM when it is freed
-  } else if (warp >= DCOPY0 && lane == 0) {
-    // Copy i: A tile i, then B tile j half h at column 4 (kHalves j + h), so that an N = 256 MMA finds the two
-    // 128-row halves side by side. TMEM slot s is free once stage s is full again: the producer refilled it
-    // only after the MMAs of the slot's previous use committed bar_empty.
-    const int cpy = warp - DCOPY0;
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait(bar_full + 8 * s, ph, prm.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sf = smem + (uint32_t)s * C::kStage + C::kA + C::kB;
-        const uint32_t slot = tmem + BN + C::kSlotCols * s;
+          for (int i = 0; i < 2 * C::kSfTiles; ++i) tc_cp_scales(slot + 4 * i, desc_scales(sf + 512 * i));
+          if (atoms >= 4) {
 #pragma unroll
-        for (int i = cpy; i < C::kCopies; i += DNCOPY) {
-          if (i < C::kSfTiles) {
-            tc_cp_scales(slot + 4 * i, desc_scales(sf + 512 * i));
+            for (int a = 0; a < 4; ++a) mma(st, slot, a, (kb > kb0 || a > 0) ? 1u : 0u);
           } else {
-            const int j = (i - C::kSfTiles) / C::kHalves, h = (i - C::kSfTiles) % C::kHalves;
-            tc_cp_scales(slot + 4 * C::kSfTiles + 4 * (C::kHalves * j + h),
-                         desc_scales(sf + C::kSfa * (1 + h) + 512 * j));
+#pragma unroll
+            for (int a = 0; a < 3; ++a)
+              if (a < atoms) mma(st, slot, a, (kb > kb0 || a > 0) ? 1u : 0u);
           }
+          tc_commit(bar_empty + 8 * s);
         }
-        tc_commit(bar_sready + 8 * s);
-        if (++s == C::kStages) {
+        __syncwarp();
+        if (++s == stages) {
           s = 0;
           ph ^= 1u;
         }
       }
+      if (ok && leader) tc_commit(bar_tfull);
     }
-    tc_commit(bar_cdrain);
-    drain_wait(bar_cdrain, 0);  // no copy may still write TMEM when it is freed
+    if (leader) {
+      tc_commit(bar_drain);
+      drain_wait(bar_drain, 0);  // no MMA may still write TMEM when it is freed
+    }
   } else if (warp < DEPI) {
-    constexpr int W = BN / 2;  // columns of one warp
     const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t tacc = tmem + (uint32_t)(W * half) + ((uint32_t)(quarter * 32) << 16);
     const float alpha = prm.alpha != nullptr ? __ldg(prm.alpha) : 1.0f;
     int tl = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++tl) {
       const int m = t % prm.mt, n = t / prm.mt;
-      const int r0 = m * DBM + quarter * 32;
-      const int r = r0 + lane, c0 = n * BN + W * half;
+      const int r0 = m * DBM + quarter * 32, c0 = n * BN + W * half;
       // the whole warp takes one decision: tcgen05.ld is warp-collective
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_tfull, (uint32_t)tl & 1u, prm.err) ? 1 : 0)) break;
+      if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) break;
       tc_fence_after();
       const bool live = r0 < prm.M && c0 < prm.N;
-      float v[W];
-      if (live) {
-        const uint32_t tacc = tmem + (uint32_t)(W * half) + ((uint32_t)(quarter * 32) << 16);
+      if (S > 1) {  // one tile a cluster
+        const int row = quarter * 32 + lane;  // of the tile
+        // row i, 16-byte chunk j of a partial tile at i * BN * 4 + (j ^ i % 8) * 16: free of bank conflicts
+        auto chunk = [&](int j) { return (uint32_t)(row * BN * 4 + ((W * half / 4 + j) ^ (row & 7)) * 16); };
+        if (z > 0) {
+          const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
+          if (live) {
 #pragma unroll
-        for (int c = 0; c < W / 32; ++c) {
-          float q[32];
-          tmem_ld32(tacc + c * 32, q);
+            for (int c = 0; c < W; c += 32) {
+              float q[32];
+              tmem_ld32(tacc + c, q);
+              tmem_ld_wait();
+              if (r0 + lane < prm.M) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[c * 32 + j] = q[j];
+                for (int j = 0; j < 8; ++j)
+                  st_async_16(dst + chunk(c / 4 + j), q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3], bar);
+              }
+            }
+          }
+          continue;
         }
-        tmem_ld_wait();
+        float v[W];
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < W; c += 32) {
+            float q[32];
+            tmem_ld32(tacc + c, q);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c + j] = q[j];
+          }
+        }
+        if (!mbar_wait_warp(bar_parts, 0, prm.err)) break;
+        if (!live) continue;
+        if (row < a_rows) {  // (the rows past M in it hold nothing that is stored)
+          for (int p = 0; p < S - 1; ++p) {
+            const uint8_t* src = smem_raw + ring + p * a_rows * BN * 4;
+#pragma unroll
+            for (int j = 0; j < W / 4; ++j) {
+              const float4 q = *reinterpret_cast<const float4*>(src + chunk(j));
+              v[4 * j] += q.x;
+              v[4 * j + 1] += q.y;
+              v[4 * j + 2] += q.z;
+              v[4 * j + 3] += q.w;
+            }
+          }
+        }
+        constexpr int COLS = 64 / (int)sizeof(T);
+#pragma unroll
+        for (int c = 0; c < W; c += COLS) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if constexpr (sizeof(T) == 4)
+              w[j] = __float_as_uint(v[c + j] * alpha);
+            else
+              w[j] = pack2<T>(v[c + 2 * j] * alpha, v[c + 2 * j + 1] * alpha);
+          }
+          if (c0 + c < prm.N)
+            store_chunk(epi_stage + warp * kEpiStage, w, static_cast<T*>(prm.out), prm.M, prm.N, r0, c0 + c, lane,
+                        prm.vec);
+        }
+        continue;
       }
+      uint32_t w[W * sizeof(T) / 4];
+      if (live) load_packed<T, W>(tacc, alpha, w);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_tempty);  // this warp's share of the accumulator is out of TMEM
-      if (live && r < prm.M) {
+      if (live) {
+        constexpr int COLS = 64 / (int)sizeof(T);
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] *= alpha;
-        T* row = static_cast<T*>(prm.out) + (size_t)r * prm.N;
-#pragma unroll
-        for (int c = 0; c < W; c += 32)
-          if (c0 + c < prm.N) store_row(row + c0 + c, v + c, prm.N - c0 - c, prm.vec != 0);
+        for (int c = 0; c < W; c += COLS)
+          if (c0 + c < prm.N)
+            store_chunk(epi_stage + warp * kEpiStage, w + c * (int)sizeof(T) / 4, static_cast<T*>(prm.out), prm.M,
+                        prm.N, r0, c0 + c, lane, prm.vec);
       }
     }
   }
 
+  if (S > 1) {
+    __syncwarp();  // the single-thread roles reconverge: cluster barriers are warp-aligned instructions
+    cluster_sync();  // on every path, no CTA leaves while another may still write to it
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, DTMEM_COLS);
+    tmem_dealloc(tmem, tmem_cols);
   }
+}
+
+// Rows of A that a tile loads.
+int rows_loaded(int M) { return M > 64 ? 128 : M > 32 ? 64 : M > 16 ? 32 : 16; }
+
+// Launch attributes of a split over S CTAs; PDL as in launch_pdl.
+cudaLaunchConfig_t dense_config(unsigned grid, int S, size_t smem, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, (unsigned)S);
+  lc.blockDim = dim3(DTHREADS);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = (unsigned)S;
+  lc.attrs = attr;
+  lc.numAttrs = S > 1 ? 2 : 1;
+  return lc;
 }
 
 template <int FMT, int BN, typename T>
@@ -315,54 +382,95 @@ bool dense_configure() {
   static int ok = -1;
   static std::once_flag once;
   std::call_once(once, [] {
-    ok = cudaFuncSetAttribute(mx_dense_kernel<FMT, BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              DenseCfg<FMT, BN>::kSmem) == cudaSuccess
+    ok = cudaFuncSetAttribute(mx_dense_kernel<FMT, BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) ==
+                 cudaSuccess
              ? 1
              : 0;
   });
   return ok == 1;
 }
 
+// Which kernel, and how. Fitted times of the variants in ns, measured back to back at 26 sizes from 1 x 4096 x 256 to
+// 8192 x 8192 x 2048 (bf16 out): the one picked is within 6 % of the fastest at all of them. KB: 256-element stages of K.
+//   128 x 64, 128 x 128    a launch, then 270 or 280 a stage and 500 a tile (measured 270 .. 310 a stage)
+//   split over S CTAs      KB / S stages; joining: 800, and a fifth of a ns for each fp32 value that is sent
+//   256 x 256 on a pair    2150 a tile beside its stages at 316, or 284 with two pairs in a cluster
+struct Plan {
+  int pairs;  // 0: this file's kernel, with bn and S
+  int bn, S;
+};
+Plan pick_plan(int M, int N, int KB, int nsm) {
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  Plan best{0, 128, 1};
+  int64_t best_ns = INT64_MAX;
+  auto offer = [&](Plan p, int64_t ns) {
+    if (ns < best_ns) {
+      best_ns = ns;
+      best = p;
+    }
+  };
+  for (int bn : {64, 128}) {
+    const int64_t tiles = up(M, DBM) * up(N, bn), stage = bn == 64 ? 270 : 280, launch = bn == 64 ? 2500 : 2650;
+    offer({0, bn, 1}, launch + up(tiles, nsm) * (KB * stage + 500));
+    if (M > 64) continue;  // more rows cost more to join than the split saves
+    for (int S : {2, 4})   // a cluster of four leaves an eighteenth of the SMs without one
+      if (S <= KB && tiles * S <= (S == 2 ? nsm : nsm - nsm / 18))
+        offer({0, bn, S}, launch + 500 + up(KB, S) * stage + 800 + (int64_t)(S - 1) * M * bn / 5);
+  }
+  for (int pairs : {1, 2}) {
+    const int64_t tiles = up(M, 256 * pairs) * up(N, 256);
+    const int64_t clusters = pairs == 1 ? nsm / 2 : (nsm - nsm / 18) / 4;
+    if (clusters > 0) offer({pairs, 0, 1}, 3200 + up(tiles, clusters) * (KB * (pairs == 1 ? 316 : 284) + 2150));
+  }
+  return best;
+}
+
 template <int FMT, int BN, typename T>
-fp4moe_status dense_run(DenseParams prm, const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
-                        int nsm, cudaStream_t st) {
+fp4moe_status dense_run(DenseParams prm, int S, const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
+                        const uint8_t* b_sf, int nsm, cudaStream_t st) {
   using C = DenseCfg<FMT, BN>;
+  prm.mt = (prm.M + DBM - 1) / DBM;
   prm.nt = (prm.N + BN - 1) / BN;
-  DenseMaps maps;
+  const int a_rows = rows_loaded(prm.M);
+  // a ring no deeper than the slice, so that the next launch's CTAs find room beside this one's
+  const int stages = std::min(C::fit(a_rows, S), (prm.KB + S - 1) / S);
+  if (stages <= 0) return FP4MOE_UNSUPPORTED;  // (not reached: pick_plan splits 64 rows or fewer, four ways at most)
+  prm.a_sf = a_sf;
+  prm.b_sf = b_sf;
+  TileMaps maps;
   const uint64_t rb = (uint64_t)mx_row_bytes(prm.K);
-  if (!encode_u8_sw128(&maps.a, a, rb, (uint64_t)prm.M, DBM) || !encode_u8_sw128(&maps.b, b, rb, (uint64_t)prm.N, BN) ||
-      !encode_scale_tiles(&maps.sfa, a_sf, (uint64_t)mx_row_tiles(prm.M) * prm.ct, C::kSfTiles) ||
-      !encode_scale_tiles(&maps.sfb, b_sf, (uint64_t)mx_row_tiles(prm.N) * prm.ct, C::kSfTiles))
+  if (!encode_u8_sw128(&maps.a, a, rb, (uint64_t)prm.M, (uint32_t)a_rows) ||
+      !encode_u8_sw128(&maps.b, b, rb, (uint64_t)prm.N, BN))
     return FP4MOE_CUDA_ERROR;
   if (!dense_configure<FMT, BN, T>()) return FP4MOE_CUDA_ERROR;
   const int tiles = prm.mt * prm.nt;
-  const unsigned grid = (unsigned)(tiles < nsm ? tiles : nsm);
-  return launch_pdl(mx_dense_kernel<FMT, BN, T>, dim3(grid), dim3(DTHREADS), C::kSmem, st, maps, prm) == cudaSuccess
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t lc =
+      dense_config((unsigned)(S > 1 ? tiles : std::min(tiles, nsm)), S, C::smem(stages, a_rows, S), st, attr);
+  return cudaLaunchKernelEx(&lc, mx_dense_kernel<FMT, BN, T>, maps, prm, stages, a_rows, C::tmem(stages)) ==
+                 cudaSuccess
              ? FP4MOE_OK
              : FP4MOE_CUDA_ERROR;
 }
 
-template <int FMT, typename T>
-fp4moe_status dense_pick(const DenseParams& prm, const uint8_t* a, const uint8_t* a_sf, const uint8_t* b,
-                         const uint8_t* b_sf, cudaStream_t st) {
-  const int nsm = sm_count();
-  if (nsm <= 0) return FP4MOE_CUDA_ERROR;
-  // 128 x 256 tiles once they fill the device; smaller products spread over more CTAs with 128 x 128 tiles.
-  if ((int64_t)prm.mt * ((prm.N + 255) / 256) >= nsm) return dense_run<FMT, 256, T>(prm, a, a_sf, b, b_sf, nsm, st);
-  return dense_run<FMT, 128, T>(prm, a, a_sf, b, b_sf, nsm, st);
+template <int FMT, int BN>
+fp4moe_status dense_typed(int32_t dtype, const DenseParams& prm, int S, const uint8_t* a, const uint8_t* a_sf,
+                          const uint8_t* b, const uint8_t* b_sf, int nsm, cudaStream_t st) {
+  switch (dtype) {
+    case FP4MOE_BF16:
+      return dense_run<FMT, BN, __nv_bfloat16>(prm, S, a, a_sf, b, b_sf, nsm, st);
+    case FP4MOE_FP16:
+      return dense_run<FMT, BN, __half>(prm, S, a, a_sf, b, b_sf, nsm, st);
+    default:
+      return dense_run<FMT, BN, float>(prm, S, a, a_sf, b, b_sf, nsm, st);
+  }
 }
 
 template <int FMT>
-fp4moe_status dense_typed(int32_t dtype, const DenseParams& prm, const uint8_t* a, const uint8_t* a_sf,
-                          const uint8_t* b, const uint8_t* b_sf, cudaStream_t st) {
-  switch (dtype) {
-    case FP4MOE_BF16:
-      return dense_pick<FMT, __nv_bfloat16>(prm, a, a_sf, b, b_sf, st);
-    case FP4MOE_FP16:
-      return dense_pick<FMT, __half>(prm, a, a_sf, b, b_sf, st);
-    default:
-      return dense_pick<FMT, float>(prm, a, a_sf, b, b_sf, st);
-  }
+fp4moe_status dense_width(int bn, int32_t dtype, const DenseParams& prm, int S, const uint8_t* a, const uint8_t* a_sf,
+                          const uint8_t* b, const uint8_t* b_sf, int nsm, cudaStream_t st) {
+  return bn == 64 ? dense_typed<FMT, 64>(dtype, prm, S, a, a_sf, b, b_sf, nsm, st)
+                  : dense_typed<FMT, 128>(dtype, prm, S, a, a_sf, b, b_sf, nsm, st);
 }
 
 }  // namespace
@@ -374,15 +482,22 @@ fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t 
   prm.M = M;
   prm.N = N;
   prm.K = K;
-  prm.KB = (K + DK - 1) / DK;
-  prm.mt = (M + DBM - 1) / DBM;
+  prm.KB = (int)(((int64_t)K + DK - 1) / DK);
   prm.ct = (int)mx_col_tiles(format, K);
   prm.alpha = alpha;
   prm.out = out;
-  prm.vec = ((int64_t)N * (dtype == FP4MOE_FP32 ? 4 : 2)) % 16 == 0 ? 1 : 0;
+  const int64_t pitch = (int64_t)N * (dtype == FP4MOE_FP32 ? 4 : 2);
+  prm.vec = pitch % 32 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 5
+            : pitch % 16 == 0                                                ? 4
+            : pitch % 4 == 0                                                 ? 2
+                                                                             : 1;
   prm.err = err;
-  return format == FP4MOE_W_MXFP4 ? dense_typed<FP4MOE_W_MXFP4>(dtype, prm, a, a_sf, b, b_sf, st)
-                                  : dense_typed<FP4MOE_W_NVFP4>(dtype, prm, a, a_sf, b, b_sf, st);
+  const int nsm = sm_count();
+  if (nsm <= 0) return FP4MOE_CUDA_ERROR;
+  const Plan plan = pick_plan(M, N, prm.KB, nsm);
+  if (plan.pairs > 0) return mx_pair_launch(format, dtype, plan.pairs, prm, a, a_sf, b, b_sf, st);
+  return format == FP4MOE_W_MXFP4 ? dense_width<FP4MOE_W_MXFP4>(plan.bn, dtype, prm, plan.S, a, a_sf, b, b_sf, nsm, st)
+                                  : dense_width<FP4MOE_W_NVFP4>(plan.bn, dtype, prm, plan.S, a, a_sf, b, b_sf, nsm, st);
 }
 
 }  // namespace fp4moe

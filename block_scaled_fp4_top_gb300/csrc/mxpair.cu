@@ -1,0 +1,412 @@
+// Dense product of two microscaled 4-bit matrices on CTA pairs: the large sizes of mxdense.cu.
+//
+// A pair of CTAs owns a 256 x 256 output tile: tcgen05.mma.cta_group::2 of M = 256, N = 256, K = 64, issued by the
+// pair's leader (its even CTA), reads 128 rows of A and 128 rows of B from each CTA's shared memory and leaves
+// 128 x 256 fp32 in each CTA's TMEM. Against 128 x 256 tiles on single CTAs that halves the B bytes an SM stages
+// and reads per MAC: those tiles need 12 KB through shared memory twice (in by TMA, out to the MMA) every 128
+// cycles, more than its 128 bytes a cycle.
+//   warps 0-7   epilogue, in both CTAs (warp w: TMEM lanes 32 (w % 4) .., columns 128 (w / 4) ..).
+//   warp 8      producer, in both CTAs: its own rows of A and B, the scale tiles of its own A rows and of all 256 B
+//               rows (the MMA reads B scales from each CTA's own TMEM). All loads signal the leader's barrier.
+//   warp 9      leader: scale copies (tcgen05.cp.cta_group::2, each CTA's tiles into its own TMEM) and MMAs.
+//               Other CTA: tells the leader that its epilogue warps have emptied the accumulator.
+// Commits that free a ring stage or hand over the accumulator arrive in both CTAs.
+//
+// PAIRS = 2: a cluster of two pairs owns 512 x 256. Both pairs need the same B, so each CTA loads half of its B rows
+// and a quarter of the B scales and multicasts them to the CTAs that need them: 25 instead of 35 KB per CTA and
+// stage out of L2. A stage is then free when both pairs' MMAs have read it.
+// The rest (scale-factor ids, K tails, bounded waits) is as in mxdense.cu.
+#include <mutex>
+
+#include "internal.h"
+#include "mxdense.cuh"
+
+namespace fp4moe {
+namespace {
+
+constexpr int PBM = 256, PBN = 256;  // the pair's tile
+constexpr int PEPI = 8;
+constexpr int PTHREADS = 32 * (PEPI + 2);
+constexpr int PPRODUCER = PEPI, PMMA = PEPI + 1;
+constexpr uint32_t PTMEM_COLS = 512;
+
+template <int FMT>
+struct PairCfg {
+  static constexpr int kSfTiles = FMT == FP4MOE_W_MXFP4 ? 2 : 4;  // scale tiles per 128 rows of a stage
+  static constexpr int kA = 128 * 128, kB = 128 * 128;            // this CTA's rows
+  static constexpr int kSfa = kSfTiles * 512, kSfb = 2 * kSfa;
+  static constexpr int kBytes = kA + kB + kSfa + kSfb;
+  static constexpr int kStage = kBytes;
+  static constexpr int kStages = FMT == FP4MOE_W_MXFP4 ? 6 : 5;
+  static constexpr int kEpiOff = kStages * kStage;  // the epilogue warps' staging areas
+  static constexpr int kBarOff = kEpiOff + PEPI * kEpiStage;
+  static constexpr int kSmem = kBarOff + 256;  // barriers, and two words of the CTA
+  static constexpr uint32_t kSlotCols = 4 * kSfTiles * 3;
+  static_assert(kStage % 1024 == 0, "stage must keep 1024-byte alignment");
+  static_assert(PBN + kSlotCols * kStages <= PTMEM_COLS, "accumulator and scale slots fit TMEM");
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(8 * (2 * kStages + 4) <= 240, "barriers fit their area");
+};
+
+// ------------------------------------------------------------- PTX, CTA pairs
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                 int32_t y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint [%0], "
+      "[%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+// The copy lands at `dst` in every CTA of `mask`, and signals `bar`'s offset in the leader of each one's pair.
+__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                           int32_t y, uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrive on this CTA's `bar` once every tcgen05 op this thread issued before has completed in both CTAs.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// The same on the barrier at this offset in every CTA of `mask`.
+__device__ __forceinline__ void pair_commit_to(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void pair_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  if constexpr (FMT == FP4MOE_W_MXFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// Arrive on a barrier of any CTA of the cluster (an address from map_cluster).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
+// Tile t: groups of 8 tile rows, so that the tiles of a wave share their operands' rows in L2.
+__device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
+  constexpr int G = 8;
+  const int g = t / (G * nt), first = g * G, rows = min(G, mt - first), in = t - g * G * nt;
+  m = first + in % rows;
+  n = in / rows;
+}
+
+template <int FMT, int PAIRS, typename T>
+__global__ void __launch_bounds__(PTHREADS, 1)
+    mx_pair_kernel(const __grid_constant__ DenseMaps maps, const DenseParams prm) {
+  using C = PairCfg<FMT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of the CTA's shared memory: no static part shifts it
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(smem_raw + C::kBarOff + 240);
+  uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + C::kBarOff + 244);
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, pair = crank >> 1, lead = crank & ~1u;
+  constexpr uint16_t kAll = (uint16_t)((1 << (2 * PAIRS)) - 1);
+  const uint32_t smem = smem_u32(smem_raw);
+  const uint32_t bar_full = smem + C::kBarOff;           // leader's: both CTAs' copies of a stage
+  const uint32_t bar_empty = bar_full + 8 * C::kStages;  // each CTA's own: every pair's MMAs have read the stage
+  const uint32_t bar_tfull = bar_empty + 8 * C::kStages; // each CTA's own: the accumulator is complete
+  const uint32_t bar_tempty = bar_tfull + 8;             // each CTA's own: its epilogue warps have read it
+  const uint32_t bar_tpeer = bar_tempty + 8;             // leader's: so have the other CTA's
+  const uint32_t bar_drain = bar_tpeer + 8;
+
+  if (warp == 0) pair_tmem_alloc(smem_u32(&s_tmem), PTMEM_COLS);
+  if (threadIdx.x == 32 * PPRODUCER) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, PAIRS);
+    }
+    mbar_init(bar_tfull, 1);
+    mbar_init(bar_tempty, PEPI);
+    mbar_init(bar_tpeer, 1);
+    mbar_init(bar_drain, 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    s_abort = (*(volatile uint32_t*)prm.err & kAbortMask) != 0 ? 1u : 0u;
+    if ((smem & 1023u) != 0) {  // the swizzle needs it, and the compiler grants it
+      raise_error(prm.err, FP4MOE_ERR_CAPACITY);
+      s_abort = 1u;
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers and TMEM of all CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
+  const int tiles = s_abort ? 0 : prm.mt * prm.nt;  // an earlier timeout poisons the call
+  const int KB = prm.KB, clusters = gridDim.x / (2 * PAIRS), cluster = blockIdx.x / (2 * PAIRS);
+
+  if (warp == PPRODUCER && lane == 0) {
+    const uint64_t pol = policy_evict_normal();
+    const uint32_t full0 = map_cluster(bar_full, lead);
+    int it = 0;
+    bool ok = true;
+    for (int t = cluster; ok && t < tiles; t += clusters) {
+      int m, n;
+      tile_of(t, prm.mt, prm.nt, m, n);
+      const int ar = 2 * (PAIRS * m + (int)pair) + (int)rank;  // 128-row tile of A
+      for (int kb = 0; kb < KB; ++kb, ++it) {
+        const int s = it % C::kStages;
+        if (!mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / C::kStages) & 1u) ^ 1u, prm.err)) {
+          ok = false;
+          break;
+        }
+        const uint32_t st = smem + s * C::kStage, full = full0 + 8 * s, sf = st + C::kA + C::kB;
+        if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * C::kBytes);
+        tma_load_2d_pair(st, &maps.a, full, kb * 128, ar * 128, pol);
+        tma_load_2d_pair(sf, &maps.sfa, full, 0, ar * prm.ct + kb * C::kSfTiles, pol);
+        if constexpr (PAIRS == 1) {
+          tma_load_2d_pair(st + C::kA, &maps.b, full, kb * 128, (2 * n + (int)rank) * 128, pol);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d_pair(sf + C::kSfa * (1 + h), &maps.sfb, full, 0, (2 * n + h) * prm.ct + kb * C::kSfTiles, pol);
+        } else {  // rows 64 pair .. of this rank's 128 B rows; half of the scale tiles of B rows 128 rank ..
+          tma_load_2d_pair_multicast(st + C::kA + pair * 8192u, &maps.b, full, kb * 128,
+                                     (2 * n + (int)rank) * 128 + 64 * (int)pair, (uint16_t)(5u << rank), pol);
+          constexpr int Q = C::kSfTiles / 2;
+          tma_load_2d_pair_multicast(sf + C::kSfa * (1 + rank) + 512u * Q * pair, &maps.sfb, full, 0,
+                                     (2 * n + (int)rank) * prm.ct + kb * C::kSfTiles + Q * (int)pair, kAll, pol);
+        }
+      }
+    }
+    // Let the copies already issued land before the CTA exits. A leader's barrier counts every copy into its
+    // pair. A CTA that gave up may have issued some that no leader armed: it leaves them time to land.
+    if (rank == 0) {
+      for (int j = max(0, it - C::kStages); j < it; ++j)
+        drain_wait(bar_full + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
+    }
+    if (!ok) {
+      for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
+      }
+    }
+  } else if (warp == PMMA && rank == 0) {
+    const bool leader = elect_one();
+    const uint16_t own = (uint16_t)(3u << lead);
+    int tl = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto mma = [&](uint32_t st, uint32_t slot, int a, uint32_t acc) {
+      constexpr bool mx = FMT == FP4MOE_W_MXFP4;
+      const int tile = mx ? a >> 1 : a;
+      pair_mma<FMT>(tmem, desc_sw128(st + 32 * a), desc_sw128(st + C::kA + 32 * a),
+                    idesc_mx<FMT>(PBM, PBN, mx ? 2 * (a & 1) : 0), slot + 4 * tile, slot + 4 * C::kSfTiles + 8 * tile,
+                    acc);
+    };
+    for (int t = cluster; ok && t < tiles; t += clusters, ++tl) {
+      // both epilogues have moved the previous tile's accumulator out of TMEM
+      const uint32_t tph = ((uint32_t)tl & 1u) ^ 1u;
+      if (!mbar_wait_warp(bar_tempty, tph, prm.err) || !mbar_wait_warp(bar_tpeer, tph, prm.err)) break;
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the peer's arrival comes from another CTA
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!mbar_wait_warp(bar_full + 8 * s, ph, prm.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = smem + (uint32_t)s * C::kStage, slot = tmem + PBN + C::kSlotCols * s;
+        const int atoms = (prm.K - kb * DK + 63) / 64;  // of this stage and those behind it
+        if (leader) {
+          // A tile i, then B tile j half h at column 4 (2 j + h): an N = 256 MMA takes the two halves side by side.
+          // Copies and MMAs of one thread execute in order, and slot s is free: its last MMAs committed bar_empty.
+          const uint32_t sf = st + C::kA + C::kB;
+#pragma unroll
+          for (int i = 0; i < C::kSfTiles; ++i) pair_cp_scales(slot + 4 * i, desc_scales(sf + 512 * i));
+#pragma unroll
+          for (int j = 0; j < C::kSfTiles; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              pair_cp_scales(slot + 4 * C::kSfTiles + 4 * (2 * j + h), desc_scales(sf + C::kSfa * (1 + h) + 512 * j));
+          if (atoms >= 4) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) mma(st, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int a = 0; a < 3; ++a)
+              if (a < atoms) mma(st, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
+          }
+          pair_commit_to(bar_empty + 8 * s, kAll);
+        }
+        __syncwarp();
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (ok && leader) pair_commit_to(bar_tfull, own);
+    }
+    if (leader) {
+      pair_commit(bar_drain);
+      drain_wait(bar_drain, 0);  // no MMA may still write TMEM when it is freed
+    }
+  } else if (warp == PMMA && lane == 0) {
+    // One arrival for eight warps, ahead of their stores: an arrival of each warp waited behind the stores of the
+    // warps before it, and the next tile began 1.2 us after the accumulator was read, not 0.5.
+    const uint32_t tpeer = map_cluster(bar_tpeer, lead);
+    int tl = 0;
+    for (int t = cluster; t < tiles; t += clusters, ++tl) {
+      if (!mbar_wait(bar_tempty, (uint32_t)tl & 1u, prm.err)) break;
+      mbar_arrive_cluster(tpeer);
+    }
+  } else if (warp < PEPI) {
+    constexpr int W = PBN / 2;  // columns of one warp
+    const int quarter = warp & 3, half = warp >> 2;
+    uint8_t* stage = smem_raw + C::kEpiOff + warp * kEpiStage;
+    const float alpha = prm.alpha != nullptr ? __ldg(prm.alpha) : 1.0f;
+    // Every pair ends its tile at the same time, and 10 MB of stores at once hold up the loads of the next tile. So
+    // all tiles but a pair's last spread theirs over about half of the next tile's MMAs (75 ns each): 8192 x 4096 x
+    // 4096 takes 53.1 us so, 55.2 without.
+    constexpr int kChunks = W * (int)sizeof(T) / 64;
+    const uint32_t pace = min(1000u, 150u * (uint32_t)KB / kChunks);
+    int tl = 0;
+    for (int t = cluster; t < tiles; t += clusters, ++tl) {
+      int m, n;
+      tile_of(t, prm.mt, prm.nt, m, n);
+      const int r0 = (PAIRS * m + (int)pair) * PBM + (int)rank * 128 + quarter * 32;
+      const int c0 = n * PBN + W * half;
+      // the whole warp takes one decision: tcgen05.ld is warp-collective
+      if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) break;
+      tc_fence_after();
+      const bool live = r0 < prm.M && c0 < prm.N;
+      uint32_t w[W * sizeof(T) / 4];
+      if (live) load_packed<T, W>(tmem + (uint32_t)(W * half) + ((uint32_t)(quarter * 32) << 16), alpha, w);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_tempty);  // this warp's share of the accumulator is out of TMEM
+      if (live) {
+        constexpr int COLS = 64 / (int)sizeof(T);
+#pragma unroll
+        for (int c = 0; c < W; c += COLS)
+          if (c0 + c < prm.N) {
+            if (t + clusters < tiles) __nanosleep(pace);
+            store_chunk(stage, w + c * (int)sizeof(T) / 4, static_cast<T*>(prm.out), prm.M, prm.N, r0, c0 + c, lane,
+                        prm.vec);
+          }
+      }
+    }
+  }
+  __syncwarp();  // the single-thread roles reconverge: cluster barriers are warp-aligned instructions
+  tc_fence_before();
+  cluster_sync();  // no CTA reads or signals another any more
+  if (warp == 0) {
+    tc_fence_after();
+    pair_tmem_dealloc(tmem, PTMEM_COLS);
+  }
+}
+
+// The cluster shape's launch attributes; PDL as in launch_pdl.
+template <int PAIRS>
+cudaLaunchConfig_t pair_config(unsigned clusters, size_t smem, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(2u * PAIRS * clusters);
+  lc.blockDim = dim3(PTHREADS);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * PAIRS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  return lc;
+}
+
+// Clusters that the device holds at once (the persistent grid); 0 on error. Cached per device.
+template <int FMT, int PAIRS, typename T>
+int pair_clusters() {
+  constexpr int kMaxDevices = 64;
+  static std::once_flag once[kMaxDevices];
+  static int count[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::call_once(once[dev], [dev] {
+    int n = 0;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t lc = pair_config<PAIRS>(1, PairCfg<FMT>::kSmem, nullptr, attr);
+    lc.numAttrs = 1;  // the cluster shape alone
+    if (cudaFuncSetAttribute(mx_pair_kernel<FMT, PAIRS, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PairCfg<FMT>::kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<FMT, PAIRS, T>, &lc) != cudaSuccess)
+      n = 0;
+    count[dev] = n;
+  });
+  return count[dev];
+}
+
+template <int FMT, int PAIRS, typename T>
+fp4moe_status pair_run(DenseParams prm, const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
+                       cudaStream_t st) {
+  using C = PairCfg<FMT>;
+  prm.mt = (prm.M + PAIRS * PBM - 1) / (PAIRS * PBM);
+  prm.nt = (prm.N + PBN - 1) / PBN;
+  DenseMaps maps;
+  const uint64_t rb = (uint64_t)mx_row_bytes(prm.K);
+  if (!encode_u8_sw128(&maps.a, a, rb, (uint64_t)prm.M, 128) ||
+      !encode_u8_sw128(&maps.b, b, rb, (uint64_t)prm.N, 128 / PAIRS) ||
+      !encode_scale_tiles(&maps.sfa, a_sf, (uint64_t)mx_row_tiles(prm.M) * prm.ct, C::kSfTiles) ||
+      !encode_scale_tiles(&maps.sfb, b_sf, (uint64_t)mx_row_tiles(prm.N) * prm.ct, C::kSfTiles / PAIRS))
+    return FP4MOE_CUDA_ERROR;
+  const int most = pair_clusters<FMT, PAIRS, T>(), tiles = prm.mt * prm.nt;
+  if (most <= 0) return FP4MOE_CUDA_ERROR;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t lc = pair_config<PAIRS>((unsigned)(tiles < most ? tiles : most), C::kSmem, st, attr);
+  return cudaLaunchKernelEx(&lc, mx_pair_kernel<FMT, PAIRS, T>, maps, prm) == cudaSuccess ? FP4MOE_OK
+                                                                                        : FP4MOE_CUDA_ERROR;
+}
+
+template <int FMT>
+fp4moe_status pair_typed(int32_t dtype, int pairs, const DenseParams& prm, const uint8_t* a, const uint8_t* a_sf,
+                         const uint8_t* b, const uint8_t* b_sf, cudaStream_t st) {
+  switch (dtype) {
+    case FP4MOE_BF16:
+      return pairs == 2 ? pair_run<FMT, 2, __nv_bfloat16>(prm, a, a_sf, b, b_sf, st)
+                        : pair_run<FMT, 1, __nv_bfloat16>(prm, a, a_sf, b, b_sf, st);
+    case FP4MOE_FP16:
+      return pairs == 2 ? pair_run<FMT, 2, __half>(prm, a, a_sf, b, b_sf, st)
+                        : pair_run<FMT, 1, __half>(prm, a, a_sf, b, b_sf, st);
+    default:
+      return pairs == 2 ? pair_run<FMT, 2, float>(prm, a, a_sf, b, b_sf, st)
+                        : pair_run<FMT, 1, float>(prm, a, a_sf, b, b_sf, st);
+  }
+}
+
+}  // namespace
+
+fp4moe_status mx_pair_launch(int32_t format, int32_t dtype, int pairs, const DenseParams& prm, const uint8_t* a,
+                             const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, cudaStream_t st) {
+  return format == FP4MOE_W_MXFP4 ? pair_typed<FP4MOE_W_MXFP4>(dtype, pairs, prm, a, a_sf, b, b_sf, st)
+                                  : pair_typed<FP4MOE_W_NVFP4>(dtype, pairs, prm, a, a_sf, b, b_sf, st);
+}
+
+}  // namespace fp4moe

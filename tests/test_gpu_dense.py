@@ -18,6 +18,7 @@ from oracle import codecs, nvfp4
 
 pytestmark = pytest.mark.gpu
 DTYPES = ["bfloat16", "float16", "float32"]
+OVERFLOW = {"bfloat16": 3.39e38, "float16": 65520.0, "float32": 3.4e38}
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -272,6 +273,14 @@ def gemm_operands(fmt, M, N, K, seed):
     return out
 
 
+def hold_product(got, ref, mag, K, dtype):
+    bar = mag * (K / 64 + 8) * 2.0 ** -22 + np.abs(ref) * (HALF_STEP[dtype] + 2.0 ** -23) + TINY[dtype]
+    e = np.abs(got - ref)
+    # past the type's range a result rounds to infinity (fp16: from 65520 on)
+    over = (e > bar) & ~(np.isinf(got) & (np.sign(got) == np.sign(ref)) & (np.abs(ref) + bar >= OVERFLOW[dtype]))
+    assert not over.any(), f"{over.sum()} of {over.size} over, first {np.argwhere(over)[:4].tolist()}, worst {(e / bar).max()}"
+
+
 def check_gemm(fmt, M, N, K, dtype, seed=0, alpha=None, operands=None):
     import torch
     from block_scaled_fp4_top_gb300 import api
@@ -286,10 +295,7 @@ def check_gemm(fmt, M, N, K, dtype, seed=0, alpha=None, operands=None):
     sc = 1.0 if alpha is None else float(np.float32(alpha))
     ref = av @ bv.T * sc
     mag = np.abs(av) @ np.abs(bv).T * abs(sc)
-    bar = mag * (K / 64 + 8) * 2.0 ** -22 + np.abs(ref) * (HALF_STEP[dtype] + 2.0 ** -23) + TINY[dtype]
-    e = np.abs(f64(ob.t) - ref)
-    over = e > bar
-    assert not over.any(), f"{over.sum()} of {over.size} over, first {np.argwhere(over)[:4].tolist()}, worst {(e / bar).max()}"
+    hold_product(f64(ob.t), ref, mag, K, dtype)
     return ob.t
 
 
@@ -311,7 +317,57 @@ def test_gemm_types_and_many_tiles(fmt, dtype, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", [NV, MX])
-@pytest.mark.parametrize("M,N,K", [(5, 300, 512), (700, 4096, 1024)])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1000, 4096), (16, 1024, 1280), (17, 333, 1100), (33, 257, 2047), (64, 64, 8192),     # K over four CTAs
+    (1, 4096, 4095), (20, 4090, 4096), (64, 4000, 3999),                                     # over two
+    (65, 65, 4096), (129, 2000, 600),                                                        # 128 x 64 tiles
+    (400, 8000, 300), (513, 4104, 1999),                                                     # 128 x 128
+    (1025, 3001, 2100), (2000, 1528, 2048), (1500, 3000, 2000),                              # two pairs in a cluster
+])
+def test_gemm_every_kernel(fmt, dtype, M, N, K):
+    check_gemm(fmt, M, N, K, dtype, seed=M, alpha=2.0 ** -9 if dtype == "float16" else -1.75)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(8192, 4096, 2048), (8100, 4051, 2080)])                  # one pair a cluster
+def test_gemm_pairs_many_rounds(fmt, dtype, M, N, K):
+    """Large products against fp64 matmul on the device, at sampled rows and every column."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    rng = np.random.default_rng(K)
+    codes, sfs, vals = [], [], []
+    for rows in (M, N):
+        q = rng.integers(0, 16, (rows, -(-K // 32) * 32), dtype=np.uint8)
+        q[:, K:] = 0
+        s = rng.integers(117, 133, (rows, -(-K // 32))) if fmt == MX else rng.integers(0, 0x7F, (rows, -(-K // 16)))
+        pc, ps = pack(fmt, q, s.astype(np.uint8), K)
+        codes.append(torch.from_numpy(pc).cuda())
+        sfs.append(torch.from_numpy(ps).cuda())
+        vals.append((q, s.astype(np.uint8)))
+    out = Guarded((M, N), getattr(torch, dtype))
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    al = torch.tensor([2.0 ** -9], device="cuda")
+    api.fp4moe_mx_gemm(fmt, K, codes[0], sfs[0], codes[1], sfs[1], al, out.t, err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    out.check()
+    pick = np.unique(np.concatenate([np.arange(0, M, 97), [127, 128, 255, 256, 511, 512, M - 1]]))
+    av = torch.from_numpy(values(fmt, vals[0][0][pick], vals[0][1][pick], K)).cuda()
+    bv = torch.from_numpy(values(fmt, *vals[1], K)).cuda()
+    ref = (av @ bv.T).cpu().numpy() * 2.0 ** -9
+    mag = (av.abs() @ bv.abs().T).cpu().numpy() * 2.0 ** -9
+    hold_product(f64(out.t[torch.from_numpy(pick).cuda()]), ref, mag, K, dtype)
+    # every other row was computed too: the same product again, bit for bit, and no canary value left
+    again = torch.empty_like(out.t)
+    api.fp4moe_mx_gemm(fmt, K, codes[0], sfs[0], codes[1], sfs[1], al, again, err)
+    torch.cuda.synchronize()
+    assert torch.equal(out.t, again)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("M,N,K", [(5, 300, 512), (700, 4096, 1024), (8, 1024, 4096), (64, 4096, 4096)])
 def test_gemm_is_deterministic(fmt, M, N, K):
     import torch
     ops = gemm_operands(fmt, M, N, K, 4)
