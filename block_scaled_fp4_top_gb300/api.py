@@ -7,7 +7,8 @@ layer's arithmetic runs in the CUDA kernels of libfp4moe.so.
 
 ``MoELayer`` is a convenience owner of the buffers (allocated through torch)
 for one configuration. It also runs the load-time prep: weight quantisation,
-calibration and alpha tables.
+calibration and alpha tables. ``MxLinear`` is the same for a projection with
+microscaled 4-bit weights.
 """
 from __future__ import annotations
 
@@ -256,38 +257,59 @@ def moe_forward_shared_fp8(cfg, T, x, x_codes, x_scales, router_w, router_bias, 
 
 # ---------------------------------------------------------- dense operators
 # Their sizes and types come from the tensors, so the shapes are checked here: the library sees only pointers.
+# A small call is bound by the host, so each tensor is checked and turned into its pointer in one go.
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
 _BYTE_TYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _dtype(t) -> int:
+def _arg(name, t, shape, dtype):
+    """The pointer of a contiguous CUDA tensor of this shape and type; None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape:
+        raise Fp4MoeError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _arg_bytes(name, t, nbytes):
+    if t.dtype is not torch.uint8 or t.numel() != nbytes:
+        raise Fp4MoeError(f"{name}: expected {nbytes} bytes (uint8), got {t.numel()} of {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _arg_scalar(name, t):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() < 1:
+        raise Fp4MoeError(f"{name}: expected one float32, got {t.numel()} of {t.dtype}")
+    return _p(t)
+
+
+def _arg_matrix(name, t):
+    """(rows, columns, fp4moe_dtype, pointer) of a matrix whose sizes the call takes."""
     d = _DTYPES.get(t.dtype)
     if d is None:
-        raise Fp4MoeError(f"unsupported dtype {t.dtype}: bfloat16, float16 or float32")
-    return d
-
-
-def _want(name, t, shape, dtypes):
-    if t.shape != shape or t.dtype not in dtypes:
-        raise Fp4MoeError(f"{name}: expected {tuple(shape)} of {' or '.join(map(str, dtypes))}, got "
-                          f"{tuple(t.shape)} of {t.dtype}")
-
-
-def _want_bytes(name, t, nbytes):
-    if t.dtype != torch.uint8 or t.numel() != nbytes:
-        raise Fp4MoeError(f"{name}: expected {nbytes} bytes (uint8), got {t.numel()} of {t.dtype}")
-
-
-def _want_scalar(name, t):
-    if t.dtype != torch.float32 or t.numel() < 1:
-        raise Fp4MoeError(f"{name}: expected one float32")
+        raise Fp4MoeError(f"{name}: unsupported dtype {t.dtype}: bfloat16, float16 or float32")
+    if t.dim() != 2:
+        raise Fp4MoeError(f"{name}: expected a matrix, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
+    rows, cols = t.shape
+    return rows, cols, d, t.data_ptr()
 
 
 def _check_fp8(codes, scales, T, H):
-    _want("x_codes", codes, (T, H), _BYTE_TYPES)
-    if scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != (H + 127) // 128 \
+    """Shape and type of block-FP8 activations: codes [T, H], scales [ceil(H / 128), at least T]."""
+    if codes.dtype not in _BYTE_TYPES or codes.shape != (T, H):
+        raise Fp4MoeError(f"codes: expected {(T, H)} of {' or '.join(map(str, _BYTE_TYPES))}, got "
+                          f"{tuple(codes.shape)} of {codes.dtype}")
+    if scales.dtype is not torch.float32 or scales.dim() != 2 or scales.shape[0] != (H + 127) // 128 \
             or scales.shape[1] < T:
-        raise Fp4MoeError(f"x_scales: expected [{(H + 127) // 128}, at least {T}] of torch.float32, got "
+        raise Fp4MoeError(f"scales: expected [{(H + 127) // 128}, at least {T}] of torch.float32, got "
                           f"{tuple(scales.shape)} of {scales.dtype}")
 
 
@@ -298,21 +320,15 @@ def fp4moe_add_rmsnorm(x, residual, gamma, eps, residual_out, y, y_codes=None, y
     x [T, H] bfloat16, float16 or float32, and residual, residual_out, y, gamma [H] of its type. residual with
     residual_out, and y_codes with y_scales, may be None; so may gamma (ones), and y where y_codes is given.
     residual_out and y may each be x or residual."""
-    if x.dim() != 2:
-        raise Fp4MoeError(f"x: expected [T, H], got {tuple(x.shape)}")
-    T, H = x.shape
-    own = (x.dtype,)
-    d = _dtype(x)
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        if t is not None:
-            _want(name, t, (T, H), own)
-    if gamma is not None:
-        _want("gamma", gamma, (H,), own)
+    T, H, d, px = _arg_matrix("x", x)
+    shape, dt = x.shape, x.dtype
     stride = 0
     if y_codes is not None and y_scales is not None:
         _check_fp8(y_codes, y_scales, T, H)
         stride = y_scales.shape[1]
-    _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, _p(x), _p(residual), _p(gamma), eps, _p(residual_out), _p(y),
+    _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, px, _arg("residual", residual, shape, dt),
+                                          _arg("gamma", gamma, (H,), dt), eps,
+                                          _arg("residual_out", residual_out, shape, dt), _arg("y", y, shape, dt),
                                           _p(y_codes), _p(y_scales), stride, _s(stream)), "fp4moe_add_rmsnorm")
 
 
@@ -323,8 +339,8 @@ def mx_row_bytes(K: int) -> int:
 
 def mx_sf_bytes(fmt: int, rows: int, K: int) -> int:
     """Bytes of a microscaled matrix's scale tiles (128 rows x 4 scale columns, 512 bytes each)."""
-    block = 32 if fmt == _lib.W_MXFP4 else 16
-    return (rows + 127) // 128 * (((K + block - 1) // block + 3) // 4) * 512
+    span = 128 if fmt == _lib.W_MXFP4 else 64  # elements of K across a tile
+    return (rows + 127) // 128 * ((K + span - 1) // span) * 512
 
 
 def fp4moe_mx_bytes(fmt: int, rows: int, K: int):
@@ -334,45 +350,35 @@ def fp4moe_mx_bytes(fmt: int, rows: int, K: int):
     return tuple(x.value for x in v)
 
 
-def _check_mx(fmt, rows, K, codes, sf, gs):
-    _want_bytes("codes", codes, rows * mx_row_bytes(K))
-    _want_bytes("sf", sf, mx_sf_bytes(fmt, rows, K))
-    if gs is not None:
-        _want_scalar("gs", gs)
-
-
 def fp4moe_mx_quantize(fmt, x, gs, codes, sf, stream=None):
     """x [rows, K] to E2M1 codes and block scales (fmt W_MXFP4, or W_NVFP4 under the global scale gs)."""
-    if x.dim() != 2:
-        raise Fp4MoeError(f"x: expected [rows, K], got {tuple(x.shape)}")
-    rows, K = x.shape
-    _check_mx(fmt, rows, K, codes, sf, gs)
-    _check(_lib.load().fp4moe_mx_quantize(fmt, _dtype(x), rows, K, _p(x), _p(gs), _p(codes), _p(sf), _s(stream)),
+    rows, K, d, px = _arg_matrix("x", x)
+    _check(_lib.load().fp4moe_mx_quantize(fmt, d, rows, K, px, _arg_scalar("gs", gs),
+                                          _arg_bytes("codes", codes, rows * mx_row_bytes(K)),
+                                          _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K)), _s(stream)),
            "fp4moe_mx_quantize")
 
 
 def fp4moe_mx_dequantize(fmt, codes, sf, gs, out, stream=None):
     """The values of a microscaled matrix into out [rows, K]."""
-    if out.dim() != 2:
-        raise Fp4MoeError(f"out: expected [rows, K], got {tuple(out.shape)}")
-    rows, K = out.shape
-    _check_mx(fmt, rows, K, codes, sf, gs)
-    _check(_lib.load().fp4moe_mx_dequantize(fmt, _dtype(out), rows, K, _p(codes), _p(sf), _p(gs), _p(out),
-                                            _s(stream)), "fp4moe_mx_dequantize")
+    rows, K, d, po = _arg_matrix("out", out)
+    _check(_lib.load().fp4moe_mx_dequantize(fmt, d, rows, K, _arg_bytes("codes", codes, rows * mx_row_bytes(K)),
+                                            _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K)), _arg_scalar("gs", gs),
+                                            po, _s(stream)), "fp4moe_mx_dequantize")
 
 
 def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream=None):
     """out [M, N] = alpha * A B^T for microscaled A [M, K] and B [N, K]; alpha a device float32 or None (1); err a
     zeroed device word (int32) that the caller keeps."""
-    if out.dim() != 2:
-        raise Fp4MoeError(f"out: expected [M, N], got {tuple(out.shape)}")
-    M, N = out.shape
-    _check_mx(fmt, M, K, a_codes, a_sf, alpha)
-    _check_mx(fmt, N, K, b_codes, b_sf, None)
+    M, N, d, po = _arg_matrix("out", out)
+    row = mx_row_bytes(K)
     if err.element_size() * err.numel() < 4:
         raise Fp4MoeError("err: expected a device word of 4 bytes")
-    _check(_lib.load().fp4moe_mx_gemm(fmt, _dtype(out), M, N, K, _p(a_codes), _p(a_sf), _p(b_codes), _p(b_sf),
-                                      _p(alpha), _p(out), _p(err), _s(stream)), "fp4moe_mx_gemm")
+    _check(_lib.load().fp4moe_mx_gemm(fmt, d, M, N, K, _arg_bytes("a_codes", a_codes, M * row),
+                                      _arg_bytes("a_sf", a_sf, mx_sf_bytes(fmt, M, K)),
+                                      _arg_bytes("b_codes", b_codes, N * row),
+                                      _arg_bytes("b_sf", b_sf, mx_sf_bytes(fmt, N, K)), _arg_scalar("alpha", alpha),
+                                      po, _p(err), _s(stream)), "fp4moe_mx_gemm")
 
 
 # --------------------------------------------------------------------------
@@ -505,8 +511,17 @@ class MoELayer:
 
     # ---- hot path
     def forward(self, x: torch.Tensor, y: torch.Tensor, topk_ids: torch.Tensor | None = None,
-                topk_w: torch.Tensor | None = None, stream=None):
+                topk_w: torch.Tensor | None = None, stream=None, x_fp8=None):
+        """y [T, H] of x [T, H]. x_fp8 = (codes, scales), x's block-FP8 copy as fp4moe_add_rmsnorm writes it, spares a
+        layer with a shared expert that expert's quantisation of x."""
         W = self.weights
+        if x_fp8 is not None:
+            if self.shared is None:
+                raise Fp4MoeError("x_fp8: the layer has no shared expert")
+            moe_forward_shared_fp8(self.cfg, x.shape[0], x, x_fp8[0], x_fp8[1], self.router_w, self.router_bias,
+                                   self.gs1, self.gs2, W.w1_fp4, W.w1_sf, self.alpha1, W.w2_fp4, W.w2_sf, self.alpha2,
+                                   self.shared, y, topk_ids, topk_w, self.ws, stream)
+            return
         if self.shared is not None:  # routed experts plus the shared expert, one combine
             moe_forward_shared(self.cfg, x.shape[0], x, self.router_w, self.router_bias, self.gs1, self.gs2,
                                W.w1_fp4, W.w1_sf, self.alpha1, W.w2_fp4, W.w2_sf, self.alpha2, self.shared, y,
@@ -525,3 +540,55 @@ class MoELayer:
     def refresh_gs2(self, stream=None):
         """gs2 and alpha2 from the amax|h| of the calls since the last refresh (lagged, on the device)."""
         fp4moe_refresh_gs2(self.cfg, self.ws, self.weights.gw2, self.gs2, self.alpha2, stream)
+
+
+class MxLinear:
+    """A projection y = x W^T with microscaled 4-bit weights and activations (W [N, K], at most max_tokens rows of x).
+
+    fmt W_MXFP4 needs nothing more. fmt W_NVFP4 has a global scale for each operand: the weights' is taken from W here,
+    the activations' from a warm-up batch (calibrate) or set by the caller (set_activation_scale)."""
+
+    def __init__(self, weight: torch.Tensor, max_tokens: int, fmt: int = _lib.W_MXFP4):
+        self.N, self.K = weight.shape
+        self.fmt, self.max_tokens = fmt, max_tokens
+        u8 = dict(dtype=torch.uint8, device=weight.device)
+        code_bytes, sf_bytes = fp4moe_mx_bytes(fmt, self.N, self.K)
+        self.w_codes, self.w_sf = torch.empty(code_bytes, **u8), torch.empty(sf_bytes, **u8)
+        self.gw = self.gx = self.alpha = None
+        if fmt == _lib.W_NVFP4:
+            self.gw = self._global_scale(weight)
+            self.gx = torch.ones_like(self.gw)
+            self.alpha = torch.empty_like(self.gw)
+            fp4moe_make_alpha(1, self.gx, self.gw, self.alpha)
+        fp4moe_mx_quantize(fmt, weight.contiguous(), self.gw, self.w_codes, self.w_sf)
+        self.x_codes = torch.empty(max_tokens * mx_row_bytes(self.K), **u8)
+        self.x_sf = torch.empty(mx_sf_bytes(fmt, max_tokens, self.K), **u8)
+        self.err = torch.zeros(4, dtype=torch.int32, device=weight.device)
+
+    @staticmethod
+    def _global_scale(t):
+        amax = t.abs().amax().to(torch.float32).reshape(1)
+        return torch.where(amax > 0, 2688.0 / amax, torch.ones_like(amax))
+
+    def calibrate(self, x_warm: torch.Tensor):
+        """NVFP4: the activations' global scale RN(2688 / amax) from a warm-up batch (outside any graph)."""
+        if self.fmt == _lib.W_NVFP4:
+            self.set_activation_scale(self._global_scale(x_warm))
+
+    def set_activation_scale(self, gs):
+        self.gx.copy_(torch.as_tensor(gs, dtype=torch.float32).reshape(1))
+        fp4moe_make_alpha(1, self.gx, self.gw, self.alpha)
+
+    def forward(self, x: torch.Tensor, out: torch.Tensor, stream=None):
+        """out [T, N] (bfloat16, float16 or float32) of x [T, K]."""
+        T = x.shape[0]
+        if T > self.max_tokens or x.shape[1] != self.K or out.shape != (T, self.N):
+            raise Fp4MoeError(f"expected x [at most {self.max_tokens}, {self.K}] and out [T, {self.N}], got "
+                              f"{tuple(x.shape)} and {tuple(out.shape)}")
+        codes = self.x_codes[:T * mx_row_bytes(self.K)]
+        sf = self.x_sf[:mx_sf_bytes(self.fmt, T, self.K)]
+        fp4moe_mx_quantize(self.fmt, x, self.gx, codes, sf, stream)
+        fp4moe_mx_gemm(self.fmt, self.K, codes, sf, self.w_codes, self.w_sf, self.alpha, out, self.err, stream)
+
+    def read_error(self, clear=True) -> int:
+        return fp4moe_read_error(self.err, clear)
