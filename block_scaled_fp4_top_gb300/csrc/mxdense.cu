@@ -390,11 +390,13 @@ bool dense_configure() {
   return ok == 1;
 }
 
-// Which kernel, and how. Fitted times of the variants in ns, measured back to back at 26 sizes from 1 x 4096 x 256 to
-// 8192 x 8192 x 2048 (bf16 out): the one picked is within 6 % of the fastest at all of them. KB: 256-element stages of K.
-//   128 x 64, 128 x 128    a launch, then 270 or 280 a stage and 500 a tile (measured 270 .. 310 a stage)
-//   split over S CTAs      KB / S stages; joining: 800, and a fifth of a ns for each fp32 value that is sent
-//   256 x 256 on a pair    2150 a tile beside its stages at 316, or 284 with two pairs in a cluster
+// Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 40 sizes from 1 x 4096 x 256 to
+// 8192 x 8192 x 2048 (bf16 out): the one picked is within 7 % of the fastest at all of them. KB: 256-element stages
+// of K.
+//   128 x 64, 128 x 128    a launch, 700 a tile and 270 .. 300 a stage
+//   split over S CTAs      KB / S stages; joining: 1100, and a fifth of a ns for each fp32 value that is sent
+//   256 x 256 on a pair    1350 a tile and 316 a stage, or 1250 and 284 with two pairs in a cluster (36 clusters of
+//                          four fit on 152 SMs, 76 of two)
 struct Plan {
   int pairs;  // 0: this file's kernel, with bn and S
   int bn, S;
@@ -410,17 +412,19 @@ Plan pick_plan(int M, int N, int KB, int nsm) {
     }
   };
   for (int bn : {64, 128}) {
-    const int64_t tiles = up(M, DBM) * up(N, bn), stage = bn == 64 ? 270 : 280, launch = bn == 64 ? 2500 : 2650;
-    offer({0, bn, 1}, launch + up(tiles, nsm) * (KB * stage + 500));
+    const int64_t tiles = up(M, DBM) * up(N, bn), stage = bn == 128 && M > 64 ? 300 : 270;
+    const int64_t launch = bn == 64 ? 1700 : 1800;
+    offer({0, bn, 1}, launch + up(tiles, nsm) * (KB * stage + 700));
     if (M > 64) continue;  // more rows cost more to join than the split saves
     for (int S : {2, 4})   // a cluster of four leaves an eighteenth of the SMs without one
       if (S <= KB && tiles * S <= (S == 2 ? nsm : nsm - nsm / 18))
-        offer({0, bn, S}, launch + 500 + up(KB, S) * stage + 800 + (int64_t)(S - 1) * M * bn / 5);
+        offer({0, bn, S}, launch + 700 + up(KB, S) * stage + 1100 + (int64_t)(S - 1) * M * bn / 5);
   }
   for (int pairs : {1, 2}) {
     const int64_t tiles = up(M, 256 * pairs) * up(N, 256);
     const int64_t clusters = pairs == 1 ? nsm / 2 : (nsm - nsm / 18) / 4;
-    if (clusters > 0) offer({pairs, 0, 1}, 3200 + up(tiles, clusters) * (KB * (pairs == 1 ? 316 : 284) + 2150));
+    if (clusters > 0)
+      offer({pairs, 0, 1}, 3600 + up(tiles, clusters) * (pairs == 1 ? KB * 316 + 1350 : KB * 284 + 1250));
   }
   return best;
 }

@@ -67,17 +67,23 @@ constexpr int kEpiStage = 32 * 64;
 // words of T. 16-bit types are packed as they arrive: fp32 columns of a whole tile do not fit the registers.
 template <typename T, int W>
 __device__ __forceinline__ void load_packed(uint32_t tacc, float alpha, uint32_t (&w)[W * sizeof(T) / 4]) {
+  constexpr int STEP = W < 64 ? W : 64;
 #pragma unroll
-  for (int c = 0; c < W; c += 32) {
-    float q[32];
-    tmem_ld32(tacc + c, q);
+  for (int c = 0; c < W; c += STEP) {
+    float q[STEP / 32][32];
+#pragma unroll
+    for (int i = 0; i < STEP / 32; ++i) tmem_ld32(tacc + c + 32 * i, q[i]);
     tmem_ld_wait();
-    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) w[c + j] = __float_as_uint(q[j] * alpha);
-    } else {
+    for (int i = 0; i < STEP / 32; ++i) {
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[c / 2 + j] = pack2<T>(q[2 * j] * alpha, q[2 * j + 1] * alpha);
+        for (int j = 0; j < 32; ++j) w[c + 32 * i + j] = __float_as_uint(q[i][j] * alpha);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[(c + 32 * i) / 2 + j] = pack2<T>(q[i][2 * j] * alpha, q[i][2 * j + 1] * alpha);
+      }
     }
   }
 }

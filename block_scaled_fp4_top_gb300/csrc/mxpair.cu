@@ -106,9 +106,11 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bd
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-// Arrive on a barrier of any CTA of the cluster (an address from map_cluster).
+// Arrive on a barrier of any CTA of the cluster (an address from map_cluster). It publishes no memory writes: what it
+// orders are TMEM reads, with the tcgen05 fences of both sides. A release at cluster scope here and a fence at the
+// other end cost 1.1 us of a tile's 7.8.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
 // Tile t: groups of 8 tile rows, so that the tiles of a wave share their operands' rows in L2.
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       // both epilogues have moved the previous tile's accumulator out of TMEM
       const uint32_t tph = ((uint32_t)tl & 1u) ^ 1u;
       if (!mbar_wait_warp(bar_tempty, tph, prm.err) || !mbar_wait_warp(bar_tpeer, tph, prm.err)) break;
-      asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the peer's arrival comes from another CTA
+      tc_fence_after();
       for (int kb = 0; kb < KB; ++kb) {
         if (!mbar_wait_warp(bar_full + 8 * s, ph, prm.err)) {
           ok = false;
@@ -269,8 +271,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       drain_wait(bar_drain, 0);  // no MMA may still write TMEM when it is freed
     }
   } else if (warp == PMMA && lane == 0) {
-    // One arrival for eight warps, ahead of their stores: an arrival of each warp waited behind the stores of the
-    // warps before it, and the next tile began 1.2 us after the accumulator was read, not 0.5.
+    // one arrival for eight warps, ahead of their stores: an arrival of each warp would queue behind the stores of the
+    // warps before it
     const uint32_t tpeer = map_cluster(bar_tpeer, lead);
     int tl = 0;
     for (int t = cluster; t < tiles; t += clusters, ++tl) {
@@ -282,11 +284,6 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     const int quarter = warp & 3, half = warp >> 2;
     uint8_t* stage = smem_raw + C::kEpiOff + warp * kEpiStage;
     const float alpha = prm.alpha != nullptr ? __ldg(prm.alpha) : 1.0f;
-    // Every pair ends its tile at the same time, and 10 MB of stores at once hold up the loads of the next tile. So
-    // all tiles but a pair's last spread theirs over about half of the next tile's MMAs (75 ns each): 8192 x 4096 x
-    // 4096 takes 53.1 us so, 55.2 without.
-    constexpr int kChunks = W * (int)sizeof(T) / 64;
-    const uint32_t pace = min(1000u, 150u * (uint32_t)KB / kChunks);
     int tl = 0;
     for (int t = cluster; t < tiles; t += clusters, ++tl) {
       int m, n;
@@ -306,11 +303,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         constexpr int COLS = 64 / (int)sizeof(T);
 #pragma unroll
         for (int c = 0; c < W; c += COLS)
-          if (c0 + c < prm.N) {
-            if (t + clusters < tiles) __nanosleep(pace);
+          if (c0 + c < prm.N)
             store_chunk(stage, w + c * (int)sizeof(T) / 4, static_cast<T*>(prm.out), prm.M, prm.N, r0, c0 + c, lane,
                         prm.vec);
-          }
       }
     }
   }
