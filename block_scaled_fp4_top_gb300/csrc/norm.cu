@@ -9,9 +9,10 @@
 // The sum of squares and the statistics are fp32; h is rounded to its storage type first, so the norm is
 // that of the stream a later layer reads back.
 //
-// Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps
-// it in registers between the two uses: NV 16-byte vectors a thread. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip back, so
-// they take the most threads (NV = 1); many rows take two vectors a thread.
+// Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
+// between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
+// back (1 x 4096 bf16 1.9 us, 64 rows 2.1 us), so they take the most threads; many rows take two 16-byte vectors a
+// thread (8192 x 4096 bf16 with the FP8 copy 47 us, 6.4 TB/s, 95 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -19,7 +20,7 @@
 namespace fp4moe {
 namespace {
 
-constexpr int NORM_THREADS = 256;
+constexpr int NORM_THREADS = 1024;
 
 // Sum over the CTA, the same value in every thread.
 __device__ __forceinline__ float cta_sum(float v, float* s_red) {
@@ -57,7 +58,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[N / 
     *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-// Widths too large for a CTA's registers: element accesses, and the row is read again for its second use. A warp takes whole 128-element
+// Widths too large for a CTA's registers: element accesses, and the row is read again for its second use
+// (500 x 40960 bf16 with the FP8 copy 71 us, 2.6 TB/s; with 256 threads 111 us). A warp takes whole 128-element
 // groups, four elements a lane (lane, lane + 32, ...).
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)
@@ -119,87 +121,29 @@ __device__ __forceinline__ uint4 ld_vec(const void* p) {
   return q;
 }
 
-// 16 bytes from byte 16 - back of the 32 bytes (prev, cur); back is the same in the whole CTA, 0 .. 14 and even.
-__device__ __forceinline__ uint4 shifted(uint4 prev, uint4 cur, int back) {
-  if (back == 0) return cur;
-  uint32_t w[8] = {prev.x, prev.y, prev.z, prev.w, cur.x, cur.y, cur.z, cur.w};
-  shift_words<8, 4>(w, 16 - back);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Vector q of a row, in a thread's slot i, is q = i * blockDim + threadIdx.
-//
-// SHIFT: rows whose length no vector divides start at any element of a vector. x, residual, h_out and y then
-// all start at the same one (their bases are 16-byte aligned), and so do the codes in units of N bytes. So the
-// kernel cuts a row at the addresses that N divides: vector q holds elements N q - off .. N q - off + N - 1,
-// off = the row's first element modulo N, and only the first and the last vector of a row are partly outside.
-// gamma starts aligned, so its N elements come from two vectors, shifted into place. The vectors of one FP8
-// group are 128 / N neighbouring lanes, except that the first `off` elements of the first of them belong to
-// the group before: their maximum goes through shared memory (s_head), like the group's own (s_main).
-// Elements outside the row are zeros all the way (a NaN statistic makes them NaN, and then its row is, too).
-template <typename T, int NV, bool SHIFT>
+// Widths that 16-byte vectors divide. Vector q of a row, in a thread's slot i, is q = i * blockDim + threadIdx; the
+// vectors of one FP8 group are 128 / N neighbouring lanes.
+template <typename T, int NV>
 __global__ void __launch_bounds__(1024)
     add_rmsnorm_vec_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
                            T* y, uint8_t* codes, float* scales, int64_t scale_stride) {
   constexpr int N = 16 / (int)sizeof(T), LANES = 128 / N;
   __shared__ float s_red[32];
-  __shared__ float s_main[SHIFT ? NV * 1024 / LANES : 1], s_head[SHIFT ? NV * 1024 / LANES + 1 : 1];
-  __shared__ Fp8Scale s_scale[SHIFT ? NV * 1024 / LANES : 1];
   pdl_wait();
   pdl_trigger();
   const size_t row = (size_t)blockIdx.x * H;
-  const int off = SHIFT ? (int)(row % N) : 0;
-  // first element of slot i's vector; whole: every element is in the row; edge: some are
-  auto at = [&](int i) { return (i * (int)blockDim.x + (int)threadIdx.x) * N - off; };
-  auto whole = [&](int j) { return SHIFT ? (j >= 0 && j + N <= H) : j < H; };
-  auto edge = [&](int j) { return SHIFT && j < H && (j < 0 || j + N > H); };
-  auto inside = [&](int j, int k) { return (unsigned)(j + k) < (unsigned)H; };
-  auto store = [&](T* p, int j, uint4 v) {
-    if (whole(j)) {
-      *reinterpret_cast<uint4*>(p + row + j) = v;
-    } else if (edge(j)) {
-      alignas(16) T e[N];
-      *reinterpret_cast<uint4*>(e) = v;
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (inside(j, k)) p[row + j + k] = e[k];
-    }
-  };
+  auto at = [&](int i) { return (i * (int)blockDim.x + (int)threadIdx.x) * N; };
   // Every load of the row is issued before the first is waited for. gamma waits until x and the residual are
   // joined where its registers would cost occupancy: 8192 x 4096 bf16 without a residual 24.7 against 29.7 us.
-  constexpr bool kGammaFirst = SHIFT || NV == 1;
-  uint4 hv[NV], rv[NV], gv[NV], gp[SHIFT ? NV : 1];
+  uint4 hv[NV], rv[NV], gv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = at(i);
     hv[i] = rv[i] = gv[i] = make_uint4(0, 0, 0, 0);
-    if (whole(j)) hv[i] = ld_vec(x + row + j);
-    if (residual != nullptr && whole(j)) rv[i] = ld_vec(residual + row + j);
-    if (kGammaFirst && gamma != nullptr && j + off + N <= H) gv[i] = __ldg(reinterpret_cast<const uint4*>(gamma + j + off));
-    if constexpr (SHIFT) {
-      gp[i] = make_uint4(0, 0, 0, 0);
-      if (gamma != nullptr && off > 0 && j + off > 0 && j + off + N <= H)
-        gp[i] = __ldg(reinterpret_cast<const uint4*>(gamma + j + off - N));
-    }
-  }
-  if constexpr (SHIFT) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = at(i);
-      gv[i] = shifted(gp[i], gv[i], off * (int)sizeof(T));
-      if (j < H && (j < 0 || j + off + N > H)) {  // the row's first or last elements, or gamma's last
-        alignas(16) T ex[N], er[N], eg[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const bool in = inside(j, k);
-          ex[k] = in ? x[row + j + k] : from_f32<T>(0.0f);
-          er[k] = in && residual != nullptr ? residual[row + j + k] : from_f32<T>(0.0f);
-          eg[k] = in && gamma != nullptr ? gamma[j + k] : from_f32<T>(0.0f);
-        }
-        hv[i] = *reinterpret_cast<const uint4*>(ex);
-        rv[i] = *reinterpret_cast<const uint4*>(er);
-        gv[i] = *reinterpret_cast<const uint4*>(eg);
-      }
+    if (j < H) {
+      hv[i] = ld_vec(x + row + j);
+      if (residual != nullptr) rv[i] = ld_vec(residual + row + j);
+      if (NV == 1 && gamma != nullptr) gv[i] = __ldg(reinterpret_cast<const uint4*>(gamma + j));
     }
   }
   if (residual != nullptr) {
@@ -211,10 +155,10 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int k = 0; k < N; ++k) h[k] = __fadd_rn(h[k], r[k]);
       hv[i] = pack<T>(h);
-      store(h_out, at(i), hv[i]);
+      if (at(i) < H) *reinterpret_cast<uint4*>(h_out + row + at(i)) = hv[i];
     }
   }
-  if constexpr (!kGammaFirst) {
+  if constexpr (NV > 1) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (gamma != nullptr && at(i) < H) gv[i] = __ldg(reinterpret_cast<const uint4*>(gamma + at(i)));
@@ -229,94 +173,196 @@ __global__ void __launch_bounds__(1024)
   }
   ss = cta_sum(ss, s_red);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
-
-  // fmax_nan: a NaN takes its whole group along (NaN scale, NaN codes)
-  float n[NV][N];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = at(i);
-    float a = 0.0f, head = 0.0f;
-    unpack<T>(hv[i], n[i]);
+    float n[N], a = 0.0f;
+    unpack<T>(hv[i], n);
 #pragma unroll
-    for (int k = 0; k < N; ++k) n[i][k] *= rstd;
+    for (int k = 0; k < N; ++k) n[k] *= rstd;
     if (gamma != nullptr) {
       float g[N];
       unpack<T>(gv[i], g);
 #pragma unroll
-      for (int k = 0; k < N; ++k) n[i][k] *= g[k];
+      for (int k = 0; k < N; ++k) n[k] *= g[k];
     }
-    if (y != nullptr) store(y, j, pack<T>(n[i]));
-    if (codes != nullptr) {
+    if (y != nullptr && j < H) *reinterpret_cast<uint4*>(y + row + j) = pack<T>(n);
+    if (codes == nullptr) continue;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (SHIFT && k < off)
-          head = fmax_nan(head, fabsf(n[i][k]));
-        else
-          a = fmax_nan(a, fabsf(n[i][k]));
-      }
-      const bool first = (j + off) % 128 == 0;
-      if (SHIFT && !first) a = fmax_nan(a, head);
+    for (int k = 0; k < N; ++k) a = fmax_nan(a, fabsf(n[k]));  // a NaN takes its whole group along
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-      if constexpr (SHIFT) {
-        if (first) {
-          s_main[(j + off) / 128] = a;
-          s_head[(j + off) / 128] = head;
-        }
-      } else if (j < H) {
-        const float s = __fdiv_rn(a, 448.0f);
-        const Fp8Scale f = fp8_scale(s);
-        uint32_t w[N / 4];
+    for (int o = LANES / 2; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    if (j >= H) continue;
+    const float s = __fdiv_rn(a, 448.0f);
+    const Fp8Scale f = fp8_scale(s);
+    uint32_t w[N / 4];
 #pragma unroll
-        for (int k = 0; k < N; ++k) n[i][k] = n[i][k] * f.up * f.inv;
-        make_codes<N>(w, n[i]);
-        store_codes<N>(codes + row + j, w);
-        if (first) scales[(size_t)(j / 128) * scale_stride + blockIdx.x] = s;
-      }
-    }
+    for (int k = 0; k < N; ++k) n[k] = n[k] * f.up * f.inv;
+    make_codes<N>(w, n);
+    store_codes<N>(codes + row + j, w);
+    if (j % 128 == 0) scales[(size_t)(j / 128) * scale_stride + blockIdx.x] = s;
   }
-  if constexpr (SHIFT) {
-    if (codes == nullptr) return;
-    const int G = (H + 127) / 128;
-    if (threadIdx.x == 0) s_head[NV * (int)blockDim.x / LANES] = 0.0f;  // no vector follows the last group
-    __syncthreads();
-    for (int g = threadIdx.x; g < G; g += blockDim.x) {  // one thread a group
-      const float s = __fdiv_rn(fmax_nan(s_main[g], s_head[g + 1]), 448.0f);
-      scales[(size_t)g * scale_stride + blockIdx.x] = s;
-      s_scale[g] = fp8_scale(s);
+}
+
+// U elements of a row in one access of U * sizeof(T) bytes: 2, 4 or 8.
+template <typename T, int U>
+using Raw = std::conditional_t<U * sizeof(T) == 2, uint16_t, std::conditional_t<U * sizeof(T) == 4, uint32_t, uint2>>;
+template <typename T, int U>
+__device__ __forceinline__ void unpack_raw(Raw<T, U> q, float (&v)[U]) {
+  if constexpr (U == 1) {
+    v[0] = to_f32(*reinterpret_cast<const T*>(&q));
+  } else {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(q) == 4) {
+      w.x = q;
+    } else {
+      w.x = q.x;
+      w.y = q.y;
     }
-    __syncthreads();
+    float f[16 / sizeof(T)];
+    unpack<T>(w, f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = at(i), g = (j + off) / 128;  // the group of all its elements but, in the first, `off` of them
+    for (int k = 0; k < U; ++k) v[k] = f[k];
+  }
+}
+template <typename T, int U>
+__device__ __forceinline__ Raw<T, U> pack_raw(const float (&v)[U]) {
+  if constexpr (U == 1) {
+    const T t = from_f32<T>(v[0]);
+    return *reinterpret_cast<const Raw<T, 1>*>(&t);
+  } else if constexpr (sizeof(T) == 4) {
+    return make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1]));
+  } else if constexpr (U == 2) {
+    return pack2<T>(v[0], v[1]);
+  } else {
+    return make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  }
+}
+
+// The largest of 32 lanes, NaN if any is, in every lane.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Widths that the 16-byte vectors do not divide. Rows then start at any element, and a vector that is aligned for
+// one row is not for the next, so a lane reads and writes U elements at a time, the most that divide H (4, 2 or
+// 1), in accesses that are contiguous over the warp. A warp takes whole FP8 groups: NG of them, in registers, and
+// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 52 us, 8192 x 4092 49 us, 8192 x 4095
+// (single elements: bound by the accesses) 75 us, against 77, 75 and 78 us with whole vectors that were cut at the
+// aligned addresses and shifted into place, and 47 us at 4096.
+template <typename T, int U, int NG>
+__global__ void __launch_bounds__(1024)
+    add_rmsnorm_group_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
+                             T* y, uint8_t* codes, float* scales, int64_t scale_stride) {
+  constexpr int S = 4 / U;
+  using R = Raw<T, U>;
+  __shared__ float s_red[32];
+  pdl_wait();
+  pdl_trigger();
+  const size_t row = (size_t)blockIdx.x * H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  auto at = [&](int i, int s) { return (i * warps + warp) * 128 + (s * 32 + lane) * U; };
+  R hv[NG][S], rv[NG][S], gv[NG][S];
+#pragma unroll
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int j = at(i, s);
+      hv[i][s] = rv[i][s] = gv[i][s] = R{};
+      if (j < H) {
+        hv[i][s] = *reinterpret_cast<const R*>(x + row + j);
+        if (residual != nullptr) rv[i][s] = *reinterpret_cast<const R*>(residual + row + j);
+        if (NG == 1 && gamma != nullptr) gv[i][s] = __ldg(reinterpret_cast<const R*>(gamma + j));
+      }
+    }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int j = at(i, s);
+      float h[U], r[U];
+      unpack_raw<T, U>(hv[i][s], h);
+      if (residual != nullptr) {
+        unpack_raw<T, U>(rv[i][s], r);
+#pragma unroll
+        for (int k = 0; k < U; ++k) h[k] = __fadd_rn(h[k], r[k]);
+        hv[i][s] = pack_raw<T, U>(h);
+        if (j < H) *reinterpret_cast<R*>(h_out + row + j) = hv[i][s];
+        unpack_raw<T, U>(hv[i][s], h);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) ss = fmaf(h[k], h[k], ss);
+    }
+  if constexpr (NG > 1) {  // with several groups gamma takes the residual's registers
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (gamma != nullptr && at(i, s) < H) gv[i][s] = __ldg(reinterpret_cast<const R*>(gamma + at(i, s)));
+  }
+  ss = cta_sum(ss, s_red);
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int g = i * warps + warp;
+    if (g * 128 >= H) break;
+    float n[S][U], a = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int j = at(i, s);
+      unpack_raw<T, U>(hv[i][s], n[s]);
+#pragma unroll
+      for (int k = 0; k < U; ++k) n[s][k] *= rstd;
+      if (gamma != nullptr) {
+        float w[U];
+        unpack_raw<T, U>(gv[i][s], w);
+#pragma unroll
+        for (int k = 0; k < U; ++k) n[s][k] *= w[k];
+      }
+      if (y != nullptr && j < H) *reinterpret_cast<R*>(y + row + j) = pack_raw<T, U>(n[s]);
+#pragma unroll
+      for (int k = 0; k < U; ++k) a = fmax_nan(a, fabsf(n[s][k]));
+    }
+    if (codes == nullptr) continue;
+    const float sc = __fdiv_rn(warp_max_nan(a), 448.0f);  // a NaN takes its whole group along
+    const Fp8Scale f = fp8_scale(sc);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const int j = at(i, s);
       if (j >= H) continue;
-      const Fp8Scale f = s_scale[min(g, G - 1)], f0 = (j + off) % 128 == 0 ? s_scale[max(g - 1, 0)] : f;
-      uint32_t w[N / 4];
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const Fp8Scale fk = k < off ? f0 : f;
-        n[i][k] = n[i][k] * fk.up * fk.inv;
-      }
-      make_codes<N>(w, n[i]);
-      if (whole(j)) {
-        store_codes<N>(codes + row + j, w);
+      for (int k = 0; k < U; ++k) n[s][k] = n[s][k] * f.up * f.inv;
+      if constexpr (U == 4) {
+        uint32_t w[1];
+        make_codes<4>(w, n[s]);
+        *reinterpret_cast<uint32_t*>(codes + row + j) = w[0];
+      } else if constexpr (U == 2) {
+        *reinterpret_cast<uint16_t*>(codes + row + j) = (uint16_t)cvt_e4m3x2(n[s][0], n[s][1]);
       } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-          if (inside(j, k)) codes[row + j + k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+        codes[row + j] = (uint8_t)cvt_e4m3x2(n[s][0], 0.0f);
       }
     }
+    if (lane == 0) scales[(size_t)g * scale_stride + blockIdx.x] = sc;
   }
 }
 
 template <typename T>
 using NormKernel = void (*)(int, const T*, const T*, const T*, float, T*, T*, uint8_t*, float*, int64_t);
 
-template <typename T, bool SHIFT>
+template <typename T>
 NormKernel<T> vec_kernel(int nv) {
-  return nv == 1   ? add_rmsnorm_vec_kernel<T, 1, SHIFT>
-         : nv == 2 ? add_rmsnorm_vec_kernel<T, 2, SHIFT>
-                   : add_rmsnorm_vec_kernel<T, 4, SHIFT>;
+  return nv == 1   ? add_rmsnorm_vec_kernel<T, 1>
+         : nv == 2 ? add_rmsnorm_vec_kernel<T, 2>
+                   : add_rmsnorm_vec_kernel<T, 4>;
+}
+template <typename T, int U>
+NormKernel<T> group_kernel(int ng) {
+  if constexpr (sizeof(T) == 2 && U > 1)
+    if (ng == 8) return add_rmsnorm_group_kernel<T, U, 8>;
+  return ng == 1 ? add_rmsnorm_group_kernel<T, U, 1> : add_rmsnorm_group_kernel<T, U, 4>;
 }
 
 template <typename T>
@@ -328,15 +374,22 @@ fp4moe_status norm_launch(int32_t rows, int32_t H, const void* x, const void* re
   int threads = NORM_THREADS;
   const int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
-  const bool shift = H % N != 0;
-  // vectors of a row: one more where its first element lies inside a vector
-  const int64_t vecs = shift ? ((int64_t)H + 2 * N - 2) / N : H / N;
-  if (vecs <= 4 * 1024) {
+  const int64_t vecs = ((int64_t)H + N - 1) / N, groups = ((int64_t)H + 127) / 128;
+  if (H % N == 0 && vecs <= 4 * 1024) {
     // vectors a thread: one while the rows leave SMs idle, then two, and as many as 1024 threads need
     int nv = rows <= nsm ? 1 : 2;
     while ((vecs + nv - 1) / nv > 1024) nv *= 2;
     threads = (int)((vecs + nv - 1) / nv + 31) / 32 * 32;
-    kernel = shift ? vec_kernel<T, true>(nv) : vec_kernel<T, false>(nv);
+    kernel = vec_kernel<T>(nv);
+  } else if (H % N != 0 && groups <= (sizeof(T) == 2 && H % 2 == 0 ? 8 : 4) * 32) {
+    // groups a warp: one while the rows leave SMs idle, then four (8192 x 4090 bf16 52 us; one 85, two 58, eight 53),
+    // and eight where 32 warps need them and their registers suffice
+    const int ng = groups > 4 * 32 ? 8 : rows > nsm || groups > 32 ? 4 : 1;
+    threads = (int)((groups + ng - 1) / ng) * 32;
+    if constexpr (sizeof(T) == 4)
+      kernel = H % 2 == 0 ? group_kernel<T, 2>(ng) : group_kernel<T, 1>(ng);
+    else
+      kernel = H % 4 == 0 ? group_kernel<T, 4>(ng) : H % 2 == 0 ? group_kernel<T, 2>(ng) : group_kernel<T, 1>(ng);
   }
   const cudaError_t r =
       launch_pdl(kernel, dim3((unsigned)rows), dim3((unsigned)threads), 0, st, H, static_cast<const T*>(x),
