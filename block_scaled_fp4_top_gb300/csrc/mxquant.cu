@@ -12,9 +12,9 @@
 // product may read those, and a zero scale byte is a finite scale in either format.
 //
 // Both directions are bound by memory: 8192 x 4096 bf16 is 84 MB in and out, 12.4 us at the copy rate, and takes
-// 15.6 us to MXFP4 and 16.3 to NVFP4, 15.7 and 16.6 us back. A thread takes 32 bytes of the plain matrix, one whole
+// 15.5 us to MXFP4 and 16.4 to NVFP4, 14.9 and 16.2 us back. A thread takes 32 bytes of the plain matrix, one whole
 // sector, in one 256-bit access where rows are 32-byte aligned (two 16-byte ones: 19.5 us). Rows at any other
-// element are read and written in aligned vectors too, shifted into place in registers (8192 x 4095: 21 and 23 us).
+// element are read and written in aligned vectors too, shifted into place in registers (8192 x 4095: 20 and 23 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,8 +26,9 @@ namespace {
 
 constexpr int MQ_THREADS = 256;
 // More rows than this many CTAs an SM take are looped over, with the next row's loads in flight: 8192 x 4096 bf16 to
-// MXFP4 takes 15.6 us with 8, 15.8 with 4, 16.6 with 16 and 21.5 without a loop; the inverse 15.6, 15.9, 15.0, 16.5.
-constexpr int kCtasPerSm = 8;
+// MXFP4 takes 15.5 us with 8, 15.6 with 4, 15.9 with 12 and 21.5 without a loop; the inverse, whose CTAs hold fewer
+// registers, 15.4, 15.8, 14.9 and 16.5.
+constexpr int kCtasPerSm = 8, kCtasPerSmInverse = 12;
 
 // 2^-X for X in [-127, 125]
 __device__ __forceinline__ float exp2_neg(int X) { return __uint_as_float((uint32_t)(127 - X) << 23); }
@@ -134,14 +135,25 @@ __global__ void __launch_bounds__(MQ_THREADS)
   const int left = K - seg * 16;  // elements of a row from this piece on
   const int64_t step = (int64_t)gridDim.y * blockDim.y;
   int64_t r = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
-  Piece16<T, WIDE> next;
-  if (r < rows && left > 0) next.load(x, r * K + (int64_t)seg * 16, n);
+  Piece16<T, WIDE> piece;
+  auto fetch = [&](int64_t row) {
+    if (row < rows && left > 0) piece.load(x, row * K + (int64_t)seg * 16, n);
+  };
+  fetch(r);
   for (; r < row_end; r += step) {
-    Piece16<T, WIDE> cur = next;
-    if (r + step < rows && left > 0) next.load(x, (r + step) * K + (int64_t)seg * 16, n);
     const bool any = r < rows && left > 0;
     float v[16];
-    if (any) cur.get(v);
+    // The next row's load goes out as soon as its registers are free: after the unpacking, which shifts and widens,
+    // or after a copy where the piece is only eight registers (8192 x 4096 bf16 to NVFP4 16.3 against 18.5 us;
+    // unaligned and fp32 pieces are better unpacked first, 4096 x 4095 fp32 14.5 against 18.5 us).
+    if constexpr (WIDE && sizeof(T) == 2) {
+      Piece16<T, WIDE> cur = piece;
+      fetch(r + step);
+      if (any) cur.get(v);
+    } else {
+      if (any) piece.get(v);
+      fetch(r + step);
+    }
     if (left < 16 || !any) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) v[k] = any && k < left ? v[k] : 0.0f;
@@ -181,7 +193,7 @@ __device__ __forceinline__ void piece_values(uint32_t w0, uint32_t w1, uint32_t 
     t1 = __fdiv_rn(s, g);
     t15 = __fdiv_rn(1.5f * s, g);
     const float a = fabsf(t1);
-    exact = a >= 0x1p-100f && a <= 0x1p100f;
+    exact = (a >= 0x1p-100f && a <= 0x1p100f) || (s == 0.0f && a == 0.0f);  // a block of zeros is zeros
   }
   if constexpr (sizeof(T) == 2) {
     float mag[8] = {0.0f, 0.5f * t1, t1, t15, 2.0f * t1, 2.0f * t15, 4.0f * t1, 4.0f * t15};
@@ -351,12 +363,12 @@ __global__ void __launch_bounds__(MQ_THREADS)
 struct Shape {
   dim3 grid, block;
 };
-Shape row_shape(int64_t rows, int64_t pieces) {
+Shape row_shape(int64_t rows, int64_t pieces, int ctas_per_sm) {
   unsigned tx = 8;
   while (tx < MQ_THREADS && tx < pieces) tx *= 2;
   const unsigned ty = MQ_THREADS / tx;
   const int64_t gx = (pieces + tx - 1) / tx, want = (rows + ty - 1) / ty;
-  const int64_t fill = std::max<int64_t>(1, (int64_t)sm_count() * kCtasPerSm / gx);
+  const int64_t fill = std::max<int64_t>(1, (int64_t)sm_count() * ctas_per_sm / gx);
   return {dim3((unsigned)gx, (unsigned)std::min<int64_t>({want, fill, 65535})), dim3(tx, ty)};
 }
 
@@ -365,7 +377,7 @@ fp4moe_status quantize_launch(int32_t rows, int32_t K, const void* x, const floa
                               cudaStream_t st) {
   const int64_t ct = mx_col_tiles(FMT, K), segs = ct * 4 * MxFormat<FMT>::kBlock / 16;
   const int64_t row_end = mx_row_tiles(rows) * 128;
-  const Shape s = row_shape(row_end, segs);
+  const Shape s = row_shape(row_end, segs, kCtasPerSm);
   const bool wide = K % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
   return launch_pdl(wide ? mx_quantize_kernel<FMT, T, true> : mx_quantize_kernel<FMT, T, false>, s.grid, s.block, 0, st, rows, row_end, K, (int)segs, ct,
                     mx_row_bytes(K), static_cast<const T*>(x), gs, codes, sf) == cudaSuccess
@@ -377,7 +389,7 @@ template <int FMT, typename T>
 fp4moe_status dequantize_launch(int32_t rows, int32_t K, const uint8_t* codes, const uint8_t* sf, const float* gs,
                                 void* out, cudaStream_t st) {
   const bool shift = K % (16 / sizeof(T)) != 0;
-  const Shape s = row_shape(rows, ((int64_t)K * (int)sizeof(T) + 31) / 32);
+  const Shape s = row_shape(rows, ((int64_t)K * (int)sizeof(T) + 31) / 32, kCtasPerSmInverse);
   const bool wide = K % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   return launch_pdl(shift  ? mx_dequantize_kernel<FMT, T, true, false>
                     : wide ? mx_dequantize_kernel<FMT, T, false, true>
