@@ -11,8 +11,8 @@
 //
 // Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
 // between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
-// back (1 x 4096 bf16 1.9 us, 64 rows 2.1 us), so they take the most threads; many rows take two 16-byte vectors a
-// thread (8192 x 4096 bf16 with the FP8 copy 47 us, 6.4 TB/s, 95 % of a copy's rate).
+// back (1 x 4096 bf16 1.9 us, 64 rows 2.1 us), so they take the most threads; many rows take two or four 16-byte
+// vectors a thread (8192 x 4096 bf16 with the FP8 copy 47 us, 6.4 TB/s, 95 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(1024)
   pdl_trigger();
   const size_t row = (size_t)blockIdx.x * H;
   auto at = [&](int i) { return (i * (int)blockDim.x + (int)threadIdx.x) * N; };
-  // Every load of the row is issued before the first is waited for. gamma waits until x and the residual are
-  // joined where its registers would cost occupancy: 8192 x 4096 bf16 without a residual 24.7 against 29.7 us.
+  // Every load of the row is issued before the first is waited for. gamma waits until x and the residual are joined
+  // where its registers would cost occupancy: 8192 x 4096 bf16 without a residual, two vectors, 27 against 30 us.
   uint4 hv[NV], rv[NV], gv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -376,8 +376,11 @@ fp4moe_status norm_launch(int32_t rows, int32_t H, const void* x, const void* re
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
   const int64_t vecs = ((int64_t)H + N - 1) / N, groups = ((int64_t)H + 127) / 128;
   if (H % N == 0 && vecs <= 4 * 1024) {
-    // vectors a thread: one while the rows leave SMs idle, then two, and as many as 1024 threads need
-    int nv = rows <= nsm ? 1 : 2;
+    // vectors a thread: one while the rows leave SMs idle, two while an SM has one row or two or a row leaves four
+    // warps idle, else four, and as many as 1024 threads need (bf16 with the FP8 copy, two and four: 300 x 4096 2.8
+    // and 3.3 us, 8192 x 2048 24.9 and 25.7, 8192 x 4096 47.4 and 47.6, 4096 x 7168 48.6 and 43.0, 2000 x 8192 27.3
+    // and 25.4)
+    int nv = rows <= nsm ? 1 : rows <= 2 * nsm || vecs < 512 ? 2 : 4;
     while ((vecs + nv - 1) / nv > 1024) nv *= 2;
     threads = (int)((vecs + nv - 1) / nv + 31) / 32 * 32;
     kernel = vec_kernel<T>(nv);
