@@ -751,10 +751,12 @@ fp4moe_status fp4moe_refresh_gs2(const fp4moe_config* cfg, void* ws, const float
 namespace {
 bool dtype_ok(int32_t d) { return d == FP4MOE_BF16 || d == FP4MOE_FP16 || d == FP4MOE_FP32; }
 bool format_ok(int32_t f) { return f == FP4MOE_W_NVFP4 || f == FP4MOE_W_MXFP4; }
+// Column indices are 32-bit, and kernels step past a row's end by a CTA's width at most.
+constexpr int32_t kMaxWidth = INT32_MAX - 8192;
 // A matrix of the dense operators: its scale tiles are addressed with 32-bit tile indices by TMA.
 fp4moe_status check_mx(int32_t format, int32_t rows, int32_t K) {
   if (rows < 0 || K <= 0) return FP4MOE_INVALID_ARG;
-  if (!format_ok(format)) return FP4MOE_UNSUPPORTED;
+  if (!format_ok(format) || K > kMaxWidth) return FP4MOE_UNSUPPORTED;
   if (mx_row_tiles(rows) * mx_col_tiles(format, K) > INT32_MAX) return FP4MOE_UNSUPPORTED;
   return FP4MOE_OK;
 }
@@ -764,7 +766,7 @@ fp4moe_status fp4moe_add_rmsnorm(int32_t dtype, int32_t T, int32_t H, const void
                                  const void* gamma, float eps, void* residual_out, void* y, uint8_t* y_codes,
                                  float* y_scales, int64_t scale_stride, fp4moe_stream_t stream) {
   if (T < 0 || H <= 0 || !(eps >= 0.0f) || std::isinf(eps)) return FP4MOE_INVALID_ARG;
-  if (!dtype_ok(dtype)) return FP4MOE_UNSUPPORTED;
+  if (!dtype_ok(dtype) || H > kMaxWidth) return FP4MOE_UNSUPPORTED;
   if (T == 0) return FP4MOE_OK;  // an empty batch's buffers may be null
   if ((residual == nullptr) != (residual_out == nullptr)) return FP4MOE_INVALID_ARG;
   if ((y_codes == nullptr) != (y_scales == nullptr)) return FP4MOE_INVALID_ARG;

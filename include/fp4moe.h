@@ -526,7 +526,8 @@ typedef enum fp4moe_dtype { FP4MOE_BF16 = 0, FP4MOE_FP16 = 1, FP4MOE_FP32 = 2 } 
  *   not shifted), but not the same buffer as each other.
  * A NaN or an infinity in a row reaches y as the formula has it. A group of n
  * that holds a NaN has a NaN scale and NaN codes (0x7F or 0xFF).
- * Any T >= 0, H >= 1, finite eps >= 0; else FP4MOE_INVALID_ARG.
+ * Any T >= 0, H >= 1, finite eps >= 0; else FP4MOE_INVALID_ARG. H within 8192
+ * of 2^31 is FP4MOE_UNSUPPORTED.
  */
 fp4moe_status fp4moe_add_rmsnorm(int32_t dtype, int32_t T, int32_t H, const void* x, const void* residual,
                                  const void* gamma, float eps, void* residual_out, void* y, uint8_t* y_codes,
@@ -544,7 +545,7 @@ fp4moe_status fp4moe_add_rmsnorm(int32_t dtype, int32_t T, int32_t H, const void
  *     4; bytes past the matrix must be zero (fp4moe_mx_quantize writes them).
  * fp4moe_mx_bytes gives both sizes (host arithmetic; any output may be NULL).
  * Any rows >= 0 and K >= 1 (else FP4MOE_INVALID_ARG); fewer than 2^31 scale
- * tiles (else FP4MOE_UNSUPPORTED).
+ * tiles and K not within 8192 of 2^31 (else FP4MOE_UNSUPPORTED).
  */
 fp4moe_status fp4moe_mx_bytes(int32_t format, int32_t rows, int32_t K, size_t* code_bytes, size_t* sf_bytes);
 

@@ -87,6 +87,16 @@ def test_norm_refusals(lib):
     assert n(T=0, stride=0) == _lib.OK
 
 
+def test_widths_whose_column_index_would_pass_32_bits(lib):
+    from block_scaled_fp4_top_gb300 import _lib
+    top = 2**31 - 1 - 8192
+    for K, want in ((top, _lib.OK), (top + 1, _lib.UNSUPPORTED), (2**31 - 1, _lib.UNSUPPORTED)):
+        assert lib.fp4moe_mx_bytes(MX, 1, K, None, None) == want
+        assert lib.fp4moe_mx_quantize(MX, 0, 0, K, None, None, None, None, None) == want
+        assert lib.fp4moe_mx_dequantize(MX, 0, 0, K, None, None, None, None, None) == want
+        assert lib.fp4moe_add_rmsnorm(0, 0, K, None, None, None, 1e-6, None, None, None, None, 0, None) == want
+
+
 def test_shared_fp8_refusals(lib):
     from block_scaled_fp4_top_gb300 import _lib, api
     cfg = api.config(4096, 2048, 256, 6, 64, 10.0, shared_inter=2048)
