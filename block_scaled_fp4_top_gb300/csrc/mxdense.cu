@@ -390,12 +390,14 @@ bool dense_configure() {
   return ok == 1;
 }
 
-// Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 40 sizes from 1 x 4096 x 256 to
-// 8192 x 8192 x 2048 (bf16 out): the one picked is within 7 % of the fastest at all of them. KB: 256-element stages
-// of K.
+// Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 41 sizes from 1 x 4096 x 256 to
+// 8192 x 8192 x 2048: the one picked is within 5 % of the fastest at all of them (bn64 / bn128 / pair / two pairs, us:
+// 64 x 8192 x 4096 MXFP4 7.2 7.3 8.8 10.1, 512 x 4096 x 4096 12.0 7.9 9.3 9.4, 768 x 4096 x 4096 16.6 12.6 9.9 10.2,
+// 8192 x 4096 x 2048 70 43 28.9 29.5, 1500 x 3000 x 2000 19 14 10.6 9.7; split in two or four 1 x 4096 x 4096 takes
+// 5.9 and 5.6 instead of 6.9, 64 x 4096 x 4096 6.5 and 9.8 instead of 6.9). KB: 256-element stages of K.
 //   128 x 64, 128 x 128    a launch, 700 a tile and 270 .. 300 a stage
 //   split over S CTAs      KB / S stages; joining: 1100, and a fifth of a ns for each fp32 value that is sent
-//   256 x 256 on a pair    1350 a tile and 316 a stage, or 1250 and 284 with two pairs in a cluster (36 clusters of
+//   256 x 256 on a pair    1050 a tile and 306 a stage, or 1000 and 290 with two pairs in a cluster (36 clusters of
 //                          four fit on 152 SMs, 76 of two)
 struct Plan {
   int pairs;  // 0: this file's kernel, with bn and S
@@ -424,7 +426,7 @@ Plan pick_plan(int M, int N, int KB, int nsm) {
     const int64_t tiles = up(M, 256 * pairs) * up(N, 256);
     const int64_t clusters = pairs == 1 ? nsm / 2 : (nsm - nsm / 18) / 4;
     if (clusters > 0)
-      offer({pairs, 0, 1}, 3600 + up(tiles, clusters) * (pairs == 1 ? KB * 316 + 1350 : KB * 284 + 1250));
+      offer({pairs, 0, 1}, 3600 + up(tiles, clusters) * (pairs == 1 ? KB * 306 + 1050 : KB * 290 + 1000));
   }
   return best;
 }

@@ -6,15 +6,25 @@
 // and reads per MAC: those tiles need 12 KB through shared memory twice (in by TMA, out to the MMA) every 128
 // cycles, more than its 128 bytes a cycle.
 //   warps 0-7   epilogue, in both CTAs (warp w: TMEM lanes 32 (w % 4) .., columns 128 (w / 4) ..).
-//   warp 8      producer, in both CTAs: its own rows of A and B, the scale tiles of its own A rows and of all 256 B
-//               rows (the MMA reads B scales from each CTA's own TMEM). All loads signal the leader's barrier.
+//   warp 8      producer, in both CTAs: its own rows of A and B, the scale tiles of its own A rows, and those of its B
+//               rows for both CTAs by multicast (the MMA reads the scales of all 256 B rows from each CTA's own TMEM).
+//               All loads signal the leader's barrier.
 //   warp 9      leader: scale copies (tcgen05.cp.cta_group::2, each CTA's tiles into its own TMEM) and MMAs.
-//               Other CTA: tells the leader that its epilogue warps have emptied the accumulator.
-// Commits that free a ring stage or hand over the accumulator arrive in both CTAs.
+// Commits that free a ring stage or hand over the accumulator arrive in both CTAs, and all sixteen epilogue warps tell
+// the leader that the accumulator is empty.
 //
 // PAIRS = 2: a cluster of two pairs owns 512 x 256. Both pairs need the same B, so each CTA loads half of its B rows
-// and a quarter of the B scales and multicasts them to the CTAs that need them: 25 instead of 35 KB per CTA and
-// stage out of L2. A stage is then free when both pairs' MMAs have read it.
+// and a quarter of the B scales and multicasts them to the CTAs that need them: 25 instead of 34 KB per CTA and
+// stage out of L2. A stage is then free when both pairs' MMAs have read it. Fewer bytes, but only 144 of the 152 SMs
+// have a place in a cluster of four: 9216 x 4096 x 4096 MXFP4 takes 48.8 instead of 50.1 us (eight rounds of tiles
+// either way), 8192 x 4096 x 4096 47.3 instead of 45.1 (eight against seven).
+//
+// 8192 x 4096 x 4096: MXFP4 44.8 us, 6.1 PFLOP/s of the 9.4 that the MMAs reach alone, NVFP4 48.0; 8192^3 152 us, 7.2.
+// Bounds: operands from L2 (34 KB a stage and SM, 600 cycles for MMAs of 512; five ring stages 48 us, four 51; the B
+// scales loaded by both CTAs 46.4 instead of 45.0), and 1000 ns between the last MMA of a tile and the first of the next, in which the
+// epilogue empties TMEM: two accumulators of 256 columns and the scales do not fit its 512. Not faster: the output by
+// TMA from shared memory (45.0 and 46.9, but 8192 x 8192 x 2048 57 instead of 53), all 128 columns of an epilogue
+// warp in flight at once (spills, 53), a stage's scale copies ahead of the MMAs before it (50).
 // The rest (scale-factor ids, K tails, bounded waits) is as in mxdense.cu.
 #include <mutex>
 
@@ -45,7 +55,7 @@ struct PairCfg {
   static_assert(kStage % 1024 == 0, "stage must keep 1024-byte alignment");
   static_assert(PBN + kSlotCols * kStages <= PTMEM_COLS, "accumulator and scale slots fit TMEM");
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(8 * (2 * kStages + 4) <= 240, "barriers fit their area");
+  static_assert(8 * (2 * kStages + 3) <= 240, "barriers fit their area");
 };
 
 // ------------------------------------------------------------- PTX, CTA pairs
@@ -107,15 +117,16 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bd
         : "memory");
 }
 // Arrive on a barrier of any CTA of the cluster (an address from map_cluster). It publishes no memory writes: what it
-// orders are TMEM reads, with the tcgen05 fences of both sides. A release at cluster scope here and a fence at the
-// other end cost 1.1 us of a tile's 7.8.
+// orders are TMEM reads, complete at the arriving warp's tcgen05.wait::ld, with the tcgen05 fences of both sides. A
+// release at cluster scope here and a fence at the other end cost 1.1 us a tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
-// Tile t: groups of 8 tile rows, so that the tiles of a wave share their operands' rows in L2.
+// Tile t: groups of 4 tile rows, so that the tiles of a wave share their operands' rows in L2 (8192 x 4096 x 4096
+// MXFP4 44.7 us; groups of 8 45.0, 16 45.3, 32 46.4).
 __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
-  constexpr int G = 8;
+  constexpr int G = 4;
   const int g = t / (G * nt), first = g * G, rows = min(G, mt - first), in = t - g * G * nt;
   m = first + in % rows;
   n = in / rows;
@@ -136,9 +147,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   const uint32_t bar_full = smem + C::kBarOff;           // leader's: both CTAs' copies of a stage
   const uint32_t bar_empty = bar_full + 8 * C::kStages;  // each CTA's own: every pair's MMAs have read the stage
   const uint32_t bar_tfull = bar_empty + 8 * C::kStages; // each CTA's own: the accumulator is complete
-  const uint32_t bar_tempty = bar_tfull + 8;             // each CTA's own: its epilogue warps have read it
-  const uint32_t bar_tpeer = bar_tempty + 8;             // leader's: so have the other CTA's
-  const uint32_t bar_drain = bar_tpeer + 8;
+  const uint32_t bar_tempty = bar_tfull + 8;             // leader's: both CTAs' epilogue warps have read it
+  const uint32_t bar_drain = bar_tempty + 8;
 
   if (warp == 0) pair_tmem_alloc(smem_u32(&s_tmem), PTMEM_COLS);
   if (threadIdx.x == 32 * PPRODUCER) {
@@ -147,8 +157,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       mbar_init(bar_empty + 8 * s, PAIRS);
     }
     mbar_init(bar_tfull, 1);
-    mbar_init(bar_tempty, PEPI);
-    mbar_init(bar_tpeer, 1);
+    mbar_init(bar_tempty, 2 * PEPI);
     mbar_init(bar_drain, 1);
     fence_mbar_init();
   }
@@ -187,18 +196,15 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * C::kBytes);
         tma_load_2d_pair(st, &maps.a, full, kb * 128, ar * 128, pol);
         tma_load_2d_pair(sf, &maps.sfa, full, 0, ar * prm.ct + kb * C::kSfTiles, pol);
-        if constexpr (PAIRS == 1) {
+        if constexpr (PAIRS == 1)
           tma_load_2d_pair(st + C::kA, &maps.b, full, kb * 128, (2 * n + (int)rank) * 128, pol);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d_pair(sf + C::kSfa * (1 + h), &maps.sfb, full, 0, (2 * n + h) * prm.ct + kb * C::kSfTiles, pol);
-        } else {  // rows 64 pair .. of this rank's 128 B rows; half of the scale tiles of B rows 128 rank ..
+        else  // rows 64 pair .. of this rank's 128 B rows, for this rank of both pairs
           tma_load_2d_pair_multicast(st + C::kA + pair * 8192u, &maps.b, full, kb * 128,
                                      (2 * n + (int)rank) * 128 + 64 * (int)pair, (uint16_t)(5u << rank), pol);
-          constexpr int Q = C::kSfTiles / 2;
-          tma_load_2d_pair_multicast(sf + C::kSfa * (1 + rank) + 512u * Q * pair, &maps.sfb, full, 0,
-                                     (2 * n + (int)rank) * prm.ct + kb * C::kSfTiles + Q * (int)pair, kAll, pol);
-        }
+        // this CTA's share of the scale tiles of B rows 128 rank .., for every CTA
+        constexpr int Q = C::kSfTiles / PAIRS;
+        tma_load_2d_pair_multicast(sf + C::kSfa * (1 + rank) + 512u * Q * pair, &maps.sfb, full, 0,
+                                   (2 * n + (int)rank) * prm.ct + kb * C::kSfTiles + Q * (int)pair, kAll, pol);
       }
     }
     // Let the copies already issued land before the CTA exits. A leader's barrier counts every copy into its
@@ -227,7 +233,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     for (int t = cluster; ok && t < tiles; t += clusters, ++tl) {
       // both epilogues have moved the previous tile's accumulator out of TMEM
       const uint32_t tph = ((uint32_t)tl & 1u) ^ 1u;
-      if (!mbar_wait_warp(bar_tempty, tph, prm.err) || !mbar_wait_warp(bar_tpeer, tph, prm.err)) break;
+      if (!mbar_wait_warp(bar_tempty, tph, prm.err)) break;
       tc_fence_after();
       for (int kb = 0; kb < KB; ++kb) {
         if (!mbar_wait_warp(bar_full + 8 * s, ph, prm.err)) {
@@ -270,19 +276,11 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       pair_commit(bar_drain);
       drain_wait(bar_drain, 0);  // no MMA may still write TMEM when it is freed
     }
-  } else if (warp == PMMA && lane == 0) {
-    // one arrival for eight warps, ahead of their stores: an arrival of each warp would queue behind the stores of the
-    // warps before it
-    const uint32_t tpeer = map_cluster(bar_tpeer, lead);
-    int tl = 0;
-    for (int t = cluster; t < tiles; t += clusters, ++tl) {
-      if (!mbar_wait(bar_tempty, (uint32_t)tl & 1u, prm.err)) break;
-      mbar_arrive_cluster(tpeer);
-    }
   } else if (warp < PEPI) {
     constexpr int W = PBN / 2;  // columns of one warp
     const int quarter = warp & 3, half = warp >> 2;
     uint8_t* stage = smem_raw + C::kEpiOff + warp * kEpiStage;
+    const uint32_t tempty = map_cluster(bar_tempty, lead);
     const float alpha = prm.alpha != nullptr ? __ldg(prm.alpha) : 1.0f;
     int tl = 0;
     for (int t = cluster; t < tiles; t += clusters, ++tl) {
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       if (live) load_packed<T, W>(tmem + (uint32_t)(W * half) + ((uint32_t)(quarter * 32) << 16), alpha, w);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_tempty);  // this warp's share of the accumulator is out of TMEM
+      if (lane == 0) mbar_arrive_cluster(tempty);  // this warp's share of the accumulator is out of TMEM
       if (live) {
         constexpr int COLS = 64 / (int)sizeof(T);
 #pragma unroll
