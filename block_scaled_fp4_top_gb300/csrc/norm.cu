@@ -11,8 +11,8 @@
 //
 // Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
 // between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
-// back (1 x 4096 bf16 1.9 us, 64 rows 2.1 us), so they take the most threads; many rows take two or four 16-byte
-// vectors a thread (8192 x 4096 bf16 with the FP8 copy 47 us, 6.4 TB/s, 95 % of a copy's rate).
+// back (1 x 4096 bf16 2.0 us, 64 rows 2.1 us), so they take the most threads; many rows take two or four 16-byte
+// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48 us, 6.3 TB/s, 93 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -33,15 +33,24 @@ __device__ __forceinline__ float cta_sum(float v, float* s_red) {
   return v;
 }
 
-// n / s as (n * up) * inv, to within two units of fp32's last place; 0 where s == 0. One reciprocal serves a group:
-// exact enough for a value that E4M3 rounds to four bits. Below 2^-120 it would overflow, so n and s are first
-// scaled up by 2^100, exactly (a subnormal n included).
+// n / s, to half a unit of fp32's last place in all but rare cases; 0 where s == 0. One reciprocal serves a group, and
+// two fused steps per element take its error out (n * inv alone is off by up to two units, as much as n itself, and
+// codes near a tie between two E4M3 values go the wrong way that much more often). Below 2^-120 the reciprocal would overflow, so n and s are
+// first scaled up by 2^100, exactly (a subnormal n included). s = inf: finite n give 0, infinite ones NaN.
 struct Fp8Scale {
-  float up, inv;
+  float up, s, inv;
 };
 __device__ __forceinline__ Fp8Scale fp8_scale(float s) {
-  if (s < 0x1p-120f) return s == 0.0f ? Fp8Scale{0.0f, 0.0f} : Fp8Scale{0x1p100f, __frcp_rn(s * 0x1p100f)};
-  return Fp8Scale{1.0f, __frcp_rn(s)};
+  if (s < 0x1p-120f) {
+    if (s == 0.0f) return Fp8Scale{0.0f, 0.0f, 0.0f};
+    return Fp8Scale{0x1p100f, s * 0x1p100f, __frcp_rn(s * 0x1p100f)};
+  }
+  return Fp8Scale{1.0f, isinf(s) ? 0.0f : s, __frcp_rn(s)};
+}
+__device__ __forceinline__ float fp8_quotient(float n, const Fp8Scale& f) {
+  n *= f.up;
+  const float q = n * f.inv;
+  return fmaf(fmaf(-q, f.s, n), f.inv, q);
 }
 // N codes of the quotients q.
 template <int N>
@@ -104,7 +113,7 @@ __global__ void __launch_bounds__(NORM_THREADS)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = g * 128 + 32 * i + lane;
-        if (j < H) codes[row + j] = (uint8_t)cvt_e4m3x2(n[i] * f.up * f.inv, 0.0f);
+        if (j < H) codes[row + j] = (uint8_t)cvt_e4m3x2(fp8_quotient(n[i], f), 0.0f);
       }
       if (lane == 0) scales[(size_t)g * scale_stride + blockIdx.x] = s;
     }
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(1024)
     const Fp8Scale f = fp8_scale(s);
     uint32_t w[N / 4];
 #pragma unroll
-    for (int k = 0; k < N; ++k) n[k] = n[k] * f.up * f.inv;
+    for (int k = 0; k < N; ++k) n[k] = fp8_quotient(n[k], f);
     make_codes<N>(w, n);
     store_codes<N>(codes + row + j, w);
     if (j % 128 == 0) scales[(size_t)(j / 128) * scale_stride + blockIdx.x] = s;
@@ -249,9 +258,9 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 // Widths that the 16-byte vectors do not divide. Rows then start at any element, and a vector that is aligned for
 // one row is not for the next, so a lane reads and writes U elements at a time, the most that divide H (4, 2 or
 // 1), in accesses that are contiguous over the warp. A warp takes whole FP8 groups: NG of them, in registers, and
-// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 52 us, 8192 x 4092 49 us, 8192 x 4095
-// (single elements: bound by the accesses) 75 us, against 77, 75 and 78 us with whole vectors that were cut at the
-// aligned addresses and shifted into place, and 47 us at 4096.
+// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 54 us, 8192 x 4092 50 us, 8192 x 4095
+// (single elements: bound by the accesses) 79 us, against 77, 75 and 78 us with whole vectors that were cut at the
+// aligned addresses and shifted into place, and 48 us at 4096. 1000 x 4090 fp16: 8.9 against 12.2 us.
 template <typename T, int U, int NG>
 __global__ void __launch_bounds__(1024)
     add_rmsnorm_group_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
@@ -334,7 +343,7 @@ __global__ void __launch_bounds__(1024)
       const int j = at(i, s);
       if (j >= H) continue;
 #pragma unroll
-      for (int k = 0; k < U; ++k) n[s][k] = n[s][k] * f.up * f.inv;
+      for (int k = 0; k < U; ++k) n[s][k] = fp8_quotient(n[s][k], f);
       if constexpr (U == 4) {
         uint32_t w[1];
         make_codes<4>(w, n[s]);
