@@ -44,10 +44,14 @@ def _p(t):
     return t.data_ptr()
 
 
+# torch's own calls behind torch.cuda.current_stream(), absent from a build without CUDA
+_raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+
+
 def _s(stream):
     # the raw handle of the current stream, without building a torch.cuda.Stream (0.2 against 3 us a call)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_device())
     return stream.cuda_stream
 
 
@@ -260,6 +264,7 @@ def moe_forward_shared_fp8(cfg, T, x, x_codes, x_scales, router_w, router_bias, 
 # A small call is bound by the host, so each tensor is checked and turned into its pointer in one go.
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
 _BYTE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+_U8, _F32 = torch.uint8, torch.float32
 
 
 def _arg(name, t, shape, dtype):
@@ -274,7 +279,7 @@ def _arg(name, t, shape, dtype):
 
 
 def _arg_bytes(name, t, nbytes):
-    if t.dtype is not torch.uint8 or t.numel() != nbytes:
+    if t.dtype is not _U8 or t.numel() != nbytes:
         raise Fp4MoeError(f"{name}: expected {nbytes} bytes (uint8), got {t.numel()} of {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
@@ -284,33 +289,34 @@ def _arg_bytes(name, t, nbytes):
 def _arg_scalar(name, t):
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.numel() < 1:
+    if t.dtype is not _F32 or t.numel() < 1:
         raise Fp4MoeError(f"{name}: expected one float32, got {t.numel()} of {t.dtype}")
     return _p(t)
 
 
 def _arg_matrix(name, t):
-    """(rows, columns, fp4moe_dtype, pointer) of a matrix whose sizes the call takes."""
-    d = _DTYPES.get(t.dtype)
+    """(shape, dtype, fp4moe_dtype, pointer) of a matrix whose sizes the call takes."""
+    dt, shape = t.dtype, t.shape
+    d = _DTYPES.get(dt)
     if d is None:
-        raise Fp4MoeError(f"{name}: unsupported dtype {t.dtype}: bfloat16, float16 or float32")
-    if t.dim() != 2:
-        raise Fp4MoeError(f"{name}: expected a matrix, got {tuple(t.shape)}")
+        raise Fp4MoeError(f"{name}: unsupported dtype {dt}: bfloat16, float16 or float32")
+    if len(shape) != 2:
+        raise Fp4MoeError(f"{name}: expected a matrix, got {tuple(shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
-    rows, cols = t.shape
-    return rows, cols, d, t.data_ptr()
+    return shape, dt, d, t.data_ptr()
 
 
 def _check_fp8(codes, scales, T, H):
-    """Shape and type of block-FP8 activations: codes [T, H], scales [ceil(H / 128), at least T]."""
+    """Shape and type of block-FP8 activations: codes [T, H], scales [ceil(H / 128), at least T]. The scales' columns."""
     if codes.dtype not in _BYTE_TYPES or codes.shape != (T, H):
         raise Fp4MoeError(f"codes: expected {(T, H)} of {' or '.join(map(str, _BYTE_TYPES))}, got "
                           f"{tuple(codes.shape)} of {codes.dtype}")
-    if scales.dtype is not torch.float32 or scales.dim() != 2 or scales.shape[0] != (H + 127) // 128 \
-            or scales.shape[1] < T:
+    shape = scales.shape
+    if scales.dtype is not _F32 or len(shape) != 2 or shape[0] != (H + 127) // 128 or shape[1] < T:
         raise Fp4MoeError(f"scales: expected [{(H + 127) // 128}, at least {T}] of torch.float32, got "
-                          f"{tuple(scales.shape)} of {scales.dtype}")
+                          f"{tuple(shape)} of {scales.dtype}")
+    return shape[1]
 
 
 def fp4moe_add_rmsnorm(x, residual, gamma, eps, residual_out, y, y_codes=None, y_scales=None, stream=None):
@@ -320,12 +326,11 @@ def fp4moe_add_rmsnorm(x, residual, gamma, eps, residual_out, y, y_codes=None, y
     x [T, H] bfloat16, float16 or float32, and residual, residual_out, y, gamma [H] of its type. residual with
     residual_out, and y_codes with y_scales, may be None; so may gamma (ones), and y where y_codes is given.
     residual_out and y may each be x or residual."""
-    T, H, d, px = _arg_matrix("x", x)
-    shape, dt = x.shape, x.dtype
+    shape, dt, d, px = _arg_matrix("x", x)
+    T, H = shape
     stride = 0
     if y_codes is not None and y_scales is not None:
-        _check_fp8(y_codes, y_scales, T, H)
-        stride = y_scales.shape[1]
+        stride = _check_fp8(y_codes, y_scales, T, H)
     _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, px, _arg("residual", residual, shape, dt),
                                           _arg("gamma", gamma, (H,), dt), eps,
                                           _arg("residual_out", residual_out, shape, dt), _arg("y", y, shape, dt),
@@ -352,7 +357,7 @@ def fp4moe_mx_bytes(fmt: int, rows: int, K: int):
 
 def fp4moe_mx_quantize(fmt, x, gs, codes, sf, stream=None):
     """x [rows, K] to E2M1 codes and block scales (fmt W_MXFP4, or W_NVFP4 under the global scale gs)."""
-    rows, K, d, px = _arg_matrix("x", x)
+    (rows, K), _, d, px = _arg_matrix("x", x)
     _check(_lib.load().fp4moe_mx_quantize(fmt, d, rows, K, px, _arg_scalar("gs", gs),
                                           _arg_bytes("codes", codes, rows * mx_row_bytes(K)),
                                           _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K)), _s(stream)),
@@ -361,7 +366,7 @@ def fp4moe_mx_quantize(fmt, x, gs, codes, sf, stream=None):
 
 def fp4moe_mx_dequantize(fmt, codes, sf, gs, out, stream=None):
     """The values of a microscaled matrix into out [rows, K]."""
-    rows, K, d, po = _arg_matrix("out", out)
+    (rows, K), _, d, po = _arg_matrix("out", out)
     _check(_lib.load().fp4moe_mx_dequantize(fmt, d, rows, K, _arg_bytes("codes", codes, rows * mx_row_bytes(K)),
                                             _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K)), _arg_scalar("gs", gs),
                                             po, _s(stream)), "fp4moe_mx_dequantize")
@@ -370,7 +375,7 @@ def fp4moe_mx_dequantize(fmt, codes, sf, gs, out, stream=None):
 def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream=None):
     """out [M, N] = alpha * A B^T for microscaled A [M, K] and B [N, K]; alpha a device float32 or None (1); err a
     zeroed device word (int32) that the caller keeps."""
-    M, N, d, po = _arg_matrix("out", out)
+    (M, N), _, d, po = _arg_matrix("out", out)
     row = mx_row_bytes(K)
     if err.element_size() * err.numel() < 4:
         raise Fp4MoeError("err: expected a device word of 4 bytes")

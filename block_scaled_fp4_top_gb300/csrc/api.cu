@@ -776,6 +776,7 @@ fp4moe_status fp4moe_add_rmsnorm(int32_t dtype, int32_t T, int32_t H, const void
   for (const void* p : {residual, gamma, (const void*)residual_out, (const void*)y, (const void*)y_codes,
                         (const void*)y_scales})
     FP4_TRY(check_opt(p));
+  if (y != nullptr && y == residual_out) return FP4MOE_INVALID_ARG;  // two results, one buffer
   return add_rmsnorm_launch(dtype, T, H, x, residual, gamma, eps, residual_out, y, y_codes, y_scales, scale_stride,
                             (cudaStream_t)stream);
 }

@@ -523,7 +523,7 @@ typedef enum fp4moe_dtype { FP4MOE_BF16 = 0, FP4MOE_FP16 = 1, FP4MOE_FP32 = 2 } 
  *   y_codes [T][H] and y_scales (ceil(H / 128) rows of scale_stride floats,
  *   scale_stride >= T) are both given or both NULL.
  *   residual_out and y may each be the same buffer as x or residual (exactly,
- *   not shifted), but not the same buffer as each other.
+ *   not shifted), but not the same buffer as each other (FP4MOE_INVALID_ARG).
  * A NaN or an infinity in a row reaches y as the formula has it. A group of n
  * that holds a NaN has a NaN scale and NaN codes (0x7F or 0xFF).
  * Any T >= 0, H >= 1, finite eps >= 0; else FP4MOE_INVALID_ARG. H within 8192

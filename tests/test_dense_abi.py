@@ -87,6 +87,12 @@ def test_norm_refusals(lib):
     assert n(T=0, stride=0) == _lib.OK
 
 
+def test_norm_refuses_one_buffer_for_two_results(lib):
+    from block_scaled_fp4_top_gb300 import _lib
+    other = ctypes.c_void_p(0x20000)
+    assert lib.fp4moe_add_rmsnorm(0, 4, 256, P, P, None, 1e-6, other, other, None, None, 0, None) == _lib.INVALID_ARG
+
+
 def test_widths_whose_column_index_would_pass_32_bits(lib):
     from block_scaled_fp4_top_gb300 import _lib
     top = 2**31 - 1 - 8192
