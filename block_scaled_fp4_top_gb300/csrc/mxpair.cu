@@ -213,6 +213,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       for (int j = max(0, it - C::kStages); j < it; ++j)
         drain_wait(bar_full + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
     }
+    if (ok) {  // and the signals of every pair that they have been used
+      for (int j = max(0, it - C::kStages); j < it; ++j)
+        drain_wait(bar_empty + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
+    }
     if (!ok) {
       for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
       }
