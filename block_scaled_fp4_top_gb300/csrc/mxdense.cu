@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(DTHREADS, 1)
     // A scale tile has one TMEM column for 32 rows, and a scale address is even (an odd one raises "misaligned
     // address"), so an output tile begins at row 0 or 64 of a scale tile and none is narrower than 64.
     uint32_t sfb_col = 0;
-    auto mma = [&](uint32_t st, uint32_t slot, int a, uint32_t acc) {
+    auto mma = [&](uint64_t adesc, uint64_t bdesc, uint32_t slot, int a, uint32_t acc) {
       constexpr bool mx = FMT == FP4MOE_W_MXFP4;
       const int tile = mx ? a >> 1 : a;
-      tc_mma_mx<FMT>(tmem, desc_sw128(st + 32 * a), desc_sw128(st + a_bytes + 32 * a),
+      tc_mma_mx<FMT>(tmem, adesc + 2 * a, bdesc + 2 * a,
                      idesc_mx<FMT>(DBM, BN, mx ? 2 * (a & 1) : 0), slot + 4 * tile,
                      slot + 4 * C::kSfTiles + 4 * tile + sfb_col, acc);
     };
@@ -227,16 +227,17 @@ __global__ void __launch_bounds__(DTHREADS, 1)
         const int atoms = (prm.K - kb * DK + 63) / 64;  // of this stage and those behind it
         if (leader) {
           // Copies and MMAs of one thread execute in order, and slot s is free: its last MMAs committed bar_empty.
-          const uint32_t sf = st + a_bytes + C::kB;
+          // Descriptors hold addresses in units of 16 bytes; within a stage they are added to.
+          const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + a_bytes), sd = desc_scales(st + a_bytes + C::kB);
 #pragma unroll
-          for (int i = 0; i < 2 * C::kSfTiles; ++i) tc_cp_scales(slot + 4 * i, desc_scales(sf + 512 * i));
+          for (int i = 0; i < 2 * C::kSfTiles; ++i) tc_cp_scales(slot + 4 * i, sd + 32 * i);
           if (atoms >= 4) {
 #pragma unroll
-            for (int a = 0; a < 4; ++a) mma(st, slot, a, (kb > kb0 || a > 0) ? 1u : 0u);
+            for (int a = 0; a < 4; ++a) mma(ad, bd, slot, a, (kb > kb0 || a > 0) ? 1u : 0u);
           } else {
 #pragma unroll
             for (int a = 0; a < 3; ++a)
-              if (a < atoms) mma(st, slot, a, (kb > kb0 || a > 0) ? 1u : 0u);
+              if (a < atoms) mma(ad, bd, slot, a, (kb > kb0 || a > 0) ? 1u : 0u);
           }
           tc_commit(bar_empty + 8 * s);
         }

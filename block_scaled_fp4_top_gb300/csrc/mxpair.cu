@@ -227,10 +227,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     int tl = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    auto mma = [&](uint32_t st, uint32_t slot, int a, uint32_t acc) {
+    auto mma = [&](uint64_t adesc, uint64_t bdesc, uint32_t slot, int a, uint32_t acc) {
       constexpr bool mx = FMT == FP4MOE_W_MXFP4;
       const int tile = mx ? a >> 1 : a;
-      pair_mma<FMT>(tmem, desc_sw128(st + 32 * a), desc_sw128(st + C::kA + 32 * a),
+      pair_mma<FMT>(tmem, adesc + 2 * a, bdesc + 2 * a,
                     idesc_mx<FMT>(PBM, PBN, mx ? 2 * (a & 1) : 0), slot + 4 * tile, slot + 4 * C::kSfTiles + 8 * tile,
                     acc);
     };
@@ -250,21 +250,22 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         if (leader) {
           // A tile i, then B tile j half h at column 4 (2 j + h): an N = 256 MMA takes the two halves side by side.
           // Copies and MMAs of one thread execute in order, and slot s is free: its last MMAs committed bar_empty.
-          const uint32_t sf = st + C::kA + C::kB;
+          // Descriptors hold addresses in units of 16 bytes; within a stage they are added to.
+          const uint64_t ad = desc_sw128(st), bd = desc_sw128(st + C::kA), sd = desc_scales(st + C::kA + C::kB);
 #pragma unroll
-          for (int i = 0; i < C::kSfTiles; ++i) pair_cp_scales(slot + 4 * i, desc_scales(sf + 512 * i));
+          for (int i = 0; i < C::kSfTiles; ++i) pair_cp_scales(slot + 4 * i, sd + 32 * i);
 #pragma unroll
           for (int j = 0; j < C::kSfTiles; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              pair_cp_scales(slot + 4 * C::kSfTiles + 4 * (2 * j + h), desc_scales(sf + C::kSfa * (1 + h) + 512 * j));
+              pair_cp_scales(slot + 4 * C::kSfTiles + 4 * (2 * j + h), sd + C::kSfa / 16 * (1 + h) + 32 * j);
           if (atoms >= 4) {
 #pragma unroll
-            for (int a = 0; a < 4; ++a) mma(st, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
+            for (int a = 0; a < 4; ++a) mma(ad, bd, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
           } else {
 #pragma unroll
             for (int a = 0; a < 3; ++a)
-              if (a < atoms) mma(st, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
+              if (a < atoms) mma(ad, bd, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
           }
           pair_commit_to(bar_empty + 8 * s, kAll);
         }
