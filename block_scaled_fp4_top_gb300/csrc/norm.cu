@@ -11,8 +11,8 @@
 //
 // Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
 // between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
-// back (1 x 4096 bf16 2.0 us, 64 rows 2.1 us), so they take the most threads; many rows take two or four 16-byte
-// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48 us, 6.3 TB/s, 93 % of a copy's rate).
+// back (1 x 4096 bf16 2.1 us, 64 rows 2.3 us), so they take the most threads; many rows take two or four 16-byte
+// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48.6 us, 6.2 TB/s, 92 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -33,24 +33,32 @@ __device__ __forceinline__ float cta_sum(float v, float* s_red) {
   return v;
 }
 
-// n / s, to half a unit of fp32's last place in all but rare cases; 0 where s == 0. One reciprocal serves a group, and
-// two fused steps per element take its error out (n * inv alone is off by up to two units, as much as n itself, and
-// codes near a tie between two E4M3 values go the wrong way that much more often). Below 2^-120 the reciprocal would overflow, so n and s are
-// first scaled up by 2^100, exactly (a subnormal n included). s = inf: finite n give 0, infinite ones NaN.
-struct Fp8Scale {
-  float up, s, inv;
+// The codes of a group are RN_E4M3(v / t), v and t being n and s up to one factor. The quotient is off by half a unit
+// of fp32's last place in all but rare cases: one reciprocal serves a group, and two fused steps per element take its
+// error out.
+struct Fp8Ratio {
+  float t, inv;
 };
-__device__ __forceinline__ Fp8Scale fp8_scale(float s) {
-  if (s < 0x1p-120f) {
-    if (s == 0.0f) return Fp8Scale{0.0f, 0.0f, 0.0f};
-    return Fp8Scale{0x1p100f, s * 0x1p100f, __frcp_rn(s * 0x1p100f)};
-  }
-  return Fp8Scale{1.0f, isinf(s) ? 0.0f : s, __frcp_rn(s)};
+__device__ __forceinline__ float fp8_quotient(float v, const Fp8Ratio& f) {
+  const float q = v * f.inv;
+  return fmaf(fmaf(-q, f.t, v), f.inv, q);
 }
-__device__ __forceinline__ float fp8_quotient(float n, const Fp8Scale& f) {
-  n *= f.up;
-  const float q = n * f.inv;
-  return fmaf(fmaf(-q, f.s, n), f.inv, q);
+// rstd is a factor of n and s, so it is left out: v = p = h * gamma, which the 16-bit types hold in fp32 without a
+// rounding, and t = amax|p| / 448. n, amax and s would bring four more roundings, and each puts codes near a tie
+// between two E4M3 values on the wrong side (2-norm error of the codes of 1000 x 4090 fp16 0.5e-4 .. 1.9e-4, from n
+// and s 0.8e-4 .. 2.6e-4; 8192 x 4096 bf16 48.6 us, from n and s 47.9). Needs p, rstd and their products well inside
+// fp32's range.
+__device__ __forceinline__ bool in_range(float v) { return v > 0x1p-50f && v < 0x1p50f; }
+__device__ __forceinline__ Fp8Ratio fp8_ratio(float a) {
+  const float t = __fdiv_rn(a, 448.0f);
+  return Fp8Ratio{t, __frcp_rn(t)};
+}
+// Any other group: v = n * up, t = s * up; 0 where s == 0. Below 2^-120 the reciprocal would overflow, so n and s are
+// first scaled up by 2^100, exactly (a subnormal n included). s = inf: finite n give 0, infinite ones NaN.
+__device__ __forceinline__ Fp8Ratio fp8_scale(float s, float& up) {
+  up = s == 0.0f ? 0.0f : s < 0x1p-120f ? 0x1p100f : 1.0f;
+  const float t = s * (s < 0x1p-120f ? 0x1p100f : 1.0f);
+  return Fp8Ratio{isinf(s) ? 0.0f : t, s == 0.0f ? 0.0f : __frcp_rn(t)};
 }
 // N codes of the quotients q.
 template <int N>
@@ -109,11 +117,12 @@ __global__ void __launch_bounds__(NORM_THREADS)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
       const float s = __fdiv_rn(a, 448.0f);
-      const Fp8Scale f = fp8_scale(s);
+      float up;
+      const Fp8Ratio f = fp8_scale(s, up);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = g * 128 + 32 * i + lane;
-        if (j < H) codes[row + j] = (uint8_t)cvt_e4m3x2(fp8_quotient(n[i], f), 0.0f);
+        if (j < H) codes[row + j] = (uint8_t)cvt_e4m3x2(fp8_quotient(n[i] * up, f), 0.0f);
       }
       if (lane == 0) scales[(size_t)g * scale_stride + blockIdx.x] = s;
     }
@@ -182,31 +191,57 @@ __global__ void __launch_bounds__(1024)
   }
   ss = cta_sum(ss, s_red);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
+  auto group_max = [](float a) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    return a;
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = at(i);
-    float n[N], a = 0.0f;
-    unpack<T>(hv[i], n);
+    float p[N], g[N], n[N];
+    unpack<T>(hv[i], p);
+    unpack<T>(gv[i], g);
+    auto norm = [&]() {
+      float h[N];
+      unpack<T>(hv[i], h);
 #pragma unroll
-    for (int k = 0; k < N; ++k) n[k] *= rstd;
-    if (gamma != nullptr) {
-      float g[N];
-      unpack<T>(gv[i], g);
-#pragma unroll
-      for (int k = 0; k < N; ++k) n[k] *= g[k];
+      for (int k = 0; k < N; ++k) n[k] = gamma != nullptr ? h[k] * rstd * g[k] : h[k] * rstd;
+    };
+    if (codes == nullptr) {
+      norm();
+      if (j < H) *reinterpret_cast<uint4*>(y + row + j) = pack<T>(n);
+      continue;
     }
-    if (y != nullptr && j < H) *reinterpret_cast<uint4*>(y + row + j) = pack<T>(n);
-    if (codes == nullptr) continue;
+    float a = 0.0f, s;
 #pragma unroll
-    for (int k = 0; k < N; ++k) a = fmax_nan(a, fabsf(n[k]));  // a NaN takes its whole group along
+    for (int k = 0; k < N; ++k) {
+      if (gamma != nullptr) p[k] *= g[k];
+      a = fmax_nan(a, fabsf(p[k]));
+    }
+    a = group_max(a);
+    Fp8Ratio f;
+    if (__all_sync(0xFFFFFFFFu, j >= H || (in_range(a) && in_range(rstd)))) {
+      f = fp8_ratio(a);
+      s = f.t * rstd;
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+      for (int k = 0; k < N; ++k) n[k] = p[k] * rstd;
+    } else {
+      norm();
+      a = 0.0f;
+#pragma unroll
+      for (int k = 0; k < N; ++k) a = fmax_nan(a, fabsf(n[k]));  // a NaN takes its whole group along
+      s = __fdiv_rn(group_max(a), 448.0f);
+      float up;
+      f = fp8_scale(s, up);
+#pragma unroll
+      for (int k = 0; k < N; ++k) p[k] = n[k] * up;
+    }
     if (j >= H) continue;
-    const float s = __fdiv_rn(a, 448.0f);
-    const Fp8Scale f = fp8_scale(s);
-    uint32_t w[N / 4];
+    if (y != nullptr) *reinterpret_cast<uint4*>(y + row + j) = pack<T>(n);
 #pragma unroll
-    for (int k = 0; k < N; ++k) n[k] = fp8_quotient(n[k], f);
+    for (int k = 0; k < N; ++k) n[k] = fp8_quotient(p[k], f);
+    uint32_t w[N / 4];
     make_codes<N>(w, n);
     store_codes<N>(codes + row + j, w);
     if (j % 128 == 0) scales[(size_t)(j / 128) * scale_stride + blockIdx.x] = s;
@@ -258,9 +293,9 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 // Widths that the 16-byte vectors do not divide. Rows then start at any element, and a vector that is aligned for
 // one row is not for the next, so a lane reads and writes U elements at a time, the most that divide H (4, 2 or
 // 1), in accesses that are contiguous over the warp. A warp takes whole FP8 groups: NG of them, in registers, and
-// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 54 us, 8192 x 4092 50 us, 8192 x 4095
-// (single elements: bound by the accesses) 79 us, against 77, 75 and 78 us with whole vectors that were cut at the
-// aligned addresses and shifted into place, and 48 us at 4096. 1000 x 4090 fp16: 8.9 against 12.2 us.
+// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 58 us, 8192 x 4092 51 us, 8192 x 4095
+// (single elements: bound by the accesses) 80 us, against 77, 75 and 78 us with whole vectors that were cut at the
+// aligned addresses and shifted into place, and 48 us at 4096. 1000 x 4090 fp16: 9.0 against 12.2 us.
 template <typename T, int U, int NG>
 __global__ void __launch_bounds__(1024)
     add_rmsnorm_group_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
@@ -318,32 +353,65 @@ __global__ void __launch_bounds__(1024)
   for (int i = 0; i < NG; ++i) {
     const int g = i * warps + warp;
     if (g * 128 >= H) break;
-    float n[S][U], a = 0.0f;
+    float n[S][U], p[S][U], w[S][U];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int j = at(i, s);
-      unpack_raw<T, U>(hv[i][s], n[s]);
-#pragma unroll
-      for (int k = 0; k < U; ++k) n[s][k] *= rstd;
-      if (gamma != nullptr) {
-        float w[U];
-        unpack_raw<T, U>(gv[i][s], w);
-#pragma unroll
-        for (int k = 0; k < U; ++k) n[s][k] *= w[k];
-      }
-      if (y != nullptr && j < H) *reinterpret_cast<R*>(y + row + j) = pack_raw<T, U>(n[s]);
-#pragma unroll
-      for (int k = 0; k < U; ++k) a = fmax_nan(a, fabsf(n[s][k]));
+      unpack_raw<T, U>(hv[i][s], p[s]);
+      unpack_raw<T, U>(gv[i][s], w[s]);
     }
-    if (codes == nullptr) continue;
-    const float sc = __fdiv_rn(warp_max_nan(a), 448.0f);  // a NaN takes its whole group along
-    const Fp8Scale f = fp8_scale(sc);
+    auto norm = [&]() {
+      float h[S][U];
+#pragma unroll
+      for (int s = 0; s < S; ++s) unpack_raw<T, U>(hv[i][s], h[s]);
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int k = 0; k < U; ++k) n[s][k] = gamma != nullptr ? h[s][k] * rstd * w[s][k] : h[s][k] * rstd;
+    };
+    float a = 0.0f, sc = 0.0f;
+    Fp8Ratio f{};
+    if (codes == nullptr) {
+      norm();
+    } else {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          if (gamma != nullptr) p[s][k] *= w[s][k];
+          a = fmax_nan(a, fabsf(p[s][k]));
+        }
+      a = warp_max_nan(a);
+      if (in_range(a) && in_range(rstd)) {
+        f = fp8_ratio(a);
+        sc = f.t * rstd;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int k = 0; k < U; ++k) n[s][k] = p[s][k] * rstd;
+      } else {
+        norm();
+        a = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int k = 0; k < U; ++k) a = fmax_nan(a, fabsf(n[s][k]));
+        sc = __fdiv_rn(warp_max_nan(a), 448.0f);  // a NaN takes its whole group along
+        float up;
+        f = fp8_scale(sc, up);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int k = 0; k < U; ++k) p[s][k] = n[s][k] * up;
+      }
+    }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const int j = at(i, s);
       if (j >= H) continue;
+      if (y != nullptr) *reinterpret_cast<R*>(y + row + j) = pack_raw<T, U>(n[s]);
+      if (codes == nullptr) continue;
 #pragma unroll
-      for (int k = 0; k < U; ++k) n[s][k] = fp8_quotient(n[s][k], f);
+      for (int k = 0; k < U; ++k) n[s][k] = fp8_quotient(p[s][k], f);
       if constexpr (U == 4) {
         uint32_t w[1];
         make_codes<4>(w, n[s]);
@@ -354,7 +422,7 @@ __global__ void __launch_bounds__(1024)
         codes[row + j] = (uint8_t)cvt_e4m3x2(n[s][0], 0.0f);
       }
     }
-    if (lane == 0) scales[(size_t)g * scale_stride + blockIdx.x] = sc;
+    if (codes != nullptr && lane == 0) scales[(size_t)g * scale_stride + blockIdx.x] = sc;
   }
 }
 

@@ -130,6 +130,19 @@ def test_norm_zero_and_tiny_rows(H):
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("H", [512, 333])
+@pytest.mark.parametrize("opts", [dict(), dict(gamma=False), dict(eps=0.0), dict(residual=False, eps=0.0)])
+def test_norm_rows_of_many_magnitudes(dtype, H, opts):
+    """Both ways to the FP8 codes, and the border between them, in rows side by side and in groups of one row."""
+    import torch
+    e = torch.tensor([-55, -51, -50, -49, -30, 0, 30, 49, 50, 51, 55], dtype=torch.float32, device="cuda")
+    x = rnd((len(e), H), dtype, 7, 0.0) * torch.exp2(e)[:, None].to(getattr(torch, dtype))
+    x[5, 128:256] = 0
+    x[6, :128] *= 2.0 ** -100
+    check_norm(len(e), H, dtype, seed=8, x=x, **opts)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("H", [512, 333])
 def test_norm_nonfinite_rows_stay_in_their_row(dtype, H):
     import torch
     from block_scaled_fp4_top_gb300 import api
