@@ -269,6 +269,31 @@ def test_quantize_nonfinite_blocks(fmt, dtype):
     assert torch.equal(out[~hit], ref[~hit])
 
 
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [64, 36])
+def test_dequantize_every_code_under_every_scale(fmt, dtype, K):
+    """One scale byte a row, zero scales under nonzero codes among them; K = 36: rows that no vector divides."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    scales = np.arange(0, 0x7F if fmt == NV else 0xFF, dtype=np.uint8)
+    rows = len(scales)
+    q = np.tile(np.arange(16, dtype=np.uint8), (rows, 4))
+    q[:, K:] = 0
+    s = np.repeat(scales[:, None], -(-K // BLOCK[fmt]), axis=1)
+    pc, ps = (torch.from_numpy(t).cuda() for t in pack(fmt, q, s, K))
+    v = values(fmt, q, s, K).astype(np.float32)
+    for g in (1.0, 1e-3, 3e20, 2.0 ** -120) if fmt == NV else (1.0,):
+        gt = torch.tensor([g], dtype=torch.float32, device="cuda")
+        ob = Guarded((rows, K), getattr(torch, dtype))
+        api.fp4moe_mx_dequantize(fmt, pc, ps, gt, ob.t)
+        torch.cuda.synchronize()
+        ob.check()
+        with np.errstate(over="ignore"):
+            w = v / np.float32(g) if fmt == NV else v
+        assert torch.equal(ob.t.cpu(), torch.from_numpy(w).to(getattr(torch, dtype))), g
+
+
 # ------------------------------------------------------------------------- product
 def gemm_operands(fmt, M, N, K, seed):
     """Codes and scales with every code value and a range of scales, as the library stores them; their values."""
