@@ -12,7 +12,7 @@
 // Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
 // between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
 // back (1 x 4096 bf16 2.1 us, 64 rows 2.3 us), so they take the most threads; many rows take two or four 16-byte
-// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48.6 us, 6.2 TB/s, 92 % of a copy's rate).
+// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48.4 us, 6.3 TB/s, 92 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -43,16 +43,12 @@ __device__ __forceinline__ float fp8_quotient(float v, const Fp8Ratio& f) {
   const float q = v * f.inv;
   return fmaf(fmaf(-q, f.t, v), f.inv, q);
 }
-// rstd is a factor of n and s, so it is left out: v = p = h * gamma, which the 16-bit types hold in fp32 without a
-// rounding, and t = amax|p| / 448. n, amax and s would bring four more roundings, and each puts codes near a tie
-// between two E4M3 values on the wrong side (2-norm error of the codes of 1000 x 4090 fp16 0.5e-4 .. 1.9e-4, from n
-// and s 0.8e-4 .. 2.6e-4; 8192 x 4096 bf16 48.6 us, from n and s 47.9). Needs p, rstd and their products well inside
-// fp32's range.
+// rstd is a factor of n and s, so it is left out: v = 448 p with p = h * gamma, t = amax|p|. In bf16 these are exact
+// in fp32 (19 and 16 bits), so quotients that lie on a tie between two E4M3 values stay on it, no others come as near
+// as the last rounding, and the codes are those of exact arithmetic. (fp16: v has one rounding at most; fp32: p and v
+// each.) n, amax and s would bring six roundings. Needs p, rstd and their products well inside fp32's range.
 __device__ __forceinline__ bool in_range(float v) { return v > 0x1p-50f && v < 0x1p50f; }
-__device__ __forceinline__ Fp8Ratio fp8_ratio(float a) {
-  const float t = __fdiv_rn(a, 448.0f);
-  return Fp8Ratio{t, __frcp_rn(t)};
-}
+__device__ __forceinline__ Fp8Ratio fp8_ratio(float a) { return Fp8Ratio{a, __frcp_rn(a)}; }
 // Any other group: v = n * up, t = s * up; 0 where s == 0. Below 2^-120 the reciprocal would overflow, so n and s are
 // first scaled up by 2^100, exactly (a subnormal n included). s = inf: finite n give 0, infinite ones NaN.
 __device__ __forceinline__ Fp8Ratio fp8_scale(float s, float& up) {
@@ -223,9 +219,12 @@ __global__ void __launch_bounds__(1024)
     Fp8Ratio f;
     if (__all_sync(0xFFFFFFFFu, j >= H || (in_range(a) && in_range(rstd)))) {
       f = fp8_ratio(a);
-      s = f.t * rstd;
+      s = __fdiv_rn(a, 448.0f) * rstd;
 #pragma unroll
-      for (int k = 0; k < N; ++k) n[k] = p[k] * rstd;
+      for (int k = 0; k < N; ++k) {
+        n[k] = p[k] * rstd;
+        p[k] *= 448.0f;
+      }
     } else {
       norm();
       a = 0.0f;
@@ -293,9 +292,9 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 // Widths that the 16-byte vectors do not divide. Rows then start at any element, and a vector that is aligned for
 // one row is not for the next, so a lane reads and writes U elements at a time, the most that divide H (4, 2 or
 // 1), in accesses that are contiguous over the warp. A warp takes whole FP8 groups: NG of them, in registers, and
-// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 58 us, 8192 x 4092 51 us, 8192 x 4095
-// (single elements: bound by the accesses) 80 us, against 77, 75 and 78 us with whole vectors that were cut at the
-// aligned addresses and shifted into place, and 48 us at 4096. 1000 x 4090 fp16: 9.0 against 12.2 us.
+// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 56 us, 8192 x 4092 52 us, 8192 x 4095
+// (single elements: bound by the accesses) 81 us, against 77, 75 and 78 us with whole vectors that were cut at the
+// aligned addresses and shifted into place, and 48 us at 4096. 1000 x 4090 fp16: 8.9 against 12.2 us.
 template <typename T, int U, int NG>
 __global__ void __launch_bounds__(1024)
     add_rmsnorm_group_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
@@ -383,11 +382,14 @@ __global__ void __launch_bounds__(1024)
       a = warp_max_nan(a);
       if (in_range(a) && in_range(rstd)) {
         f = fp8_ratio(a);
-        sc = f.t * rstd;
+        sc = __fdiv_rn(a, 448.0f) * rstd;
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
-          for (int k = 0; k < U; ++k) n[s][k] = p[s][k] * rstd;
+          for (int k = 0; k < U; ++k) {
+            n[s][k] = p[s][k] * rstd;
+            p[s][k] *= 448.0f;
+          }
       } else {
         norm();
         a = 0.0f;

@@ -512,8 +512,9 @@ typedef enum fp4moe_dtype { FP4MOE_BF16 = 0, FP4MOE_FP16 = 1, FP4MOE_FP32 = 2 } 
  *   and per 1 x 128 group g of n (the last one may be short):
  *   s    = RN(amax / 448)                      -> y_scales[g * scale_stride + t]
  *   code = E4M3_satfinite(n / s), 0 where s == 0       -> y_codes[t][:]
- *          (the exact n / s, to within two units of fp32's last place, before
- *          E4M3 rounds)
+ *          (from the exact n / s where x is bf16 and no value of the group is
+ *          near the ends of fp32's range, else to within two units of fp32's
+ *          last place, before E4M3 rounds)
  * RN rounds once to the storage type `dtype` of x, residual, gamma,
  * residual_out and y (an fp4moe_dtype). The norm is that of the rounded h, the
  * stream that residual_out holds; the codes are taken from n before its

@@ -163,6 +163,33 @@ def test_norm_nonfinite_rows_stay_in_their_row(dtype, H):
     assert y[clean].isfinite().all() and scales[:, clean].isfinite().all() and (codes[clean] & 127 != 127).all()
 
 
+@pytest.mark.parametrize("gamma", [False, True])
+@pytest.mark.parametrize("T,H", [(16, 4096), (200, 512), (9, 1001), (200, 1002)])
+def test_norm_codes_of_bf16_are_those_of_exact_arithmetic(T, H, gamma):
+    """n / s is 448 p / max|p| with p = h * gamma: in fp64 that side and a midpoint of the E4M3 grid times max|p| are
+    exact products, so every code, ties to even included, follows from comparisons."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    h = rnd((T, H), "bfloat16", H, 0.5)
+    g = rnd((H,), "bfloat16", H + 1, 0.0) if gamma else None
+    y, codes = torch.empty_like(h), torch.empty(T, H, dtype=torch.uint8, device="cuda")
+    G = (H + 127) // 128
+    api.fp4moe_add_rmsnorm(h, None, g, 1e-6, None, y, codes, torch.empty(G, T, device="cuda"))
+    p = np.zeros((T, G * 128))
+    p[:, :H] = f64(h) * (f64(g) if gamma else 1.0)
+    top = np.repeat(np.abs(p).reshape(T, G, 128).max(2), 128, axis=1)
+    grid = codecs.E4M3_TABLE[:127].astype(np.float64)
+    want = np.zeros(p.shape, dtype=np.int64)
+    for i, mid in enumerate((grid[1:] + grid[:-1]) / 2):
+        side, bar = 448.0 * np.abs(p), mid * top
+        want += (side > bar) | ((side == bar) & (i % 2 == 1))
+    want |= (p < 0) << 7
+    torch.cuda.synchronize()
+    got = codes.cpu().numpy().astype(np.int64)
+    differ = (got != want[:, :H]) & ~((got & 127 == 0) & (want[:, :H] & 127 == 0))     # the sign of a zero is free
+    assert not differ.any(), f"{differ.sum()} codes of {differ.size}"
+
+
 def test_norm_empty():
     import torch
     from block_scaled_fp4_top_gb300 import api
