@@ -308,7 +308,7 @@ def _arg_matrix(name, t):
 
 
 def _check_fp8(codes, scales, T, H):
-    """Shape and type of block-FP8 activations: codes [T, H], scales [ceil(H / 128), at least T]. The scales' columns."""
+    """Check block-FP8 activations: codes [T, H], scales [ceil(H / 128), at least T]. Returns the scales' columns."""
     if codes.dtype not in _BYTE_TYPES or codes.shape != (T, H):
         raise Fp4MoeError(f"codes: expected {(T, H)} of {' or '.join(map(str, _BYTE_TYPES))}, got "
                           f"{tuple(codes.shape)} of {codes.dtype}")

@@ -13,7 +13,7 @@
 //               the leading 16, 32, 64 or 128 rows that hold M; rows and columns past the matrices arrive as
 //               zeros) and their scale tiles by bulk copies.
 //   warp 10     per stage, tcgen05.cp of the scale tiles into the stage's TMEM slot, then the MMAs.
-// A stage takes about 280 ns whatever its width (four MMAs of at least 65 cycles, the scale copies and the barriers
+// A stage takes about 260 ns whatever its width (four MMAs of at least 65 cycles, the scale copies and the barriers
 // around them), so a product with fewer tiles than SMs splits K over a cluster of S CTAs. The CTAs of ranks 1 .. send
 // their fp32 partial tiles into buffers of rank 0's shared memory (st.async, counted in bytes on a barrier there),
 // and rank 0 adds them to its own in rank order: deterministic, and one trip between SMs instead of a barrier of the
@@ -100,7 +100,8 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t adesc, uint64_t b
     tc_mma_nvf4(d, adesc, bdesc, idesc, sfa, sfb, accumulate);
 }
 
-// Grid (tiles or persistent CTAs, 1, S), cluster (1, 1, S). stages: ring depth; tmem_cols: a power of two that holds the accumulator and the stages' scales.
+// Grid (tiles or persistent CTAs, 1, S), cluster (1, 1, S). stages: ring depth; tmem_cols: a power of two that holds
+// the accumulator and the stages' scales.
 template <int FMT, int BN, typename T>
 __global__ void __launch_bounds__(DTHREADS, 1)
     mx_dense_kernel(const __grid_constant__ TileMaps maps, const DenseParams prm, int stages, int a_rows,
@@ -392,10 +393,10 @@ bool dense_configure() {
 }
 
 // Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 41 sizes from 1 x 4096 x 256 to
-// 8192 x 8192 x 2048: the one picked is within 5 % of the fastest at all of them (bn64 / bn128 / pair / two pairs, us:
-// 64 x 8192 x 4096 MXFP4 7.2 7.3 8.8 10.1, 512 x 4096 x 4096 12.0 7.9 9.3 9.4, 768 x 4096 x 4096 16.6 12.6 9.9 10.2,
-// 8192 x 4096 x 2048 70 43 28.9 29.5, 1500 x 3000 x 2000 19 14 10.6 9.7; split in two or four 1 x 4096 x 4096 takes
-// 5.9 and 5.6 instead of 6.9, 64 x 4096 x 4096 6.5 and 9.8 instead of 6.9). KB: 256-element stages of K.
+// 8192 x 8192 x 2048: the one picked is within 7 % of the fastest at all of them (bn64 / bn128 / pair / two pairs, us:
+// 64 x 8192 x 4096 MXFP4 6.9 7.0 9.0 10.2, 512 x 4096 x 4096 11.1 7.9 9.3 9.4, 768 x 4096 x 4096 15.4 12.0 9.9 10.1,
+// 8192 x 4096 x 2048 65 43 28.6 29.9, 1500 x 3000 x 2000 19 14 10.4 9.6; split in two or four 1 x 4096 x 4096 takes
+// 6.0 and 5.5 instead of 6.6, 64 x 4096 x 4096 6.4 and 9.8 instead of 6.5). KB: 256-element stages of K.
 //   128 x 64, 128 x 128    a launch, 700 a tile and 270 .. 300 a stage
 //   split over S CTAs      KB / S stages; joining: 1100, and a fifth of a ns for each fp32 value that is sent
 //   256 x 256 on a pair    1050 a tile and 306 a stage, or 1000 and 290 with two pairs in a cluster (36 clusters of

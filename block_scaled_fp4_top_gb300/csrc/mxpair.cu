@@ -19,12 +19,12 @@
 // have a place in a cluster of four: 9216 x 4096 x 4096 MXFP4 takes 48.8 instead of 50.1 us (eight rounds of tiles
 // either way), 8192 x 4096 x 4096 47.3 instead of 45.1 (eight against seven).
 //
-// 8192 x 4096 x 4096: MXFP4 44.8 us, 6.1 PFLOP/s of the 9.4 that the MMAs reach alone, NVFP4 48.0; 8192^3 152 us, 7.2.
+// 8192 x 4096 x 4096: MXFP4 44.8 us, 6.1 PFLOP/s of the 9.4 that the MMAs reach alone, NVFP4 48.1; 8192^3 152 us, 7.2.
 // Bounds: operands from L2 (34 KB a stage and SM, 600 cycles for MMAs of 512; five ring stages 48 us, four 51; the B
-// scales loaded by both CTAs 46.4 instead of 45.0), and 1000 ns between the last MMA of a tile and the first of the next, in which the
-// epilogue empties TMEM: two accumulators of 256 columns and the scales do not fit its 512. Not faster: the output by
-// TMA from shared memory (45.0 and 46.9, but 8192 x 8192 x 2048 57 instead of 53), all 128 columns of an epilogue
-// warp in flight at once (spills, 53), a stage's scale copies ahead of the MMAs before it (50).
+// scales loaded by both CTAs 46.4 instead of 45.0), and 1000 ns between the last MMA of a tile and the first of the
+// next, in which the epilogue empties TMEM: two accumulators of 256 columns and the scales do not fit its 512. Not
+// faster: the output by TMA from shared memory (45.0 and 46.9, but 8192 x 8192 x 2048 57 instead of 53), all 128
+// columns of an epilogue warp in flight at once (spills, 53), a stage's scale copies ahead of the MMAs before it (50).
 // The rest (scale-factor ids, K tails, bounded waits) is as in mxdense.cu.
 #include <mutex>
 
@@ -68,8 +68,8 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 // The copy lands at `dst` in every CTA of `mask`, and signals `bar`'s offset in the leader of each one's pair.
-__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
-                                                           int32_t y, uint16_t mask, uint64_t policy) {
+__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                           int32_t x, int32_t y, uint16_t mask, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
       ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),

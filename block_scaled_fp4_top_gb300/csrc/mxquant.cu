@@ -379,8 +379,9 @@ fp4moe_status quantize_launch(int32_t rows, int32_t K, const void* x, const floa
   const int64_t row_end = mx_row_tiles(rows) * 128;
   const Shape s = row_shape(row_end, segs, kCtasPerSm);
   const bool wide = K % 16 == 0 && (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
-  return launch_pdl(wide ? mx_quantize_kernel<FMT, T, true> : mx_quantize_kernel<FMT, T, false>, s.grid, s.block, 0, st, rows, row_end, K, (int)segs, ct,
-                    mx_row_bytes(K), static_cast<const T*>(x), gs, codes, sf) == cudaSuccess
+  return launch_pdl(wide ? mx_quantize_kernel<FMT, T, true> : mx_quantize_kernel<FMT, T, false>, s.grid, s.block, 0,
+                    st, rows, row_end, K, (int)segs, ct, mx_row_bytes(K), static_cast<const T*>(x), gs, codes,
+                    sf) == cudaSuccess
              ? FP4MOE_OK
              : FP4MOE_CUDA_ERROR;
 }

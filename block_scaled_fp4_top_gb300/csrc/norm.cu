@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(1024)
   const size_t row = (size_t)blockIdx.x * H;
   auto at = [&](int i) { return (i * (int)blockDim.x + (int)threadIdx.x) * N; };
   // Every load of the row is issued before the first is waited for. gamma waits until x and the residual are joined
-  // where its registers would cost occupancy: 8192 x 4096 bf16 without a residual, two vectors, 27 against 30 us.
+  // where its registers would cost occupancy (8192 x 4096 bf16, the norm alone, two vectors: 27 against 30 us).
   uint4 hv[NV], rv[NV], gv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -456,16 +456,16 @@ fp4moe_status norm_launch(int32_t rows, int32_t H, const void* x, const void* re
   const int64_t vecs = ((int64_t)H + N - 1) / N, groups = ((int64_t)H + 127) / 128;
   if (H % N == 0 && vecs <= 4 * 1024) {
     // vectors a thread: one while the rows leave SMs idle, two while an SM has one row or two or a row leaves four
-    // warps idle, else four, and as many as 1024 threads need (bf16 with the FP8 copy, two and four: 300 x 4096 2.8
-    // and 3.3 us, 8192 x 2048 24.9 and 25.7, 8192 x 4096 47.4 and 47.6, 4096 x 7168 48.6 and 43.0, 2000 x 8192 27.3
-    // and 25.4)
+    // warps idle, else four, and as many as 1024 threads need (bf16 with the FP8 copy, two and four: 300 x 4096 2.9
+    // and 3.5 us, 8192 x 2048 25.5 and 26.4, 8192 x 4096 50.7 and 48.4, 4096 x 7168 50.1 and 43.5, 2000 x 8192 28.3
+    // and 26.2)
     int nv = rows <= nsm ? 1 : rows <= 2 * nsm || vecs < 512 ? 2 : 4;
     while ((vecs + nv - 1) / nv > 1024) nv *= 2;
     threads = (int)((vecs + nv - 1) / nv + 31) / 32 * 32;
     kernel = vec_kernel<T>(nv);
   } else if (H % N != 0 && groups <= (sizeof(T) == 2 && H % 2 == 0 ? 8 : 4) * 32) {
-    // groups a warp: one while the rows leave SMs idle, then four (8192 x 4090 bf16 52 us; one 85, two 58, eight 53),
-    // and eight where 32 warps need them and their registers suffice
+    // groups a warp: one while the rows leave SMs idle (64 x 4090 bf16 2.7 us, with eight 4.5), then four (8192 x 4090
+    // 56 us; one 95, eight 58), and eight where 32 warps need them and their registers suffice
     const int ng = groups > 4 * 32 ? 8 : rows > nsm || groups > 32 ? 4 : 1;
     threads = (int)((groups + ng - 1) / ng) * 32;
     if constexpr (sizeof(T) == 4)
