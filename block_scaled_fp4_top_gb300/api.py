@@ -586,14 +586,17 @@ class MxLinear:
 
     def forward(self, x: torch.Tensor, out: torch.Tensor, stream=None):
         """out [T, N] (bfloat16, float16 or float32) of x [T, K]."""
-        T = x.shape[0]
-        if T > self.max_tokens or x.shape[1] != self.K or out.shape != (T, self.N):
+        # fp4moe_mx_quantize and fp4moe_mx_gemm on this object's own buffers, which need no checks (nor slices for T)
+        (T, K), _, dx, px = _arg_matrix("x", x)
+        shape, _, do, po = _arg_matrix("out", out)
+        if T > self.max_tokens or K != self.K or shape != (T, self.N):
             raise Fp4MoeError(f"expected x [at most {self.max_tokens}, {self.K}] and out [T, {self.N}], got "
-                              f"{tuple(x.shape)} and {tuple(out.shape)}")
-        codes = self.x_codes[:T * mx_row_bytes(self.K)]
-        sf = self.x_sf[:mx_sf_bytes(self.fmt, T, self.K)]
-        fp4moe_mx_quantize(self.fmt, x, self.gx, codes, sf, stream)
-        fp4moe_mx_gemm(self.fmt, self.K, codes, sf, self.w_codes, self.w_sf, self.alpha, out, self.err, stream)
+                              f"{(T, K)} and {tuple(shape)}")
+        lib, s = _lib.load(), _s(stream)
+        codes, sf = self.x_codes.data_ptr(), self.x_sf.data_ptr()
+        _check(lib.fp4moe_mx_quantize(self.fmt, dx, T, K, px, _p(self.gx), codes, sf, s), "fp4moe_mx_quantize")
+        _check(lib.fp4moe_mx_gemm(self.fmt, do, T, self.N, K, codes, sf, self.w_codes.data_ptr(),
+                                  self.w_sf.data_ptr(), _p(self.alpha), po, self.err.data_ptr(), s), "fp4moe_mx_gemm")
 
     def read_error(self, clear=True) -> int:
         return fp4moe_read_error(self.err, clear)

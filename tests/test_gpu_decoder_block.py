@@ -214,3 +214,38 @@ def test_example_runs():
                        text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "graph replay equals eager: True" in r.stdout and "error word 0x0" in r.stdout
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("dtype,out_dtype", [("bfloat16", "bfloat16"), ("float16", "float32"), ("float32", "float16")])
+def test_linear_is_its_two_calls(fmt, dtype, out_dtype):
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    N, K, most = 200, 300, 130
+    gen = torch.Generator("cuda").manual_seed(5)
+    w = torch.randn(N, K, generator=gen, device="cuda")
+    lin = api.MxLinear(w, most, fmt)
+    x = torch.randn(most, K, generator=gen, device="cuda").to(getattr(torch, dtype))
+    lin.calibrate(x)
+    for T in (1, 129, 64, 0, most):
+        out = torch.full((T, N), 7.0, dtype=getattr(torch, out_dtype), device="cuda")
+        lin.forward(x[:T], out)
+        codes = torch.empty(T * api.mx_row_bytes(K), dtype=torch.uint8, device="cuda")
+        sf = torch.empty(api.mx_sf_bytes(fmt, T, K), dtype=torch.uint8, device="cuda")
+        ref = torch.empty_like(out)
+        api.fp4moe_mx_quantize(fmt, x[:T], lin.gx, codes, sf)
+        api.fp4moe_mx_gemm(fmt, K, codes, sf, lin.w_codes, lin.w_sf, lin.alpha, ref, lin.err)
+        assert torch.equal(out, ref), T
+    assert lin.read_error() == 0
+
+
+def test_linear_refusals():
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    lin = api.MxLinear(torch.randn(64, 96, device="cuda"), 8, MX)
+    ok = lambda t, n: torch.zeros(t, n, dtype=torch.bfloat16, device="cuda")
+    for x, out in ((ok(9, 96), ok(9, 64)), (ok(4, 95), ok(4, 64)), (ok(4, 96), ok(4, 63)), (ok(4, 96), ok(5, 64)),
+                   (ok(4, 96).cpu(), ok(4, 64)), (ok(4, 96), ok(4, 64).cpu()), (ok(4, 192)[:, ::2], ok(4, 64)),
+                   (ok(4, 96).double(), ok(4, 64)), (ok(4, 96)[0], ok(4, 64))):
+        with pytest.raises(api.Fp4MoeError):
+            lin.forward(x, out)
