@@ -396,9 +396,11 @@ bool dense_configure() {
 // 8192 x 8192 x 2048: the one picked is within 7 % of the fastest at all of them (bn64 / bn128 / pair / two pairs, us:
 // 64 x 8192 x 4096 MXFP4 6.9 7.0 9.0 10.2, 512 x 4096 x 4096 11.1 7.9 9.3 9.4, 768 x 4096 x 4096 15.4 12.0 9.9 10.1,
 // 8192 x 4096 x 2048 65 43 28.6 29.9, 1500 x 3000 x 2000 19 14 10.4 9.6; split in two or four 1 x 4096 x 4096 takes
-// 6.0 and 5.5 instead of 6.6, 64 x 4096 x 4096 6.4 and 9.8 instead of 6.5). KB: 256-element stages of K.
+// 6.0 and 5.5 instead of 6.6, 64 x 4096 x 4096 6.4 and 9.8 instead of 6.5, 128 x 2048 x 8192 8.9 and 10.4 instead of
+// 10.3, 128 x 1024 x 14336 11.6 and 10.1 instead of 15.9). KB: 256-element stages of K.
 //   128 x 64, 128 x 128    a launch, 700 a tile and 270 .. 300 a stage
-//   split over S CTAs      KB / S stages; joining: 1100, and a fifth of a ns for each fp32 value that is sent
+//   split over S CTAs      KB / S stages; joining: 1100 (1600 for tiles of more than 64 rows), and a fifth of a ns for
+//                          each fp32 value that is sent
 //   256 x 256 on a pair    1050 a tile and 306 a stage, or 1000 and 290 with two pairs in a cluster (36 clusters of
 //                          four fit on 152 SMs, 76 of two)
 struct Plan {
@@ -419,10 +421,11 @@ Plan pick_plan(int M, int N, int KB, int nsm) {
     const int64_t tiles = up(M, DBM) * up(N, bn), stage = bn == 128 && M > 64 ? 300 : 270;
     const int64_t launch = bn == 64 ? 1700 : 1800;
     offer({0, bn, 1}, launch + up(tiles, nsm) * (KB * stage + 700));
-    if (M > 64) continue;  // more rows cost more to join than the split saves
-    for (int S : {2, 4})   // a cluster of four leaves an eighteenth of the SMs without one
+    if (M > 64 && bn == 128) continue;  // such partial tiles cost more to join than the split saves
+    const int64_t rows = std::min(M, DBM), join = M > 64 ? 1600 : 1100;
+    for (int S : {2, 4})  // a cluster of four leaves an eighteenth of the SMs without one
       if (S <= KB && tiles * S <= (S == 2 ? nsm : nsm - nsm / 18))
-        offer({0, bn, S}, launch + 700 + up(KB, S) * stage + 1100 + (int64_t)(S - 1) * M * bn / 5);
+        offer({0, bn, S}, launch + 700 + up(KB, S) * stage + join + (S - 1) * rows * bn / 5);
   }
   for (int pairs : {1, 2}) {
     const int64_t tiles = up(M, 256 * pairs) * up(N, 256);
@@ -442,7 +445,7 @@ fp4moe_status dense_run(DenseParams prm, int S, const uint8_t* a, const uint8_t*
   const int a_rows = rows_loaded(prm.M);
   // a ring no deeper than the slice, so that the next launch's CTAs find room beside this one's
   const int stages = std::min(C::fit(a_rows, S), (prm.KB + S - 1) / S);
-  if (stages <= 0) return FP4MOE_UNSUPPORTED;  // (not reached: pick_plan splits 64 rows or fewer, four ways at most)
+  if (stages <= 0) return FP4MOE_UNSUPPORTED;  // (not reached: what pick_plan splits, four ways at most, leaves four stages)
   prm.a_sf = a_sf;
   prm.b_sf = b_sf;
   TileMaps maps;

@@ -432,6 +432,13 @@ def test_gemm_pairs_many_rounds(fmt, dtype, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(128, 1024, 14336), (65, 100, 9000), (200, 513, 8200), (513, 130, 8192)])
+def test_gemm_k_split_of_more_than_64_rows(fmt, dtype, M, N, K):
+    check_gemm(fmt, M, N, K, dtype, seed=M)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
 @pytest.mark.parametrize("M,N,K", [(5, 300, 512), (700, 4096, 1024), (8, 1024, 4096), (64, 4096, 4096)])
 def test_gemm_is_deterministic(fmt, M, N, K):
     import torch
