@@ -100,6 +100,12 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t adesc, uint64_t b
     tc_mma_nvf4(d, adesc, bdesc, idesc, sfa, sfb, accumulate);
 }
 
+// Where a partial tile holds the 16-byte chunk j of its row i: free of bank conflicts.
+template <int BN>
+__device__ __forceinline__ uint32_t part_chunk(int i, int j) {
+  return (uint32_t)(i * BN * 4 + (j ^ (i & 7)) * 16);
+}
+
 // Grid (tiles or persistent CTAs, 1, S), cluster (1, 1, S). stages: ring depth; tmem_cols: a power of two that holds
 // the accumulator and the stages' scales.
 template <int FMT, int BN, typename T>
@@ -124,6 +130,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   const uint32_t bar_parts = bar_drain + 8;  // rank 0: the partial tiles of the others have arrived
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 240);
   uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 244);
+  uint8_t* const s_sent = smem_raw + bar_off + 248;  // ranks 1 ..: whether each epilogue warp has sent its part
 
   if (warp == 0) {
     tmem_alloc(smem_u32(&s_tmem), tmem_cols);
@@ -147,6 +154,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) {
+    for (int w = 0; w < DEPI; ++w) s_sent[w] = 0;
     s_abort = (*(volatile uint32_t*)prm.err & kAbortMask) != 0 ? 1u : 0u;
     if ((smem & 1023u) != 0) {  // the swizzle needs it, and the compiler grants it
       raise_error(prm.err, FP4MOE_ERR_CAPACITY);
@@ -160,6 +168,18 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   // an earlier timeout poisons the call: no role takes a tile
   const int tiles = s_abort ? 0 : prm.mt * prm.nt;
   const int kb0 = prm.KB * z / S, kb1 = prm.KB * (z + 1) / S;  // this slice's stages, one at least
+
+  // S > 1, ranks 1 ..: columns c .. c + 31 of this lane's row of its warp's part of the partial tile, to rank 0
+  auto send_part = [&](int c, const float (&q)[32]) {
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
+    if ((int)blockIdx.x % prm.mt * DBM + row < prm.M) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        st_async_16(dst + part_chunk<BN>(row, (W * half + c) / 4 + j), q[4 * j], q[4 * j + 1], q[4 * j + 2],
+                    q[4 * j + 3], bar);
+    }
+  };
 
   if (S > 1 && z == 0 && threadIdx.x == 32 * DMMA) {
     // bytes that the others send: their columns in N by halves of the tile, rows in M
@@ -268,22 +288,16 @@ __global__ void __launch_bounds__(DTHREADS, 1)
       const bool live = r0 < prm.M && c0 < prm.N;
       if (S > 1) {  // one tile a cluster
         const int row = quarter * 32 + lane;  // of the tile
-        // row i, 16-byte chunk j of a partial tile at i * BN * 4 + (j ^ i % 8) * 16: free of bank conflicts
-        auto chunk = [&](int j) { return (uint32_t)(row * BN * 4 + ((W * half / 4 + j) ^ (row & 7)) * 16); };
         if (z > 0) {
-          const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
           if (live) {
 #pragma unroll
             for (int c = 0; c < W; c += 32) {
               float q[32];
               tmem_ld32(tacc + c, q);
               tmem_ld_wait();
-              if (r0 + lane < prm.M) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  st_async_16(dst + chunk(c / 4 + j), q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3], bar);
-              }
+              send_part(c, q);
             }
+            if (lane == 0) s_sent[warp] = 1;
           }
           continue;
         }
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
             const uint8_t* src = smem_raw + ring + p * a_rows * BN * 4;
 #pragma unroll
             for (int j = 0; j < W / 4; ++j) {
-              const float4 q = *reinterpret_cast<const float4*>(src + chunk(j));
+              const float4 q = *reinterpret_cast<const float4*>(src + part_chunk<BN>(row, W * half / 4 + j));
               v[4 * j] += q.x;
               v[4 * j + 1] += q.y;
               v[4 * j + 2] += q.z;
@@ -348,7 +362,18 @@ __global__ void __launch_bounds__(DTHREADS, 1)
 
   if (S > 1) {
     __syncwarp();  // the single-thread roles reconverge: cluster barriers are warp-aligned instructions
-    cluster_sync();  // on every path, no CTA leaves while another may still write to it
+    // On every path rank 0 stays until all that was sent to it has landed. The cluster's barrier does not order
+    // st.async, so that is bar_parts' phase, and it completes whoever gave up: each rank sends its part once, with
+    // zeros in it (which nobody uses) if it had none by the time that all ranks were done.
+    cluster_sync();
+    const bool part = (int)blockIdx.x % prm.mt * DBM + (warp & 3) * 32 < prm.M &&
+                      (int)blockIdx.x / prm.mt * BN + W * (warp >> 2) < prm.N;
+    if (z > 0 && warp < DEPI && part && s_sent[warp] == 0) {
+      const float zero[32] = {};
+#pragma unroll
+      for (int c = 0; c < W; c += 32) send_part(c, zero);
+    }
+    if (z == 0 && threadIdx.x == 0) drain_wait(bar_parts, 0);
   }
   tc_fence_before();
   __syncthreads();

@@ -536,3 +536,61 @@ def test_chain_on_a_side_stream_and_in_a_graph(fmt):
         got = outputs()
         chain()
         assert all(torch.equal(a, b) for a, b in zip(got, outputs())), seed
+
+
+# ------------------------------------------------------------------------- calls that find or meet an error
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (64, 4096, 4096), (20, 8192, 4096), (128, 1024, 14336)])
+def test_gemm_k_split_under_a_raised_error_word(fmt, M, N, K):
+    """Every CTA of a cluster skips its part, and the next call's partial sums are whole."""
+    import torch
+    from block_scaled_fp4_top_gb300 import _lib, api
+    ops = gemm_operands(fmt, M, N, K, 5)
+    a, asf, _, b, bsf, _ = ops
+    want = check_gemm(fmt, M, N, K, "float32", operands=ops).clone()
+    ob = Guarded((M, N), torch.float32)
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        ob.t.fill_(7.0)
+        err[0] = _lib.ERR_TIMEOUT
+        for _ in range(3):
+            api.fp4moe_mx_gemm(fmt, K, a, asf, b, bsf, None, ob.t, err)
+        torch.cuda.synchronize()
+        assert (ob.t == 7.0).all() and api.fp4moe_read_error(err) == _lib.ERR_TIMEOUT
+        api.fp4moe_mx_gemm(fmt, K, a, asf, b, bsf, None, ob.t, err)
+        torch.cuda.synchronize()
+        assert int(err[0]) == 0 and torch.equal(ob.t, want)
+        ob.check()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (64, 8192, 8192), (128, 1024, 14336), (512, 4096, 4096)])
+def test_gemm_under_an_error_word_that_is_raised_while_it_runs(M, N, K):
+    """CTAs of one cluster may see it at different times. Each call ends, and leaves nothing to the next one."""
+    import torch
+    from block_scaled_fp4_top_gb300 import _lib, api
+    ops = gemm_operands(MX, M, N, K, 6)
+    a, asf, _, b, bsf, _ = ops
+    ob = Guarded((M, N), torch.float32)
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    raised = torch.full((1,), _lib.ERR_TIMEOUT, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    call = lambda: api.fp4moe_mx_gemm(MX, K, a, asf, b, bsf, None, ob.t, err)
+    call()
+    torch.cuda.synchronize()
+    want = ob.t.clone()
+    for i in range(24):
+        gate = torch.cuda.Event()
+        torch.cuda._sleep(200_000)
+        gate.record()
+        for _ in range(8):
+            call()
+        with torch.cuda.stream(side):
+            side.wait_event(gate)
+            torch.cuda._sleep(1 + 4000 * i)
+            err[:1].copy_(raised)
+        torch.cuda.synchronize()
+        assert api.fp4moe_read_error(err) == _lib.ERR_TIMEOUT
+        ob.check()
+        call()
+        torch.cuda.synchronize()
+        assert int(err[0]) == 0 and torch.equal(ob.t, want)
