@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(1024)
     float p[N], g[N], n[N];
     unpack<T>(hv[i], p);
     unpack<T>(gv[i], g);
-    auto norm = [&]() {
+    auto norm = [&]() {  // one order of the products, whether or not there are codes
       float h[N];
       unpack<T>(hv[i], h);
 #pragma unroll
@@ -216,17 +216,14 @@ __global__ void __launch_bounds__(1024)
       a = fmax_nan(a, fabsf(p[k]));
     }
     a = group_max(a);
+    norm();
     Fp8Ratio f;
     if (__all_sync(0xFFFFFFFFu, j >= H || (in_range(a) && in_range(rstd)))) {
       f = fp8_ratio(a);
       s = __fdiv_rn(a, 448.0f) * rstd;
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        n[k] = p[k] * rstd;
-        p[k] *= 448.0f;
-      }
+      for (int k = 0; k < N; ++k) p[k] *= 448.0f;
     } else {
-      norm();
       a = 0.0f;
 #pragma unroll
       for (int k = 0; k < N; ++k) a = fmax_nan(a, fabsf(n[k]));  // a NaN takes its whole group along
@@ -358,7 +355,7 @@ __global__ void __launch_bounds__(1024)
       unpack_raw<T, U>(hv[i][s], p[s]);
       unpack_raw<T, U>(gv[i][s], w[s]);
     }
-    auto norm = [&]() {
+    auto norm = [&]() {  // one order of the products, whether or not there are codes
       float h[S][U];
 #pragma unroll
       for (int s = 0; s < S; ++s) unpack_raw<T, U>(hv[i][s], h[s]);
@@ -369,9 +366,8 @@ __global__ void __launch_bounds__(1024)
     };
     float a = 0.0f, sc = 0.0f;
     Fp8Ratio f{};
-    if (codes == nullptr) {
-      norm();
-    } else {
+    norm();
+    if (codes != nullptr) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -386,12 +382,8 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            n[s][k] = p[s][k] * rstd;
-            p[s][k] *= 448.0f;
-          }
+          for (int k = 0; k < U; ++k) p[s][k] *= 448.0f;
       } else {
-        norm();
         a = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; ++s)
