@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(1024)
     add_rmsnorm_vec_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
                            T* y, uint8_t* codes, float* scales, int64_t scale_stride) {
   constexpr int N = 16 / (int)sizeof(T), LANES = 128 / N;
+  static_assert(LANES == 16 || LANES == 32, "a group is a warp or half of one");
   __shared__ float s_red[32];
   pdl_wait();
   pdl_trigger();
@@ -187,9 +188,9 @@ __global__ void __launch_bounds__(1024)
   }
   ss = cta_sum(ss, s_red);
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
-  auto group_max = [](float a) {
+  auto group_max = [](float a, uint32_t lanes) {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(lanes, a, o));
     return a;
   };
 #pragma unroll
@@ -215,10 +216,10 @@ __global__ void __launch_bounds__(1024)
       if (gamma != nullptr) p[k] *= g[k];
       a = fmax_nan(a, fabsf(p[k]));
     }
-    a = group_max(a);
+    a = group_max(a, 0xFFFFFFFFu);
     norm();
     Fp8Ratio f;
-    if (__all_sync(0xFFFFFFFFu, j >= H || (in_range(a) && in_range(rstd)))) {
+    if (in_range(a) && in_range(rstd)) {
       f = fp8_ratio(a);
       s = __fdiv_rn(a, 448.0f) * rstd;
 #pragma unroll
@@ -227,7 +228,9 @@ __global__ void __launch_bounds__(1024)
       a = 0.0f;
 #pragma unroll
       for (int k = 0; k < N; ++k) a = fmax_nan(a, fabsf(n[k]));  // a NaN takes its whole group along
-      s = __fdiv_rn(group_max(a), 448.0f);
+      // the way to the codes is the group's own: the warp's other group may have gone the short one
+      const uint32_t mates = LANES == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16u);
+      s = __fdiv_rn(group_max(a, mates), 448.0f);
       float up;
       f = fp8_scale(s, up);
 #pragma unroll

@@ -1,9 +1,12 @@
-"""GPU: the residual norm's results do not depend on what else a call computes: y is bit-equal with and without the
-FP8 copy."""
+"""GPU: the residual norm's results do not depend on what else a call computes, nor on a row's other groups: y is
+bit-equal with and without the FP8 copy, and the copy's codes are those of exact arithmetic (bf16) beside groups of any
+magnitude."""
+import numpy as np
 import pytest
 
 from helpers import ensure_built
-from test_gpu_dense import DTYPES, rnd
+from oracle import codecs
+from test_gpu_dense import DTYPES, f64, rnd
 
 pytestmark = pytest.mark.gpu
 # 16-byte vectors with one, two and four a thread; 8-, 4- and 2-byte accesses; rows that no CTA's registers hold
@@ -30,6 +33,31 @@ def norm(x, residual, gamma, fp8=True, eps=1e-6):
     return h, y, codes, scales
 
 
+def exact_codes(h, g):
+    """E4M3 codes of n / s = 448 p / max|p| with p = h * gamma, for bf16 h and gamma: in fp64 that side and a midpoint of
+    the E4M3 grid times max|p| are exact products, so every code, ties to even included, follows from comparisons."""
+    T, H = h.shape
+    G = (H + 127) // 128
+    p = np.zeros((T, G * 128))
+    p[:, :H] = f64(h) * (f64(g) if g is not None else 1.0)
+    top = np.repeat(np.abs(p).reshape(T, G, 128).max(2), 128, axis=1)
+    grid = codecs.E4M3_TABLE[:127].astype(np.float64)
+    want = np.zeros(p.shape, dtype=np.int64)
+    for i, mid in enumerate((grid[1:] + grid[:-1]) / 2):
+        side, bar = 448.0 * np.abs(p), mid * top
+        want += (side > bar) | ((side == bar) & (i % 2 == 1) & (top > 0))
+    return want[:, :H], p[:, :H] < 0
+
+
+def hold_codes(codes, h, g, where=None):
+    want, negative = exact_codes(h, g)
+    got = codes.cpu().numpy().astype(np.int64)
+    differ = ((got & 127) != want) | ((got >> 7 != negative) & (want != 0))     # the sign of a zero is free
+    if where is not None:
+        differ &= where
+    assert not differ.any(), f"{differ.sum()} codes of {differ.size}"
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,H", SIZES)
 @pytest.mark.parametrize("gamma", [False, True])
@@ -49,3 +77,16 @@ def test_a_call_repeats_itself(dtype, T, H):
     first = norm(x, r, g)
     for _ in range(10):
         assert all(torch.equal(a, b) for a, b in zip(first, norm(x, r, g)))
+
+
+@pytest.mark.parametrize("T,H", [(64, 4096), (400, 4096), (200, 1002)])
+@pytest.mark.parametrize("other", [0.0, 2.0 ** -90])
+def test_codes_do_not_depend_on_the_group_beside(T, H, other):
+    """Every second group is zeros, or too small for the short way to the codes."""
+    h, g = rnd((T, H), "bfloat16", H, 0.5), rnd((H,), "bfloat16", H + 1, 0.0)
+    group = np.arange(H) // 128
+    for odd in (0, 1):
+        x = h.clone()
+        x[:, group % 2 == odd] *= other
+        _, _, codes, _ = norm(x, None, g)
+        hold_codes(codes, x, g, np.broadcast_to(group % 2 != odd, (T, H)))
