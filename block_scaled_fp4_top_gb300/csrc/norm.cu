@@ -33,6 +33,13 @@ __device__ __forceinline__ float cta_sum(float v, float* s_red) {
   return v;
 }
 
+// The largest of 32 lanes, NaN if any is, in every lane.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // The codes of a group are RN_E4M3(v / t), v and t being n and s up to one factor. The quotient is off by half a unit
 // of fp32's last place in all but rare cases: one reciprocal serves a group, and two fused steps per element take its
 // error out.
@@ -92,11 +99,11 @@ __global__ void __launch_bounds__(NORM_THREADS)
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int g = warp; g * 128 < H; g += NORM_THREADS / 32) {
-    float n[4], a = 0.0f;
+    float n[4], p[4], a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = g * 128 + 32 * i + lane;
-      n[i] = 0.0f;
+      n[i] = p[i] = 0.0f;
       if (j < H) {
         float h = to_f32(x[row + j]);
         if (residual != nullptr) {
@@ -104,21 +111,36 @@ __global__ void __launch_bounds__(NORM_THREADS)
           h = to_f32(r);
           h_out[row + j] = r;
         }
-        n[i] = h * rstd * (gamma != nullptr ? to_f32(gamma[j]) : 1.0f);
+        const float w = gamma != nullptr ? to_f32(gamma[j]) : 1.0f;
+        n[i] = h * rstd * w;
+        p[i] = h * w;
         if (y != nullptr) y[row + j] = from_f32<T>(n[i]);
       }
-      a = fmax_nan(a, fabsf(n[i]));  // a NaN takes its whole group along: NaN scale, NaN codes
+      a = fmax_nan(a, fabsf(p[i]));
     }
     if (codes != nullptr) {
+      a = warp_max_nan(a);
+      float s;
+      Fp8Ratio f;
+      if (in_range(a) && in_range(rstd)) {
+        f = fp8_ratio(a);
+        s = __fdiv_rn(a, 448.0f) * rstd;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a = fmax_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-      const float s = __fdiv_rn(a, 448.0f);
-      float up;
-      const Fp8Ratio f = fp8_scale(s, up);
+        for (int i = 0; i < 4; ++i) p[i] *= 448.0f;
+      } else {
+        a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = fmax_nan(a, fabsf(n[i]));
+        s = __fdiv_rn(warp_max_nan(a), 448.0f);  // a NaN takes its whole group along: NaN scale, NaN codes
+        float up;
+        f = fp8_scale(s, up);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = n[i] * up;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = g * 128 + 32 * i + lane;
-        if (j < H) codes[row + j] = (uint8_t)cvt_e4m3x2(fp8_quotient(n[i] * up, f), 0.0f);
+        if (j < H) codes[row + j] = (uint8_t)cvt_e4m3x2(fp8_quotient(p[i], f), 0.0f);
       }
       if (lane == 0) scales[(size_t)g * scale_stride + blockIdx.x] = s;
     }
@@ -280,13 +302,6 @@ __device__ __forceinline__ Raw<T, U> pack_raw(const float (&v)[U]) {
   } else {
     return make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
   }
-}
-
-// The largest of 32 lanes, NaN if any is, in every lane.
-__device__ __forceinline__ float warp_max_nan(float v) {
-  float r;
-  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 // Widths that the 16-byte vectors do not divide. Rows then start at any element, and a vector that is aligned for

@@ -1,6 +1,6 @@
-"""GPU: the residual norm's results do not depend on what else a call computes, nor on a row's other groups: y is
-bit-equal with and without the FP8 copy, and the copy's codes are those of exact arithmetic (bf16) beside groups of any
-magnitude."""
+"""GPU: the residual norm's results do not depend on what else a call computes, nor on a row's other groups, nor on the
+kernel that the width selects: y is bit-equal with and without the FP8 copy, and the copy's codes are those of exact
+arithmetic (bf16) in every kernel, beside groups of any magnitude."""
 import numpy as np
 import pytest
 
@@ -90,3 +90,12 @@ def test_codes_do_not_depend_on_the_group_beside(T, H, other):
         x[:, group % 2 == odd] *= other
         _, _, codes, _ = norm(x, None, g)
         hold_codes(codes, x, g, np.broadcast_to(group % 2 != odd, (T, H)))
+
+
+@pytest.mark.parametrize("T,H", [(40, 40960), (40, 40962)])
+@pytest.mark.parametrize("gamma", [False, True])
+def test_codes_of_wide_rows_are_those_of_exact_arithmetic(T, H, gamma):
+    h = rnd((T, H), "bfloat16", H, 0.5)
+    g = rnd((H,), "bfloat16", H + 1, 0.0) if gamma else None
+    _, _, codes, _ = norm(h, None, g)
+    hold_codes(codes, h, g)
