@@ -2,17 +2,18 @@
 //
 //   h[t]  = RN(x[t] + residual[t])                    (the stored residual stream; h = x without a residual)
 //   n[t]  = h[t] * rsqrt(mean_j h[t, j]^2 + eps) * gamma
-//   y[t]  = RN(n[t]),   s[t, g] = RN(amax_g |n| / 448),   code = E4M3_satfinite(n / s), 0 where s == 0
+//   y[t]  = RN(n[t]),   s[t, g] = amax_g |n| / 448,   code = E4M3_satfinite(n / s), 0 where s == 0
 // for the 1 x 128 groups g of a row: the activation format of the block-FP8 shared expert (segemm.cu). The
-// codes are taken from n in fp32, before the rounding to y's type, so they carry one rounding, not two.
+// codes are not taken from the y that was rounded to its type, so they carry one rounding, not two. n has one order of
+// products, (h rstd) gamma, in every kernel, with and without the codes; these come from h gamma (Fp8Ratio).
 //
 // The sum of squares and the statistics are fp32; h is rounded to its storage type first, so the norm is
 // that of the stream a later layer reads back.
 //
 // Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
 // between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
-// back (1 x 4096 bf16 2.1 us, 64 rows 2.3 us), so they take the most threads; many rows take two or four 16-byte
-// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48.4 us, 6.3 TB/s, 92 % of a copy's rate).
+// back (1 x 4096 bf16 2.0 us, 64 rows 2.3 us), so they take the most threads; many rows take two or four 16-byte
+// vectors a thread (8192 x 4096 bf16 with the FP8 copy 49.0 us, 6.2 TB/s, 91 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -79,7 +80,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[N / 
 }
 
 // Widths too large for a CTA's registers: element accesses, and the row is read again for its second use
-// (500 x 40960 bf16 with the FP8 copy 71 us, 2.6 TB/s; with 256 threads 111 us). A warp takes whole 128-element
+// (500 x 40960 bf16 with the FP8 copy 74 us, 2.5 TB/s; with 256 threads 111 us). A warp takes whole 128-element
 // groups, four elements a lane (lane, lane + 32, ...).
 template <typename T>
 __global__ void __launch_bounds__(NORM_THREADS)

@@ -510,11 +510,15 @@ typedef enum fp4moe_dtype { FP4MOE_BF16 = 0, FP4MOE_FP16 = 1, FP4MOE_FP32 = 2 } 
  *   n    = h * rsqrt(mean(h^2) + eps) * gamma  (fp32)
  *   y    = RN(n)
  *   and per 1 x 128 group g of n (the last one may be short):
- *   s    = RN(amax / 448)                      -> y_scales[g * scale_stride + t]
+ *   s    = amax / 448                          -> y_scales[g * scale_stride + t]
  *   code = E4M3_satfinite(n / s), 0 where s == 0       -> y_codes[t][:]
- *          (from the exact n / s where x is bf16 and no value of the group is
- *          near the ends of fp32's range, else to within two units of fp32's
- *          last place, before E4M3 rounds)
+ * n is (h * rstd) * gamma, each product rounded to fp32, with or without the
+ * codes. For the codes rstd cancels: where p = max|h * gamma| of the group and
+ * rstd lie in (2^-50, 2^50),
+ *   s    = RN(RN(p / 448) * rstd), code = E4M3_satfinite(448 h gamma / p),
+ * the codes of exact arithmetic where x is bf16, else from a quotient within two
+ * units of fp32's last place. In any other group s = RN(max|n| / 448), and
+ * code = E4M3_satfinite(n / s) of such a quotient.
  * RN rounds once to the storage type `dtype` of x, residual, gamma,
  * residual_out and y (an fp4moe_dtype). The norm is that of the rounded h, the
  * stream that residual_out holds; the codes are taken from n before its
