@@ -106,6 +106,26 @@ __device__ __forceinline__ uint32_t part_chunk(int i, int j) {
   return (uint32_t)(i * BN * 4 + (j ^ (i & 7)) * 16);
 }
 
+// The end of a K split in a CTA where an epilogue warp gave up (a bit of `gave_up`), once every CTA of the cluster is
+// done: rank 0 stays until all that is sent to it has landed. The cluster's barrier does not order st.async, so that is
+// the phase of `bar`, and it completes whoever gave up: a warp of another rank that has not sent its part of the partial
+// tile sends zeros, which nobody uses. (Where no warp of rank 0 gave up, its epilogue has waited for that phase.) `parts`
+// is this CTA's address of the buffers. Out of line: inside the kernel these instructions cost every call 0.2 us.
+template <int BN>
+static __device__ __noinline__ void settle_split(uint32_t parts, uint32_t bar, int a_rows, int M, int N, int mt,
+                                                 uint32_t gave_up) {
+  const int z = blockIdx.z, warp = (int)threadIdx.x >> 5;
+  if (z == 0) {
+    if (threadIdx.x == 0) drain_wait(bar, 0);
+    return;
+  }
+  if (warp >= DEPI || (gave_up >> warp & 1) == 0) return;
+  const int row = (int)threadIdx.x & 127, c0 = BN / 2 * (warp >> 2);  // of the cluster's tile
+  if ((int)blockIdx.x % mt * DBM + row >= M || (int)blockIdx.x / mt * BN + c0 >= N) return;
+  const uint32_t dst = map_cluster(parts + (uint32_t)((z - 1) * a_rows * BN * 4), 0), cbar = map_cluster(bar, 0);
+  for (int j = 0; j < BN / 8; ++j) st_async_16(dst + part_chunk<BN>(row, c0 / 4 + j), 0.0f, 0.0f, 0.0f, 0.0f, cbar);
+}
+
 // Grid (tiles or persistent CTAs, 1, S), cluster (1, 1, S). stages: ring depth; tmem_cols: a power of two that holds
 // the accumulator and the stages' scales.
 template <int FMT, int BN, typename T>
@@ -130,7 +150,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   const uint32_t bar_parts = bar_drain + 8;  // rank 0: the partial tiles of the others have arrived
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 240);
   uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 244);
-  uint8_t* const s_sent = smem_raw + bar_off + 248;  // ranks 1 ..: whether each epilogue warp has sent its part
+  uint32_t& s_gave_up = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 248);  // a bit for each epilogue warp
 
   if (warp == 0) {
     tmem_alloc(smem_u32(&s_tmem), tmem_cols);
@@ -154,12 +174,12 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int w = 0; w < DEPI; ++w) s_sent[w] = 0;
     s_abort = (*(volatile uint32_t*)prm.err & kAbortMask) != 0 ? 1u : 0u;
     if ((smem & 1023u) != 0) {  // the swizzle needs it, and the compiler grants it
       raise_error(prm.err, FP4MOE_ERR_CAPACITY);
       s_abort = 1u;
     }
+    s_gave_up = s_abort ? ~0u : 0u;
   }
   tc_fence_before();
   __syncthreads();
@@ -168,18 +188,6 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   // an earlier timeout poisons the call: no role takes a tile
   const int tiles = s_abort ? 0 : prm.mt * prm.nt;
   const int kb0 = prm.KB * z / S, kb1 = prm.KB * (z + 1) / S;  // this slice's stages, one at least
-
-  // S > 1, ranks 1 ..: columns c .. c + 31 of this lane's row of its warp's part of the partial tile, to rank 0
-  auto send_part = [&](int c, const float (&q)[32]) {
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
-    if ((int)blockIdx.x % prm.mt * DBM + row < prm.M) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        st_async_16(dst + part_chunk<BN>(row, (W * half + c) / 4 + j), q[4 * j], q[4 * j + 1], q[4 * j + 2],
-                    q[4 * j + 3], bar);
-    }
-  };
 
   if (S > 1 && z == 0 && threadIdx.x == 32 * DMMA) {
     // bytes that the others send: their columns in N by halves of the tile, rows in M
@@ -283,21 +291,29 @@ __global__ void __launch_bounds__(DTHREADS, 1)
       const int m = t % prm.mt, n = t / prm.mt;
       const int r0 = m * DBM + quarter * 32, c0 = n * BN + W * half;
       // the whole warp takes one decision: tcgen05.ld is warp-collective
-      if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) break;
+      if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) {
+        if (lane == 0) atomicOr(&s_gave_up, 1u << warp);
+        break;
+      }
       tc_fence_after();
       const bool live = r0 < prm.M && c0 < prm.N;
       if (S > 1) {  // one tile a cluster
         const int row = quarter * 32 + lane;  // of the tile
         if (z > 0) {
           if (live) {
+            const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
 #pragma unroll
             for (int c = 0; c < W; c += 32) {
               float q[32];
               tmem_ld32(tacc + c, q);
               tmem_ld_wait();
-              send_part(c, q);
+              if (r0 + lane < prm.M) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  st_async_16(dst + part_chunk<BN>(row, (W * half + c) / 4 + j), q[4 * j], q[4 * j + 1], q[4 * j + 2],
+                              q[4 * j + 3], bar);
+              }
             }
-            if (lane == 0) s_sent[warp] = 1;
           }
           continue;
         }
@@ -312,7 +328,10 @@ __global__ void __launch_bounds__(DTHREADS, 1)
             for (int j = 0; j < 32; ++j) v[c + j] = q[j];
           }
         }
-        if (!mbar_wait_warp(bar_parts, 0, prm.err)) break;
+        if (!mbar_wait_warp(bar_parts, 0, prm.err)) {
+          if (lane == 0) atomicOr(&s_gave_up, 1u << warp);
+          break;
+        }
         if (!live) continue;
         if (row < a_rows) {  // (the rows past M in it hold nothing that is stored)
           for (int p = 0; p < S - 1; ++p) {
@@ -362,18 +381,9 @@ __global__ void __launch_bounds__(DTHREADS, 1)
 
   if (S > 1) {
     __syncwarp();  // the single-thread roles reconverge: cluster barriers are warp-aligned instructions
-    // On every path rank 0 stays until all that was sent to it has landed. The cluster's barrier does not order
-    // st.async, so that is bar_parts' phase, and it completes whoever gave up: each rank sends its part once, with
-    // zeros in it (which nobody uses) if it had none by the time that all ranks were done.
     cluster_sync();
-    const bool part = (int)blockIdx.x % prm.mt * DBM + (warp & 3) * 32 < prm.M &&
-                      (int)blockIdx.x / prm.mt * BN + W * (warp >> 2) < prm.N;
-    if (z > 0 && warp < DEPI && part && s_sent[warp] == 0) {
-      const float zero[32] = {};
-#pragma unroll
-      for (int c = 0; c < W; c += 32) send_part(c, zero);
-    }
-    if (z == 0 && threadIdx.x == 0) drain_wait(bar_parts, 0);
+    if (s_gave_up != 0)
+      settle_split<BN>(smem + ring, bar_parts, a_rows, prm.M, prm.N, prm.mt, s_gave_up);
   }
   tc_fence_before();
   __syncthreads();
