@@ -106,26 +106,6 @@ __device__ __forceinline__ uint32_t part_chunk(int i, int j) {
   return (uint32_t)(i * BN * 4 + (j ^ (i & 7)) * 16);
 }
 
-// The end of a K split in a CTA where an epilogue warp gave up (a bit of `gave_up`), once every CTA of the cluster is
-// done: rank 0 stays until all that is sent to it has landed. The cluster's barrier does not order st.async, so that is
-// the phase of `bar`, and it completes whoever gave up: a warp of another rank that has not sent its part of the partial
-// tile sends zeros, which nobody uses. (Where no warp of rank 0 gave up, its epilogue has waited for that phase.) `parts`
-// is this CTA's address of the buffers. Out of line: inside the kernel these instructions cost every call 0.2 us.
-template <int BN>
-static __device__ __noinline__ void settle_split(uint32_t parts, uint32_t bar, int a_rows, int M, int N, int mt,
-                                                 uint32_t gave_up) {
-  const int z = blockIdx.z, warp = (int)threadIdx.x >> 5;
-  if (z == 0) {
-    if (threadIdx.x == 0) drain_wait(bar, 0);
-    return;
-  }
-  if (warp >= DEPI || (gave_up >> warp & 1) == 0) return;
-  const int row = (int)threadIdx.x & 127, c0 = BN / 2 * (warp >> 2);  // of the cluster's tile
-  if ((int)blockIdx.x % mt * DBM + row >= M || (int)blockIdx.x / mt * BN + c0 >= N) return;
-  const uint32_t dst = map_cluster(parts + (uint32_t)((z - 1) * a_rows * BN * 4), 0), cbar = map_cluster(bar, 0);
-  for (int j = 0; j < BN / 8; ++j) st_async_16(dst + part_chunk<BN>(row, c0 / 4 + j), 0.0f, 0.0f, 0.0f, 0.0f, cbar);
-}
-
 // Grid (tiles or persistent CTAs, 1, S), cluster (1, 1, S). stages: ring depth; tmem_cols: a power of two that holds
 // the accumulator and the stages' scales.
 template <int FMT, int BN, typename T>
@@ -147,7 +127,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   const uint32_t bar_tfull = bar_empty + 8 * C::kMaxStages;
   const uint32_t bar_tempty = bar_tfull + 8;
   const uint32_t bar_drain = bar_tempty + 8;
-  const uint32_t bar_parts = bar_drain + 8;  // rank 0: the partial tiles of the others have arrived
+  const uint32_t bar_parts = bar_drain + 8;  // rank 0: every epilogue warp of the others has sent its part
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 240);
   uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 244);
   uint32_t& s_gave_up = *reinterpret_cast<uint32_t*>(smem_raw + bar_off + 248);  // a bit for each epilogue warp
@@ -164,7 +144,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
     mbar_init(bar_tfull, 1);
     mbar_init(bar_tempty, DEPI);
     mbar_init(bar_drain, 1);
-    mbar_init(bar_parts, 1);
+    mbar_init(bar_parts, S > 1 ? (uint32_t)((S - 1) * DEPI) : 1u);
     fence_mbar_init();
     prefetch_map(&maps.a);
     prefetch_map(&maps.b);
@@ -189,13 +169,6 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   const int tiles = s_abort ? 0 : prm.mt * prm.nt;
   const int kb0 = prm.KB * z / S, kb1 = prm.KB * (z + 1) / S;  // this slice's stages, one at least
 
-  if (S > 1 && z == 0 && threadIdx.x == 32 * DMMA) {
-    // bytes that the others send: their columns in N by halves of the tile, rows in M
-    const int n = (int)blockIdx.x / prm.mt * BN, m = (int)blockIdx.x % prm.mt * DBM;
-    const int halves = prm.N - n > W ? 2 : 1;
-    mbar_arrive_expect_tx(bar_parts, (uint32_t)((S - 1) * min(prm.M - m, DBM) * halves * W * 4));
-  }
-  __syncwarp();
   if ((warp == DPRODUCER || warp == DPRODUCER + 1) && lane == 0) {
     const bool is_b = warp != DPRODUCER;
     const uint64_t pol = policy_evict_normal();
@@ -300,8 +273,9 @@ __global__ void __launch_bounds__(DTHREADS, 1)
       if (S > 1) {  // one tile a cluster
         const int row = quarter * 32 + lane;  // of the tile
         if (z > 0) {
+          const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
+          if (lane == 0) mbar_arrive_expect_tx_cluster(bar, live ? min(prm.M - r0, 32) * W * 4 : 0);
           if (live) {
-            const uint32_t dst = map_cluster(smem + ring + (z - 1) * a_rows * BN * 4, 0), bar = map_cluster(bar_parts, 0);
 #pragma unroll
             for (int c = 0; c < W; c += 32) {
               float q[32];
@@ -382,8 +356,17 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   if (S > 1) {
     __syncwarp();  // the single-thread roles reconverge: cluster barriers are warp-aligned instructions
     cluster_sync();
-    if (s_gave_up != 0)
-      settle_split<BN>(smem + ring, bar_parts, a_rows, prm.M, prm.N, prm.mt, s_gave_up);
+    // Rank 0 stays until all that was sent to it has landed. The cluster's barrier does not order st.async, so that is
+    // bar_parts' phase. Where no warp of rank 0 gave up, its epilogue has waited for it. Else the warps of the other
+    // ranks that have not sent their part make up for their arrivals here, so that it completes. (A form of this that
+    // sent zeros instead, or in a function of its own, cost calls that end well 0.2 to 0.4 us.)
+    if (s_gave_up != 0) {
+      if (z > 0) {
+        if (lane == 0 && warp < DEPI && (s_gave_up >> warp & 1u) != 0) mbar_arrive_cluster(map_cluster(bar_parts, 0));
+      } else if (threadIdx.x == 0) {
+        drain_wait(bar_parts, 0);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -116,13 +116,6 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bd
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-// Arrive on a barrier of any CTA of the cluster (an address from map_cluster). It publishes no memory writes: what it
-// orders are TMEM reads, complete at the arriving warp's tcgen05.wait::ld, with the tcgen05 fences of both sides. A
-// release at cluster scope here and a fence at the other end cost 1.1 us a tile.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
-}
-
 // Tile t: groups of 4 tile rows, so that the tiles of a wave share their operands' rows in L2 (8192 x 4096 x 4096
 // MXFP4 44.7 us; groups of 8 45.0, 16 45.3, 32 46.4).
 __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
@@ -285,6 +278,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     constexpr int W = PBN / 2;  // columns of one warp
     const int quarter = warp & 3, half = warp >> 2;
     uint8_t* stage = smem_raw + C::kEpiOff + warp * kEpiStage;
+    // Arrivals here publish no memory writes: what they order are TMEM reads, complete at the arriving warp's
+    // tcgen05.wait::ld, with the tcgen05 fences of both sides. A release at cluster scope and a fence at the other end
+    // cost 1.1 us a tile.
     const uint32_t tempty = map_cluster(bar_tempty, lead);
     const float alpha = prm.alpha != nullptr ? __ldg(prm.alpha) : 1.0f;
     int tl = 0;
