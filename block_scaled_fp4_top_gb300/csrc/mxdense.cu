@@ -410,24 +410,23 @@ bool dense_configure() {
   return ok == 1;
 }
 
-// Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 41 sizes from 1 x 4096 x 256 to
-// 8192 x 8192 x 2048: the one picked is within 7 % of the fastest at all of them (bn64 / bn128 / pair / two pairs, us:
-// 64 x 8192 x 4096 MXFP4 6.9 7.0 9.0 10.2, 512 x 4096 x 4096 11.1 7.9 9.3 9.4, 768 x 4096 x 4096 15.4 12.0 9.9 10.1,
-// 8192 x 4096 x 2048 65 43 28.6 29.9, 1500 x 3000 x 2000 19 14 10.4 9.6; split in two or four 1 x 4096 x 4096 takes
-// 6.0 and 5.5 instead of 6.6, 64 x 4096 x 4096 6.4 and 9.8 instead of 6.5, 128 x 2048 x 8192 8.9 and 10.4 instead of
-// 10.3, 128 x 1024 x 14336 11.6 and 10.1 instead of 15.9). KB: 256-element stages of K.
+// Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 55 sizes from 1 x 4096 x 256 to
+// 8192 x 8192 x 8192: the one picked is within 7 % of the fastest at all of them (bn64 / bn128 / pair, us: 64 x 8192 x
+// 4096 MXFP4 6.8 7.0 9.0, 512 x 4096 x 4096 11.0 7.8 9.3, 768 x 4096 x 4096 15.2 12.0 10.1, 8192 x 4096 x 2048 65 42
+// 28.9, 1500 x 3000 x 2000 19 14 10.5; split in two or four 1 x 4096 x 4096 takes 6.0 and 5.6 instead of 6.5, 64 x 4096 x
+// 4096 6.4 and 9.9 instead of 6.5, 128 x 2048 x 8192 8.8 and 10.4 instead of 10.1, 128 x 1024 x 14336 11.5 and 10.0
+// instead of 15.6). KB: 256-element stages of K.
 //   128 x 64, 128 x 128    a launch, 700 a tile and 270 .. 300 a stage
 //   split over S CTAs      KB / S stages; joining: 1100 (1600 for tiles of more than 64 rows), and a fifth of a ns for
 //                          each fp32 value that is sent
-//   256 x 256 on a pair    1050 a tile and 306 a stage, or 1000 and 290 with two pairs in a cluster (36 clusters of
-//                          four fit on 152 SMs, 76 of two)
+//   256 x 256 on a pair    1050 a tile and 306 a stage, two SMs a tile
 struct Plan {
-  int pairs;  // 0: this file's kernel, with bn and S
+  bool pair;  // mxpair.cu's kernel; else this file's, with bn and S
   int bn, S;
 };
 Plan pick_plan(int M, int N, int KB, int nsm) {
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  Plan best{0, 128, 1};
+  Plan best{false, 128, 1};
   int64_t best_ns = INT64_MAX;
   auto offer = [&](Plan p, int64_t ns) {
     if (ns < best_ns) {
@@ -438,19 +437,14 @@ Plan pick_plan(int M, int N, int KB, int nsm) {
   for (int bn : {64, 128}) {
     const int64_t tiles = up(M, DBM) * up(N, bn), stage = bn == 128 && M > 64 ? 300 : 270;
     const int64_t launch = bn == 64 ? 1700 : 1800;
-    offer({0, bn, 1}, launch + up(tiles, nsm) * (KB * stage + 700));
+    offer({false, bn, 1}, launch + up(tiles, nsm) * (KB * stage + 700));
     if (M > 64 && bn == 128) continue;  // such partial tiles cost more to join than the split saves
     const int64_t rows = std::min(M, DBM), join = M > 64 ? 1600 : 1100;
     for (int S : {2, 4})  // a cluster of four leaves an eighteenth of the SMs without one
       if (S <= KB && tiles * S <= (S == 2 ? nsm : nsm - nsm / 18))
-        offer({0, bn, S}, launch + 700 + up(KB, S) * stage + join + (S - 1) * rows * bn / 5);
+        offer({false, bn, S}, launch + 700 + up(KB, S) * stage + join + (S - 1) * rows * bn / 5);
   }
-  for (int pairs : {1, 2}) {
-    const int64_t tiles = up(M, 256 * pairs) * up(N, 256);
-    const int64_t clusters = pairs == 1 ? nsm / 2 : (nsm - nsm / 18) / 4;
-    if (clusters > 0)
-      offer({pairs, 0, 1}, 3600 + up(tiles, clusters) * (pairs == 1 ? KB * 306 + 1050 : KB * 290 + 1000));
-  }
+  offer({true, 256, 1}, 3600 + up(up(M, 256) * up(N, 256), std::max(1, nsm / 2)) * ((int64_t)KB * 306 + 1050));
   return best;
 }
 
@@ -524,7 +518,7 @@ fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t 
   const int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
   const Plan plan = pick_plan(M, N, prm.KB, nsm);
-  if (plan.pairs > 0) return mx_pair_launch(format, dtype, plan.pairs, prm, a, a_sf, b, b_sf, st);
+  if (plan.pair) return mx_pair_launch(format, dtype, prm, a, a_sf, b, b_sf, st);
   return format == FP4MOE_W_MXFP4 ? dense_width<FP4MOE_W_MXFP4>(plan.bn, dtype, prm, plan.S, a, a_sf, b, b_sf, nsm, st)
                                   : dense_width<FP4MOE_W_NVFP4>(plan.bn, dtype, prm, plan.S, a, a_sf, b, b_sf, nsm, st);
 }

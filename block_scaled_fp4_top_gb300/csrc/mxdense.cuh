@@ -7,7 +7,8 @@
 namespace fp4moe {
 
 bool encode_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint32_t box_rows);
-bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles);
+bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t row_tiles, uint64_t col_tiles, uint32_t box_rows,
+                        uint32_t box_cols);
 
 constexpr int DK = 256;  // K elements per ring stage: 128 bytes of codes, 4 MMAs of K = 64
 
@@ -152,8 +153,8 @@ __device__ __forceinline__ void store_chunk(uint8_t* stage, const uint32_t* w, T
   __syncwarp();
 }
 
-// mxpair.cu: 256 x 256 tiles on CTA pairs, pairs (1 or 2) of them in a cluster. prm.mt and prm.nt are set there.
-fp4moe_status mx_pair_launch(int32_t format, int32_t dtype, int pairs, const DenseParams& prm, const uint8_t* a,
+// mxpair.cu: 256 x 256 tiles on CTA pairs. prm.mt and prm.nt are set there.
+fp4moe_status mx_pair_launch(int32_t format, int32_t dtype, const DenseParams& prm, const uint8_t* a,
                              const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, cudaStream_t st);
 
 }  // namespace fp4moe

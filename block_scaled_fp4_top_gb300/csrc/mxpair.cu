@@ -6,25 +6,22 @@
 // and reads per MAC: those tiles need 12 KB through shared memory twice (in by TMA, out to the MMA) every 128
 // cycles, more than its 128 bytes a cycle.
 //   warps 0-7   epilogue, in both CTAs (warp w: TMEM lanes 32 (w % 4) .., columns 128 (w / 4) ..).
-//   warp 8      producer, in both CTAs: its own rows of A and B, the scale tiles of its own A rows, and those of its B
-//               rows for both CTAs by multicast (the MMA reads the scales of all 256 B rows from each CTA's own TMEM).
-//               All loads signal the leader's barrier.
+//   warp 8      producer, in both CTAs: its own rows of A and B, the scale tiles of its own A rows, and those of all 256
+//               B rows (the MMA reads the scales of all 256 B rows from each CTA's own TMEM). All loads signal the
+//               leader's barrier. Each CTA loads what it needs itself: the library also runs as replicas on several
+//               GPUs, and a load that writes into several CTAs is kept out of it.
 //   warp 9      leader: scale copies (tcgen05.cp.cta_group::2, each CTA's tiles into its own TMEM) and MMAs.
 // Commits that free a ring stage or hand over the accumulator arrive in both CTAs, and all sixteen epilogue warps tell
 // the leader that the accumulator is empty.
 //
-// PAIRS = 2: a cluster of two pairs owns 512 x 256. Both pairs need the same B, so each CTA loads half of its B rows
-// and a quarter of the B scales and multicasts them to the CTAs that need them: 25 instead of 34 KB per CTA and
-// stage out of L2. A stage is then free when both pairs' MMAs have read it. Fewer bytes, but only 144 of the 152 SMs
-// have a place in a cluster of four: 9216 x 4096 x 4096 MXFP4 takes 48.8 instead of 50.1 us (eight rounds of tiles
-// either way), 8192 x 4096 x 4096 47.3 instead of 45.1 (eight against seven).
-//
-// 8192 x 4096 x 4096: MXFP4 44.8 us, 6.1 PFLOP/s of the 9.4 that the MMAs reach alone, NVFP4 48.1; 8192^3 152 us, 7.2.
-// Bounds: operands from L2 (34 KB a stage and SM, 600 cycles for MMAs of 512; five ring stages 48 us, four 51; the B
-// scales loaded by both CTAs 46.4 instead of 45.0), and 1000 ns between the last MMA of a tile and the first of the
-// next, in which the epilogue empties TMEM: two accumulators of 256 columns and the scales do not fit its 512. Not
-// faster: the output by TMA from shared memory (45.0 and 46.9, but 8192 x 8192 x 2048 57 instead of 53), all 128
-// columns of an epilogue warp in flight at once (spills, 53), a stage's scale copies ahead of the MMAs before it (50).
+// 8192 x 4096 x 4096: MXFP4 45.2 us, 6.1 PFLOP/s of the 9.4 that the MMAs reach alone with K = 64, NVFP4 47.8; 8192^3
+// 154.6 us, 7.1. The scales of both halves of B are one load of a 3-D map: with a load for each a stage takes 16 ns more
+// (46.3, 51.2 and 161 us). What bounds it: a stage of 306 ns, 600 cycles, for MMAs of 512, in which 34 KB enter the SM
+// (a quarter fewer of them out of L2 made a stage 5 % faster; five ring stages instead of six 48 us, four 51), and
+// 1000 ns between the last MMA of a tile and the first of the next, in which the epilogue empties TMEM: two accumulators
+// of 256 columns and the scales do not fit its 512. Not faster: the output by TMA from shared memory (45.0 and 46.9, but
+// 8192 x 8192 x 2048 57 instead of 53), all 128 columns of an epilogue warp in flight at once (spills, 53), a stage's
+// scale copies ahead of the MMAs before it (50).
 // The rest (scale-factor ids, K tails, bounded waits) is as in mxdense.cu.
 #include <mutex>
 
@@ -67,13 +64,13 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "l"(policy)
       : "memory");
 }
-// The copy lands at `dst` in every CTA of `mask`, and signals `bar`'s offset in the leader of each one's pair.
-__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                                           int32_t x, int32_t y, uint16_t mask, uint64_t policy) {
+// Scale tiles [z ..][y ..] of a 3-D map.
+__device__ __forceinline__ void tma_load_scales_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t y,
+                                                     int32_t z, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
-      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint [%0], "
+      "[%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(0), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -88,11 +85,11 @@ __device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// The same on the barrier at this offset in every CTA of `mask`.
-__device__ __forceinline__ void pair_commit_to(uint32_t bar, uint16_t mask) {
+// The same on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void pair_commit_both(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
+      "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ void pair_cp_scales(uint32_t taddr, uint64_t sdesc) {
@@ -125,7 +122,7 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
   n = in / rows;
 }
 
-template <int FMT, int PAIRS, typename T>
+template <int FMT, typename T>
 __global__ void __launch_bounds__(PTHREADS, 1)
     mx_pair_kernel(const __grid_constant__ DenseMaps maps, const DenseParams prm) {
   using C = PairCfg<FMT>;
@@ -134,11 +131,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + C::kBarOff + 244);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, pair = crank >> 1, lead = crank & ~1u;
-  constexpr uint16_t kAll = (uint16_t)((1 << (2 * PAIRS)) - 1);
+  const uint32_t rank = cluster_ctarank();
   const uint32_t smem = smem_u32(smem_raw);
   const uint32_t bar_full = smem + C::kBarOff;           // leader's: both CTAs' copies of a stage
-  const uint32_t bar_empty = bar_full + 8 * C::kStages;  // each CTA's own: every pair's MMAs have read the stage
+  const uint32_t bar_empty = bar_full + 8 * C::kStages;  // each CTA's own: the pair's MMAs have read the stage
   const uint32_t bar_tfull = bar_empty + 8 * C::kStages; // each CTA's own: the accumulator is complete
   const uint32_t bar_tempty = bar_tfull + 8;             // leader's: both CTAs' epilogue warps have read it
   const uint32_t bar_drain = bar_tempty + 8;
@@ -147,7 +143,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   if (threadIdx.x == 32 * PPRODUCER) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, PAIRS);
+      mbar_init(bar_empty + 8 * s, 1);
     }
     mbar_init(bar_tfull, 1);
     mbar_init(bar_tempty, 2 * PEPI);
@@ -168,17 +164,17 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
   const int tiles = s_abort ? 0 : prm.mt * prm.nt;  // an earlier timeout poisons the call
-  const int KB = prm.KB, clusters = gridDim.x / (2 * PAIRS), cluster = blockIdx.x / (2 * PAIRS);
+  const int KB = prm.KB, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
   if (warp == PPRODUCER && lane == 0) {
     const uint64_t pol = policy_evict_normal();
-    const uint32_t full0 = map_cluster(bar_full, lead);
+    const uint32_t full0 = map_cluster(bar_full, 0);
     int it = 0;
     bool ok = true;
-    for (int t = cluster; ok && t < tiles; t += clusters) {
+    for (int t = pair; ok && t < tiles; t += pairs) {
       int m, n;
       tile_of(t, prm.mt, prm.nt, m, n);
-      const int ar = 2 * (PAIRS * m + (int)pair) + (int)rank;  // 128-row tile of A
+      const int ar = 2 * m + (int)rank, br = 2 * n;  // 128-row tiles of A, of B
       for (int kb = 0; kb < KB; ++kb, ++it) {
         const int s = it % C::kStages;
         if (!mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / C::kStages) & 1u) ^ 1u, prm.err)) {
@@ -188,25 +184,18 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         const uint32_t st = smem + s * C::kStage, full = full0 + 8 * s, sf = st + C::kA + C::kB;
         if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * C::kBytes);
         tma_load_2d_pair(st, &maps.a, full, kb * 128, ar * 128, pol);
-        tma_load_2d_pair(sf, &maps.sfa, full, 0, ar * prm.ct + kb * C::kSfTiles, pol);
-        if constexpr (PAIRS == 1)
-          tma_load_2d_pair(st + C::kA, &maps.b, full, kb * 128, (2 * n + (int)rank) * 128, pol);
-        else  // rows 64 pair .. of this rank's 128 B rows, for this rank of both pairs
-          tma_load_2d_pair_multicast(st + C::kA + pair * 8192u, &maps.b, full, kb * 128,
-                                     (2 * n + (int)rank) * 128 + 64 * (int)pair, (uint16_t)(5u << rank), pol);
-        // this CTA's share of the scale tiles of B rows 128 rank .., for every CTA
-        constexpr int Q = C::kSfTiles / PAIRS;
-        tma_load_2d_pair_multicast(sf + C::kSfa * (1 + rank) + 512u * Q * pair, &maps.sfb, full, 0,
-                                   (2 * n + (int)rank) * prm.ct + kb * C::kSfTiles + Q * (int)pair, kAll, pol);
+        tma_load_scales_pair(sf, &maps.sfa, full, kb * C::kSfTiles, ar, pol);
+        tma_load_2d_pair(st + C::kA, &maps.b, full, kb * 128, (br + (int)rank) * 128, pol);
+        tma_load_scales_pair(sf + C::kSfa, &maps.sfb, full, kb * C::kSfTiles, br, pol);  // rows br and br + 1
       }
     }
-    // Let the copies already issued land before the CTA exits. A leader's barrier counts every copy into its
+    // Let the copies already issued land before the CTA exits. The leader's barrier counts every copy into the
     // pair. A CTA that gave up may have issued some that no leader armed: it leaves them time to land.
     if (rank == 0) {
       for (int j = max(0, it - C::kStages); j < it; ++j)
         drain_wait(bar_full + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
     }
-    if (ok) {  // and the signals of every pair that they have been used
+    if (ok) {  // and the signals that they have been used
       for (int j = max(0, it - C::kStages); j < it; ++j)
         drain_wait(bar_empty + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
     }
@@ -216,7 +205,6 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     }
   } else if (warp == PMMA && rank == 0) {
     const bool leader = elect_one();
-    const uint16_t own = (uint16_t)(3u << lead);
     int tl = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -227,7 +215,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
                     idesc_mx<FMT>(PBM, PBN, mx ? 2 * (a & 1) : 0), slot + 4 * tile, slot + 4 * C::kSfTiles + 8 * tile,
                     acc);
     };
-    for (int t = cluster; ok && t < tiles; t += clusters, ++tl) {
+    for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
       // both epilogues have moved the previous tile's accumulator out of TMEM
       const uint32_t tph = ((uint32_t)tl & 1u) ^ 1u;
       if (!mbar_wait_warp(bar_tempty, tph, prm.err)) break;
@@ -260,7 +248,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
             for (int a = 0; a < 3; ++a)
               if (a < atoms) mma(ad, bd, slot, a, (kb > 0 || a > 0) ? 1u : 0u);
           }
-          pair_commit_to(bar_empty + 8 * s, kAll);
+          pair_commit_both(bar_empty + 8 * s);
         }
         __syncwarp();
         if (++s == C::kStages) {
@@ -268,7 +256,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           ph ^= 1u;
         }
       }
-      if (ok && leader) pair_commit_to(bar_tfull, own);
+      if (ok && leader) pair_commit_both(bar_tfull);
     }
     if (leader) {
       pair_commit(bar_drain);
@@ -281,13 +269,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     // Arrivals here publish no memory writes: what they order are TMEM reads, complete at the arriving warp's
     // tcgen05.wait::ld, with the tcgen05 fences of both sides. A release at cluster scope and a fence at the other end
     // cost 1.1 us a tile.
-    const uint32_t tempty = map_cluster(bar_tempty, lead);
+    const uint32_t tempty = map_cluster(bar_tempty, 0);
     const float alpha = prm.alpha != nullptr ? __ldg(prm.alpha) : 1.0f;
     int tl = 0;
-    for (int t = cluster; t < tiles; t += clusters, ++tl) {
+    for (int t = pair; t < tiles; t += pairs, ++tl) {
       int m, n;
       tile_of(t, prm.mt, prm.nt, m, n);
-      const int r0 = (PAIRS * m + (int)pair) * PBM + (int)rank * 128 + quarter * 32;
+      const int r0 = m * PBM + (int)rank * 128 + quarter * 32;
       const int c0 = n * PBN + W * half;
       // the whole warp takes one decision: tcgen05.ld is warp-collective
       if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) break;
@@ -318,15 +306,14 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 }
 
 // The cluster shape's launch attributes; PDL as in launch_pdl.
-template <int PAIRS>
-cudaLaunchConfig_t pair_config(unsigned clusters, size_t smem, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
+cudaLaunchConfig_t pair_config(unsigned pairs, size_t smem, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(2u * PAIRS * clusters);
+  lc.gridDim = dim3(2u * pairs);
   lc.blockDim = dim3(PTHREADS);
   lc.dynamicSmemBytes = smem;
   lc.stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * PAIRS;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -336,9 +323,9 @@ cudaLaunchConfig_t pair_config(unsigned clusters, size_t smem, cudaStream_t st, 
   return lc;
 }
 
-// Clusters that the device holds at once (the persistent grid); 0 on error. Cached per device.
-template <int FMT, int PAIRS, typename T>
-int pair_clusters() {
+// Pairs that the device holds at once (the persistent grid); 0 on error. Cached per device.
+template <int FMT, typename T>
+int pair_count() {
   constexpr int kMaxDevices = 64;
   static std::once_flag once[kMaxDevices];
   static int count[kMaxDevices];
@@ -347,60 +334,57 @@ int pair_clusters() {
   std::call_once(once[dev], [dev] {
     int n = 0;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t lc = pair_config<PAIRS>(1, PairCfg<FMT>::kSmem, nullptr, attr);
+    cudaLaunchConfig_t lc = pair_config(1, PairCfg<FMT>::kSmem, nullptr, attr);
     lc.numAttrs = 1;  // the cluster shape alone
-    if (cudaFuncSetAttribute(mx_pair_kernel<FMT, PAIRS, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(mx_pair_kernel<FMT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PairCfg<FMT>::kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<FMT, PAIRS, T>, &lc) != cudaSuccess)
+        cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<FMT, T>, &lc) != cudaSuccess)
       n = 0;
     count[dev] = n;
   });
   return count[dev];
 }
 
-template <int FMT, int PAIRS, typename T>
+template <int FMT, typename T>
 fp4moe_status pair_run(DenseParams prm, const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
                        cudaStream_t st) {
   using C = PairCfg<FMT>;
-  prm.mt = (prm.M + PAIRS * PBM - 1) / (PAIRS * PBM);
+  prm.mt = (prm.M + PBM - 1) / PBM;
   prm.nt = (prm.N + PBN - 1) / PBN;
   DenseMaps maps;
   const uint64_t rb = (uint64_t)mx_row_bytes(prm.K);
   if (!encode_u8_sw128(&maps.a, a, rb, (uint64_t)prm.M, 128) ||
-      !encode_u8_sw128(&maps.b, b, rb, (uint64_t)prm.N, 128 / PAIRS) ||
-      !encode_scale_tiles(&maps.sfa, a_sf, (uint64_t)mx_row_tiles(prm.M) * prm.ct, C::kSfTiles) ||
-      !encode_scale_tiles(&maps.sfb, b_sf, (uint64_t)mx_row_tiles(prm.N) * prm.ct, C::kSfTiles / PAIRS))
+      !encode_u8_sw128(&maps.b, b, rb, (uint64_t)prm.N, 128) ||
+      !encode_scale_tiles(&maps.sfa, a_sf, (uint64_t)mx_row_tiles(prm.M), (uint64_t)prm.ct, 1, C::kSfTiles) ||
+      !encode_scale_tiles(&maps.sfb, b_sf, (uint64_t)mx_row_tiles(prm.N), (uint64_t)prm.ct, 2, C::kSfTiles))
     return FP4MOE_CUDA_ERROR;
-  const int most = pair_clusters<FMT, PAIRS, T>(), tiles = prm.mt * prm.nt;
+  const int most = pair_count<FMT, T>(), tiles = prm.mt * prm.nt;
   if (most <= 0) return FP4MOE_CUDA_ERROR;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t lc = pair_config<PAIRS>((unsigned)(tiles < most ? tiles : most), C::kSmem, st, attr);
-  return cudaLaunchKernelEx(&lc, mx_pair_kernel<FMT, PAIRS, T>, maps, prm) == cudaSuccess ? FP4MOE_OK
+  const cudaLaunchConfig_t lc = pair_config((unsigned)(tiles < most ? tiles : most), C::kSmem, st, attr);
+  return cudaLaunchKernelEx(&lc, mx_pair_kernel<FMT, T>, maps, prm) == cudaSuccess ? FP4MOE_OK
                                                                                         : FP4MOE_CUDA_ERROR;
 }
 
 template <int FMT>
-fp4moe_status pair_typed(int32_t dtype, int pairs, const DenseParams& prm, const uint8_t* a, const uint8_t* a_sf,
+fp4moe_status pair_typed(int32_t dtype, const DenseParams& prm, const uint8_t* a, const uint8_t* a_sf,
                          const uint8_t* b, const uint8_t* b_sf, cudaStream_t st) {
   switch (dtype) {
     case FP4MOE_BF16:
-      return pairs == 2 ? pair_run<FMT, 2, __nv_bfloat16>(prm, a, a_sf, b, b_sf, st)
-                        : pair_run<FMT, 1, __nv_bfloat16>(prm, a, a_sf, b, b_sf, st);
+      return pair_run<FMT, __nv_bfloat16>(prm, a, a_sf, b, b_sf, st);
     case FP4MOE_FP16:
-      return pairs == 2 ? pair_run<FMT, 2, __half>(prm, a, a_sf, b, b_sf, st)
-                        : pair_run<FMT, 1, __half>(prm, a, a_sf, b, b_sf, st);
+      return pair_run<FMT, __half>(prm, a, a_sf, b, b_sf, st);
     default:
-      return pairs == 2 ? pair_run<FMT, 2, float>(prm, a, a_sf, b, b_sf, st)
-                        : pair_run<FMT, 1, float>(prm, a, a_sf, b, b_sf, st);
+      return pair_run<FMT, float>(prm, a, a_sf, b, b_sf, st);
   }
 }
 
 }  // namespace
 
-fp4moe_status mx_pair_launch(int32_t format, int32_t dtype, int pairs, const DenseParams& prm, const uint8_t* a,
+fp4moe_status mx_pair_launch(int32_t format, int32_t dtype, const DenseParams& prm, const uint8_t* a,
                              const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, cudaStream_t st) {
-  return format == FP4MOE_W_MXFP4 ? pair_typed<FP4MOE_W_MXFP4>(dtype, pairs, prm, a, a_sf, b, b_sf, st)
-                                  : pair_typed<FP4MOE_W_NVFP4>(dtype, pairs, prm, a, a_sf, b, b_sf, st);
+  return format == FP4MOE_W_MXFP4 ? pair_typed<FP4MOE_W_MXFP4>(dtype, prm, a, a_sf, b, b_sf, st)
+                                  : pair_typed<FP4MOE_W_NVFP4>(dtype, prm, a, a_sf, b, b_sf, st);
 }
 
 }  // namespace fp4moe

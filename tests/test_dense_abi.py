@@ -167,3 +167,19 @@ def test_binding_refuses_wrong_shapes_and_types():
         api.fp4moe_mx_gemm(MX, 100, codes, sf, codes, sf, None, z(4, 4), err)
     with pytest.raises(E):
         api.fp4moe_mx_quantize(MX, x, None, codes, sf)
+
+
+def test_no_load_writes_into_several_ctas():
+    """The library also runs as replicas on several GPUs, where a bulk or tensor load that writes into more than one CTA
+    of a cluster must not be part of it. (A commit that signals two CTAs' barriers is no load.)"""
+    import os
+    import re
+    from helpers import ROOT
+    load = re.compile(r"\bcp\.(?:reduce\.)?async\.bulk[^;\[]*" + "multi" + "cast")
+    csrc = os.path.join(ROOT, "block_scaled_fp4_top_gb300", "csrc")
+    names = [n for n in sorted(os.listdir(csrc)) if n.endswith((".cu", ".cuh", ".h"))]
+    assert len(names) > 10
+    for name in names:
+        with open(os.path.join(csrc, name)) as f:
+            text = re.sub(r'"\s*\n\s*"', "", f.read())  # adjacent string literals are one instruction
+        assert not load.search(text), name

@@ -594,3 +594,36 @@ def test_gemm_under_an_error_word_that_is_raised_while_it_runs(M, N, K):
         call()
         torch.cuda.synchronize()
         assert int(err[0]) == 0 and torch.equal(ob.t, want)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(9216, 4096, 1000), (2049, 3841, 4097)])
+def test_gemm_large_tiles_with_every_scale_row(fmt, dtype, M, N, K):
+    """Scales that differ from row to row across both halves of a 256 x 256 tile, and tile rows past the matrices."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    gen = torch.Generator("cuda").manual_seed(K)
+    sides = []
+    for rows in (M, N):
+        x = torch.randn(rows, K, generator=gen, device="cuda") * torch.exp2(torch.arange(rows, device="cuda") % 9 - 4.0)[:, None]
+        c, s = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in api.fp4moe_mx_bytes(fmt, rows, K))
+        gs = torch.full((1,), 8.0, device="cuda")
+        api.fp4moe_mx_quantize(fmt, x, gs, c, s)
+        v = torch.empty(rows, K, device="cuda")
+        one = torch.ones(1, device="cuda")
+        api.fp4moe_mx_dequantize(fmt, c, s, one, v)                   # exact in fp32: tested on its own
+        sides.append((c, s, v))
+    (a, asf, av), (b, bsf, bv) = sides
+    out = Guarded((M, N), getattr(torch, dtype))
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    al = torch.tensor([2.0 ** -6 if fmt == NV else 1.0], device="cuda")
+    api.fp4moe_mx_gemm(fmt, K, a, asf, b, bsf, al, out.t, err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    out.check()
+    pick = torch.unique(torch.tensor([*range(0, M, 61), 127, 128, 255, 256, 383, 384, M - 1], device="cuda"))
+    ap, bp = av[pick].double(), bv.double()
+    ref = (ap @ bp.T * al.double()).cpu().numpy()
+    mag = (ap.abs() @ bp.abs().T * al.double()).cpu().numpy()
+    hold_product(f64(out.t[pick]), ref, mag, K, dtype)
