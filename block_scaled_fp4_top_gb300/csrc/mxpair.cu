@@ -47,12 +47,12 @@ struct PairCfg {
   static constexpr int kStages = FMT == FP4MOE_W_MXFP4 ? 6 : 5;
   static constexpr int kEpiOff = kStages * kStage;  // the epilogue warps' staging areas
   static constexpr int kBarOff = kEpiOff + PEPI * kEpiStage;
-  static constexpr int kSmem = kBarOff + 256;  // barriers, and two words of the CTA
+  static constexpr int kSmem = kBarOff + 256;  // barriers, and a few words of the CTA
   static constexpr uint32_t kSlotCols = 4 * kSfTiles * 3;
   static_assert(kStage % 1024 == 0, "stage must keep 1024-byte alignment");
   static_assert(PBN + kSlotCols * kStages <= PTMEM_COLS, "accumulator and scale slots fit TMEM");
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(8 * (2 * kStages + 3) <= 240, "barriers fit their area");
+  static_assert(8 * (2 * kStages + 3) <= 224, "barriers fit their area");
 };
 
 // ------------------------------------------------------------- PTX, CTA pairs
@@ -113,6 +113,16 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t adesc, uint64_t bd
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
+// A word of another CTA of the cluster (an address from map_cluster), ordered by the cluster's barrier.
+__device__ __forceinline__ void st_cluster_u32(uint32_t caddr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
+  return v;
+}
+
 // Tile t: groups of 4 tile rows, so that the tiles of a wave share their operands' rows in L2 (8192 x 4096 x 4096
 // MXFP4 44.7 us; groups of 8 45.0, 16 45.3, 32 46.4).
 __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
@@ -129,6 +139,12 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // all of the CTA's shared memory: no static part shifts it
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(smem_raw + C::kBarOff + 240);
   uint32_t& s_abort = *reinterpret_cast<uint32_t*>(smem_raw + C::kBarOff + 244);
+  // What the CTAs of a pair tell each other at the end: that one gave up (set in both), the ring stages that this CTA's
+  // producer has loaded, the stages and tiles that the leader has committed.
+  volatile uint32_t* const s_gave_up = reinterpret_cast<uint32_t*>(smem_raw + C::kBarOff + 224);
+  volatile int* const s_loaded = reinterpret_cast<int*>(smem_raw + C::kBarOff + 228);
+  volatile int* const s_used = reinterpret_cast<int*>(smem_raw + C::kBarOff + 232);
+  volatile int* const s_tiles = reinterpret_cast<int*>(smem_raw + C::kBarOff + 236);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -158,6 +174,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       raise_error(prm.err, FP4MOE_ERR_CAPACITY);
       s_abort = 1u;
     }
+    *s_gave_up = 0u;
   }
   tc_fence_before();
   cluster_sync();  // barriers and TMEM of all CTAs are ready
@@ -166,46 +183,46 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   const int tiles = s_abort ? 0 : prm.mt * prm.nt;  // an earlier timeout poisons the call
   const int KB = prm.KB, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
+  const uint32_t far_end = map_cluster(smem + C::kBarOff, rank ^ 1u);  // the words above in the other CTA
+  auto give_up = [&]() {
+    *s_gave_up = 1u;
+    st_cluster_u32(far_end + 224, 1u);
+  };
+  // this CTA's loads of stage kb of tile (m, n), the it-th that it loads
+  const uint32_t full0 = map_cluster(bar_full, 0);
+  auto load_stage = [&](int it, int m, int n, int kb, uint64_t pol) {
+    const int s = it % C::kStages, ar = 2 * m + (int)rank, br = 2 * n;  // 128-row tiles of A, of B
+    const uint32_t st = smem + s * C::kStage, full = full0 + 8 * s, sf = st + C::kA + C::kB;
+    if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * C::kBytes);
+    tma_load_2d_pair(st, &maps.a, full, kb * 128, ar * 128, pol);
+    tma_load_scales_pair(sf, &maps.sfa, full, kb * C::kSfTiles, ar, pol);
+    tma_load_2d_pair(st + C::kA, &maps.b, full, kb * 128, (br + (int)rank) * 128, pol);
+    tma_load_scales_pair(sf + C::kSfa, &maps.sfb, full, kb * C::kSfTiles, br, pol);  // rows br and br + 1
+  };
+
   if (warp == PPRODUCER && lane == 0) {
     const uint64_t pol = policy_evict_normal();
-    const uint32_t full0 = map_cluster(bar_full, 0);
     int it = 0;
-    bool ok = true;
+    bool ok = s_abort == 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
       int m, n;
       tile_of(t, prm.mt, prm.nt, m, n);
-      const int ar = 2 * m + (int)rank, br = 2 * n;  // 128-row tiles of A, of B
       for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int s = it % C::kStages;
-        if (!mbar_wait(bar_empty + 8 * s, ((uint32_t)(it / C::kStages) & 1u) ^ 1u, prm.err)) {
+        if (!mbar_wait(bar_empty + 8 * (it % C::kStages), ((uint32_t)(it / C::kStages) & 1u) ^ 1u, prm.err)) {
           ok = false;
           break;
         }
-        const uint32_t st = smem + s * C::kStage, full = full0 + 8 * s, sf = st + C::kA + C::kB;
-        if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * s, 2 * C::kBytes);
-        tma_load_2d_pair(st, &maps.a, full, kb * 128, ar * 128, pol);
-        tma_load_scales_pair(sf, &maps.sfa, full, kb * C::kSfTiles, ar, pol);
-        tma_load_2d_pair(st + C::kA, &maps.b, full, kb * 128, (br + (int)rank) * 128, pol);
-        tma_load_scales_pair(sf + C::kSfa, &maps.sfb, full, kb * C::kSfTiles, br, pol);  // rows br and br + 1
+        load_stage(it, m, n, kb, pol);
       }
     }
-    // Let the copies already issued land before the CTA exits. The leader's barrier counts every copy into the
-    // pair. A CTA that gave up may have issued some that no leader armed: it leaves them time to land.
-    if (rank == 0) {
-      for (int j = max(0, it - C::kStages); j < it; ++j)
-        drain_wait(bar_full + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
-    }
-    if (ok) {  // and the signals that they have been used
-      for (int j = max(0, it - C::kStages); j < it; ++j)
-        drain_wait(bar_empty + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
-    }
-    if (!ok) {
-      for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
-      }
-    }
+    // the signals that the last stages have been used, and so loaded, are in before the CTA leaves
+    for (int j = max(0, it - C::kStages); ok && j < it; ++j)
+      ok = mbar_wait(bar_empty + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u, prm.err);
+    *s_loaded = it;
+    if (!ok) give_up();
   } else if (warp == PMMA && rank == 0) {
     const bool leader = elect_one();
-    int tl = 0, s = 0;
+    int tl = 0, s = 0, used = 0;
     uint32_t ph = 0;
     bool ok = true;
     auto mma = [&](uint64_t adesc, uint64_t bdesc, uint32_t slot, int a, uint32_t acc) {
@@ -215,12 +232,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
                     idesc_mx<FMT>(PBM, PBN, mx ? 2 * (a & 1) : 0), slot + 4 * tile, slot + 4 * C::kSfTiles + 8 * tile,
                     acc);
     };
-    for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
+    for (int t = pair; t < tiles; t += pairs, ++tl) {
       // both epilogues have moved the previous tile's accumulator out of TMEM
       const uint32_t tph = ((uint32_t)tl & 1u) ^ 1u;
-      if (!mbar_wait_warp(bar_tempty, tph, prm.err)) break;
+      ok = mbar_wait_warp(bar_tempty, tph, prm.err);
+      if (!ok) break;
       tc_fence_after();
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb = 0; kb < KB; ++kb, ++used) {
         if (!mbar_wait_warp(bar_full + 8 * s, ph, prm.err)) {
           ok = false;
           break;
@@ -256,9 +274,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           ph ^= 1u;
         }
       }
-      if (ok && leader) pair_commit_both(bar_tfull);
+      if (!ok) break;
+      if (leader) pair_commit_both(bar_tfull);
     }
     if (leader) {
+      *s_used = used;
+      *s_tiles = tl;
+      if (!ok) give_up();
       pair_commit(bar_drain);
       drain_wait(bar_drain, 0);  // no MMA may still write TMEM when it is freed
     }
@@ -278,7 +300,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const int r0 = m * PBM + (int)rank * 128 + quarter * 32;
       const int c0 = n * PBN + W * half;
       // the whole warp takes one decision: tcgen05.ld is warp-collective
-      if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) break;
+      if (!mbar_wait_warp(bar_tfull, (uint32_t)tl & 1u, prm.err)) {
+        if (lane == 0) give_up();
+        break;
+      }
       tc_fence_after();
       const bool live = r0 < prm.M && c0 < prm.N;
       uint32_t w[W * sizeof(T) / 4];
@@ -298,7 +323,32 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   }
   __syncwarp();  // the single-thread roles reconverge: cluster barriers are warp-aligned instructions
   tc_fence_before();
-  cluster_sync();  // no CTA reads or signals another any more
+  cluster_sync();  // no CTA reads or signals another any more, unless one gave up
+  if (*s_gave_up != 0) {
+    // All that is in flight lands before either CTA leaves. The leader's barrier for a stage counts the loads of both
+    // CTAs, so the one whose producer stopped first loads what the other has loaded already (into stages that no MMA
+    // reads any more, at most a ring's worth); and commits signal both CTAs.
+    if (warp == PPRODUCER && lane == 0) {
+      const int other = (int)ld_cluster_u32(far_end + 228);
+      const int mine = *s_loaded, loaded = max(mine, other);
+      for (int j = mine; j < loaded; ++j) {
+        int m, n;
+        tile_of(pair + j / KB * pairs, prm.mt, prm.nt, m, n);
+        load_stage(j, m, n, j % KB, policy_evict_normal());
+      }
+      if (rank == 0) {
+        for (int j = max(0, loaded - C::kStages); j < loaded; ++j)
+          drain_wait(bar_full + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
+      }
+      const int used = rank == 0 ? *s_used : (int)ld_cluster_u32(far_end + 232);
+      const int done = rank == 0 ? *s_tiles : (int)ld_cluster_u32(far_end + 236);
+      for (int j = max(0, used - C::kStages); j < used; ++j)
+        drain_wait(bar_empty + 8 * (j % C::kStages), (uint32_t)(j / C::kStages) & 1u);
+      if (done > 0) drain_wait(bar_tfull, (uint32_t)(done - 1) & 1u);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 0) {
     tc_fence_after();
     pair_tmem_dealloc(tmem, PTMEM_COLS);

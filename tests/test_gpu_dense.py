@@ -627,3 +627,32 @@ def test_gemm_large_tiles_with_every_scale_row(fmt, dtype, M, N, K):
     ref = (ap @ bp.T * al.double()).cpu().numpy()
     mag = (ap.abs() @ bp.abs().T * al.double()).cpu().numpy()
     hold_product(f64(out.t[pick]), ref, mag, K, dtype)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("M,N,K", [(1025, 3001, 2100), (2000, 3600, 520)])
+def test_gemm_on_pairs_under_a_raised_error_word(fmt, M, N, K):
+    import torch
+    from block_scaled_fp4_top_gb300 import _lib, api
+    ops = gemm_operands(fmt, M, N, K, 5)
+    a, asf, _, b, bsf, _ = ops
+    want = check_gemm(fmt, M, N, K, "float32", operands=ops).clone()
+    ob = Guarded((M, N), torch.float32)
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        ob.t.fill_(7.0)
+        err[0] = _lib.ERR_TIMEOUT
+        for _ in range(3):
+            api.fp4moe_mx_gemm(fmt, K, a, asf, b, bsf, None, ob.t, err)
+        torch.cuda.synchronize()
+        assert (ob.t == 7.0).all() and api.fp4moe_read_error(err) == _lib.ERR_TIMEOUT
+        api.fp4moe_mx_gemm(fmt, K, a, asf, b, bsf, None, ob.t, err)
+        torch.cuda.synchronize()
+        assert int(err[0]) == 0 and torch.equal(ob.t, want)
+        ob.check()
+
+
+@pytest.mark.parametrize("M,N,K", [(1025, 3001, 2100), (2048, 4096, 2048), (2000, 3600, 520)])
+def test_gemm_on_pairs_under_an_error_word_that_is_raised_while_it_runs(M, N, K):
+    """The two CTAs of a pair may see it at different stages. Each call ends, and leaves nothing to the next one."""
+    test_gemm_under_an_error_word_that_is_raised_while_it_runs(M, N, K)
