@@ -32,7 +32,6 @@
 // copies and MMAs in flight are drained, and the CTA frees its TMEM and returns.
 #include <algorithm>
 #include <climits>
-#include <mutex>
 
 #include "internal.h"
 #include "mxdense.cuh"
@@ -397,17 +396,18 @@ cudaLaunchConfig_t dense_config(unsigned grid, int S, size_t smem, cudaStream_t 
   return lc;
 }
 
+// The kernel may take all of a CTA's shared memory (an attribute of each device).
 template <int FMT, int BN, typename T>
 bool dense_configure() {
-  static int ok = -1;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    ok = cudaFuncSetAttribute(mx_dense_kernel<FMT, BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) ==
-                 cudaSuccess
-             ? 1
-             : 0;
-  });
-  return ok == 1;
+  static PerDevice done;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  return done.get(dev, [] {
+    return cudaFuncSetAttribute(mx_dense_kernel<FMT, BN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) ==
+                   cudaSuccess
+               ? 1
+               : 0;
+  }) > 0;
 }
 
 // Which kernel, and how. Fitted times of the variants in ns, from back-to-back calls at 55 sizes from 1 x 4096 x 256 to

@@ -3,6 +3,7 @@
 
 #include "common.cuh"
 #include "dense.cuh"
+#include "perdevice.h"
 
 namespace fp4moe {
 

@@ -23,8 +23,6 @@
 // 8192 x 8192 x 2048 57 instead of 53), all 128 columns of an epilogue warp in flight at once (spills, 53), a stage's
 // scale copies ahead of the MMAs before it (50).
 // The rest (scale-factor ids, K tails, bounded waits) is as in mxdense.cu.
-#include <mutex>
-
 #include "internal.h"
 #include "mxdense.cuh"
 
@@ -373,15 +371,13 @@ cudaLaunchConfig_t pair_config(unsigned pairs, size_t smem, cudaStream_t st, cud
   return lc;
 }
 
-// Pairs that the device holds at once (the persistent grid); 0 on error. Cached per device.
+// Pairs that the device holds at once (the persistent grid); 0 on error. Kept for each device.
 template <int FMT, typename T>
 int pair_count() {
-  constexpr int kMaxDevices = 64;
-  static std::once_flag once[kMaxDevices];
-  static int count[kMaxDevices];
+  static PerDevice count;
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  std::call_once(once[dev], [dev] {
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return count.get(dev, [] {
     int n = 0;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t lc = pair_config(1, PairCfg<FMT>::kSmem, nullptr, attr);
@@ -390,9 +386,8 @@ int pair_count() {
                              PairCfg<FMT>::kSmem) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<FMT, T>, &lc) != cudaSuccess)
       n = 0;
-    count[dev] = n;
+    return n;
   });
-  return count[dev];
 }
 
 template <int FMT, typename T>
