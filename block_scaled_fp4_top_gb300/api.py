@@ -48,6 +48,13 @@ def _p(t):
 _raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
+def _current_device():
+    try:
+        return _device()
+    except (RuntimeError, TypeError):  # no driver, or a build without CUDA: no tensor is there
+        return -2
+
+
 def _s(stream):
     # the raw handle of the current stream, without building a torch.cuda.Stream (0.2 against 3 us a call)
     if stream is None:
@@ -243,7 +250,7 @@ def fp4moe_refresh_gs2(cfg, ws, gw2, gs2_inout, alpha2_out, stream=None):
 
 def moe_shared_expert_fp8(cfg, T, x_codes, x_scales, se, o_shared, ws, stream=None):
     """moe_shared_expert on the FP8 copy that fp4moe_add_rmsnorm writes (x_scales [H / 128, at least T])."""
-    _check_fp8(x_codes, x_scales, T, cfg.hidden)
+    _check_fp8(x_codes, x_scales, T, cfg.hidden, _current_device())
     _check(_lib.load().moe_shared_expert_fp8(ctypes.byref(cfg), T, _p(x_codes), _p(x_scales), x_scales.shape[1],
                                              _sw(se), _p(o_shared), _p(ws), _s(stream)), "moe_shared_expert_fp8")
 
@@ -251,7 +258,7 @@ def moe_shared_expert_fp8(cfg, T, x_codes, x_scales, se, o_shared, ws, stream=No
 def moe_forward_shared_fp8(cfg, T, x, x_codes, x_scales, router_w, router_bias, gs1, gs2, w1_fp4, w1_sf, alpha1,
                            w2_fp4, w2_sf, alpha2, se, y, topk_ids_out, topk_w_out, ws, stream=None):
     """moe_forward_shared with the shared expert fed from x's FP8 copy."""
-    _check_fp8(x_codes, x_scales, T, cfg.hidden)
+    _check_fp8(x_codes, x_scales, T, cfg.hidden, _current_device())
     _check(_lib.load().moe_forward_shared_fp8(ctypes.byref(cfg), T, _p(x), _p(x_codes), _p(x_scales),
                                               x_scales.shape[1], _p(router_w), _p(router_bias), _p(gs1), _p(gs2),
                                               _p(w1_fp4), _p(w1_sf), _p(alpha1), _p(w2_fp4), _p(w2_sf), _p(alpha2),
@@ -261,40 +268,47 @@ def moe_forward_shared_fp8(cfg, T, x, x_codes, x_scales, router_w, router_bias, 
 
 # ---------------------------------------------------------- dense operators
 # Their sizes and types come from the tensors, so the shapes are checked here: the library sees only pointers.
-# A small call is bound by the host, so each tensor is checked and turned into its pointer in one go.
+# A small call is bound by the host, so each tensor is checked and turned into its pointer in one go. `dev` is the
+# current device: kernels run there, and a matrix on another one would be read through a peer mapping or not at all.
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
 _BYTE_TYPES = (torch.uint8, torch.float8_e4m3fn)
 _U8, _F32 = torch.uint8, torch.float32
 
 
-def _arg(name, t, shape, dtype):
-    """The pointer of a contiguous CUDA tensor of this shape and type; None stays None."""
+def _place(name, t, dev):
+    if t.get_device() != dev or not t.is_contiguous():  # (-1 for a CPU tensor)
+        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor on the current device")
+
+
+def _arg(name, t, shape, dtype, dev):
+    """The pointer of a contiguous tensor of this shape and type on the device; None stays None."""
     if t is None:
         return None
     if t.dtype is not dtype or t.shape != shape:
         raise Fp4MoeError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        _place(name, t, dev)
     return t.data_ptr()
 
 
-def _arg_bytes(name, t, nbytes):
+def _arg_bytes(name, t, nbytes, dev):
     if t.dtype is not _U8 or t.numel() != nbytes:
         raise Fp4MoeError(f"{name}: expected {nbytes} bytes (uint8), got {t.numel()} of {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        _place(name, t, dev)
     return t.data_ptr()
 
 
-def _arg_scalar(name, t):
+def _arg_scalar(name, t, dev):
     if t is None:
         return None
     if t.dtype is not _F32 or t.numel() < 1:
         raise Fp4MoeError(f"{name}: expected one float32, got {t.numel()} of {t.dtype}")
-    return _p(t)
+    _place(name, t, dev)
+    return t.data_ptr()
 
 
-def _arg_matrix(name, t):
+def _arg_matrix(name, t, dev):
     """(shape, dtype, fp4moe_dtype, pointer) of a matrix whose sizes the call takes."""
     dt, shape = t.dtype, t.shape
     d = _DTYPES.get(dt)
@@ -302,12 +316,12 @@ def _arg_matrix(name, t):
         raise Fp4MoeError(f"{name}: unsupported dtype {dt}: bfloat16, float16 or float32")
     if len(shape) != 2:
         raise Fp4MoeError(f"{name}: expected a matrix, got {tuple(shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise Fp4MoeError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        _place(name, t, dev)
     return shape, dt, d, t.data_ptr()
 
 
-def _check_fp8(codes, scales, T, H):
+def _check_fp8(codes, scales, T, H, dev):
     """Check block-FP8 activations: codes [T, H], scales [ceil(H / 128), at least T]. Returns the scales' columns."""
     if codes.dtype not in _BYTE_TYPES or codes.shape != (T, H):
         raise Fp4MoeError(f"codes: expected {(T, H)} of {' or '.join(map(str, _BYTE_TYPES))}, got "
@@ -316,6 +330,8 @@ def _check_fp8(codes, scales, T, H):
     if scales.dtype is not _F32 or len(shape) != 2 or shape[0] != (H + 127) // 128 or shape[1] < T:
         raise Fp4MoeError(f"scales: expected [{(H + 127) // 128}, at least {T}] of torch.float32, got "
                           f"{tuple(shape)} of {scales.dtype}")
+    _place("codes", codes, dev)
+    _place("scales", scales, dev)
     return shape[1]
 
 
@@ -326,14 +342,16 @@ def fp4moe_add_rmsnorm(x, residual, gamma, eps, residual_out, y, y_codes=None, y
     x [T, H] bfloat16, float16 or float32, and residual, residual_out, y, gamma [H] of its type. residual with
     residual_out, and y_codes with y_scales, may be None; so may gamma (ones), and y where y_codes is given.
     residual_out and y may each be x or residual."""
-    shape, dt, d, px = _arg_matrix("x", x)
+    dev = _current_device()
+    shape, dt, d, px = _arg_matrix("x", x, dev)
     T, H = shape
     stride = 0
     if y_codes is not None and y_scales is not None:
-        stride = _check_fp8(y_codes, y_scales, T, H)
-    _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, px, _arg("residual", residual, shape, dt),
-                                          _arg("gamma", gamma, (H,), dt), eps,
-                                          _arg("residual_out", residual_out, shape, dt), _arg("y", y, shape, dt),
+        stride = _check_fp8(y_codes, y_scales, T, H, dev)
+    _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, px, _arg("residual", residual, shape, dt, dev),
+                                          _arg("gamma", gamma, (H,), dt, dev), eps,
+                                          _arg("residual_out", residual_out, shape, dt, dev),
+                                          _arg("y", y, shape, dt, dev),
                                           _p(y_codes), _p(y_scales), stride, _s(stream)), "fp4moe_add_rmsnorm")
 
 
@@ -357,33 +375,39 @@ def fp4moe_mx_bytes(fmt: int, rows: int, K: int):
 
 def fp4moe_mx_quantize(fmt, x, gs, codes, sf, stream=None):
     """x [rows, K] to E2M1 codes and block scales (fmt W_MXFP4, or W_NVFP4 under the global scale gs)."""
-    (rows, K), _, d, px = _arg_matrix("x", x)
-    _check(_lib.load().fp4moe_mx_quantize(fmt, d, rows, K, px, _arg_scalar("gs", gs),
-                                          _arg_bytes("codes", codes, rows * mx_row_bytes(K)),
-                                          _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K)), _s(stream)),
+    dev = _current_device()
+    (rows, K), _, d, px = _arg_matrix("x", x, dev)
+    _check(_lib.load().fp4moe_mx_quantize(fmt, d, rows, K, px, _arg_scalar("gs", gs, dev),
+                                          _arg_bytes("codes", codes, rows * mx_row_bytes(K), dev),
+                                          _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K), dev), _s(stream)),
            "fp4moe_mx_quantize")
 
 
 def fp4moe_mx_dequantize(fmt, codes, sf, gs, out, stream=None):
     """The values of a microscaled matrix into out [rows, K]."""
-    (rows, K), _, d, po = _arg_matrix("out", out)
-    _check(_lib.load().fp4moe_mx_dequantize(fmt, d, rows, K, _arg_bytes("codes", codes, rows * mx_row_bytes(K)),
-                                            _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K)), _arg_scalar("gs", gs),
-                                            po, _s(stream)), "fp4moe_mx_dequantize")
+    dev = _current_device()
+    (rows, K), _, d, po = _arg_matrix("out", out, dev)
+    _check(_lib.load().fp4moe_mx_dequantize(fmt, d, rows, K,
+                                            _arg_bytes("codes", codes, rows * mx_row_bytes(K), dev),
+                                            _arg_bytes("sf", sf, mx_sf_bytes(fmt, rows, K), dev),
+                                            _arg_scalar("gs", gs, dev), po, _s(stream)), "fp4moe_mx_dequantize")
 
 
 def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream=None):
     """out [M, N] = alpha * A B^T for microscaled A [M, K] and B [N, K]; alpha a device float32 or None (1); err a
     zeroed device word (int32) that the caller keeps."""
-    (M, N), _, d, po = _arg_matrix("out", out)
+    dev = _current_device()
+    (M, N), _, d, po = _arg_matrix("out", out, dev)
     row = mx_row_bytes(K)
     if err.element_size() * err.numel() < 4:
         raise Fp4MoeError("err: expected a device word of 4 bytes")
-    _check(_lib.load().fp4moe_mx_gemm(fmt, d, M, N, K, _arg_bytes("a_codes", a_codes, M * row),
-                                      _arg_bytes("a_sf", a_sf, mx_sf_bytes(fmt, M, K)),
-                                      _arg_bytes("b_codes", b_codes, N * row),
-                                      _arg_bytes("b_sf", b_sf, mx_sf_bytes(fmt, N, K)), _arg_scalar("alpha", alpha),
-                                      po, _p(err), _s(stream)), "fp4moe_mx_gemm")
+    _place("err", err, dev)
+    _check(_lib.load().fp4moe_mx_gemm(fmt, d, M, N, K, _arg_bytes("a_codes", a_codes, M * row, dev),
+                                      _arg_bytes("a_sf", a_sf, mx_sf_bytes(fmt, M, K), dev),
+                                      _arg_bytes("b_codes", b_codes, N * row, dev),
+                                      _arg_bytes("b_sf", b_sf, mx_sf_bytes(fmt, N, K), dev),
+                                      _arg_scalar("alpha", alpha, dev), po, err.data_ptr(), _s(stream)),
+           "fp4moe_mx_gemm")
 
 
 # --------------------------------------------------------------------------
@@ -587,8 +611,11 @@ class MxLinear:
     def forward(self, x: torch.Tensor, out: torch.Tensor, stream=None):
         """out [T, N] (bfloat16, float16 or float32) of x [T, K]."""
         # fp4moe_mx_quantize and fp4moe_mx_gemm on this object's own buffers, which need no checks (nor slices for T)
-        (T, K), _, dx, px = _arg_matrix("x", x)
-        shape, _, do, po = _arg_matrix("out", out)
+        dev = _current_device()
+        (T, K), _, dx, px = _arg_matrix("x", x, dev)
+        shape, _, do, po = _arg_matrix("out", out, dev)
+        if self.err.get_device() != dev:
+            raise Fp4MoeError(f"the weights are on device {self.err.get_device()}, the current one is {dev}")
         if T > self.max_tokens or K != self.K or shape != (T, self.N):
             raise Fp4MoeError(f"expected x [at most {self.max_tokens}, {self.K}] and out [T, {self.N}], got "
                               f"{(T, K)} and {tuple(shape)}")

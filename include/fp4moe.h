@@ -497,9 +497,10 @@ fp4moe_status moe_forward_shared_fp8(const fp4moe_config* cfg, int32_t T, const 
  * activations, fp4moe_mx_gemm), and the residual addition with the norm whose
  * output the router, the routed experts (y) and the shared expert (its FP8
  * copy) read. They need no fp4moe_config and no workspace. The layer's
- * conventions hold: device pointers 16-byte aligned, work enqueued on
- * `stream`, no allocation, no synchronisation, capturable after a first call
- * outside capture. Matrices are contiguous and row-major. Inference only: no
+ * conventions hold: device pointers 16-byte aligned and of the current device's
+ * own memory (not a peer's, nor the host's), work enqueued on `stream`, no
+ * allocation, no synchronisation, capturable after a first call outside
+ * capture. Matrices are contiguous and row-major. Inference only: no
  * call computes gradients.
  */
 typedef enum fp4moe_dtype { FP4MOE_BF16 = 0, FP4MOE_FP16 = 1, FP4MOE_FP32 = 2 } fp4moe_dtype;

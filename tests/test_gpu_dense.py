@@ -656,3 +656,32 @@ def test_gemm_on_pairs_under_a_raised_error_word(fmt, M, N, K):
 def test_gemm_on_pairs_under_an_error_word_that_is_raised_while_it_runs(M, N, K):
     """The two CTAs of a pair may see it at different stages. Each call ends, and leaves nothing to the next one."""
     test_gemm_under_an_error_word_that_is_raised_while_it_runs(M, N, K)
+
+
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    """Seen from device 1, every tensor of this process is on another device. Nothing is launched."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    x = rnd((8, 128), "bfloat16", 1)
+    y, codes8, scales = torch.empty_like(x), torch.empty(8, 128, dtype=torch.uint8, device="cuda"), torch.empty(1, 8, device="cuda")
+    a, asf, _, b, bsf, _ = gemm_operands(MX, 8, 16, 128, 1)
+    out, err = torch.full((8, 16), 7.0, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    lin = api.MxLinear(rnd((16, 128), "float32", 2), 8)
+    q, s = (torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in api.fp4moe_mx_bytes(MX, 8, 128))
+    calls = [lambda: api.fp4moe_add_rmsnorm(x, None, None, 1e-6, None, y, codes8, scales),
+             lambda: api.fp4moe_mx_quantize(MX, x, None, q, s),
+             lambda: api.fp4moe_mx_dequantize(MX, q, s, None, y),
+             lambda: api.fp4moe_mx_gemm(MX, 128, a, asf, b, bsf, None, out, err),
+             lambda: lin.forward(x, out)]
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        m.setattr(api, "_device", lambda: 1)
+        for call in calls:
+            with pytest.raises(api.Fp4MoeError, match="current"):
+                call()
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and (q == 7).all()
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0 and (out != 7.0).any()
