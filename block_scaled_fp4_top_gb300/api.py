@@ -575,7 +575,11 @@ class MxLinear:
     """A projection y = x W^T with microscaled 4-bit weights and activations (W [N, K], at most max_tokens rows of x).
 
     fmt W_MXFP4 needs nothing more. fmt W_NVFP4 has a global scale for each operand: the weights' is taken from W here,
-    the activations' from a warm-up batch (calibrate) or set by the caller (set_activation_scale)."""
+    the activations' from a warm-up batch (calibrate) or set by the caller (set_activation_scale); forward refuses to
+    run before it has one.
+
+    All calls of one object use its buffers of codes and its error word, so they must be ordered on one stream (or by
+    events), like calls of the layer that share a workspace."""
 
     def __init__(self, weight: torch.Tensor, max_tokens: int, fmt: int = _lib.W_MXFP4):
         self.N, self.K = weight.shape
@@ -586,13 +590,12 @@ class MxLinear:
         self.gw = self.gx = self.alpha = None
         if fmt == _lib.W_NVFP4:
             self.gw = self._global_scale(weight)
-            self.gx = torch.ones_like(self.gw)
-            self.alpha = torch.empty_like(self.gw)
-            fp4moe_make_alpha(1, self.gx, self.gw, self.alpha)
+            self.gx, self.alpha = torch.empty_like(self.gw), torch.empty_like(self.gw)
         fp4moe_mx_quantize(fmt, weight.contiguous(), self.gw, self.w_codes, self.w_sf)
         self.x_codes = torch.empty(max_tokens * mx_row_bytes(self.K), **u8)
         self.x_sf = torch.empty(mx_sf_bytes(fmt, max_tokens, self.K), **u8)
         self.err = torch.zeros(4, dtype=torch.int32, device=weight.device)
+        self.calibrated = fmt != _lib.W_NVFP4
 
     @staticmethod
     def _global_scale(t):
@@ -605,8 +608,12 @@ class MxLinear:
             self.set_activation_scale(self._global_scale(x_warm))
 
     def set_activation_scale(self, gs):
+        """NVFP4: the activations' global scale."""
+        if self.gx is None:
+            raise Fp4MoeError("set_activation_scale: MXFP4 has no global scale")
         self.gx.copy_(torch.as_tensor(gs, dtype=torch.float32).reshape(1))
         fp4moe_make_alpha(1, self.gx, self.gw, self.alpha)
+        self.calibrated = True
 
     def forward(self, x: torch.Tensor, out: torch.Tensor, stream=None):
         """out [T, N] (bfloat16, float16 or float32) of x [T, K]."""
@@ -615,10 +622,12 @@ class MxLinear:
         (T, K), _, dx, px = _arg_matrix("x", x, dev)
         shape, _, do, po = _arg_matrix("out", out, dev)
         if self.err.get_device() != dev:
-            raise Fp4MoeError(f"the weights are on device {self.err.get_device()}, the current one is {dev}")
+            raise Fp4MoeError(f"MxLinear: the weights are on device {self.err.get_device()}, the current one is {dev}")
         if T > self.max_tokens or K != self.K or shape != (T, self.N):
             raise Fp4MoeError(f"expected x [at most {self.max_tokens}, {self.K}] and out [T, {self.N}], got "
                               f"{(T, K)} and {tuple(shape)}")
+        if not self.calibrated:
+            raise Fp4MoeError("MxLinear: NVFP4 activations have no global scale yet (calibrate, set_activation_scale)")
         lib, s = _lib.load(), _s(stream)
         codes, sf = self.x_codes.data_ptr(), self.x_sf.data_ptr()
         _check(lib.fp4moe_mx_quantize(self.fmt, dx, T, K, px, _p(self.gx), codes, sf, s), "fp4moe_mx_quantize")

@@ -249,3 +249,26 @@ def test_linear_refusals():
                    (ok(4, 96).double(), ok(4, 64)), (ok(4, 96)[0], ok(4, 64))):
         with pytest.raises(api.Fp4MoeError):
             lin.forward(x, out)
+
+
+def test_linear_in_nvfp4_needs_an_activation_scale():
+    """Without one, small blocks' scales would underflow and large ones saturate without a word."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    w, x = torch.randn(64, 96, device="cuda"), torch.randn(4, 96, device="cuda").to(torch.bfloat16)
+    lin, out = api.MxLinear(w, 8, NV), torch.full((4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(api.Fp4MoeError, match="scale"):
+        lin.forward(x, out)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all()
+    lin.calibrate(x)
+    lin.forward(x, out)
+    gs = lin.gx.item()
+    other, again = api.MxLinear(w, 8, NV), torch.empty_like(out)
+    other.set_activation_scale(gs)
+    other.forward(x, again)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again) and lin.read_error() == 0 and other.read_error() == 0
+    with pytest.raises(api.Fp4MoeError, match="global scale"):
+        api.MxLinear(w, 8, MX).set_activation_scale(1.0)
+    api.MxLinear(w, 8, MX).forward(x, out)
