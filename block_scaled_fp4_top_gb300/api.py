@@ -330,8 +330,10 @@ def _check_fp8(codes, scales, T, H, dev):
     if scales.dtype is not _F32 or len(shape) != 2 or shape[0] != (H + 127) // 128 or shape[1] < T:
         raise Fp4MoeError(f"scales: expected [{(H + 127) // 128}, at least {T}] of torch.float32, got "
                           f"{tuple(shape)} of {scales.dtype}")
-    _place("codes", codes, dev)
-    _place("scales", scales, dev)
+    if codes.get_device() != dev or not codes.is_contiguous():
+        _place("codes", codes, dev)
+    if scales.get_device() != dev or not scales.is_contiguous():
+        _place("scales", scales, dev)
     return shape[1]
 
 
@@ -345,14 +347,16 @@ def fp4moe_add_rmsnorm(x, residual, gamma, eps, residual_out, y, y_codes=None, y
     dev = _current_device()
     shape, dt, d, px = _arg_matrix("x", x, dev)
     T, H = shape
-    stride = 0
     if y_codes is not None and y_scales is not None:
         stride = _check_fp8(y_codes, y_scales, T, H, dev)
+        pc, ps = y_codes.data_ptr(), y_scales.data_ptr()
+    else:  # both None, or refused by the call
+        stride, pc, ps = 0, _p(y_codes), _p(y_scales)
     _check(_lib.load().fp4moe_add_rmsnorm(d, T, H, px, _arg("residual", residual, shape, dt, dev),
                                           _arg("gamma", gamma, (H,), dt, dev), eps,
                                           _arg("residual_out", residual_out, shape, dt, dev),
                                           _arg("y", y, shape, dt, dev),
-                                          _p(y_codes), _p(y_scales), stride, _s(stream)), "fp4moe_add_rmsnorm")
+                                          pc, ps, stride, _s(stream)), "fp4moe_add_rmsnorm")
 
 
 def mx_row_bytes(K: int) -> int:
