@@ -455,8 +455,11 @@ fp4moe_status dense_run(DenseParams prm, int S, const uint8_t* a, const uint8_t*
   prm.mt = (prm.M + DBM - 1) / DBM;
   prm.nt = (prm.N + BN - 1) / BN;
   const int a_rows = rows_loaded(prm.M);
-  // a ring no deeper than the slice, so that the next launch's CTAs find room beside this one's
-  const int stages = std::min(C::fit(a_rows, S), (prm.KB + S - 1) / S);
+  const int tiles = prm.mt * prm.nt, ctas = S > 1 ? tiles : std::min(tiles, nsm);
+  // as many ring stages as fit, but no more than a CTA's tiles have: the producers run on into the next tile while the
+  // epilogue empties the accumulator (1300 x 4100 x 160 MXFP4, one stage a tile: 9.2 with a ring of one, 8.9 us)
+  const int64_t work = (int64_t)((prm.KB + S - 1) / S) * ((tiles + ctas - 1) / ctas);
+  const int stages = (int)std::min<int64_t>(C::fit(a_rows, S), work);
   if (stages <= 0) return FP4MOE_UNSUPPORTED;  // (not reached: what pick_plan splits, four ways at most, leaves four stages)
   prm.a_sf = a_sf;
   prm.b_sf = b_sf;
@@ -466,10 +469,8 @@ fp4moe_status dense_run(DenseParams prm, int S, const uint8_t* a, const uint8_t*
       !encode_u8_sw128(&maps.b, b, rb, (uint64_t)prm.N, BN))
     return FP4MOE_CUDA_ERROR;
   if (!dense_configure<FMT, BN, T>()) return FP4MOE_CUDA_ERROR;
-  const int tiles = prm.mt * prm.nt;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t lc =
-      dense_config((unsigned)(S > 1 ? tiles : std::min(tiles, nsm)), S, C::smem(stages, a_rows, S), st, attr);
+  const cudaLaunchConfig_t lc = dense_config((unsigned)ctas, S, C::smem(stages, a_rows, S), st, attr);
   return cudaLaunchKernelEx(&lc, mx_dense_kernel<FMT, BN, T>, maps, prm, stages, a_rows, C::tmem(stages)) ==
                  cudaSuccess
              ? FP4MOE_OK
