@@ -75,6 +75,7 @@ SIGNATURES = {
     "fp4moe_mx_bytes": (c_i32, [c_i32] * 3 + [ctypes.POINTER(c_sz)] * 2),
     "fp4moe_mx_quantize": (c_i32, [c_i32] * 4 + [c_vp] * 5),
     "fp4moe_mx_dequantize": (c_i32, [c_i32] * 4 + [c_vp] * 5),
+    "fp4moe_mx_gemm_plan": (c_i32, [c_i32] * 4 + [ctypes.POINTER(c_i32)] * 3),
     "fp4moe_mx_gemm": (c_i32, [c_i32] * 5 + [c_vp] * 8),
 }
 

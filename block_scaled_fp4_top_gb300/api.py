@@ -397,6 +397,13 @@ def fp4moe_mx_dequantize(fmt, codes, sf, gs, out, stream=None):
                                             _arg_scalar("gs", gs, dev), po, _s(stream)), "fp4moe_mx_dequantize")
 
 
+def fp4moe_mx_gemm_plan(M: int, N: int, K: int, sms: int):
+    """(tile rows, tile columns, K slices) of an M x N x K product on a device of `sms` SMs (host arithmetic)."""
+    v = [ctypes.c_int32() for _ in range(3)]
+    _check(_lib.load().fp4moe_mx_gemm_plan(M, N, K, sms, *[ctypes.byref(x) for x in v]), "fp4moe_mx_gemm_plan")
+    return tuple(x.value for x in v)
+
+
 def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream=None):
     """out [M, N] = alpha * A B^T for microscaled A [M, K] and B [N, K]; alpha a device float32 or None (1); err a
     zeroed device word (int32) that the caller keeps."""

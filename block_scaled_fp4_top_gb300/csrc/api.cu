@@ -808,6 +808,18 @@ fp4moe_status fp4moe_mx_dequantize(int32_t format, int32_t dtype, int32_t rows, 
   return mx_dequantize_launch(format, dtype, rows, K, codes, sf, gs, out, (cudaStream_t)stream);
 }
 
+fp4moe_status fp4moe_mx_gemm_plan(int32_t M, int32_t N, int32_t K, int32_t sms, int32_t* tile_rows,
+                                  int32_t* tile_cols, int32_t* k_slices) {
+  if (M <= 0 || N <= 0 || K <= 0 || sms <= 0) return FP4MOE_INVALID_ARG;
+  FP4_TRY(check_mx(FP4MOE_W_NVFP4, M, K));
+  FP4_TRY(check_mx(FP4MOE_W_NVFP4, N, K));
+  const MxPlan p = mx_plan(M, N, K, sms);
+  if (tile_rows) *tile_rows = p.pair ? 256 : 128;
+  if (tile_cols) *tile_cols = p.bn;
+  if (k_slices) *k_slices = p.S;
+  return FP4MOE_OK;
+}
+
 fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N, int32_t K, const uint8_t* a_codes,
                              const uint8_t* a_sf, const uint8_t* b_codes, const uint8_t* b_sf, const float* alpha,
                              void* out, uint32_t* err, fp4moe_stream_t stream) {

@@ -148,6 +148,12 @@ fp4moe_status mx_quantize_launch(int32_t format, int32_t dtype, int32_t rows, in
                                  const float* gs, uint8_t* codes, uint8_t* sf, cudaStream_t st);
 fp4moe_status mx_dequantize_launch(int32_t format, int32_t dtype, int32_t rows, int32_t K, const uint8_t* codes,
                                    const uint8_t* sf, const float* gs, void* out, cudaStream_t st);
+// mxdense.cu: which kernel takes a product, and how, on a device of `sms` SMs
+struct MxPlan {
+  bool pair;  // mxpair.cu's kernel, 256 x 256 tiles on two CTAs; else mxdense.cu's, 128 x bn tiles
+  int bn, S;  // columns of a tile; slices of K, one CTA of a cluster each
+};
+MxPlan mx_plan(int M, int N, int K, int sms);
 // mxdense.cu: out [M][N] = alpha * A B^T
 fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t N, int32_t K, const uint8_t* a,
                               const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, const float* alpha,

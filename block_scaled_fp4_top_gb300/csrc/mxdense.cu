@@ -420,15 +420,11 @@ bool dense_configure() {
 //   split over S CTAs      KB / S stages; joining: 1100 (1600 for tiles of more than 64 rows), and a fifth of a ns for
 //                          each fp32 value that is sent
 //   256 x 256 on a pair    1050 a tile and 306 a stage, two SMs a tile
-struct Plan {
-  bool pair;  // mxpair.cu's kernel; else this file's, with bn and S
-  int bn, S;
-};
-Plan pick_plan(int M, int N, int KB, int nsm) {
+MxPlan pick_plan(int M, int N, int KB, int nsm) {
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  Plan best{false, 128, 1};
+  MxPlan best{false, 128, 1};
   int64_t best_ns = INT64_MAX;
-  auto offer = [&](Plan p, int64_t ns) {
+  auto offer = [&](MxPlan p, int64_t ns) {
     if (ns < best_ns) {
       best_ns = ns;
       best = p;
@@ -499,6 +495,8 @@ fp4moe_status dense_width(int bn, int32_t dtype, const DenseParams& prm, int S, 
 
 }  // namespace
 
+MxPlan mx_plan(int M, int N, int K, int sms) { return pick_plan(M, N, (int)(((int64_t)K + DK - 1) / DK), sms); }
+
 fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t N, int32_t K, const uint8_t* a,
                               const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
                               void* out, uint32_t* err, cudaStream_t st) {
@@ -518,7 +516,7 @@ fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t 
   prm.err = err;
   const int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
-  const Plan plan = pick_plan(M, N, prm.KB, nsm);
+  const MxPlan plan = mx_plan(M, N, K, nsm);
   if (plan.pair) return mx_pair_launch(format, dtype, prm, a, a_sf, b, b_sf, st);
   return format == FP4MOE_W_MXFP4 ? dense_width<FP4MOE_W_MXFP4>(plan.bn, dtype, prm, plan.S, a, a_sf, b, b_sf, nsm, st)
                                   : dense_width<FP4MOE_W_NVFP4>(plan.bn, dtype, prm, plan.S, a, a_sf, b, b_sf, nsm, st);

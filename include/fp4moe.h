@@ -592,6 +592,17 @@ fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N
                              const uint8_t* a_sf, const uint8_t* b_codes, const uint8_t* b_sf, const float* alpha,
                              void* out, uint32_t* err, fp4moe_stream_t stream);
 
+/*
+ * fp4moe_mx_gemm_plan: how fp4moe_mx_gemm divides an M x N x K product on a
+ * device of `sms` SMs (host arithmetic; any output may be NULL): output tiles
+ * of tile_rows x tile_cols, 128 x 64 or 128 x 128 on one CTA each or 256 x 256
+ * on a pair of CTAs, with K in k_slices slices on that many CTAs of a cluster.
+ * Results differ between plans by the order of fp32 additions only. M, N, K or
+ * sms below 1: FP4MOE_INVALID_ARG; sizes as in fp4moe_mx_bytes.
+ */
+fp4moe_status fp4moe_mx_gemm_plan(int32_t M, int32_t N, int32_t K, int32_t sms, int32_t* tile_rows, int32_t* tile_cols,
+                                  int32_t* k_slices);
+
 /* ------------------------------------------------------------------ prep --
  * Load-time helpers. They run outside the timed hot path and may use
  * cudaMemsetAsync. They still never synchronise.

@@ -183,3 +183,36 @@ def test_no_load_writes_into_several_ctas():
         with open(os.path.join(csrc, name)) as f:
             text = re.sub(r'"\s*\n\s*"', "", f.read())  # adjacent string literals are one instruction
         assert not load.search(text), name
+
+
+def test_mx_gemm_plans_of_the_test_sizes(lib):
+    """The sizes that stand for each kernel do take it: a change of the choice shows here."""
+    from block_scaled_fp4_top_gb300 import api
+    from mx_plans import CASES, SMS
+    for plan, size in CASES:
+        assert api.fp4moe_mx_gemm_plan(*size, SMS) == plan, size
+
+
+def test_mx_gemm_plans_hold_over_the_range(lib):
+    """Every size has a plan of a kernel that there is; K is split only where each slice has a stage of 256 elements."""
+    import random
+    from block_scaled_fp4_top_gb300 import api
+    from mx_plans import PLANS
+    rng = random.Random(1)
+    size = lambda: int(2 ** rng.uniform(0, 15))
+    for _ in range(5000):
+        M, N, K, sms = size(), size(), size(), rng.choice((1, 8, 84, 148, 152))
+        plan = api.fp4moe_mx_gemm_plan(M, N, K, sms)
+        assert plan in PLANS and plan[2] <= -(-K // 256), (M, N, K, sms)
+    top = 2**31 - 1 - 8192
+    for s in ((1, 1, top), (1, 100, top), (129, 1, top), (top, 1, 1), (1, top, 1)):
+        assert api.fp4moe_mx_gemm_plan(*s, 152) in PLANS, s
+
+
+def test_mx_gemm_plan_refusals(lib):
+    from block_scaled_fp4_top_gb300 import _lib
+    p = lib.fp4moe_mx_gemm_plan
+    for bad in ((0, 1, 1, 152), (1, 0, 1, 152), (1, 1, 0, 152), (1, 1, 1, 0), (-1, 1, 1, 152)):
+        assert p(*bad, None, None, None) == _lib.INVALID_ARG
+    assert p(1, 1, 2**31 - 1, 152, None, None, None) == _lib.UNSUPPORTED
+    assert p(4, 4, 64, 152, None, None, None) == _lib.OK         # outputs optional

@@ -11,6 +11,7 @@ Tolerances are sums of the roundings that the definitions allow:
 import numpy as np
 import pytest
 
+import mx_plans
 from dense_ref import (BLOCK, HALF_STEP, MX, NV, TINY, Guarded, e4m3_half_step, pack, quantize, rms_norm,
                        scale_tile_shape, values)
 from helpers import ensure_built
@@ -685,3 +686,47 @@ def test_tensors_on_another_device_are_refused(monkeypatch):
         call()
     torch.cuda.synchronize()
     assert int(err[0]) == 0 and (out != 7.0).any()
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("index", range(len(mx_plans.CASES)))
+def test_gemm_every_plan(fmt, index):
+    """Each kernel at the sizes that take it, and every element is written: a second result over other old values."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    plan, (M, N, K) = mx_plans.CASES[index]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert api.fp4moe_mx_gemm_plan(M, N, K, sms) == plan
+    dtype = DTYPES[index % 3]
+    alpha = 2.0 ** -9 if dtype == "float16" else -1.75
+    ops = gemm_operands(fmt, M, N, K, index)
+    got = check_gemm(fmt, M, N, K, dtype, alpha=alpha, operands=ops)
+    again = torch.full_like(got, float("nan"))
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    api.fp4moe_mx_gemm(fmt, K, ops[0], ops[1], ops[3], ops[4], torch.tensor([alpha], device="cuda"), again, err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0 and not again.isnan().any() and torch.equal(got, again)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", [(8192, 4096, 2048), (8100, 4051, 2080)])
+def test_gemm_writes_every_element_of_many_rounds(fmt, dtype, M, N, K):
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    gen = torch.Generator("cuda").manual_seed(K)
+    sides = []
+    for rows in (M, N):
+        c, s = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in api.fp4moe_mx_bytes(fmt, rows, K))
+        api.fp4moe_mx_quantize(fmt, torch.randn(rows, K, generator=gen, device="cuda"), torch.ones(1, device="cuda"), c, s)
+        sides += [c, s]
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    outs = []
+    for old in (float("nan"), 7.0):
+        ob = Guarded((M, N), getattr(torch, dtype))
+        ob.t.fill_(old)
+        api.fp4moe_mx_gemm(fmt, K, *sides, None, ob.t, err)
+        torch.cuda.synchronize()
+        ob.check()
+        outs.append(ob.t)
+    assert int(err[0]) == 0 and not outs[0].isnan().any() and torch.equal(*outs)
