@@ -456,7 +456,7 @@ fp4moe_status dense_run(DenseParams prm, int S, const uint8_t* a, const uint8_t*
   // epilogue empties the accumulator (1300 x 4100 x 160 MXFP4, one stage a tile: 9.2 with a ring of one, 8.9 us)
   const int64_t work = (int64_t)((prm.KB + S - 1) / S) * ((tiles + ctas - 1) / ctas);
   const int stages = (int)std::min<int64_t>(C::fit(a_rows, S), work);
-  if (stages <= 0) return FP4MOE_UNSUPPORTED;  // (not reached: what pick_plan splits, four ways at most, leaves four stages)
+  if (stages <= 0) return FP4MOE_UNSUPPORTED;  // (not reached: a split in four, the most, leaves room for four stages)
   prm.a_sf = a_sf;
   prm.b_sf = b_sf;
   TileMaps maps;

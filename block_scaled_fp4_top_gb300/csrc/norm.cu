@@ -13,7 +13,7 @@
 // Bound by memory: a row is read and written once. One CTA takes a row and, where it fits, keeps it in registers
 // between the two uses. Few rows leave the device empty and the time is one trip to memory, a reduction and a trip
 // back (1 x 4096 bf16 2.0 us, 64 rows 2.3 us), so they take the most threads; many rows take two or four 16-byte
-// vectors a thread (8192 x 4096 bf16 with the FP8 copy 49.0 us, 6.2 TB/s, 91 % of a copy's rate).
+// vectors a thread (8192 x 4096 bf16 with the FP8 copy 48.6 us, 6.2 TB/s, 92 % of a copy's rate).
 #include "common.cuh"
 #include "dense.cuh"
 #include "internal.h"
@@ -308,9 +308,9 @@ __device__ __forceinline__ Raw<T, U> pack_raw(const float (&v)[U]) {
 // Widths that the 16-byte vectors do not divide. Rows then start at any element, and a vector that is aligned for
 // one row is not for the next, so a lane reads and writes U elements at a time, the most that divide H (4, 2 or
 // 1), in accesses that are contiguous over the warp. A warp takes whole FP8 groups: NG of them, in registers, and
-// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 56 us, 8192 x 4092 52 us, 8192 x 4095
-// (single elements: bound by the accesses) 81 us, against 77, 75 and 78 us with whole vectors that were cut at the
-// aligned addresses and shifted into place, and 48 us at 4096. 1000 x 4090 fp16: 8.9 against 12.2 us.
+// a group's maximum is one warp reduction. 8192 x 4090 bf16 with the FP8 copy 57 us, 8192 x 4092 53 us, 8192 x 4095
+// (single elements: bound by the accesses) 82 us, against 77, 75 and 78 us with whole vectors that were cut at the
+// aligned addresses and shifted into place, and 49 us at 4096. 1000 x 4090 fp16: 8.9 against 12.2 us.
 template <typename T, int U, int NG>
 __global__ void __launch_bounds__(1024)
     add_rmsnorm_group_kernel(int H, const T* x, const T* residual, const T* __restrict__ gamma, float eps, T* h_out,
@@ -467,16 +467,16 @@ fp4moe_status norm_launch(int32_t rows, int32_t H, const void* x, const void* re
   const int64_t vecs = ((int64_t)H + N - 1) / N, groups = ((int64_t)H + 127) / 128;
   if (H % N == 0 && vecs <= 4 * 1024) {
     // vectors a thread: one while the rows leave SMs idle, two while an SM has one row or two or a row leaves four
-    // warps idle, else four, and as many as 1024 threads need (bf16 with the FP8 copy, two and four: 300 x 4096 2.9
-    // and 3.5 us, 8192 x 2048 25.5 and 26.4, 8192 x 4096 50.7 and 48.4, 4096 x 7168 50.1 and 43.5, 2000 x 8192 28.3
-    // and 26.2)
+    // warps idle, else four, and as many as 1024 threads need (bf16 with the FP8 copy, two and four: 300 x 4096 3.0
+    // and 3.6 us, 8192 x 2048 25.4 and 26.4, 8192 x 4096 50.8 and 48.5, 4096 x 7168 50.4 and 43.7, 2000 x 8192 28.5
+    // and 26.5)
     int nv = rows <= nsm ? 1 : rows <= 2 * nsm || vecs < 512 ? 2 : 4;
     while ((vecs + nv - 1) / nv > 1024) nv *= 2;
     threads = (int)((vecs + nv - 1) / nv + 31) / 32 * 32;
     kernel = vec_kernel<T>(nv);
   } else if (H % N != 0 && groups <= (sizeof(T) == 2 && H % 2 == 0 ? 8 : 4) * 32) {
-    // groups a warp: one while the rows leave SMs idle (64 x 4090 bf16 2.7 us, with eight 4.5), then four (8192 x 4090
-    // 56 us; one 95, eight 58), and eight where 32 warps need them and their registers suffice
+    // groups a warp: one while the rows leave SMs idle (64 x 4090 bf16 2.7 us, with eight 4.7), then four (8192 x 4090
+    // 57 us; one 96, eight 62), and eight where 32 warps need them and their registers suffice
     const int ng = groups > 4 * 32 ? 8 : rows > nsm || groups > 32 ? 4 : 1;
     threads = (int)((groups + ng - 1) / ng) * 32;
     if constexpr (sizeof(T) == 4)

@@ -150,9 +150,9 @@ __global__ void __launch_bounds__(SE_THREADS, 1)
 
   if (prm.wait_first) pdl_wait();
   pdl_trigger();
-  // The weights depend on no earlier kernel (or the wait above covers them), so the producer starts streaming them before it waits
-  // for the previous kernel (programmatic dependent launch); every other read of a predecessor's
-  // output waits first. Every CTA runs to the end (cluster peers read its shared memory), so an
+  // The weights depend on no earlier kernel (or the wait above covers them), so the producer starts streaming
+  // them before it waits for the previous kernel (programmatic dependent launch); every other read of a
+  // predecessor's output waits first. Every CTA runs to the end (cluster peers read its shared memory), so an
   // abort raised elsewhere only skips work.
   const int nt = blockIdx.x, mt = blockIdx.y, S = gridDim.z, z = blockIdx.z;
   const int px = nt % CX;  // position in the W1 pair
