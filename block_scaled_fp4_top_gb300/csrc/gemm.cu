@@ -504,21 +504,6 @@ bool encode_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner_bytes, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Scale tiles (512 bytes each) as a 3-D tensor [row_tiles][col_tiles][128 words], unswizzled boxes of
-// box_rows x box_cols whole tiles.
-bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t row_tiles, uint64_t col_tiles, uint32_t box_rows,
-                        uint32_t box_cols) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[3] = {128, col_tiles, row_tiles};
-  cuuint64_t strides[2] = {512, 512 * col_tiles};
-  cuuint32_t box[3] = {128, box_cols, box_rows};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 namespace {
 template <int MODE>
 bool configure_once() {

@@ -8,8 +8,6 @@
 namespace fp4moe {
 
 bool encode_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint32_t box_rows);
-bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t row_tiles, uint64_t col_tiles, uint32_t box_rows,
-                        uint32_t box_cols);
 
 constexpr int DK = 256;  // K elements per ring stage: 128 bytes of codes, 4 MMAs of K = 64
 

@@ -23,6 +23,8 @@
 // 8192 x 8192 x 2048 57 instead of 53), all 128 columns of an epilogue warp in flight at once (spills, 53), a stage's
 // scale copies ahead of the MMAs before it (50).
 // The rest (scale-factor ids, K tails, bounded waits) is as in mxdense.cu.
+#include <atomic>
+
 #include "internal.h"
 #include "mxdense.cuh"
 
@@ -351,6 +353,33 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     tc_fence_after();
     pair_tmem_dealloc(tmem, PTMEM_COLS);
   }
+}
+
+// The driver's cuTensorMapEncodeTiled, reached at run time: the library loads where there is no driver.
+decltype(&cuTensorMapEncodeTiled) tiled_encoder() {
+  static std::atomic<void*> known{nullptr};
+  void* p = known.load(std::memory_order_acquire);
+  if (p == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    known.store(p, std::memory_order_release);
+  }
+  return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(p);
+}
+
+// Scale tiles (512 bytes each) as a 3-D tensor [row_tiles][col_tiles][128 words], unswizzled boxes of
+// box_rows x box_cols whole tiles.
+bool encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t row_tiles, uint64_t col_tiles, uint32_t box_rows,
+                        uint32_t box_cols) {
+  const auto encode = tiled_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {128, col_tiles, row_tiles}, strides[2] = {512, 512 * col_tiles};
+  const cuuint32_t box[3] = {128, box_cols, box_rows}, es[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The cluster shape's launch attributes; PDL as in launch_pdl.
