@@ -730,3 +730,14 @@ def test_gemm_writes_every_element_of_many_rounds(fmt, dtype, M, N, K):
         ob.check()
         outs.append(ob.t)
     assert int(err[0]) == 0 and not outs[0].isnan().any() and torch.equal(*outs)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("M,N,K", [(8192, 8192, 1), (8192, 8192, 32), (8192, 4096, 100), (6000, 6000, 128), (5000, 7000, 129)])
+def test_gemm_large_tiles_of_less_than_a_stage(fmt, M, N, K):
+    """Fewer scale tiles across K than a load's box takes."""
+    from block_scaled_fp4_top_gb300 import api
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert api.fp4moe_mx_gemm_plan(M, N, K, sms) == (256, 256, 1)
+    test_gemm_large_tiles_with_every_scale_row(fmt, "float32", M, N, K)
