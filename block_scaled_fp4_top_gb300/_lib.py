@@ -14,10 +14,11 @@ c_i32, c_u32, c_f32, c_sz, c_vp = ctypes.c_int32, ctypes.c_uint32, ctypes.c_floa
 c_i64 = ctypes.c_int64
 
 OK, INVALID_ARG, MISALIGNED, CAPACITY, UNSUPPORTED, CUDA_ERROR = range(6)
-ERR_TIMEOUT, ERR_EXPERT_ID, ERR_CAPACITY, ERR_NAN, ERR_SCALE_RANGE = 0x1, 0x2, 0x4, 0x8, 0x10
+ERR_TIMEOUT, ERR_EXPERT_ID, ERR_CAPACITY, ERR_NAN, ERR_SCALE_RANGE, ERR_PAGE = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 SAT_L1, SAT_L2 = 0x1, 0x2
 W_NVFP4, W_MXFP4 = 0, 1
 BF16, FP16, FP32 = 0, 1, 2
+KV_MAX_SEQS, ATTENTION_WORKSPACE_BYTES = 8192, 64 << 20
 
 
 class Config(ctypes.Structure):
@@ -31,8 +32,15 @@ class SharedWeights(ctypes.Structure):
     _fields_ = [("w1", c_vp), ("w1_scales", c_vp), ("w2", c_vp), ("w2_scales", c_vp)]
 
 
+class KvCache(ctypes.Structure):
+    """fp4moe_kv_cache: sizes and strides of a paged key-value cache."""
+    _fields_ = [("dtype", c_i32), ("kv_heads", c_i32), ("head_dim", c_i32), ("page_size", c_i32), ("num_pages", c_i32),
+                ("page_stride", c_i64), ("token_stride", c_i64), ("head_stride", c_i64)]
+
+
 CP = ctypes.POINTER(Config)
 SWP = ctypes.POINTER(SharedWeights)
+KVP = ctypes.POINTER(KvCache)
 
 # name -> (restype, argtypes); pointers to device memory are passed as c_void_p
 SIGNATURES = {
@@ -77,6 +85,11 @@ SIGNATURES = {
     "fp4moe_mx_dequantize": (c_i32, [c_i32] * 4 + [c_vp] * 5),
     "fp4moe_mx_gemm_plan": (c_i32, [c_i32] * 4 + [ctypes.POINTER(c_i32)] * 3),
     "fp4moe_mx_gemm": (c_i32, [c_i32] * 5 + [c_vp] * 8),
+    "fp4moe_kv_plan": (c_i32, [c_i32] * 3 + [c_vp] * 3 + [c_i32] + [c_vp] * 5 + [c_i32] + [c_vp] * 4),
+    "fp4moe_rope_cache": (c_i32, [KVP, c_i32, c_i32] + [c_vp, c_i64] * 3 + [c_vp] * 2 + [c_i32] * 3 +
+                          [c_vp, c_f32, c_vp, c_i64] + [c_vp] * 4),
+    "fp4moe_paged_attention": (c_i32, [KVP, c_vp, c_vp] + [c_i32] * 3 + [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_f32,
+                                                                     c_i32, c_i32, c_vp, c_i64] + [c_vp] * 4),
 }
 
 _lib = None

@@ -8,11 +8,13 @@ layer's arithmetic runs in the CUDA kernels of libfp4moe.so.
 ``MoELayer`` is a convenience owner of the buffers (allocated through torch)
 for one configuration. It also runs the load-time prep: weight quantisation,
 calibration and alpha tables. ``MxLinear`` is the same for a projection with
-microscaled 4-bit weights.
+microscaled 4-bit weights, ``PagedKvCache`` for a key-value cache and the
+attention over it.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 
 import torch
@@ -421,6 +423,169 @@ def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream
            "fp4moe_mx_gemm")
 
 
+# ------------------------------------------------- the paged key-value cache
+_I32, _F64 = torch.int32, torch.float64
+_KV_DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16}
+
+
+def _arg_ints(name, t, n, dev):
+    """The pointer of n int32 values (n None: any number of them)."""
+    if t.dtype is not _I32 or t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise Fp4MoeError(f"{name}: expected {'a vector' if n is None else n} of {_I32}, got {tuple(t.shape)} of {t.dtype}")
+    if t.get_device() != dev or not t.is_contiguous():
+        _place(name, t, dev)
+    return t.data_ptr()
+
+
+def _arg_table(name, t, B, dev):
+    """(columns, pointer) of a page table of B rows."""
+    if t.dtype is not _I32 or t.dim() != 2 or t.shape[0] != B:
+        raise Fp4MoeError(f"{name}: expected [{B}, columns] of {_I32}, got {tuple(t.shape)} of {t.dtype}")
+    if t.get_device() != dev or not t.is_contiguous():
+        _place(name, t, dev)
+    return t.shape[1], t.data_ptr()
+
+
+def _arg_err(err, dev):
+    if err.element_size() * err.numel() < 4:
+        raise Fp4MoeError("err: expected a device word of 4 bytes")
+    _place("err", err, dev)
+    return err.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, dev):
+    """(fp4moe_kv_cache, pointer of k, pointer of v) of two caches [pages, page size, kv heads, head dim], each
+    contiguous or a view of another order of pages, tokens and heads (the same for both)."""
+    shape, dt = k_cache.shape, k_cache.dtype
+    d = _KV_DTYPES.get(dt)
+    if d is None or len(shape) != 4:
+        raise Fp4MoeError("k_cache: expected [pages, page size, kv heads, head dim] of bfloat16 or float16, got "
+                          f"{tuple(shape)} of {dt}")
+    if v_cache.shape != shape or v_cache.dtype is not dt:
+        raise Fp4MoeError(f"v_cache: expected {tuple(shape)} of {dt}, got {tuple(v_cache.shape)} of {v_cache.dtype}")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise Fp4MoeError("k_cache, v_cache: expected CUDA tensors on the current device")
+    # (the stride of a dimension of one element says nothing)
+    st = [0 if n == 1 else s for n, s in zip(shape, k_cache.stride())]
+    if st != [0 if n == 1 else s for n, s in zip(shape, v_cache.stride())] or st[3] != 1 or any(s % 8 for s in st[:3]):
+        raise Fp4MoeError("k_cache, v_cache: expected the same strides, head dim contiguous, the others multiples of 8")
+    return _lib.KvCache(d, shape[2], shape[3], shape[1], shape[0], st[0], st[1], st[2]), k_cache.data_ptr(), v_cache.data_ptr()
+
+
+def _arg_heads(name, t, T, D, dt, dev):
+    """(heads, row stride, pointer) of [T, heads, D]: whole rows, any distance apart."""
+    shape = t.shape
+    if t.dtype is not dt or len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise Fp4MoeError(f"{name}: expected [{T}, heads, {D}] of {dt}, got {tuple(shape)} of {t.dtype}")
+    row, head, one = t.stride()
+    H = shape[1]
+    if T <= 1:
+        row = H * D
+    if t.get_device() != dev or one != 1 or (H > 1 and head != D) or row % 8 or row < H * D:
+        raise Fp4MoeError(f"{name}: expected rows of contiguous heads on the current device, a multiple of 8 elements apart")
+    return H, row, t.data_ptr()
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, factor: float = 1.0, original_len: int | None = None,
+                  slow: float = 1.0, fast: float = 32.0, device="cuda") -> torch.Tensor:
+    """fp64 radians per position of the rot_dim / 2 pairs: base^(-2 i / rot_dim), scaled for contexts `factor` times as
+    long. Without original_len all are divided by factor (positions are interpolated). With it, pairs that turn at least
+    `fast` times in original_len positions keep their frequency, those that turn at most `slow` times are divided by
+    factor, and in between the two are mixed linearly in the number of turns (YaRN, arXiv:2309.00071, section 3.2, which
+    goes with an amplitude of 0.1 ln(factor) + 1)."""
+    if rot_dim < 0 or rot_dim % 2 or not base > 0 or not factor > 0 or not fast > slow:
+        raise Fp4MoeError("rope_inv_freq: rot_dim must be even, base and factor positive, fast above slow")
+    f = torch.tensor([base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], dtype=_F64)
+    if original_len is None:
+        f = f / factor
+    else:
+        keep = ((original_len * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    return f.to(device)
+
+
+def fp4moe_kv_plan(page_size, cached_len, new_len, page_table, free_pages, free_count, kv_len, free_count_out, q_offset,
+                   position, slot, err, stream=None):
+    """A step's pages, row offsets, positions and cache slots from its sequences' lengths (all int32, on the device):
+    cached_len, new_len (negative: tokens given back), kv_len [B]; page_table [B, columns]; free_pages [pages];
+    free_count, free_count_out [1]; q_offset [B + 1]; position, slot [rows]. kv_len may be cached_len and free_count_out
+    may be free_count."""
+    dev = _current_device()
+    B = cached_len.shape[0]
+    columns, pt = _arg_table("page_table", page_table, B, dev)
+    rows = slot.shape[0]
+    _check(_lib.load().fp4moe_kv_plan(B, page_size, free_pages.shape[0], _arg_ints("cached_len", cached_len, B, dev),
+                                      _arg_ints("new_len", new_len, B, dev), pt, columns,
+                                      _arg_ints("free_pages", free_pages, None, dev),
+                                      _arg_ints("free_count", free_count, 1, dev), _arg_ints("kv_len", kv_len, B, dev),
+                                      _arg_ints("free_count_out", free_count_out, 1, dev),
+                                      _arg_ints("q_offset", q_offset, B + 1, dev), rows,
+                                      _arg_ints("position", position, rows, dev), _arg_ints("slot", slot, rows, dev),
+                                      _arg_err(err, dev), _s(stream)), "fp4moe_kv_plan")
+
+
+def fp4moe_rope_cache(q, k, v, position, slot, inv_freq, q_out, k_cache, v_cache, err, first=0, interleaved=False,
+                      amplitude=1.0, stream=None):
+    """Rotary positions of q [T, heads, D] -> q_out, and of k; k and v [T, kv heads, D] -> their slots of the caches
+    [pages, page size, kv heads, D]. q, k and v may be column slices of one projection's rows; q_out may be q; q and
+    q_out, or k and v, may be None. position, slot [T] int32; inv_freq fp64: the pairs of the turned part of the head,
+    which starts at element `first` (rope_inv_freq)."""
+    dev = _current_device()
+    c, pk, pv = _kv_cache(k_cache, v_cache, dev)
+    dt, D = k_cache.dtype, c.head_dim
+    T = slot.shape[0]
+    if inv_freq.dtype is not _F64 or inv_freq.dim() != 1:
+        raise Fp4MoeError(f"inv_freq: expected a vector of {_F64}, got {tuple(inv_freq.shape)} of {inv_freq.dtype}")
+    _place("inv_freq", inv_freq, dev)
+    Hq = q_stride = q_out_stride = k_stride = v_stride = 0
+    ptr_q = ptr_qo = ptr_k = ptr_v = None
+    if (q is None) != (q_out is None) or (k is None) != (v is None):
+        raise Fp4MoeError("q and q_out, and k and v, are both given or both None")
+    if q is not None:
+        Hq, q_stride, ptr_q = _arg_heads("q", q, T, D, dt, dev)
+        Ho, q_out_stride, ptr_qo = _arg_heads("q_out", q_out, T, D, dt, dev)
+        if Ho != Hq:
+            raise Fp4MoeError(f"q_out: expected {Hq} heads, got {Ho}")
+        if ptr_q == ptr_qo and q_stride != q_out_stride:
+            raise Fp4MoeError("q_out: in place means with q's own stride")
+    if k is not None:
+        Hk, k_stride, ptr_k = _arg_heads("k", k, T, D, dt, dev)
+        Hv, v_stride, ptr_v = _arg_heads("v", v, T, D, dt, dev)
+        if Hk != c.kv_heads or Hv != c.kv_heads:
+            raise Fp4MoeError(f"k, v: expected the caches' {c.kv_heads} heads, got {Hk} and {Hv}")
+    else:
+        pk = pv = None
+    _check(_lib.load().fp4moe_rope_cache(c, T, Hq, ptr_q, q_stride, ptr_k, k_stride, ptr_v, v_stride,
+                                         _arg_ints("position", position, T, dev), _arg_ints("slot", slot, T, dev), first,
+                                         2 * inv_freq.shape[0], interleaved, inv_freq.data_ptr(), amplitude, ptr_qo,
+                                         q_out_stride, pk, pv, _arg_err(err, dev), _s(stream)), "fp4moe_rope_cache")
+
+
+def fp4moe_paged_attention(q, k_cache, v_cache, page_table, kv_len, q_offset, scale, out, lse, ws, err, causal=True,
+                           window=0, stream=None):
+    """out [T, heads, D] of q [T, heads, D] over each sequence's pages: rows q_offset[b] .. q_offset[b + 1] read the
+    kv_len[b] keys of page_table[b]. causal: they are its last tokens, and each sees the keys up to its own (window > 0:
+    the last `window` of them); else every row sees all keys. lse [T, heads] float32 or None; ws: a zeroed workspace of
+    ATTENTION_WORKSPACE_BYTES that the caller keeps."""
+    dev = _current_device()
+    c, pk, pv = _kv_cache(k_cache, v_cache, dev)
+    T, D, dt = q.shape[0], c.head_dim, k_cache.dtype
+    H, q_stride, ptr_q = _arg_heads("q", q, T, D, dt, dev)
+    Ho, out_stride, ptr_o = _arg_heads("out", out, T, D, dt, dev)
+    if Ho != H:
+        raise Fp4MoeError(f"out: expected {H} heads, got {Ho}")
+    B = kv_len.shape[0]
+    columns, pt = _arg_table("page_table", page_table, B, dev)
+    if ws.element_size() * ws.numel() < _lib.ATTENTION_WORKSPACE_BYTES:
+        raise Fp4MoeError(f"ws: expected {_lib.ATTENTION_WORKSPACE_BYTES} bytes")
+    _place("ws", ws, dev)
+    _check(_lib.load().fp4moe_paged_attention(c, pk, pv, B, T, H, ptr_q, q_stride, pt, columns,
+                                              _arg_ints("kv_len", kv_len, B, dev),
+                                              _arg_ints("q_offset", q_offset, B + 1, dev), scale, causal, window, ptr_o,
+                                              out_stride, _arg("lse", lse, (T, H), _F32, dev), ws.data_ptr(),
+                                              _arg_err(err, dev), _s(stream)), "fp4moe_paged_attention")
+
+
 # --------------------------------------------------------------------------
 @dataclass
 class Weights:
@@ -644,6 +809,50 @@ class MxLinear:
         _check(lib.fp4moe_mx_quantize(self.fmt, dx, T, K, px, _p(self.gx), codes, sf, s), "fp4moe_mx_quantize")
         _check(lib.fp4moe_mx_gemm(self.fmt, do, T, self.N, K, codes, sf, self.w_codes.data_ptr(),
                                   self.w_sf.data_ptr(), _p(self.alpha), po, self.err.data_ptr(), s), "fp4moe_mx_gemm")
+
+    def read_error(self, clear=True) -> int:
+        return fp4moe_read_error(self.err, clear)
+
+
+class PagedKvCache:
+    """Keys and values of `layers` layers in pages, for at most max_seqs sequences of at most max_len tokens and steps of at
+    most max_rows rows. The layers share page tables and lengths; every sequence starts empty.
+
+    A step: plan(new_len) once, then for each layer append(...) and attend(...). All are calls on the device's own lengths,
+    so a step of given numbers of sequences and rows can be captured into a CUDA graph; plan advances the lengths at every
+    replay. Calls of one object must be ordered on one stream (or by events)."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int, max_len: int,
+                 max_rows: int, layers: int = 1, dtype: torch.dtype = torch.bfloat16, device: str = "cuda"):
+        shape = (num_pages, page_size, kv_heads, head_dim)
+        self.k, self.v = ([torch.zeros(shape, dtype=dtype, device=device) for _ in range(layers)] for _ in range(2))
+        i32 = dict(dtype=torch.int32, device=device)
+        self.page_size = page_size
+        self.page_table = torch.full((max_seqs, (max_len + page_size - 1) // page_size), -1, **i32)
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)  # page 0 is taken first
+        self.free_count = torch.full((1,), num_pages, **i32)
+        self.kv_len = torch.zeros(max_seqs, **i32)
+        self.q_offset = torch.zeros(max_seqs + 1, **i32)
+        self.position, self.slot = torch.zeros(max_rows, **i32), torch.full((max_rows,), -1, **i32)
+        self.ws = torch.zeros(_lib.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        self.err = torch.zeros(4, **i32)
+
+    def plan(self, new_len: torch.Tensor, stream=None):
+        """new_len [max_seqs] int32 on the device: tokens that each sequence adds (negative: gives back)."""
+        fp4moe_kv_plan(self.page_size, self.kv_len, new_len, self.page_table, self.free_pages, self.free_count,
+                       self.kv_len, self.free_count, self.q_offset, self.position, self.slot, self.err, stream)
+
+    def append(self, q, k, v, inv_freq, q_out, first: int = 0, interleaved: bool = False, amplitude: float = 1.0,
+               layer: int = 0, stream=None):
+        """The step's q [T, heads, D] turned into q_out (may be q), its k and v [T, kv heads, D] into the cache."""
+        T = k.shape[0]
+        fp4moe_rope_cache(q, k, v, self.position[:T], self.slot[:T], inv_freq, q_out, self.k[layer], self.v[layer],
+                          self.err, first, interleaved, amplitude, stream)
+
+    def attend(self, q, scale: float, out, lse=None, window: int = 0, layer: int = 0, stream=None):
+        """out [T, heads, D] of the step's turned q over the sequences' pages."""
+        fp4moe_paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.kv_len, self.q_offset, scale, out,
+                               lse, self.ws, self.err, True, window, stream)
 
     def read_error(self, clear=True) -> int:
         return fp4moe_read_error(self.err, clear)

@@ -835,4 +835,95 @@ fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N
                          (cudaStream_t)stream);
 }
 
+// ------------------------------------------------- the paged key-value cache
+namespace {
+constexpr int32_t kMaxHeads = 65535;  // grid rows
+fp4moe_status check_kv_pages(int32_t page_size, int32_t num_pages) {
+  if (page_size < 1 || num_pages < 1 || (int64_t)page_size * num_pages > INT32_MAX) return FP4MOE_INVALID_ARG;
+  return FP4MOE_OK;
+}
+fp4moe_status check_kv_cache(const fp4moe_kv_cache* c) {
+  if (c == nullptr) return FP4MOE_INVALID_ARG;
+  if (c->dtype != FP4MOE_BF16 && c->dtype != FP4MOE_FP16) return FP4MOE_UNSUPPORTED;
+  if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0) return FP4MOE_UNSUPPORTED;
+  if (c->kv_heads < 1 || c->kv_heads > kMaxHeads) return FP4MOE_INVALID_ARG;
+  FP4_TRY(check_kv_pages(c->page_size, c->num_pages));
+  for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+    if (s < 0 || s >= ((int64_t)1 << 40) || s % 8 != 0) return FP4MOE_INVALID_ARG;
+  return FP4MOE_OK;
+}
+// The distance between the rows of T tokens of `width` elements each.
+bool row_stride_ok(int32_t T, int64_t stride, int64_t width) {
+  return stride % 8 == 0 && (T <= 1 || stride >= width) && stride >= 0 && stride < ((int64_t)1 << 40);
+}
+}  // namespace
+
+fp4moe_status fp4moe_kv_plan(int32_t num_seqs, int32_t page_size, int32_t num_pages, const int32_t* cached_len,
+                             const int32_t* new_len, int32_t* page_table, int32_t table_columns, int32_t* free_pages,
+                             const int32_t* free_count, int32_t* kv_len, int32_t* free_count_out, int32_t* q_offset,
+                             int32_t rows, int32_t* position, int32_t* slot, uint32_t* err, fp4moe_stream_t stream) {
+  if (num_seqs < 0 || table_columns < 0 || rows < 0) return FP4MOE_INVALID_ARG;
+  FP4_TRY(check_kv_pages(page_size, num_pages));
+  if (num_seqs > FP4MOE_KV_MAX_SEQS) return FP4MOE_UNSUPPORTED;
+  FP4_TRY(check_ptrs(free_pages, free_count, free_count_out, q_offset, err));
+  if (num_seqs > 0) FP4_TRY(check_ptrs(cached_len, new_len, kv_len));
+  if (num_seqs > 0 && table_columns > 0) FP4_TRY(check_ptrs(page_table));
+  if (rows > 0) FP4_TRY(check_ptrs(position, slot));
+  return kv_plan_launch(num_seqs, page_size, num_pages, cached_len, new_len, page_table, table_columns, free_pages,
+                        free_count, kv_len, free_count_out, q_offset, rows, position, slot, err, (cudaStream_t)stream);
+}
+
+fp4moe_status fp4moe_rope_cache(const fp4moe_kv_cache* cache, int32_t T, int32_t q_heads, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const int32_t* position, const int32_t* slot, int32_t rot_first, int32_t rot_dim,
+                                int32_t interleaved, const double* inv_freq, float amplitude, void* q_out,
+                                int64_t q_out_stride, void* k_cache, void* v_cache, uint32_t* err,
+                                fp4moe_stream_t stream) {
+  FP4_TRY(check_kv_cache(cache));
+  const int32_t D = cache->head_dim;
+  if (T < 0 || q_heads < 0 || q_heads + 2 * (int64_t)cache->kv_heads > kMaxHeads) return FP4MOE_INVALID_ARG;
+  if ((int64_t)T * (q_heads + 2 * (int64_t)cache->kv_heads) > INT32_MAX) return FP4MOE_INVALID_ARG;
+  if (rot_first < 0 || rot_dim < 0 || rot_dim % 2 != 0 || rot_first > D - rot_dim) return FP4MOE_INVALID_ARG;
+  if (std::isnan(amplitude) || std::isinf(amplitude)) return FP4MOE_INVALID_ARG;
+  if (T == 0) return FP4MOE_OK;  // an empty batch's buffers may be null
+  const bool with_q = q != nullptr, with_kv = k != nullptr;
+  if (with_q != (q_out != nullptr) || (!with_q && q_heads != 0)) return FP4MOE_INVALID_ARG;
+  if (with_kv != (v != nullptr) || with_kv != (k_cache != nullptr) || with_kv != (v_cache != nullptr))
+    return FP4MOE_INVALID_ARG;
+  if (with_q && (!row_stride_ok(T, q_stride, (int64_t)q_heads * D) || !row_stride_ok(T, q_out_stride, (int64_t)q_heads * D)))
+    return FP4MOE_INVALID_ARG;
+  const int64_t kv_width = (int64_t)cache->kv_heads * D;
+  if (with_kv && (!row_stride_ok(T, k_stride, kv_width) || !row_stride_ok(T, v_stride, kv_width))) return FP4MOE_INVALID_ARG;
+  if (!with_kv && q_heads == 0) return FP4MOE_OK;
+  FP4_TRY(check_ptrs(position, slot, err));
+  if (rot_dim > 0) FP4_TRY(check_ptrs(inv_freq));
+  for (const void* p : {q, k, v, (const void*)q_out, (const void*)k_cache, (const void*)v_cache}) FP4_TRY(check_opt(p));
+  if (with_kv && k_cache == v_cache) return FP4MOE_INVALID_ARG;  // two results, one buffer
+  return rope_cache_launch(*cache, T, q_heads, q, q_stride, k, k_stride, v, v_stride, position, slot, rot_first, rot_dim,
+                           interleaved != 0, inv_freq, amplitude, q_out, q_out_stride, k_cache, v_cache, err,
+                           (cudaStream_t)stream);
+}
+
+fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k_cache, const void* v_cache,
+                                     int32_t num_seqs, int32_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                                     const int32_t* page_table, int32_t table_columns, const int32_t* kv_len,
+                                     const int32_t* q_offset, float scale, int32_t causal, int32_t window, void* out,
+                                     int64_t out_stride, float* lse, void* ws, uint32_t* err, fp4moe_stream_t stream) {
+  FP4_TRY(check_kv_cache(cache));
+  if (num_seqs < 0 || T < 0 || table_columns < 0 || window < 0) return FP4MOE_INVALID_ARG;
+  if (num_seqs > FP4MOE_KV_MAX_SEQS) return FP4MOE_UNSUPPORTED;
+  if (q_heads < 1 || q_heads % cache->kv_heads != 0 || (int64_t)T * q_heads > INT32_MAX) return FP4MOE_INVALID_ARG;
+  if (!(scale > 0.0f) || std::isinf(scale) || (window > 0 && !causal)) return FP4MOE_INVALID_ARG;
+  const int64_t width = (int64_t)q_heads * cache->head_dim;
+  if (!row_stride_ok(T, q_stride, width) || !row_stride_ok(T, out_stride, width)) return FP4MOE_INVALID_ARG;
+  if (T == 0 || num_seqs == 0) return FP4MOE_OK;
+  FP4_TRY(check_ptrs(k_cache, v_cache, q, kv_len, q_offset, out, ws, err));
+  if (table_columns > 0) FP4_TRY(check_ptrs(page_table));
+  FP4_TRY(check_opt(lse));
+  if (out == q) return FP4MOE_INVALID_ARG;  // other tiles read q while out is written
+  return paged_attention_launch(*cache, k_cache, v_cache, num_seqs, T, q_heads, q, q_stride, page_table, table_columns,
+                                kv_len, q_offset, scale, causal != 0, window, out, out_stride, lse, ws, err,
+                                (cudaStream_t)stream);
+}
+
 }  // extern "C"

@@ -1,0 +1,469 @@
+// Attention over the paged cache for few rows a sequence and kv head (fp4moe_paged_attention): decoding, proposed tokens.
+//
+// One pass over the keys: with the running maximum m and sum l of a row, each group of 16 keys adds
+//   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), O' = O 2^(m - m') + sum 2^(s - m') v    (s in powers of two).
+// The bytes of k and v bound it: 16 rows of a tile cost 64 KFLOP for 8 KB of a group (head_dim 128), far below what
+// mma.sync gives, so the tile's M = 16 is that of mma.sync, and a warp works alone: it brings its own groups of 16 keys by
+// cp.async through a ring of its own, without any barrier between warps, and joins the others at the end of a tile only.
+// Any page size and stride: a lane works out its key's place and hands it to the lanes that copy the key's 16-byte
+// pieces; the page of the next group is looked up a group ahead.
+// Keys outside the tile's range are zeros in shared memory. Keys that only some rows of a tile see have score -infinity
+// in the others; where such a v is not finite (0 times it would be NaN) the group's product is made without those rows.
+#include "attn.cuh"
+
+namespace fp4moe {
+namespace {
+
+constexpr int AD_ROWS = 16, AD_KEYS = 16;  // of a tile, of a warp's group
+
+template <int DP>
+struct AttnCfg {
+  static constexpr int kWarps = DP == 256 ? 4 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int S = AD_KEYS * kWarps;       // keys of a slice: one group a warp
+  static constexpr int kStage = 2 * AD_KEYS * DP * 2;  // k and v of a group
+  static constexpr int kStages = 196608 / (kWarps * kStage);
+  static constexpr int kRing = kStages * kStage;   // of a warp
+  static constexpr int kSmem = kWarps * kRing;
+  static constexpr int kPitch = DP + 8;            // floats between rows of a warp's sums: no bank conflicts
+  static_assert(AD_ROWS * kPitch * 4 <= kRing, "sums fit the ring");
+  static_assert((FP4MOE_KV_MAX_SEQS + kWarps + 1) * 8 <= kSmem, "the division's sums fit");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool use) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(uint4 v) {
+  constexpr uint32_t E = std::is_same_v<T, __nv_bfloat16> ? 0x7F80u : 0x7C00u;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || ((w[i] >> 16) & E) == E;
+  return bad;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(AttnParams p) {
+  using C = AttnCfg<DP>;
+  constexpr int CH = DP / 8, KS = DP / 16, NT = DP / 8;  // 16-byte pieces of a key, MMA steps, output columns of 8
+  constexpr int RPI = 32 / CH;                           // keys that one copy instruction of the warp covers
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ float stats[C::kWarps][AD_ROWS][2];
+  __shared__ uint32_t arrived;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const AttnRun run = attn_plan<AD_ROWS, C::S, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
+  uint8_t* ring = sm + warp * C::kRing;
+  const uint32_t ring32 = smem_u32(ring);
+  const T* kbase = static_cast<const T*>(p.k);
+  const T* vbase = static_cast<const T*>(p.v);
+  const int dims = (p.D + 15) / 16 * 16;  // MMA steps past the head's own dims are left out
+  const int qr = lane >> 2, qc = (lane & 3) * 2;
+  int b = run.seq, tile = run.tile, head = run.head, s0 = run.slice;
+  for (int64_t x = run.begin; x < run.end;) {
+    const int kv = __ldg(p.kv_len + b);
+    const AttnSeq seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), kv);
+    if (tile * AD_ROWS >= seq.rows) {  // the next sequence
+      ++b;
+      tile = head = s0 = 0;
+      continue;
+    }
+    const int2 range = attn_tile_range<AD_ROWS>(p, seq, kv, tile);
+    const int n = attn_slices<C::S>(range);
+    const int s1 = (int)min((int64_t)n, s0 + (run.end - x));
+    const int row0 = tile * AD_ROWS, rows = min(AD_ROWS, seq.rows - row0);
+    // ---- this lane's two rows: q as the MMA's A, and the keys they see
+    uint32_t qa[KS][4];
+    int2 see[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = row0 + min(qr + 8 * i, rows - 1);  // rows past the last are computed with it, and dropped
+      const int tok = (int)p.group.div(r), g = r - tok * (int)p.group.d;
+      see[i] = attn_range(p, seq, kv, tok);
+      const T* q = static_cast<const T*>(p.q) + (int64_t)(seq.first + tok) * p.q_stride +
+                   (int64_t)(head * (int)p.group.d + g) * p.D + qc;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int d = ks * 16 + 8 * j;
+          qa[ks][i + 2 * j] = d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
+        }
+    }
+    // keys that every row of the tile sees
+    const int all_lo = attn_range(p, seq, kv, (int)p.group.div(row0 + rows - 1)).x;
+    const int all_hi = attn_range(p, seq, kv, (int)p.group.div(row0)).y;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+
+    const int base = range.x / C::S * C::S + warp * AD_KEYS;  // first key of this warp's group of slice 0
+    const int32_t* table = p.table + (int64_t)b * p.columns;
+    const int64_t head_off = (int64_t)head * p.map.head_stride;
+    auto page_of = [&](int s) {  // page of the key that this lane looks up in slice s; -2: none
+      const int key = base + s * C::S + (lane & 15);
+      return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
+    };
+    auto issue = [&](int s, int page, int stage) {
+      if (s < s1) {
+        const int key = base + s * C::S + (lane & 15);
+        int64_t off = -1;
+        if (page != -2) {
+          if ((uint32_t)page < (uint32_t)p.map.num_pages) {
+            off = page * p.map.page_stride +
+                  (int64_t)(key - (int)p.map.page.div(key) * (int)p.map.page.d) * p.map.token_stride + head_off;
+          } else {
+            raise_error(p.err, FP4MOE_ERR_PAGE);
+          }
+        }
+        const int c = lane % CH;
+        const uint32_t dst0 = ring32 + stage * C::kStage;
+#pragma unroll
+        for (int it = 0; it < AD_KEYS / RPI; ++it) {
+          const int r = it * RPI + lane / CH;
+          const int64_t ro = __shfl_sync(0xFFFFFFFFu, off, r);
+          const bool use = ro >= 0 && c * 8 < p.D;
+          const int64_t src = use ? ro + c * 8 : 0;
+          const uint32_t dst = dst0 + r * (DP * 2) + ((c ^ (r & 7)) << 4);
+          if (c * 8 < dims) {
+            cp_async16(dst, kbase + src, use);
+            cp_async16(dst + AD_KEYS * DP * 2, vbase + src, use);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    int next = page_of(s0);
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      const int page = next;
+      next = page_of(s0 + i + 1);
+      issue(s0 + i, page, i);
+    }
+    int stage = 0, fill = C::kStages - 1;
+    for (int s = s0; s < s1; ++s) {
+      const int page = next;
+      next = page_of(s + C::kStages);
+      cp_async_wait<C::kStages - 2>();
+      __syncwarp();
+      const int k0 = base + s * C::S;
+      const uint32_t kst = ring32 + stage * C::kStage, vst = kst + AD_KEYS * DP * 2;
+      if (k0 < range.y && k0 + AD_KEYS > range.x) {
+        float sc[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          if (ks * 16 < dims) {
+            uint32_t f[4];
+            const int key = (lane >> 4) * 8 + (lane & 7), c = ks * 2 + ((lane >> 3) & 1);
+            ldsm4(f, kst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
+            mma16816<T>(sc[0], qa[ks], f[0], f[1]);
+            mma16816<T>(sc[1], qa[ks], f[2], f[3]);
+          }
+        }
+        const bool edge = k0 < all_lo || k0 + AD_KEYS > all_hi;
+        if (edge) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = k0 + t * 8 + qc + (e & 1);
+              if (key < see[e >> 1].x || key >= see[e >> 1].y) sc[t][e] = -INFINITY;
+            }
+        }
+        float nm[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+          nm[i] = fmaxf(m[i], v);
+        }
+        if (__any_sync(0xFFFFFFFFu, nm[0] != m[0] || nm[1] != m[1])) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float f = exp2_fast((m[i] - safe_max(nm[i])) * p.scale_log2);
+            l[i] *= f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              o[t][2 * i] *= f;
+              o[t][2 * i + 1] *= f;
+            }
+            m[i] = nm[i];
+          }
+        }
+        float pr[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mb = safe_max(m[i]) * p.scale_log2;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              pr[t][2 * i + e] = exp2_fast(fmaf(sc[t][2 * i + e], p.scale_log2, -mb));
+              l[i] += pr[t][2 * i + e];
+            }
+        }
+        bool odd = false;  // a v that some rows must not touch even with weight 0
+        if (edge && (all_lo != range.x || all_hi != range.y)) {
+          for (int it = 0; it < AD_KEYS / RPI; ++it) {
+            const int r = it * RPI + lane / CH, c = lane % CH;
+            if (c * 8 < dims)
+              odd |= any_nonfinite<T>(
+                  *reinterpret_cast<const uint4*>(ring + stage * C::kStage + AD_KEYS * DP * 2 + r * (DP * 2) + ((c ^ (r & 7)) << 4)));
+          }
+          odd = __any_sync(0xFFFFFFFFu, odd);
+        }
+        if (!odd) {
+          // the weights are rounded to the cache's type for the MMA: half a step each, against a result of that type
+          const uint32_t pa[4] = {pack2<T>(pr[0][0], pr[0][1]), pack2<T>(pr[0][2], pr[0][3]), pack2<T>(pr[1][0], pr[1][1]),
+                                  pack2<T>(pr[1][2], pr[1][3])};
+#pragma unroll
+          for (int t = 0; t < NT; t += 2) {
+            if (t * 8 < dims) {
+              uint32_t f[4];
+              const int key = ((lane >> 3) & 1) * 8 + (lane & 7), c = t + (lane >> 4);
+              ldsm4_t(f, vst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
+              mma16816<T>(o[t], pa, f[0], f[1]);
+              mma16816<T>(o[t + 1], pa, f[2], f[3]);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < AD_KEYS; ++c) {
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float a = (c & 1) ? pr[0][2 * i + 1] : pr[0][2 * i], d = (c & 1) ? pr[1][2 * i + 1] : pr[1][2 * i];
+              w[i] = __shfl_sync(0xFFFFFFFFu, c < 8 ? a : d, (lane & ~3) + ((c & 7) >> 1));
+            }
+            const bool in0 = k0 + c >= see[0].x && k0 + c < see[0].y, in1 = k0 + c >= see[1].x && k0 + c < see[1].y;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if (t * 8 < dims) {
+                const T* v = reinterpret_cast<const T*>(ring + stage * C::kStage + AD_KEYS * DP * 2 + c * (DP * 2) +
+                                                        ((t ^ (c & 7)) << 4)) + qc;
+                const float v0 = to_f32(v[0]), v1 = to_f32(v[1]);
+                if (in0) {
+                  o[t][0] = fmaf(w[0], v0, o[t][0]);
+                  o[t][1] = fmaf(w[0], v1, o[t][1]);
+                }
+                if (in1) {
+                  o[t][2] = fmaf(w[1], v0, o[t][2]);
+                  o[t][3] = fmaf(w[1], v1, o[t][3]);
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      issue(s + C::kStages - 1, page, fill);
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      fill = fill + 1 == C::kStages ? 0 : fill + 1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    // ---- the warps' sums, in their rings
+    float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+      if ((lane & 3) == 0) {
+        stats[warp][qr + 8 * i][0] = m[i];
+        stats[warp][qr + 8 * i][1] = l[i];
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<float2*>(mine + (qr + 8 * i) * C::kPitch + t * 8 + qc) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
+    }
+    __syncthreads();
+    constexpr int TPR = C::kThreads / AD_ROWS, NJ = DP / (4 * TPR);  // threads of a row, vectors of a thread
+    const int r = tid / TPR, dv = (tid % TPR) * 4;
+    float M = -INFINITY, L = 0.0f;
+    float4 acc[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, stats[w][r][0]);
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      const float f = exp2_fast((stats[w][r][0] - safe_max(M)) * p.scale_log2);
+      L = fmaf(stats[w][r][1], f, L);
+      const float* src = reinterpret_cast<const float*>(sm + w * C::kRing) + r * C::kPitch + dv;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(src + j * 4 * TPR);
+        acc[j].x = fmaf(v.x, f, acc[j].x);
+        acc[j].y = fmaf(v.y, f, acc[j].y);
+        acc[j].z = fmaf(v.z, f, acc[j].z);
+        acc[j].w = fmaf(v.w, f, acc[j].w);
+      }
+    }
+    bool whole = s0 == 0 && s1 == n;
+    if (!whole) {
+      const int64_t g0 = x - s0;
+      const int c0 = attn_owner(g0, run.total, run.ctas), c1 = attn_owner(g0 + n - 1, run.total, run.ctas);
+      float2* st = reinterpret_cast<float2*>(p.ws + kAttnStats);
+      float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
+      const int64_t slot = 2 * blockIdx.x + (s0 == 0);
+      if (r < rows) {
+        if (dv == 0) __stcg(st + slot * AD_ROWS + r, make_float2(M, L));
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          __stcg(reinterpret_cast<float4*>(sums + (slot * AD_ROWS + r) * DP + dv + j * 4 * TPR), acc[j]);
+      }
+      __threadfence();
+      __syncthreads();
+      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + c0;
+      if (tid == 0) arrived = atomicAdd(count, 1u);
+      __syncthreads();
+      if (arrived == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
+        __threadfence();
+        if (tid == 0) *count = 0;
+        whole = true;
+        M = -INFINITY;
+        L = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < rows) {
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(st + (int64_t)(2 * c + (c == c0)) * AD_ROWS + r).x);
+          for (int c = c0; c <= c1; ++c) {
+            const int64_t at = (int64_t)(2 * c + (c == c0)) * AD_ROWS + r;
+            const float2 ml = __ldcg(st + at);
+            const float f = exp2_fast((ml.x - safe_max(M)) * p.scale_log2);
+            L = fmaf(ml.y, f, L);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(sums + at * DP + dv + j * 4 * TPR));
+              acc[j].x = fmaf(v.x, f, acc[j].x);
+              acc[j].y = fmaf(v.y, f, acc[j].y);
+              acc[j].z = fmaf(v.z, f, acc[j].z);
+              acc[j].w = fmaf(v.w, f, acc[j].w);
+            }
+          }
+        }
+      }
+    }
+    if (whole && r < rows) {
+      const int tok = (int)p.group.div(row0 + r), g = row0 + r - tok * (int)p.group.d;
+      const int2 sees = attn_range(p, seq, kv, tok);
+      // a row without keys is 0; one whose scores are all -infinity is 0 / 0
+      const float inv = sees.x < sees.y ? __fdiv_rn(1.0f, L) : 0.0f;
+      const bool none = sees.x >= sees.y;
+      const int64_t t = seq.first + tok;
+      const int hq = head * (int)p.group.d + g;
+      T* out = static_cast<T*>(p.out) + t * p.out_stride + (int64_t)hq * p.D;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int d = dv + j * 4 * TPR;
+        if (d < p.D) {
+          const uint2 v = none ? make_uint2(0u, 0u)
+                               : make_uint2(pack2<T>(acc[j].x * inv, acc[j].y * inv), pack2<T>(acc[j].z * inv, acc[j].w * inv));
+          *reinterpret_cast<uint2*>(out + d) = v;
+        }
+      }
+      if (p.lse != nullptr && dv == 0) p.lse[t * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(L));
+    }
+    __syncthreads();
+    // ---- on to the next tile of the run
+    x += s1 - s0;
+    s0 = 0;
+    if (++head == p.kv_heads) {
+      head = 0;
+      ++tile;
+    }
+  }
+}
+
+template <typename T, int DP>
+fp4moe_status attn_rows_run(const AttnParams& p, int nsm, cudaStream_t st) {
+  using C = AttnCfg<DP>;
+  static PerDevice done;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP4MOE_CUDA_ERROR;
+  if (done.get(dev, [] {
+        return cudaFuncSetAttribute(attn_rows_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+                       cudaSuccess
+                   ? 1
+                   : 0;
+      }) <= 0)
+    return FP4MOE_CUDA_ERROR;
+  return launch_pdl(attn_rows_kernel<T, DP>, dim3((unsigned)nsm), dim3(C::kThreads), C::kSmem, st, p) == cudaSuccess
+             ? FP4MOE_OK
+             : FP4MOE_CUDA_ERROR;
+}
+template <typename T>
+fp4moe_status attn_rows_typed(const AttnParams& p, int nsm, cudaStream_t st) {
+  return p.D <= 64 ? attn_rows_run<T, 64>(p, nsm, st) : p.D <= 128 ? attn_rows_run<T, 128>(p, nsm, st) : attn_rows_run<T, 256>(p, nsm, st);
+}
+
+}  // namespace
+
+fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cache, const void* v_cache, int32_t num_seqs,
+                                     int32_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                                     const int32_t* page_table, int32_t table_columns, const int32_t* kv_len,
+                                     const int32_t* q_offset, float scale, bool causal, int32_t window, void* out,
+                                     int64_t out_stride, float* lse, void* ws, uint32_t* err, cudaStream_t st) {
+  AttnParams p{};
+  p.map = cache_map(c);
+  p.k = k_cache;
+  p.v = v_cache;
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.table = page_table;
+  p.kv_len = kv_len;
+  p.q_offset = q_offset;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.B = num_seqs;
+  p.T = T;
+  p.q_heads = q_heads;
+  p.kv_heads = c.kv_heads;
+  p.D = c.head_dim;
+  p.columns = table_columns;
+  p.group = FastDiv((uint32_t)(q_heads / c.kv_heads));
+  p.causal = causal;
+  p.window = window;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.ws = static_cast<uint8_t*>(ws);
+  p.err = err;
+  int nsm = sm_count();
+  if (nsm <= 0) return FP4MOE_CUDA_ERROR;
+  if (nsm > kAttnMaxCtas) nsm = kAttnMaxCtas;
+  return c.dtype == FP4MOE_BF16 ? attn_rows_typed<__nv_bfloat16>(p, nsm, st) : attn_rows_typed<__half>(p, nsm, st);
+}
+
+}  // namespace fp4moe

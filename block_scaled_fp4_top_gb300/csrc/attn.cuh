@@ -1,0 +1,216 @@
+// What both attention kernels share (attn.cu, attntile.cu): the division of the work, the rows of a tile, and the join of
+// what several CTAs make of one tile.
+//
+// Rows. The rows of a sequence and kv head are its (token, query head of the group) pairs, token by token: they read the
+// same keys. A tile is BM of them. It sees the keys [lo, hi), and costs ceil(hi / S) - floor(lo / S) slices of S keys (at
+// least one: a tile without keys still has to be written).
+//
+// Division. The slices of all tiles and kv heads, in order, are cut into gridDim.x equal runs, one for each CTA, whatever
+// the lengths are: a long sequence is spread over many CTAs, and many short ones are shared out evenly. A CTA's run
+// holds parts of at most two tiles that other CTAs share: the one that it starts in (begun by an earlier CTA) and the one
+// that it ends in. Each CTA finds its run by itself from q_offset and kv_len.
+//
+// Join. A CTA leaves the unnormalised sums of its part (fp32, under its own maximum) in the workspace and counts itself
+// in; the last one adds the parts in the order of the CTAs, so equal inputs give equal bits, and sets the count back.
+#pragma once
+
+#include "paged.cuh"
+
+namespace fp4moe {
+
+constexpr int kAttnMaxCtas = 240;
+constexpr int kAttnTileRows = 256;  // of the larger kernel
+constexpr size_t kAttnCounters = 256;  // byte offset of the counters, one a CTA, zero between calls
+constexpr size_t kAttnStats = 4096;    // [2 a CTA][rows] {maximum, sum}
+constexpr size_t kAttnSums = kAttnStats + (size_t)2 * kAttnMaxCtas * kAttnTileRows * 8;  // [2 a CTA][rows][dims] fp32
+static_assert(kAttnCounters + 4 * kAttnMaxCtas <= kAttnStats, "counters fit");
+static_assert(kAttnSums + (size_t)2 * kAttnMaxCtas * kAttnTileRows * 128 * 4 <= FP4MOE_ATTENTION_WORKSPACE_BYTES,
+              "workspace");
+
+struct AttnParams {
+  CacheMap map;
+  const void *k, *v, *q;
+  void* out;
+  float* lse;
+  const int32_t *table, *kv_len, *q_offset;
+  int64_t q_stride, out_stride;
+  int B, T, q_heads, kv_heads, D, columns;
+  FastDiv group;  // query heads of a kv head
+  int causal, window;
+  float scale, scale_log2;
+  uint8_t* ws;
+  uint32_t* err;
+};
+
+// A sequence: its first row, number of rows (of one kv head) and keys.
+struct AttnSeq {
+  int first, rows, keys, tokens;
+};
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int q0, int q1, int kv) {
+  AttnSeq s;
+  q0 = max(0, min(q0, p.T));
+  q1 = max(q0, min(q1, p.T));
+  s.first = q0;
+  s.tokens = q1 - q0;
+  s.rows = s.tokens * (int)p.group.d;
+  const int64_t room = (int64_t)p.columns * p.map.page.d;
+  s.keys = kv < 0 ? 0 : (int64_t)kv > room ? (int)room : kv;
+  return s;
+}
+// Keys that token i of a sequence sees: [lo, hi).
+__device__ __forceinline__ int2 attn_range(const AttnParams& p, const AttnSeq& s, int kv, int i) {
+  // the last row's position is kv - 1; keys past the table's columns are missing
+  const int64_t pos = (int64_t)kv - s.tokens + i;
+  int64_t hi = p.causal ? pos + 1 : (int64_t)s.keys;
+  int64_t lo = p.window ? pos + 1 - p.window : 0;
+  hi = hi < 0 ? 0 : hi > s.keys ? s.keys : hi;
+  lo = lo < 0 ? 0 : lo > hi ? hi : lo;
+  return make_int2((int)lo, (int)hi);
+}
+// Keys that any row of tile `i` sees; a superset with the same ends.
+template <int BM>
+__device__ __forceinline__ int2 attn_tile_range(const AttnParams& p, const AttnSeq& s, int kv, int i) {
+  const int r0 = i * BM, r1 = min(r0 + BM, s.rows) - 1;
+  const int lo = attn_range(p, s, kv, (int)p.group.div(r0)).x, hi = attn_range(p, s, kv, (int)p.group.div(r1)).y;
+  return make_int2(min(lo, hi), hi);
+}
+template <int S>
+__device__ __forceinline__ int attn_slices(int2 r) {
+  return max(1, (r.y + S - 1) / S - r.x / S);
+}
+
+// Where a CTA's run of slices lies, and where it starts.
+struct AttnRun {
+  int64_t total, begin, end;  // slices of the call, and the CTA's own
+  int ctas;                   // CTAs that have a run: no more than there are slices, so that none of these is empty
+  int seq, tile, head;        // of slice `begin`
+  int slice;                  // its place in its tile
+};
+
+__device__ __forceinline__ int64_t attn_begin(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+// The CTA whose run holds slice x.
+__device__ __forceinline__ int attn_owner(int64_t x, int64_t total, int ctas) {
+  int c = (int)(x * ctas / total);
+  while (c + 1 < ctas && attn_begin(total, c + 1, ctas) <= x) ++c;
+  while (c > 0 && attn_begin(total, c, ctas) > x) --c;
+  return c;
+}
+
+// All threads of the CTA call this. sums: (B + THREADS / 32 + 2) * 8 bytes of shared memory, free again afterwards.
+template <int BM, int S, int THREADS>
+__device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int WARPS = THREADS / 32;
+  int64_t* part = sums;         // [WARPS + 1]
+  int64_t* upto = sums + WARPS + 1;  // [B] slices of the sequences up to and with b
+  const int per = (p.B + THREADS - 1) / THREADS;
+  uint32_t bad = 0;
+  // short sequences by their thread, those of several tiles by a warp
+  for (int i = 0; i < per; ++i) {
+    const int b = i * THREADS + tid;
+    int64_t w = 0;
+    int big = 0;
+    AttnSeq s{};
+    int kv = 0;
+    if (b < p.B) {
+      const int q0 = __ldg(p.q_offset + b), q1 = __ldg(p.q_offset + b + 1);
+      kv = __ldg(p.kv_len + b);
+      s = attn_seq(p, q0, q1, kv);
+      if (s.keys != kv && s.rows > 0) bad = 1;
+      if (s.rows > BM) big = 1;
+      else if (s.rows > 0) w = (int64_t)attn_slices<S>(attn_tile_range<BM>(p, s, kv, 0)) * p.kv_heads;
+    }
+    for (uint32_t m = __ballot_sync(0xFFFFFFFFu, big); m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      AttnSeq o;
+      o.first = __shfl_sync(0xFFFFFFFFu, s.first, src);
+      o.rows = __shfl_sync(0xFFFFFFFFu, s.rows, src);
+      o.keys = __shfl_sync(0xFFFFFFFFu, s.keys, src);
+      o.tokens = __shfl_sync(0xFFFFFFFFu, s.tokens, src);
+      const int okv = __shfl_sync(0xFFFFFFFFu, kv, src);
+      int64_t sum = 0;
+      for (int t = lane; t < (o.rows + BM - 1) / BM; t += 32) sum += attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      if (lane == src) w = sum * p.kv_heads;
+    }
+    if (b < p.B) upto[b] = w;
+  }
+  if (bad) raise_error(p.err, FP4MOE_ERR_PAGE);
+  __syncthreads();
+  // running sum: a thread's stretch of sequences, then the threads
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += upto[b];
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  int64_t before = x - mine, total = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  for (int b = b0; b < b1; ++b) {
+    before += upto[b];
+    upto[b] = before;
+  }
+  __syncthreads();
+  AttnRun r;
+  r.total = total;
+  r.ctas = (int)min(total, (int64_t)gridDim.x);
+  r.begin = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x, r.ctas) : 0;
+  r.end = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x + 1, r.ctas) : 0;
+  r.seq = r.tile = r.head = r.slice = 0;
+  if (r.begin < r.end) {
+    int lo = 0, hi = p.B - 1;  // first sequence with upto > begin
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (upto[mid] > r.begin) hi = mid;
+      else lo = mid + 1;
+    }
+    r.seq = lo;
+    int64_t left = r.begin - (lo ? upto[lo - 1] : 0);
+    const int kv = __ldg(p.kv_len + lo);
+    const AttnSeq s = attn_seq(p, __ldg(p.q_offset + lo), __ldg(p.q_offset + lo + 1), kv);
+    const int tiles = (s.rows + BM - 1) / BM;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {  // every warp for itself
+      const int t = t0 + lane;
+      const int64_t w = t < tiles ? (int64_t)attn_slices<S>(attn_tile_range<BM>(p, s, kv, t)) * p.kv_heads : 0;
+      int64_t y = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t z = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) y += z;
+      }
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < tiles && y > left);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        r.tile = t0 + src;
+        left -= __shfl_sync(0xFFFFFFFFu, y - w, src);
+        const int n = (int)(__shfl_sync(0xFFFFFFFFu, w, src) / p.kv_heads);
+        r.head = (int)(left / n);
+        r.slice = (int)(left - (int64_t)r.head * n);
+        break;
+      }
+      left -= __shfl_sync(0xFFFFFFFFu, y, 31);
+    }
+  }
+  __syncthreads();
+  return r;
+}
+
+// 2^x to 2 ulp (ex2.approx): what is rounded to 8 or 11 bits, or summed, afterwards.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The exponent's base: a row without a finite score so far has maximum -infinity, and exponentials of 0.
+__device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+}  // namespace fp4moe

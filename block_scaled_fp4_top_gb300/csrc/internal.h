@@ -159,4 +159,22 @@ fp4moe_status mx_dense_launch(int32_t format, int32_t dtype, int32_t M, int32_t 
                               const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
                               void* out, uint32_t* err, cudaStream_t st);
 
+// The paged key-value cache. kvplan.cu: a step's page tables, positions and slots
+fp4moe_status kv_plan_launch(int32_t num_seqs, int32_t page_size, int32_t num_pages, const int32_t* cached_len,
+                             const int32_t* new_len, int32_t* page_table, int32_t table_columns, int32_t* free_pages,
+                             const int32_t* free_count, int32_t* kv_len, int32_t* free_count_out, int32_t* q_offset,
+                             int32_t rows, int32_t* position, int32_t* slot, uint32_t* err, cudaStream_t st);
+// rope.cu: rotary positions of q and k, and k and v into their slots (q, or k and v, may be null)
+fp4moe_status rope_cache_launch(const fp4moe_kv_cache& c, int32_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const int32_t* position, const int32_t* slot, int32_t rot_first, int32_t rot_dim,
+                                bool interleaved, const double* inv_freq, float amplitude, void* q_out,
+                                int64_t q_out_stride, void* k_cache, void* v_cache, uint32_t* err, cudaStream_t st);
+// attn.cu: attention over the pages
+fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cache, const void* v_cache, int32_t num_seqs,
+                                     int32_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                                     const int32_t* page_table, int32_t table_columns, const int32_t* kv_len,
+                                     const int32_t* q_offset, float scale, bool causal, int32_t window, void* out,
+                                     int64_t out_stride, float* lse, void* ws, uint32_t* err, cudaStream_t st);
+
 }  // namespace fp4moe

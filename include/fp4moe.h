@@ -159,12 +159,14 @@ typedef enum fp4moe_status {
 /* Device error word bits (sticky; see fp4moe_read_error). */
 #define FP4MOE_ERR_TIMEOUT   0x1u  /* a bounded wait inside a kernel expired; its tile was skipped */
 #define FP4MOE_ERR_EXPERT_ID 0x2u  /* a routed expert id was outside [0, E) */
-#define FP4MOE_ERR_CAPACITY  0x4u  /* padded rows R exceeded CAP */
+#define FP4MOE_ERR_CAPACITY  0x4u  /* padded rows R exceeded CAP; in fp4moe_kv_plan: no free page, no table column or no
+                                      row of the step's buffers left for a sequence, which took nothing */
 #define FP4MOE_ERR_NAN       0x8u  /* a NaN reached an NVFP4 activation quantiser (x in moe_quantize_scatter,
                                       or h in the W1 epilogue or fp4moe_calibrate); the codes of that block
                                       are unspecified, and so are the outputs of its token */
 #define FP4MOE_ERR_SCALE_RANGE 0x10u /* fp4moe_mxfp4_as_nvfp4: an MX scale is NaN, or lies more than 17 binades
                                          below its matrix's largest, and has no exact E4M3 form */
+#define FP4MOE_ERR_PAGE      0x20u /* a page, slot, length or count of the paged key-value cache outside its range */
 
 /* Scale-status bits: a second sticky word of the workspace (fp4moe_read_scale_status). They are not
  * errors: a fixed activation global scale that a batch outgrows saturates its E4M3 block scales, which is
@@ -602,6 +604,149 @@ fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N
  */
 fp4moe_status fp4moe_mx_gemm_plan(int32_t M, int32_t N, int32_t K, int32_t sms, int32_t* tile_rows, int32_t* tile_cols,
                                   int32_t* k_slices);
+
+/* ------------------------------------------------- the paged key-value cache --
+ * The attention half of a decoder block, in front of the projection and the
+ * layer: fp4moe_kv_plan (pages, positions and slots of a step's new tokens, from
+ * the lengths of its sequences), fp4moe_rope_cache (rotary positions, and the
+ * step's k and v into the cache) and fp4moe_paged_attention. No call needs a
+ * host copy of a length: one CUDA graph serves every step of num_seqs sequences
+ * and T rows (rows past the last sequence are padding). The conventions of the
+ * dense operators hold: 16-byte aligned pointers to the current device's own
+ * memory, work enqueued on `stream`, no allocation, no synchronisation,
+ * capturable after a first call outside capture, inference only.
+ *
+ * A cache holds num_pages pages of page_size tokens. Token i of a page, kv head
+ * h, is head_dim elements at page * page_stride + i * token_stride + h *
+ * head_stride, in elements, for k and v alike; so [pages][tokens][heads][dims]
+ * and [pages][heads][tokens][dims] are both served. slot = page * page_size + i.
+ *   dtype FP4MOE_BF16 or FP4MOE_FP16; kv_heads >= 1; head_dim a multiple of 8
+ *   from 8 to 256; page_size >= 1; num_pages >= 1 with num_pages * page_size
+ *   below 2^31; strides multiples of 8 from 0 to 2^40 - 1.
+ * fp4moe_kv_cache fields out of range: FP4MOE_INVALID_ARG; a dtype or head_dim
+ * outside the list: FP4MOE_UNSUPPORTED.
+ */
+typedef struct fp4moe_kv_cache {
+  int32_t dtype;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+} fp4moe_kv_cache;
+
+#define FP4MOE_KV_MAX_SEQS 8192
+
+/*
+ * fp4moe_kv_plan: one step's page tables, offsets, positions and slots. For
+ * sequence b with c = cached_len[b] tokens in the cache and n = new_len[b]:
+ *   n >= 0: takes n new tokens; a = c + n
+ *   n <  0: gives its last -n tokens back (-c: is finished); a = c + n
+ *   kv_len[b]   = a
+ *   q_offset[b] = sum of max(n, 0) over the sequences before b; q_offset[num_seqs] the total
+ *   its i-th new token is row t = q_offset[b] + i of the step, with
+ *     position[t] = c + i, slot[t] = page_table[b][(c + i) / page_size] * page_size + (c + i) % page_size
+ *   rows t in [q_offset[num_seqs], rows): position 0, slot -1 (padding)
+ * Pages. free_pages [num_pages] is a stack, *free_count of its entries in use.
+ * All pages given back are put on it first, in ascending (b, page of b); then
+ * the sequences take theirs off the top, in the same order, into columns
+ * ceil(c / page_size) .. ceil(a / page_size) of their table rows. Other entries
+ * of page_table are left as they were, and so are those of free_pages past the
+ * new count.
+ *   page_table [num_seqs][table_columns] int32; position, slot [rows] int32;
+ *   q_offset [num_seqs + 1]. kv_len may be cached_len and free_count_out may
+ *   be free_count; no other output may overlap an input.
+ * A sequence takes nothing (kv_len[b] = c, slot -1 for its rows, and
+ * FP4MOE_ERR_CAPACITY in *err) if it needs more than table_columns pages, if
+ * its rows pass `rows` (q_offset is cut there), or if the stack has no pages
+ * for it and all sequences before it that have room for their tokens; then
+ * none after it takes pages either. A negative or oversized cached_len counts
+ * as the nearest allowed one, a sequence gives back no more than it has, a
+ * free_count out of range counts as the nearest in range, pages put on a full
+ * stack are lost, and a page outside [0, num_pages) gives slot -1: all with
+ * FP4MOE_ERR_PAGE.
+ * Deterministic: equal inputs give equal bits. 0 <= num_seqs <=
+ * FP4MOE_KV_MAX_SEQS (else FP4MOE_UNSUPPORTED), rows >= 0, table_columns >= 0,
+ * page_size and num_pages as above; else FP4MOE_INVALID_ARG.
+ */
+fp4moe_status fp4moe_kv_plan(int32_t num_seqs, int32_t page_size, int32_t num_pages, const int32_t* cached_len,
+                             const int32_t* new_len, int32_t* page_table, int32_t table_columns, int32_t* free_pages,
+                             const int32_t* free_count, int32_t* kv_len, int32_t* free_count_out, int32_t* q_offset,
+                             int32_t rows, int32_t* position, int32_t* slot, uint32_t* err, fp4moe_stream_t stream);
+
+/*
+ * fp4moe_rope_cache: rotary positions of T rows of q and k, and k and v into the
+ * cache. Of each head's head_dim elements, rot_dim from rot_first on are turned in
+ * pairs i = 0 .. rot_dim / 2 - 1 by the angle position[t] * inv_freq[i]:
+ *   (x, y) -> RN(amplitude * (x cos - y sin), amplitude * (y cos + x sin))
+ * interleaved = 0: x, y are elements i and i + rot_dim / 2 of the part;
+ * interleaved = 1: elements 2 i and 2 i + 1. The others are copied. Long contexts
+ * are scaled through inv_freq and amplitude.
+ *   q [T][q_heads][head_dim] of the cache's type, rows q_stride elements apart ->
+ *     q_out, rows q_out_stride apart; q_out may be q with its stride (in place),
+ *     but not otherwise overlap q, k or v. q and q_out are both given or both
+ *     NULL (then q_heads is 0).
+ *   k, v [T][kv_heads][head_dim], rows k_stride and v_stride apart -> the slots of
+ *     k_cache and v_cache. k, v, k_cache and v_cache are all given or all NULL.
+ *   position, slot [T] int32: a row with slot -1 is padding: nothing is written
+ *     for it. A slot outside the cache leaves the cache as it was (q_out is
+ *     written) and sets FP4MOE_ERR_PAGE in *err. Of two rows with one slot
+ *     either may be left in the cache.
+ *   inv_freq [rot_dim / 2] fp64 radians per position, finite. The angle is exact
+ *     to 2^-31 turns at any position (a product modulo one turn in 64 bits).
+ *   amplitude: finite fp32.
+ * Row strides are multiples of 8 and at least a row long where T > 1. 0 <= rot_first,
+ * rot_dim even, >= 0, rot_first + rot_dim <= head_dim (rot_dim = 0: inv_freq may be
+ * NULL); T >= 0, q_heads + 2 kv_heads at most 65535 and T times that below 2^31; else
+ * FP4MOE_INVALID_ARG.
+ */
+fp4moe_status fp4moe_rope_cache(const fp4moe_kv_cache* cache, int32_t T, int32_t q_heads, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const int32_t* position, const int32_t* slot, int32_t rot_first, int32_t rot_dim,
+                                int32_t interleaved, const double* inv_freq, float amplitude, void* q_out,
+                                int64_t q_out_stride, void* k_cache, void* v_cache, uint32_t* err,
+                                fp4moe_stream_t stream);
+
+/*
+ * fp4moe_paged_attention: attention of the step's rows over their sequences'
+ * pages. Sequence b has n = q_offset[b + 1] - q_offset[b] rows and L = kv_len[b]
+ * keys, key j in page page_table[b][j / page_size]; query head g reads kv head
+ * g / (q_heads / kv_heads). Row i of it sees the keys j with
+ *   causal = 1: p - window < j <= p for p = L - n + i (window = 0: j <= p),
+ *     so the new tokens' own keys are the last n of the cache;
+ *   causal = 0: j < L (attention to cached states of any other length)
+ *   s_j = scale * q . k_j; out = RN(sum e^(s_j - m) v_j / sum e^(s_j - m)), m = max s
+ *   lse = m + ln(sum e^(s_j - m)) in fp32
+ * A row that sees no key gets out = 0 and lse = -infinity. Keys that a row does not
+ * see do not reach it, whatever they hold. Sums and statistics are fp32; e^(s - m)
+ * is rounded to the cache's type in front of the product with v.
+ *   q, out [T][q_heads][head_dim] of the cache's type, rows q_stride and
+ *     out_stride elements apart (multiples of 8, at least a row long where T > 1);
+ *     out must not overlap q. lse [T][q_heads] fp32 or NULL.
+ *   q_heads a multiple of kv_heads, at least one; T * q_heads below 2^31;
+ *   0 <= num_seqs <= FP4MOE_KV_MAX_SEQS (else FP4MOE_UNSUPPORTED).
+ *   page_table [num_seqs][table_columns], kv_len [num_seqs], q_offset
+ *     [num_seqs + 1] int32 on the device, as fp4moe_kv_plan writes them. Rows past
+ *     q_offset[num_seqs] are left as they were.
+ *   scale: finite, > 0. window: >= 0; 0 where causal = 0.
+ *   ws: FP4MOE_ATTENTION_WORKSPACE_BYTES of device memory, zeroed once before
+ *     first use; a call leaves its counters at zero again. Calls (and graphs) that
+ *     share one must be ordered.
+ * Offsets out of order or past T count as the nearest in range. Of a length that is
+ * negative or longer than the table's columns, only keys that have a column count,
+ * and a page outside [0, num_pages) reads as zeros: all with FP4MOE_ERR_PAGE in
+ * *err. err also receives FP4MOE_ERR_TIMEOUT, as in fp4moe_mx_gemm.
+ * Deterministic: equal inputs give equal bits. Other arguments out of range:
+ * FP4MOE_INVALID_ARG.
+ */
+#define FP4MOE_ATTENTION_WORKSPACE_BYTES (64u << 20)
+fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k_cache, const void* v_cache,
+                                     int32_t num_seqs, int32_t T, int32_t q_heads, const void* q, int64_t q_stride,
+                                     const int32_t* page_table, int32_t table_columns, const int32_t* kv_len,
+                                     const int32_t* q_offset, float scale, int32_t causal, int32_t window, void* out,
+                                     int64_t out_stride, float* lse, void* ws, uint32_t* err, fp4moe_stream_t stream);
 
 /* ------------------------------------------------------------------ prep --
  * Load-time helpers. They run outside the timed hot path and may use
