@@ -30,12 +30,6 @@ struct AttnCfg {
   static_assert((FP4MOE_KV_MAX_SEQS + kWarps + 1) * 8 <= kSmem, "the division's sums fit");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool use) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -61,16 +55,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <typename T>
-__device__ __forceinline__ bool any_nonfinite(uint4 v) {
-  constexpr uint32_t E = std::is_same_v<T, __nv_bfloat16> ? 0x7F80u : 0x7C00u;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || ((w[i] >> 16) & E) == E;
-  return bad;
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(AttnParams p) {
   using C = AttnCfg<DP>;
@@ -89,19 +73,11 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   const T* vbase = static_cast<const T*>(p.v);
   const int dims = (p.D + 15) / 16 * 16;  // MMA steps past the head's own dims are left out
   const int qr = lane >> 2, qc = (lane & 3) * 2;
-  int b = run.seq, tile = run.tile, head = run.head, s0 = run.slice;
-  for (int64_t x = run.begin; x < run.end;) {
-    const int kv = __ldg(p.kv_len + b);
-    const AttnSeq seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), kv);
-    if (tile * AD_ROWS >= seq.rows) {  // the next sequence
-      ++b;
-      tile = head = s0 = 0;
-      continue;
-    }
-    const int2 range = attn_tile_range<AD_ROWS>(p, seq, kv, tile);
-    const int n = attn_slices<C::S>(range);
-    const int s1 = (int)min((int64_t)n, s0 + (run.end - x));
-    const int row0 = tile * AD_ROWS, rows = min(AD_ROWS, seq.rows - row0);
+  AttnWalk walk(run);
+  for (AttnUnit u; walk.next<AD_ROWS, C::S>(p, run, u);) {
+    const AttnSeq& seq = u.seq;
+    const int kv = u.kv, head = u.head, row0 = u.row0, rows = u.rows, n = u.n, s0 = u.s0, s1 = u.s1;
+    const int2 range = u.range;
     // ---- this lane's two rows: q as the MMA's A, and the keys they see
     uint32_t qa[KS][4];
     int2 see[2];
@@ -128,7 +104,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
     const int base = range.x / C::S * C::S + warp * AD_KEYS;  // first key of this warp's group of slice 0
-    const int32_t* table = p.table + (int64_t)b * p.columns;
+    const int32_t* table = p.table + (int64_t)u.b * p.columns;
     const int64_t head_off = (int64_t)head * p.map.head_stride;
     auto page_of = [&](int s) {  // page of the key that this lane looks up in slice s; -2: none
       const int key = base + s * C::S + (lane & 15);
@@ -332,8 +308,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     }
     bool whole = s0 == 0 && s1 == n;
     if (!whole) {
-      const int64_t g0 = x - s0;
-      const int c0 = attn_owner(g0, run.total, run.ctas), c1 = attn_owner(g0 + n - 1, run.total, run.ctas);
+      const int c0 = attn_owner(u.first, run.total, run.ctas), c1 = attn_owner(u.first + n - 1, run.total, run.ctas);
       float2* st = reinterpret_cast<float2*>(p.ws + kAttnStats);
       float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
       const int64_t slot = 2 * blockIdx.x + (s0 == 0);
@@ -345,7 +320,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       }
       __threadfence();
       __syncthreads();
-      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + c0;
+      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0;
       if (tid == 0) arrived = atomicAdd(count, 1u);
       __syncthreads();
       if (arrived == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
@@ -396,13 +371,6 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       if (p.lse != nullptr && dv == 0) p.lse[t * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(L));
     }
     __syncthreads();
-    // ---- on to the next tile of the run
-    x += s1 - s0;
-    s0 = 0;
-    if (++head == p.kv_heads) {
-      head = 0;
-      ++tile;
-    }
   }
 }
 
@@ -463,6 +431,7 @@ fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cac
   int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
   if (nsm > kAttnMaxCtas) nsm = kAttnMaxCtas;
+  if (c.head_dim <= 128 && (int64_t)T * p.group.d > (int64_t)32 * num_seqs) return attn_tile_launch(c.dtype, p, nsm, st);
   return c.dtype == FP4MOE_BF16 ? attn_rows_typed<__nv_bfloat16>(p, nsm, st) : attn_rows_typed<__half>(p, nsm, st);
 }
 

@@ -20,10 +20,10 @@ namespace fp4moe {
 
 constexpr int kAttnMaxCtas = 240;
 constexpr int kAttnTileRows = 256;  // of the larger kernel
-constexpr size_t kAttnCounters = 256;  // byte offset of the counters, one a CTA, zero between calls
+constexpr size_t kAttnCounters = 256;  // byte offset of the counters, two a CTA, zero between calls
 constexpr size_t kAttnStats = 4096;    // [2 a CTA][rows] {maximum, sum}
 constexpr size_t kAttnSums = kAttnStats + (size_t)2 * kAttnMaxCtas * kAttnTileRows * 8;  // [2 a CTA][rows][dims] fp32
-static_assert(kAttnCounters + 4 * kAttnMaxCtas <= kAttnStats, "counters fit");
+static_assert(kAttnCounters + 8 * kAttnMaxCtas <= kAttnStats, "counters fit");
 static_assert(kAttnSums + (size_t)2 * kAttnMaxCtas * kAttnTileRows * 128 * 4 <= FP4MOE_ATTENTION_WORKSPACE_BYTES,
               "workspace");
 
@@ -204,6 +204,69 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
   return r;
 }
 
+// What a CTA does in one go: slices [s0, s1) of one tile and kv head.
+struct AttnUnit {
+  AttnSeq seq;
+  int kv, b, tile, head;
+  int row0, rows;  // the tile's first row of the sequence, and its rows
+  int2 range;      // keys that any of them sees
+  int n, s0, s1;   // slices of the tile, and those of this unit
+  int64_t first;   // the tile's first slice among the call's
+};
+// The units of a run, one after the other.
+struct AttnWalk {
+  int64_t x;
+  int b, tile, head, slice;
+  __device__ __forceinline__ explicit AttnWalk(const AttnRun& r)
+      : x(r.begin), b(r.seq), tile(r.tile), head(r.head), slice(r.slice) {}
+  template <int BM, int S>
+  __device__ __forceinline__ bool next(const AttnParams& p, const AttnRun& r, AttnUnit& u) {
+    while (x < r.end) {
+      u.kv = __ldg(p.kv_len + b);
+      u.seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), u.kv);
+      if (tile * BM >= u.seq.rows) {
+        ++b;
+        tile = head = slice = 0;
+        continue;
+      }
+      u.b = b;
+      u.tile = tile;
+      u.head = head;
+      u.row0 = tile * BM;
+      u.rows = min(BM, u.seq.rows - u.row0);
+      u.range = attn_tile_range<BM>(p, u.seq, u.kv, tile);
+      u.n = attn_slices<S>(u.range);
+      u.s0 = slice;
+      u.s1 = (int)min((int64_t)u.n, slice + (r.end - x));
+      u.first = x - slice;
+      x += u.s1 - u.s0;
+      slice = 0;
+      if (++head == p.kv_heads) {
+        head = 0;
+        ++tile;
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool use) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(uint4 v) {
+  constexpr uint32_t E = std::is_same_v<T, __nv_bfloat16> ? 0x7F80u : 0x7C00u;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || ((w[i] >> 16) & E) == E;
+  return bad;
+}
+
 // 2^x to 2 ulp (ex2.approx): what is rounded to 8 or 11 bits, or summed, afterwards.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -212,5 +275,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 // The exponent's base: a row without a finite score so far has maximum -infinity, and exponentials of 0.
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// attntile.cu: 256-row units on the tensor cores, head_dim up to 128, on nsm CTAs
+fp4moe_status attn_tile_launch(int32_t dtype, const AttnParams& p, int nsm, cudaStream_t st);
 
 }  // namespace fp4moe

@@ -1,0 +1,615 @@
+// Attention over the paged cache for many rows a sequence and kv head (fp4moe_paged_attention): prompts and chunks of them.
+//
+// A unit is 256 rows, as two tiles of 128, against its keys in steps of 128:
+//   S = Q K^T          tcgen05.mma, M = 128, N = 128: Q and K in shared memory, S (fp32) in TMEM
+//   P = 2^(S - m)      one thread a row: S out of TMEM, P (16 bits) back into the place of S
+//   O += P V           tcgen05.mma with P out of TMEM, V in shared memory as it lies (keys x dims: transposed B), O in TMEM
+// The tensor cores work on one tile while the other's softmax runs:
+//   warps 0-3, 4-7     softmax, rescaling and output of tile 0 and 1 (warp w: TMEM lanes 32 (w % 4) ..)
+//   warp 8             MMAs: for each step, of each tile the P V of the step before and the next Q K^T
+//   warps 9, 10        loads: q, k and v by 16-byte cp.async, for any page size and stride (a lane looks a key's place up for
+//                      the lanes that copy it), into 128-byte-swizzled tiles, two loads in flight behind the one being made
+// The MMAs of one thread run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
+// take the place of S(j). O is rescaled only where a row's maximum grew by more than 2^8; until then P and its sum are
+// under the old maximum, up to 256, which neither 16-bit type minds.
+// Keys outside the tile's range are zeros in shared memory; those that a row does not see have score -infinity. Where a
+// v that only some rows see is not finite (0 times it would be NaN), the unit's rows are made again one by one.
+// Every wait is bounded, as in the layer's GEMMs.
+#include "attn.cuh"
+
+namespace fp4moe {
+namespace {
+
+constexpr int AT_BM = 256, AT_KEYS = 128;
+constexpr int AT_THREADS = 352;    // 168 registers a thread: a row of S stays in them
+constexpr int AT_LOADERS = 2;      // warps
+constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
+
+template <int DP>
+struct TileCfg {
+  static constexpr int kBlocks = DP / 64;             // 128-byte columns of a tile
+  static constexpr int kBlock = 128 * 128;            // bytes of 128 rows of one
+  static constexpr int kTile = kBlocks * kBlock;      // 128 rows of q, k or v
+  static constexpr int kStages = DP == 128 ? 2 : 4;   // of k, and of v
+  static constexpr int kK = 2 * kTile, kV = kK + kStages * kTile;
+  static constexpr int kBars = kV + kStages * kTile;
+  static constexpr int kSmem = kBars + 512 + 1024;    // and to align it
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert((FP4MOE_KV_MAX_SEQS + AT_THREADS / 32 + 1) * 8 <= kBars, "the division's sums fit");
+};
+
+// Barriers, 8 bytes each, behind the tiles.
+template <int DP>
+struct TileBars {
+  using C = TileCfg<DP>;
+  uint32_t base;
+  __device__ __forceinline__ uint32_t k_full(int s) const { return base + 8 * s; }
+  __device__ __forceinline__ uint32_t k_empty(int s) const { return base + 8 * (C::kStages + s); }
+  __device__ __forceinline__ uint32_t v_full(int s) const { return base + 8 * (2 * C::kStages + s); }
+  __device__ __forceinline__ uint32_t v_empty(int s) const { return base + 8 * (3 * C::kStages + s); }
+  __device__ __forceinline__ uint32_t q_full() const { return base + 8 * (4 * C::kStages); }
+  __device__ __forceinline__ uint32_t q_empty() const { return base + 8 * (4 * C::kStages + 1); }
+  __device__ __forceinline__ uint32_t s_full(int t) const { return base + 8 * (4 * C::kStages + 2 + t); }
+  __device__ __forceinline__ uint32_t p_full(int t) const { return base + 8 * (4 * C::kStages + 4 + t); }
+  __device__ __forceinline__ uint32_t o_full(int t) const { return base + 8 * (4 * C::kStages + 6 + t); }
+  __device__ __forceinline__ uint32_t join(int t) const { return base + 8 * (4 * C::kStages + 8 + t); }
+  __device__ __forceinline__ uint32_t done() const { return base + 8 * (4 * C::kStages + 10); }
+};
+
+// The whole warp waits, and goes on together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err));
+}
+
+// A (K-major) and B: both bf16 or both fp16, fp32 D; transposed B: stored K x N with N contiguous.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t idesc_16(int N, bool transposed_b) {
+  constexpr uint32_t F = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+  return (1u << 4) | (F << 7) | (F << 10) | ((transposed_b ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Descriptor of a transposed B tile: 64 columns (128 swizzled bytes) a row, 8 rows 1024 bytes, the next 64 columns
+// `block` bytes on.
+__device__ __forceinline__ uint64_t desc_sw128_t(uint32_t saddr, uint32_t block) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  tc_mma_bf16(d, a, b, idesc, accumulate);  // (kind::f16 is both types; idesc says which)
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+// 8 columns in and out, times f: few registers beside a row of S.
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- loads
+template <typename T, int DP>
+struct Loader {
+  using C = TileCfg<DP>;
+  static constexpr int CH = DP / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows of a warp's copy instruction
+  const AttnParams& p;
+  uint8_t* sm;
+  volatile int* odd;  // [unit % 3]: unit + 1 if a v that only some rows see is not finite
+  int warp, lane, dims;
+  // a load whose arrival is still to be told: its barrier, and the stage of v to be looked through for the unit (or -1)
+  struct Load {
+    uint32_t bar;
+    int look, unit;
+  };
+  Load older, newer;
+  int waiting;
+
+  // 32 rows from row0 on; `off` is the element offset of this lane's row, negative: zeros.
+  __device__ __forceinline__ void rows32(uint32_t tile, int row0, const T* base, int64_t off) {
+    const int c = lane % CH;
+#pragma unroll
+    for (int it = 0; it < 32 / RPI; ++it) {
+      const int r = it * RPI + lane / CH;
+      const int64_t ro = __shfl_sync(0xFFFFFFFFu, off, r);
+      const bool use = ro >= 0 && c * 8 < p.D;
+      const int row = row0 + r;
+      if (c * 8 < dims)
+        cp_async16(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4), base + (use ? ro + c * 8 : 0), use);
+    }
+  }
+  // The older load has landed: tell it.
+  __device__ __forceinline__ void tell() {
+    if (older.look >= 0) {
+      const uint8_t* tile = sm + C::kV + older.look * C::kTile;
+      bool bad = false;
+      const int c = lane % CH;
+      if (c * 8 < dims)
+        for (int it = 0; it < 64 / RPI; ++it) {
+          const int row = warp * 64 + it * RPI + lane / CH;
+          bad |= any_nonfinite<T>(*reinterpret_cast<const uint4*>(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
+        }
+      if (bad) odd[older.unit % 3] = older.unit + 1;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(older.bar);
+    older = newer;
+    --waiting;
+  }
+  __device__ __forceinline__ void drain() {
+    cp_async_wait<0>();
+    while (waiting) tell();
+  }
+  // Everything for `b` has been issued.
+  __device__ __forceinline__ void issued(uint32_t b, int look, int unit) {
+    cp_async_commit();
+    if (waiting == 2) {
+      cp_async_wait<2>();
+      tell();
+    }
+    const Load load{b, look, unit};
+    if (waiting == 0) older = load;
+    else newer = load;
+    ++waiting;
+  }
+  // A free stage; what is on its way is told first if there is none yet, for that may be what frees it.
+  __device__ __forceinline__ bool free_stage(uint32_t b, uint32_t parity) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
+    drain();
+    return warp_wait(b, parity, p.err);
+  }
+};
+
+template <typename T, int DP>
+__device__ __forceinline__ void load_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint8_t* sm,
+                                          uint32_t sm32, volatile int* odd) {
+  using C = TileCfg<DP>;
+  const int warp = (threadIdx.x >> 5) - 9, lane = lane_id();
+  Loader<T, DP> L{p, sm, odd, warp, lane, (p.D + 15) / 16 * 16, {}, {}, 0};
+  const T *kbase = static_cast<const T*>(p.k), *vbase = static_cast<const T*>(p.v);
+  int stage = 0, units = 0;
+  uint32_t phase = 1;  // of the empty barriers: the first round finds all stages free
+  bool ok = true;
+  AttnWalk walk(run);
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+    if (!(ok = L.free_stage(bar.q_empty(), (units & 1) ^ 1))) break;
+#pragma unroll 1
+    for (int part = 0; part < 4; ++part) {
+      const int row = warp * 64 + (part & 1) * 32, r = (part >> 1) * 128 + row + lane;
+      int64_t off = -1;
+      if (r < u.rows) {
+        const int tok = (int)p.group.div(u.row0 + r), g = u.row0 + r - tok * (int)p.group.d;
+        off = (int64_t)(u.seq.first + tok) * p.q_stride + (int64_t)(u.head * (int)p.group.d + g) * p.D;
+      }
+      L.rows32(sm32 + (part >> 1) * C::kTile, row, static_cast<const T*>(p.q), off);
+    }
+    L.issued(bar.q_full(), -1, units);
+    const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + u.rows - 1)).x;
+    const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0)).y;
+    const bool differ = all_lo != u.range.x || all_hi != u.range.y;
+    const int first = (u.range.x / AT_KEYS + u.s0) * AT_KEYS;
+    const int32_t* table = p.table + (int64_t)u.b * p.columns;
+    const int64_t head_off = (int64_t)u.head * p.map.head_stride;
+    auto key_of = [&](int i, int h) { return first + i * AT_KEYS + warp * 64 + h * 32 + lane; };
+    auto page_of = [&](int i, int h) {  // page of the key that this lane looks up in step i; -2: none
+      const int key = key_of(i, h);
+      return i < u.s1 - u.s0 && key >= u.range.x && key < u.range.y ? __ldg(table + p.map.page.div(key)) : -2;
+    };
+    int next[2] = {page_of(0, 0), page_of(0, 1)};
+    for (int i = 0; i < u.s1 - u.s0; ++i) {
+      int64_t off[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = key_of(i, h);
+        off[h] = -1;
+        if (next[h] != -2) {
+          if ((uint32_t)next[h] < (uint32_t)p.map.num_pages)
+            off[h] = next[h] * p.map.page_stride +
+                     (int64_t)(key - (int)p.map.page.div(key) * (int)p.map.page.d) * p.map.token_stride + head_off;
+          else
+            raise_error(p.err, FP4MOE_ERR_PAGE);
+        }
+        next[h] = page_of(i + 1, h);
+      }
+      if (!(ok = L.free_stage(bar.k_empty(stage), phase))) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) L.rows32(sm32 + C::kK + stage * C::kTile, warp * 64 + h * 32, kbase, off[h]);
+      L.issued(bar.k_full(stage), -1, units);
+      if (!(ok = L.free_stage(bar.v_empty(stage), phase))) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) L.rows32(sm32 + C::kV + stage * C::kTile, warp * 64 + h * 32, vbase, off[h]);
+      const int k0 = first + i * AT_KEYS;
+      L.issued(bar.v_full(stage), differ && (k0 < all_lo || k0 + AT_KEYS > all_hi) ? stage : -1, units);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  L.drain();
+}
+
+// ---------------------------------------------------------------- MMAs (one thread)
+template <typename T, int DP>
+__device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint32_t sm32,
+                                         uint32_t tmem) {
+  using C = TileCfg<DP>;
+  const int dims = (p.D + 15) / 16 * 16;
+  const uint32_t is = idesc_16<T>(AT_KEYS, false), io = idesc_16<T>(dims, true);
+  int ks = 0, vs = 0, units = 0;
+  uint32_t kp = 0, vp = 0, pp = 0;  // phases of the k and v stages, and of the p barriers (bit t)
+  auto qk = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      if (i * 16 < dims) {
+        const uint32_t at = (i >> 2) * C::kBlock + (i & 3) * 32;
+        mma_ss(tmem + t * 128, desc_sw128(sm32 + t * C::kTile + at), desc_sw128(sm32 + C::kK + ks * C::kTile + at), is, i > 0);
+      }
+    }
+    tc_commit(bar.s_full(t));
+  };
+  auto pv = [&](int t, bool first) {
+#pragma unroll
+    for (int i = 0; i < AT_KEYS / 16; ++i)
+      mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, desc_sw128_t(sm32 + C::kV + vs * C::kTile + i * 2048, C::kBlock), io,
+             !(first && i == 0));
+  };
+  AttnWalk walk(run);
+  bool ok = true;
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+    const int tiles = u.rows > 128 ? 2 : 1, n = u.s1 - u.s0;
+    if (!(ok = mbar_wait(bar.q_full(), units & 1, p.err))) break;
+    for (int j = 0; j <= n; ++j) {
+      if (j < n && !(ok = mbar_wait(bar.k_full(ks), kp, p.err))) break;
+      if (j > 0 && !(ok = mbar_wait(bar.v_full(vs), vp, p.err))) break;
+      for (int t = 0; t < tiles; ++t) {
+        if (j > 0) {
+          if (!(ok = mbar_wait(bar.p_full(t), (pp >> t) & 1, p.err))) break;
+          pp ^= 1u << t;
+          tc_fence_after();
+          pv(t, j == 1);
+          if (j == n) tc_commit(bar.o_full(t));
+        }
+        if (j < n) {
+          tc_fence_after();
+          qk(t);
+        }
+      }
+      if (!ok) break;
+      if (j > 0) {
+        tc_commit(bar.v_empty(vs));
+        if (++vs == C::kStages) {
+          vs = 0;
+          vp ^= 1;
+        }
+      }
+      if (j < n) {
+        tc_commit(bar.k_empty(ks));
+        if (++ks == C::kStages) {
+          ks = 0;
+          kp ^= 1;
+        }
+      }
+      if (j == n - 1) tc_commit(bar.q_empty());
+    }
+  }
+  tc_commit(bar.done());  // nothing may be in flight when the CTA gives its memory back
+  drain_wait(bar.done(), 0);
+}
+
+// ---------------------------------------------------------------- softmax, output
+// A row again, key by key: m, l, and the sums of 32 dims from d0 on.
+template <typename T>
+__device__ __noinline__ void row_again(const AttnParams& p, const AttnUnit& u, int row, int lo, int hi, int d0, float& m, float& l,
+                                       float (&o)[32]) {
+  const int tok = (int)p.group.div(u.row0 + row), g = u.row0 + row - tok * (int)p.group.d;
+  const T* q = static_cast<const T*>(p.q) + (int64_t)(u.seq.first + tok) * p.q_stride +
+               (int64_t)(u.head * (int)p.group.d + g) * p.D;
+  m = -INFINITY;
+  l = 0.0f;
+  for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+  for (int key = lo; key < hi; ++key) {
+    const int j = (int)p.map.page.div(key), page = __ldg(p.table + (int64_t)u.b * p.columns + j);
+    const bool there = (uint32_t)page < (uint32_t)p.map.num_pages;
+    const int64_t off = there ? page * p.map.page_stride + (int64_t)(key - j * (int)p.map.page.d) * p.map.token_stride +
+                                    (int64_t)u.head * p.map.head_stride
+                              : 0;
+    const T *k = static_cast<const T*>(p.k) + off, *v = static_cast<const T*>(p.v) + off;
+    float s = 0.0f;
+    if (there)
+      for (int d = 0; d < p.D; ++d) s = fmaf(to_f32(q[d]), to_f32(k[d]), s);
+    const float nm = fmaxf(m, s), f = exp2_fast((m - safe_max(nm)) * p.scale_log2);
+    const float w = exp2_fast(fmaf(s, p.scale_log2, -safe_max(nm) * p.scale_log2));
+    m = nm;
+    l = fmaf(l, f, w);
+    for (int i = 0; i < 32; ++i) o[i] = fmaf(o[i], f, there && d0 + i < p.D ? w * to_f32(v[d0 + i]) : 0.0f);
+  }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint32_t tmem,
+                                             volatile int* odd, volatile uint32_t* arrived) {
+  const int t = threadIdx.x >> 7, row = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(row & 96) << 16;  // this warp's 32 lanes of TMEM
+  const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + 256 + t * DP;
+  const int dims = (p.D + 15) / 16 * 16;
+  int units = 0;
+  uint32_t sp = 0, op = 0, jp = 0;
+  bool ok = true;
+  AttnWalk walk(run);
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+    if (t * 128 >= u.rows) continue;  // (as the MMAs leave the tile out)
+    const int last = min(u.rows, t * 128 + 128) - 1, r = min(t * 128 + row, last);
+    const bool real = t * 128 + row <= last;
+    const int2 see = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + r));
+    const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + last)).x;
+    const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + t * 128)).y;
+    float m = -INFINITY, l = 0.0f;
+    for (int j = u.s0; j < u.s1; ++j) {
+      const int k0 = (u.range.x / AT_KEYS + j) * AT_KEYS;
+      if (!(ok = warp_wait(bar.s_full(t), sp, p.err))) break;
+      sp ^= 1;
+      tc_fence_after();
+      float s[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(st + i * 32, s[i]);
+      tmem_ld_wait();
+      if (k0 < all_lo || k0 + AT_KEYS > all_hi) {
+        const int a = see.x - k0, b = see.y - k0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (i * 32 + c < a || i * 32 + c >= b) s[i][c] = -INFINITY;
+      }
+      float nm[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        nm[i] = s[i][0];
+#pragma unroll
+        for (int c = 1; c < 32; ++c) nm[i] = fmaxf(nm[i], s[i][c]);
+      }
+      const float top = fmaxf(m, fmaxf(fmaxf(nm[0], nm[1]), fmaxf(nm[2], nm[3])));
+      if (j == u.s0) {
+        m = top;
+      } else if (__any_sync(0xFFFFFFFFu, (top - safe_max(m)) * p.scale_log2 > AT_GROWTH || (m == -INFINITY && top > m))) {
+        const float f = exp2_fast((m - safe_max(top)) * p.scale_log2);
+        m = top;
+        l *= f;
+#pragma unroll 1
+        for (int d = 0; d < dims; d += 8) tmem_scale8(ot + d, f);
+      }
+      const float mb = safe_max(m) * p.scale_log2;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int i = 2 * h + (c >> 4), e = 2 * (c & 15);
+          const float a = exp2_fast(fmaf(s[i][e], p.scale_log2, -mb)), b = exp2_fast(fmaf(s[i][e + 1], p.scale_log2, -mb));
+          sum[c & 3] += a + b;
+          w[c] = pack2<T>(a, b);  // half a step of the cache's type, against a result of that type
+        }
+        tmem_st32(st + h * 32, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar.p_full(t));
+    }
+    if (!ok || !(ok = warp_wait(bar.o_full(t), op, p.err))) break;
+    op ^= 1;
+    tc_fence_after();
+    if (odd[units % 3] == units + 1) {
+      const int k0 = (u.range.x / AT_KEYS + u.s0) * AT_KEYS, k1 = (u.range.x / AT_KEYS + u.s1) * AT_KEYS;
+      for (int d = 0; d < dims; d += 32) {
+        float o[32];
+        uint32_t w[32];
+        row_again<T>(p, u, r, max(see.x, k0), min(see.y, k1), d, m, l, o);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(o[c]);
+        __syncwarp();
+        tmem_st32(ot + d, w);
+      }
+      tmem_st_wait();
+    }
+    const int tok = (int)p.group.div(u.row0 + r), g = u.row0 + r - tok * (int)p.group.d;
+    const int64_t tq = u.seq.first + tok;
+    const int hq = u.head * (int)p.group.d + g;
+    T* out = static_cast<T*>(p.out) + tq * p.out_stride + (int64_t)hq * p.D;
+    const bool none = see.x >= see.y;  // a row without keys is 0; one whose scores are all -infinity is 0 / 0
+    auto finish = [&](float (&o)[32], int d, float inv) {
+      if (!real) return;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        if (d + c < p.D) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = none ? 0.0f : o[c + e] * inv;
+          *reinterpret_cast<uint4*>(out + d + c) = pack<T>(v);
+        }
+      }
+    };
+    auto finish_lse = [&](float M, float sum) {
+      if (real && p.lse != nullptr) p.lse[tq * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(sum));
+    };
+    if (u.s0 == 0 && u.s1 == u.n) {
+      const float inv = __fdiv_rn(1.0f, l);
+#pragma unroll 1
+      for (int d = 0; d < dims; d += 32) {
+        float o[32];
+        tmem_ld32(ot + d, o);
+        tmem_ld_wait();
+        finish(o, d, inv);
+      }
+      finish_lse(m, l);
+    } else {
+      const int c0 = attn_owner(u.first, run.total, run.ctas), c1 = attn_owner(u.first + u.n - 1, run.total, run.ctas);
+      float2* stats = reinterpret_cast<float2*>(p.ws + kAttnStats);
+      float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
+      auto place = [&](int c, bool begins) { return (int64_t)(2 * c + (begins ? 1 : 0)) * AT_BM + r; };
+      const int64_t mine = place(blockIdx.x, u.s0 == 0);
+      if (real) __stcg(stats + mine, make_float2(m, l));
+#pragma unroll 1
+      for (int d = 0; d < dims; d += 32) {
+        float o[32];
+        tmem_ld32(ot + d, o);
+        tmem_ld_wait();
+        if (real) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            __stcg(reinterpret_cast<float4*>(sums + mine * DP + d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+        }
+      }
+      __threadfence();
+      mbar_arrive(bar.join(t));
+      if (!(ok = warp_wait(bar.join(t), jp, p.err))) break;
+      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0 + t;
+      if (row == 0) arrived[t] = atomicAdd(count, 1u);
+      mbar_arrive(bar.join(t));
+      if (!(ok = warp_wait(bar.join(t), jp ^ 1, p.err))) break;
+      if (arrived[t] == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
+        __threadfence();
+        if (row == 0) *count = 0;
+        if (real) {
+          float M = -INFINITY, sum = 0.0f;
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(stats + place(c, c == c0)).x);
+          for (int c = c0; c <= c1; ++c) {
+            const float2 ml = __ldcg(stats + place(c, c == c0));
+            sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
+          }
+          const float inv = __fdiv_rn(1.0f, sum);
+#pragma unroll 1
+          for (int d = 0; d < dims; d += 32) {
+            float o[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0.0f;
+            for (int c = c0; c <= c1; ++c) {
+              const int64_t at = place(c, c == c0);
+              const float f = exp2_fast((__ldcg(stats + at).x - safe_max(M)) * p.scale_log2);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(sums + at * DP + d + e));
+                o[e] = fmaf(v.x, f, o[e]);
+                o[e + 1] = fmaf(v.y, f, o[e + 1]);
+                o[e + 2] = fmaf(v.z, f, o[e + 2]);
+                o[e + 3] = fmaf(v.w, f, o[e + 3]);
+              }
+            }
+            finish(o, d, inv);
+          }
+          finish_lse(M, sum);
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before();  // O has been read: the next unit's first P V, which waits for this group's P, may overwrite it
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) {
+  using C = TileCfg<DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint32_t tmem_at, arrived[2], skip;
+  __shared__ int odd[3];
+  uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  const uint32_t sm32 = smem_u32(sm);
+  const TileBars<DP> bar{sm32 + C::kBars};
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar.k_full(s), AT_LOADERS);
+      mbar_init(bar.v_full(s), AT_LOADERS);
+      mbar_init(bar.k_empty(s), 1);
+      mbar_init(bar.v_empty(s), 1);
+    }
+    mbar_init(bar.q_full(), AT_LOADERS);
+    mbar_init(bar.q_empty(), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar.s_full(t), 1);
+      mbar_init(bar.p_full(t), 128);
+      mbar_init(bar.o_full(t), 1);
+      mbar_init(bar.join(t), 128);
+    }
+    mbar_init(bar.done(), 1);
+    fence_mbar_init();
+    odd[0] = odd[1] = odd[2] = 0;
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&tmem_at), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) skip = *(volatile uint32_t*)p.err & kAbortMask;
+  AttnRun run = attn_plan<AT_BM, AT_KEYS, AT_THREADS>(p, reinterpret_cast<int64_t*>(sm));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (skip) run.end = run.begin;  // an earlier call gave up
+  const uint32_t tmem = tmem_at;
+  if (warp < 8) {
+    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived);
+  } else if (warp == 8) {
+    if (lane_id() == 0) mma_role<T, DP>(p, run, bar, sm32, tmem);
+    __syncwarp();
+  } else {
+    load_role<T, DP>(p, run, bar, sm, sm32, odd);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int DP>
+fp4moe_status attn_tile_run(const AttnParams& p, int nsm, cudaStream_t st) {
+  using C = TileCfg<DP>;
+  static PerDevice done;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP4MOE_CUDA_ERROR;
+  if (done.get(dev, [] {
+        return cudaFuncSetAttribute(attn_tile_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+                       cudaSuccess
+                   ? 1
+                   : 0;
+      }) <= 0)
+    return FP4MOE_CUDA_ERROR;
+  return launch_pdl(attn_tile_kernel<T, DP>, dim3((unsigned)nsm), dim3(AT_THREADS), C::kSmem, st, p) == cudaSuccess
+             ? FP4MOE_OK
+             : FP4MOE_CUDA_ERROR;
+}
+
+}  // namespace
+
+fp4moe_status attn_tile_launch(int32_t dtype, const AttnParams& p, int nsm, cudaStream_t st) {
+  if (dtype == FP4MOE_BF16)
+    return p.D <= 64 ? attn_tile_run<__nv_bfloat16, 64>(p, nsm, st) : attn_tile_run<__nv_bfloat16, 128>(p, nsm, st);
+  return p.D <= 64 ? attn_tile_run<__half, 64>(p, nsm, st) : attn_tile_run<__half, 128>(p, nsm, st);
+}
+
+}  // namespace fp4moe
