@@ -7,13 +7,16 @@
 // The tensor cores work on one tile while the other's softmax runs:
 //   warps 0-3, 4-7     softmax, rescaling and output of tile 0 and 1 (warp w: TMEM lanes 32 (w % 4) ..)
 //   warp 8             MMAs: for each step, of each tile the P V of the step before and the next Q K^T
-//   warps 9, 10        loads: q, k and v by 16-byte cp.async, for any page size and stride (a lane looks a key's place up for
-//                      the lanes that copy it), into 128-byte-swizzled tiles, two loads in flight behind the one being made
+//   warp 9, warp 10    loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
+//                      swizzle atoms: a box is 64 dims of the keys that a page and a step share (gcd(page size, 128)), one
+//                      lane a box. Other page sizes by 16-byte cp.async, a lane looking a key's place up for the lanes that
+//                      copy it.
 // The MMAs of one thread run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
 // take the place of S(j). O is rescaled only where a row's maximum grew by more than 2^8; until then P and its sum are
 // under the old maximum, up to 256, which neither 16-bit type minds.
-// Keys outside the tile's range are zeros in shared memory; those that a row does not see have score -infinity. Where a
-// v that only some rows see is not finite (0 times it would be NaN), the unit's rows are made again one by one.
+// Scores of keys that a row does not see are -infinity; v of keys outside the tile's range is zeroed in shared memory, for 0
+// times what lies there may be NaN. Where a v that only some rows see is not finite, the unit's rows are made again one by
+// one.
 // Every wait is bounded, as in the layer's GEMMs.
 #include "attn.cuh"
 
@@ -22,7 +25,6 @@ namespace {
 
 constexpr int AT_BM = 256, AT_KEYS = 128;
 constexpr int AT_THREADS = 352;    // 168 registers a thread: a row of S stays in them
-constexpr int AT_LOADERS = 2;      // warps
 constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
 
 template <int DP>
@@ -54,8 +56,40 @@ struct TileBars {
   __device__ __forceinline__ uint32_t o_full(int t) const { return base + 8 * (4 * C::kStages + 6 + t); }
   __device__ __forceinline__ uint32_t join(int t) const { return base + 8 * (4 * C::kStages + 8 + t); }
   __device__ __forceinline__ uint32_t done() const { return base + 8 * (4 * C::kStages + 10); }
+  __device__ __forceinline__ uint32_t landed() const { return base + 8 * (4 * C::kStages + 11); }
 };
 
+// Tensor maps: k and v as [pages][tokens][heads][dims], boxes of `rows` tokens x 64 dims; q as [T][heads][dims], boxes of
+// 128 rows x 64 dims where the heads of a group divide 128.
+struct TileMaps {
+  CUtensorMap k, v, q;
+  int rows;   // 0: no boxes, by cp.async
+  int q_box;  // whether q has boxes
+};
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          dst),
+      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Whether the phase has completed, without waiting (try_wait may suspend the thread for microseconds).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // The whole warp waits, and goes on together.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* err) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err));
@@ -109,23 +143,17 @@ __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ---------------------------------------------------------------- loads
+// ---------------------------------------------------------------- loads (one warp for q and k, one for v)
 template <typename T, int DP>
 struct Loader {
   using C = TileCfg<DP>;
   static constexpr int CH = DP / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows of a warp's copy instruction
   const AttnParams& p;
+  const TileMaps& maps;
+  const TileBars<DP>& bar;
   uint8_t* sm;
-  volatile int* odd;  // [unit % 3]: unit + 1 if a v that only some rows see is not finite
-  int warp, lane, dims;
-  // a load whose arrival is still to be told: its barrier, and the stage of v to be looked through for the unit (or -1)
-  struct Load {
-    uint32_t bar;
-    int look, unit;
-  };
-  Load older, newer;
-  int waiting;
-
+  uint32_t sm32;
+  int lane, dims;
   // 32 rows from row0 on; `off` is the element offset of this lane's row, negative: zeros.
   __device__ __forceinline__ void rows32(uint32_t tile, int row0, const T* base, int64_t off) {
     const int c = lane % CH;
@@ -139,116 +167,182 @@ struct Loader {
         cp_async16(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4), base + (use ? ro + c * 8 : 0), use);
     }
   }
-  // The older load has landed: tell it.
-  __device__ __forceinline__ void tell() {
-    if (older.look >= 0) {
-      const uint8_t* tile = sm + C::kV + older.look * C::kTile;
-      bool bad = false;
-      const int c = lane % CH;
-      if (c * 8 < dims)
-        for (int it = 0; it < 64 / RPI; ++it) {
-          const int row = warp * 64 + it * RPI + lane / CH;
-          bad |= any_nonfinite<T>(*reinterpret_cast<const uint4*>(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
-        }
-      if (bad) odd[older.unit % 3] = older.unit + 1;
-    }
+  // All copies issued so far have landed: tell it.
+  __device__ __forceinline__ void told(uint32_t b) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(older.bar);
-    older = newer;
-    --waiting;
+    if (lane == 0) mbar_arrive(b);
   }
-  __device__ __forceinline__ void drain() {
-    cp_async_wait<0>();
-    while (waiting) tell();
-  }
-  // Everything for `b` has been issued.
-  __device__ __forceinline__ void issued(uint32_t b, int look, int unit) {
-    cp_async_commit();
-    if (waiting == 2) {
-      cp_async_wait<2>();
-      tell();
-    }
-    const Load load{b, look, unit};
-    if (waiting == 0) older = load;
-    else newer = load;
-    ++waiting;
-  }
-  // A free stage; what is on its way is told first if there is none yet, for that may be what frees it.
-  __device__ __forceinline__ bool free_stage(uint32_t b, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
-    drain();
-    return warp_wait(b, parity, p.err);
-  }
-};
-
-template <typename T, int DP>
-__device__ __forceinline__ void load_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint8_t* sm,
-                                          uint32_t sm32, volatile int* odd) {
-  using C = TileCfg<DP>;
-  const int warp = (threadIdx.x >> 5) - 9, lane = lane_id();
-  Loader<T, DP> L{p, sm, odd, warp, lane, (p.D + 15) / 16 * 16, {}, {}, 0};
-  const T *kbase = static_cast<const T*>(p.k), *vbase = static_cast<const T*>(p.v);
-  int stage = 0, units = 0;
-  uint32_t phase = 1;  // of the empty barriers: the first round finds all stages free
-  bool ok = true;
-  AttnWalk walk(run);
-  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
-    if (!(ok = L.free_stage(bar.q_empty(), (units & 1) ^ 1))) break;
+  // One tile (128 rows) of the unit's q, by cp.async.
+  __device__ __forceinline__ void q_rows(const AttnUnit& u, int t) {
 #pragma unroll 1
-    for (int part = 0; part < 4; ++part) {
-      const int row = warp * 64 + (part & 1) * 32, r = (part >> 1) * 128 + row + lane;
+    for (int r0 = 0; r0 < 128; r0 += 32) {
+      const int r = t * 128 + r0 + lane;
       int64_t off = -1;
       if (r < u.rows) {
         const int tok = (int)p.group.div(u.row0 + r), g = u.row0 + r - tok * (int)p.group.d;
         off = (int64_t)(u.seq.first + tok) * p.q_stride + (int64_t)(u.head * (int)p.group.d + g) * p.D;
       }
-      L.rows32(sm32 + (part >> 1) * C::kTile, row, static_cast<const T*>(p.q), off);
+      rows32(sm32 + t * C::kTile, r0, static_cast<const T*>(p.q), off);
     }
-    L.issued(bar.q_full(), -1, units);
+    cp_async_commit();
+    cp_async_wait<0>();
+    told(bar.q_full());
+  }
+  // Where a key of the unit lies: its page, or num_pages (zeros) if it has none or a bad one.
+  __device__ __forceinline__ int page_of(const AttnUnit& u, const int32_t* table, int key, bool there) {
+    return there && key >= u.range.x && key < u.range.y ? __ldg(table + p.map.page.div(key)) : -2;
+  }
+  __device__ __forceinline__ int checked(int page) {
+    if ((uint32_t)page < (uint32_t)p.map.num_pages) return page;
+    if (page != -2) raise_error(p.err, FP4MOE_ERR_PAGE);
+    return p.map.num_pages;
+  }
+  __device__ __forceinline__ int in_page(int key) { return key - (int)p.map.page.div(key) * (int)p.map.page.d; }
+  // 128 keys from k0 on into `tile`, by cp.async; page[h]: that of key k0 + 32 h + lane.
+  __device__ __forceinline__ void key_rows(const AttnUnit& u, uint32_t tile, const T* base, int k0, const int (&page)[4]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int pg = checked(page[h]);
+      const int64_t off = pg == p.map.num_pages ? -1
+                                                : pg * p.map.page_stride + (int64_t)in_page(k0 + h * 32 + lane) * p.map.token_stride +
+                                                      (int64_t)u.head * p.map.head_stride;
+      rows32(tile, h * 32, base, off);
+    }
+    cp_async_commit();
+  }
+};
+
+// One of the two streams: WHICH = 0 k (and q), 1 v. Stages go round; load n is told on full(n % kStages).
+template <typename T, int DP, bool BOXES, int WHICH>
+__device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& maps, const AttnRun& run, const TileBars<DP>& bar,
+                                          uint8_t* sm, uint32_t sm32, volatile int* odd) {
+  using C = TileCfg<DP>;
+  const int lane = lane_id();
+  Loader<T, DP> L{p, maps, bar, sm, sm32, lane, (p.D + 15) / 16 * 16};
+  const T* base = static_cast<const T*>(WHICH ? p.v : p.k);
+  const CUtensorMap* map = WHICH ? &maps.v : &maps.k;
+  const uint32_t tiles = WHICH ? C::kV : C::kK;
+  auto full = [&](int s) { return WHICH ? bar.v_full(s) : bar.k_full(s); };
+  auto empty = [&](int s) { return WHICH ? bar.v_empty(s) : bar.k_empty(s); };
+  const int per = BOXES ? 128 / maps.rows : 1, boxes = per * (p.D > 64 ? 2 : 1);  // of a step: one lane each
+  const int box_key = lane % per * maps.rows, box_col = lane / per;
+  int stage = 0, units = 0;
+  uint32_t phase = 0;
+  int64_t issued = 0;
+  bool ok = true;
+  // The load that is looked after once it has landed: a step of v that is not all visible to all rows, or one by cp.async.
+  struct {
+    bool any, rows;  // rows: zero those outside [lo, hi); mark: unit + 1 if those inside are looked through
+    int stage, k0, lo, hi, mark;
+    int64_t n;
+  } late{};
+  uint32_t landed = 0;
+  auto look_after = [&](bool newer) -> bool {  // newer: a cp.async load has been issued since
+    if (!late.any) return true;
+    if (BOXES) {
+      if (!warp_wait(bar.landed(), landed, p.err)) return false;
+      landed ^= 1;
+    } else {
+      if (newer) cp_async_wait<1>();
+      else cp_async_wait<0>();
+      __syncwarp();
+    }
+    late.any = false;
+    if (WHICH && (late.rows || late.mark)) {
+      bool bad = false;
+      uint8_t* tile = sm + C::kV + late.stage * C::kTile;
+      for (int i = lane; i < 128 * C::kBlocks * 8; i += 32) {  // 16 bytes each, rows in turn
+        const int row = i / (C::kBlocks * 8), c = i % (C::kBlocks * 8);
+        uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        if (late.k0 + row < late.lo || late.k0 + row >= late.hi) *at = make_uint4(0u, 0u, 0u, 0u);
+        else if (late.mark) bad |= any_nonfinite<T>(*at);
+      }
+      if (bad) odd[(late.mark - 1) % 3] = late.mark;
+    }
+    L.told(full(late.stage));
+    return true;
+  };
+  AttnWalk walk(run);
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+    const int n = u.s1 - u.s0, first = (u.range.x / AT_KEYS + u.s0) * AT_KEYS;
+    const int32_t* table = p.table + (int64_t)u.b * p.columns;
+    int page[4];
+    auto look_up = [&](int i) {
+      const int k0 = first + i * AT_KEYS;
+      if (BOXES) {
+        page[0] = L.page_of(u, table, max(k0 + box_key, u.range.x), i < n && lane < boxes && k0 + box_key + maps.rows > u.range.x);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) page[h] = L.page_of(u, table, k0 + h * 32 + lane, i < n);
+      }
+    };
+    look_up(0);
+    if (WHICH == 0 || !maps.q_box) {
+      if (!(ok = warp_wait(bar.q_empty(), (units & 1) ^ 1, p.err))) break;
+      const int qt = u.rows > 128 ? 2 : 1;
+      if (!maps.q_box) {
+        L.q_rows(u, WHICH);
+      } else {
+        const int blocks = p.D > 64 ? 2 : 1;
+        if (lane == 0) mbar_arrive_expect_tx(bar.q_full(), qt * blocks * C::kBlock);
+        __syncwarp();
+        if (lane < qt * blocks) {
+          const int t = lane / blocks, b = lane % blocks;
+          tma_load_3d(sm32 + t * C::kTile + b * C::kBlock, &maps.q, bar.q_full(), b * 64, u.head * (int)p.group.d,
+                      u.seq.first + (int)p.group.div(u.row0 + t * 128));
+        }
+      }
+    }
     const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + u.rows - 1)).x;
     const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0)).y;
-    const bool differ = all_lo != u.range.x || all_hi != u.range.y;
-    const int first = (u.range.x / AT_KEYS + u.s0) * AT_KEYS;
-    const int32_t* table = p.table + (int64_t)u.b * p.columns;
-    const int64_t head_off = (int64_t)u.head * p.map.head_stride;
-    auto key_of = [&](int i, int h) { return first + i * AT_KEYS + warp * 64 + h * 32 + lane; };
-    auto page_of = [&](int i, int h) {  // page of the key that this lane looks up in step i; -2: none
-      const int key = key_of(i, h);
-      return i < u.s1 - u.s0 && key >= u.range.x && key < u.range.y ? __ldg(table + p.map.page.div(key)) : -2;
-    };
-    int next[2] = {page_of(0, 0), page_of(0, 1)};
-    for (int i = 0; i < u.s1 - u.s0; ++i) {
-      int64_t off[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = key_of(i, h);
-        off[h] = -1;
-        if (next[h] != -2) {
-          if ((uint32_t)next[h] < (uint32_t)p.map.num_pages)
-            off[h] = next[h] * p.map.page_stride +
-                     (int64_t)(key - (int)p.map.page.div(key) * (int)p.map.page.d) * p.map.token_stride + head_off;
-          else
-            raise_error(p.err, FP4MOE_ERR_PAGE);
-        }
-        next[h] = page_of(i + 1, h);
-      }
-      if (!(ok = L.free_stage(bar.k_empty(stage), phase))) break;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) L.rows32(sm32 + C::kK + stage * C::kTile, warp * 64 + h * 32, kbase, off[h]);
-      L.issued(bar.k_full(stage), -1, units);
-      if (!(ok = L.free_stage(bar.v_empty(stage), phase))) break;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) L.rows32(sm32 + C::kV + stage * C::kTile, warp * 64 + h * 32, vbase, off[h]);
+    for (int i = 0; i < n; ++i) {
       const int k0 = first + i * AT_KEYS;
-      L.issued(bar.v_full(stage), differ && (k0 < all_lo || k0 + AT_KEYS > all_hi) ? stage : -1, units);
+      // what is late may be what frees the stage
+      if (late.any && !mbar_test(empty(stage), phase ^ 1) && !(ok = look_after(false))) break;
+      if (!(ok = warp_wait(empty(stage), phase ^ 1, p.err))) break;
+      const bool edge = k0 < u.range.x || k0 + AT_KEYS > u.range.y, some = k0 < all_lo || k0 + AT_KEYS > all_hi;
+      const bool differ = some && (all_lo != u.range.x || all_hi != u.range.y);
+      const bool look = !BOXES || (WHICH && (edge || differ));
+      const uint32_t tile = sm32 + tiles + stage * C::kTile;
+      if (BOXES) {
+        if (look && !(ok = look_after(false))) break;  // one at a time
+        const uint32_t b = look ? bar.landed() : full(stage);
+        if (lane == 0) mbar_arrive_expect_tx(b, (p.D > 64 ? 2 : 1) * C::kBlock);
+        __syncwarp();
+        if (lane < boxes)
+          tma_load_4d(tile + box_col * C::kBlock + box_key * 128, map, b, box_col * 64, u.head, L.in_page(k0 + box_key),
+                      L.checked(page[0]));
+      } else {
+        L.key_rows(u, tile, base, k0, page);
+      }
+      look_up(i + 1);
+      if (!BOXES && !(ok = look_after(true))) break;
+      if (look) {
+        late.any = true;
+        late.rows = BOXES && edge;  // (cp.async has filled them with zeros)
+        late.stage = stage;
+        late.k0 = k0;
+        late.lo = u.range.x;
+        late.hi = u.range.y;
+        late.mark = differ ? units + 1 : 0;
+        late.n = issued;
+      }
+      ++issued;
       if (++stage == C::kStages) {
         stage = 0;
         phase ^= 1;
       }
     }
+    if (ok) ok = look_after(false);
   }
-  L.drain();
+  cp_async_wait<0>();
+  if (BOXES && !ok) {  // it gave up: what is in flight still has to land
+    if (late.any) drain_wait(bar.landed(), landed);
+    for (int64_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+      if (!late.any || i != late.n) drain_wait(full(i % C::kStages), (i / C::kStages) & 1);
+  }
+  if (!ok && WHICH == 0 && maps.q_box) drain_wait(bar.q_full(), units & 1);
 }
 
 // ---------------------------------------------------------------- MMAs (one thread)
@@ -260,21 +354,24 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
   const uint32_t is = idesc_16<T>(AT_KEYS, false), io = idesc_16<T>(dims, true);
   int ks = 0, vs = 0, units = 0;
   uint32_t kp = 0, vp = 0, pp = 0;  // phases of the k and v stages, and of the p barriers (bit t)
+  // descriptors count in 16 bytes, so offsets are added to them
+  const uint64_t qd = desc_sw128(sm32), kd = desc_sw128(sm32 + C::kK), vd = desc_sw128_t(sm32 + C::kV, C::kBlock);
   auto qk = [&](int t) {
+    const uint64_t a = qd + (uint32_t)(t * (C::kTile >> 4)), b = kd + (uint32_t)(ks * (C::kTile >> 4));
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       if (i * 16 < dims) {
-        const uint32_t at = (i >> 2) * C::kBlock + (i & 3) * 32;
-        mma_ss(tmem + t * 128, desc_sw128(sm32 + t * C::kTile + at), desc_sw128(sm32 + C::kK + ks * C::kTile + at), is, i > 0);
+        constexpr uint32_t block = C::kBlock >> 4;
+        const uint32_t at = (i >> 2) * block + (i & 3) * 2;
+        mma_ss(tmem + t * 128, a + at, b + at, is, i > 0);
       }
     }
     tc_commit(bar.s_full(t));
   };
   auto pv = [&](int t, bool first) {
+    const uint64_t b = vd + (uint32_t)(vs * (C::kTile >> 4));
 #pragma unroll
-    for (int i = 0; i < AT_KEYS / 16; ++i)
-      mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, desc_sw128_t(sm32 + C::kV + vs * C::kTile + i * 2048, C::kBlock), io,
-             !(first && i == 0));
+    for (int i = 0; i < AT_KEYS / 16; ++i) mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, b + i * 128, io, !(first && i == 0));
   };
   AttnWalk walk(run);
   bool ok = true;
@@ -530,8 +627,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
   }
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) {
+template <typename T, int DP, bool BOXES>
+__global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, const __grid_constant__ TileMaps maps) {
   using C = TileCfg<DP>;
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t tmem_at, arrived[2], skip;
@@ -542,12 +639,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar.k_full(s), AT_LOADERS);
-      mbar_init(bar.v_full(s), AT_LOADERS);
+      mbar_init(bar.k_full(s), 1);
+      mbar_init(bar.v_full(s), 1);
       mbar_init(bar.k_empty(s), 1);
       mbar_init(bar.v_empty(s), 1);
     }
-    mbar_init(bar.q_full(), AT_LOADERS);
+    mbar_init(bar.q_full(), maps.q_box ? 1 : 2);  // both loading warps bring a tile without boxes
     mbar_init(bar.q_empty(), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar.s_full(t), 1);
@@ -556,6 +653,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) 
       mbar_init(bar.join(t), 128);
     }
     mbar_init(bar.done(), 1);
+    mbar_init(bar.landed(), 1);
     fence_mbar_init();
     odd[0] = odd[1] = odd[2] = 0;
   }
@@ -567,6 +665,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) 
   pdl_trigger();
   if (threadIdx.x == 0) skip = *(volatile uint32_t*)p.err & kAbortMask;
   AttnRun run = attn_plan<AT_BM, AT_KEYS, AT_THREADS>(p, reinterpret_cast<int64_t*>(sm));
+  fence_proxy_async_smem();  // the division's sums lie where loads will
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -577,8 +676,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) 
   } else if (warp == 8) {
     if (lane_id() == 0) mma_role<T, DP>(p, run, bar, sm32, tmem);
     __syncwarp();
+  } else if (warp == 9) {
+    load_role<T, DP, BOXES, 0>(p, maps, run, bar, sm, sm32, odd);
   } else {
-    load_role<T, DP>(p, run, bar, sm, sm32, odd);
+    load_role<T, DP, BOXES, 1>(p, maps, run, bar, sm, sm32, odd);
   }
   tc_fence_before();
   __syncthreads();
@@ -586,30 +687,78 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p) 
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int DP>
-fp4moe_status attn_tile_run(const AttnParams& p, int nsm, cudaStream_t st) {
+template <typename T, int DP, bool BOXES>
+fp4moe_status attn_tile_run(const AttnParams& p, const TileMaps& maps, int nsm, cudaStream_t st) {
   using C = TileCfg<DP>;
   static PerDevice done;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP4MOE_CUDA_ERROR;
   if (done.get(dev, [] {
-        return cudaFuncSetAttribute(attn_tile_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+        return cudaFuncSetAttribute(attn_tile_kernel<T, DP, BOXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
                        cudaSuccess
                    ? 1
                    : 0;
       }) <= 0)
     return FP4MOE_CUDA_ERROR;
-  return launch_pdl(attn_tile_kernel<T, DP>, dim3((unsigned)nsm), dim3(AT_THREADS), C::kSmem, st, p) == cudaSuccess
+  return launch_pdl(attn_tile_kernel<T, DP, BOXES>, dim3((unsigned)nsm), dim3(AT_THREADS), C::kSmem, st, p, maps) == cudaSuccess
              ? FP4MOE_OK
              : FP4MOE_CUDA_ERROR;
+}
+
+decltype(&cuTensorMapEncodeTiled) tiled_encoder() {
+  static const auto fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
+  }();
+  return fn;
+}
+// dims and box from the innermost on; strides of the others in elements of 2 bytes, that of a dimension of one element
+// being of no account. False where a map cannot say it.
+bool encode_boxes(CUtensorMap* m, int32_t dtype, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+                  const uint32_t* box) {
+  const auto encode = tiled_encoder();
+  if (encode == nullptr) return false;
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = box[i];
+    if (i == 0) continue;
+    s[i - 1] = dims[i] == 1 ? 16 : (cuuint64_t)strides[i - 1] * 2;
+    if (s[i - 1] == 0 || s[i - 1] >= (1ull << 40)) return false;
+  }
+  return encode(m, dtype == FP4MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+fp4moe_status attn_tile_typed(const AttnParams& p, const TileMaps& maps, int nsm, cudaStream_t st) {
+  if (maps.rows) return p.D <= 64 ? attn_tile_run<T, 64, true>(p, maps, nsm, st) : attn_tile_run<T, 128, true>(p, maps, nsm, st);
+  return p.D <= 64 ? attn_tile_run<T, 64, false>(p, maps, nsm, st) : attn_tile_run<T, 128, false>(p, maps, nsm, st);
 }
 
 }  // namespace
 
 fp4moe_status attn_tile_launch(int32_t dtype, const AttnParams& p, int nsm, cudaStream_t st) {
-  if (dtype == FP4MOE_BF16)
-    return p.D <= 64 ? attn_tile_run<__nv_bfloat16, 64>(p, nsm, st) : attn_tile_run<__nv_bfloat16, 128>(p, nsm, st);
-  return p.D <= 64 ? attn_tile_run<__half, 64>(p, nsm, st) : attn_tile_run<__half, 128>(p, nsm, st);
+  TileMaps maps{};
+  int rows = 128;  // whole 8-row swizzle atoms that divide a page
+  while (p.map.page.d % rows != 0) rows /= 2;
+  const int64_t kd[4] = {p.D, p.kv_heads, p.map.page.d, p.map.num_pages};
+  const int64_t ks[3] = {p.map.head_stride, p.map.token_stride, p.map.page_stride};
+  const uint32_t kb[4] = {64, 1, (uint32_t)rows, 1};
+  if (rows >= 8 && encode_boxes(&maps.k, dtype, p.k, 4, kd, ks, kb) && encode_boxes(&maps.v, dtype, p.v, 4, kd, ks, kb))
+    maps.rows = rows;
+  if (128 % p.group.d == 0) {
+    const int64_t qd[3] = {p.D, p.q_heads, p.T}, qs[2] = {p.D, p.q_stride};
+    const uint32_t qb[3] = {64, p.group.d, 128 / p.group.d};
+    maps.q_box = encode_boxes(&maps.q, dtype, p.q, 3, qd, qs, qb);
+  }
+  return dtype == FP4MOE_BF16 ? attn_tile_typed<__nv_bfloat16>(p, maps, nsm, st) : attn_tile_typed<__half>(p, maps, nsm, st);
 }
 
 }  // namespace fp4moe
