@@ -15,6 +15,7 @@ namespace fp4moe {
 namespace {
 
 constexpr int AD_ROWS = 16, AD_KEYS = 16;  // of a tile, of a warp's group
+constexpr int AD_OH = 1;                     // what a tile costs, in slices, beside its slices
 
 template <int DP>
 struct AttnCfg {
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const AttnRun run = attn_plan<AD_ROWS, C::S, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
+  const AttnRun run = attn_plan<AD_ROWS, C::S, AD_OH, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
   uint8_t* ring = sm + warp * C::kRing;
   const uint32_t ring32 = smem_u32(ring);
   const T* kbase = static_cast<const T*>(p.k);
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   const int dims = (p.D + 15) / 16 * 16;  // MMA steps past the head's own dims are left out
   const int qr = lane >> 2, qc = (lane & 3) * 2;
   AttnWalk walk(run);
-  for (AttnUnit u; walk.next<AD_ROWS, C::S>(p, run, u);) {
+  for (AttnUnit u; walk.next<AD_ROWS, C::S, AD_OH>(p, run, u);) {
     const AttnSeq& seq = u.seq;
     const int kv = u.kv, head = u.head, row0 = u.row0, rows = u.rows, n = u.n, s0 = u.s0, s1 = u.s1;
     const int2 range = u.range;

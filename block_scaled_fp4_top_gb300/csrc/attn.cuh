@@ -5,10 +5,11 @@
 // same keys. A tile is BM of them. It sees the keys [lo, hi), and costs ceil(hi / S) - floor(lo / S) slices of S keys (at
 // least one: a tile without keys still has to be written).
 //
-// Division. The slices of all tiles and kv heads, in order, are cut into gridDim.x equal runs, one for each CTA, whatever
-// the lengths are: a long sequence is spread over many CTAs, and many short ones are shared out evenly. A CTA's run
-// holds parts of at most two tiles that other CTAs share: the one that it starts in (begun by an earlier CTA) and the one
-// that it ends in. Each CTA finds its run by itself from q_offset and kv_len.
+// Division. A tile and kv head costs OH (to begin and end it) and one for each slice. The costs of all of them, in order,
+// are cut into gridDim.x equal runs, one for each CTA, whatever the lengths are: a long sequence is spread over many
+// CTAs, and many short ones are shared out evenly. A CTA's run holds parts of at most two tiles that other CTAs share:
+// the one that it starts in (begun by an earlier CTA) and the one that it ends in. Each CTA finds its run by itself from
+// q_offset and kv_len.
 //
 // Join. A CTA leaves the unnormalised sums of its part (fp32, under its own maximum) in the workspace and counts itself
 // in; the last one adds the parts in the order of the CTAs, so equal inputs give equal bits, and sets the count back.
@@ -79,16 +80,16 @@ __device__ __forceinline__ int attn_slices(int2 r) {
   return max(1, (r.y + S - 1) / S - r.x / S);
 }
 
-// Where a CTA's run of slices lies, and where it starts.
+// Where a CTA's run of costs lies, and where it starts.
 struct AttnRun {
-  int64_t total, begin, end;  // slices of the call, and the CTA's own
-  int ctas;                   // CTAs that have a run: no more than there are slices, so that none of these is empty
-  int seq, tile, head;        // of slice `begin`
-  int slice;                  // its place in its tile
+  int64_t total, begin, end;  // of the call, and the CTA's own
+  int ctas;                   // CTAs that have a run: no more than the total, so that none of these is empty
+  int seq, tile, head;        // of `begin`
+  int at;                     // its place in its tile and head: the first OH are before slice 0
 };
 
 __device__ __forceinline__ int64_t attn_begin(int64_t total, int cta, int ctas) { return total * cta / ctas; }
-// The CTA whose run holds slice x.
+// The CTA whose run holds x.
 __device__ __forceinline__ int attn_owner(int64_t x, int64_t total, int ctas) {
   int c = (int)(x * ctas / total);
   while (c + 1 < ctas && attn_begin(total, c + 1, ctas) <= x) ++c;
@@ -97,12 +98,12 @@ __device__ __forceinline__ int attn_owner(int64_t x, int64_t total, int ctas) {
 }
 
 // All threads of the CTA call this. sums: (B + THREADS / 32 + 2) * 8 bytes of shared memory, free again afterwards.
-template <int BM, int S, int THREADS>
+template <int BM, int S, int OH, int THREADS>
 __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int WARPS = THREADS / 32;
   int64_t* part = sums;         // [WARPS + 1]
-  int64_t* upto = sums + WARPS + 1;  // [B] slices of the sequences up to and with b
+  int64_t* upto = sums + WARPS + 1;  // [B] costs of the sequences up to and with b
   const int per = (p.B + THREADS - 1) / THREADS;
   uint32_t bad = 0;
   // short sequences by their thread, those of several tiles by a warp
@@ -118,7 +119,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
       s = attn_seq(p, q0, q1, kv);
       if (s.keys != kv && s.rows > 0) bad = 1;
       if (s.rows > BM) big = 1;
-      else if (s.rows > 0) w = (int64_t)attn_slices<S>(attn_tile_range<BM>(p, s, kv, 0)) * p.kv_heads;
+      else if (s.rows > 0) w = (int64_t)(OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, 0))) * p.kv_heads;
     }
     for (uint32_t m = __ballot_sync(0xFFFFFFFFu, big); m; m &= m - 1) {
       const int src = __ffs(m) - 1;
@@ -129,7 +130,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
       o.tokens = __shfl_sync(0xFFFFFFFFu, s.tokens, src);
       const int okv = __shfl_sync(0xFFFFFFFFu, kv, src);
       int64_t sum = 0;
-      for (int t = lane; t < (o.rows + BM - 1) / BM; t += 32) sum += attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
+      for (int t = lane; t < (o.rows + BM - 1) / BM; t += 32) sum += OH + attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
       if (lane == src) w = sum * p.kv_heads;
@@ -165,7 +166,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
   r.ctas = (int)min(total, (int64_t)gridDim.x);
   r.begin = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x, r.ctas) : 0;
   r.end = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x + 1, r.ctas) : 0;
-  r.seq = r.tile = r.head = r.slice = 0;
+  r.seq = r.tile = r.head = r.at = 0;
   if (r.begin < r.end) {
     int lo = 0, hi = p.B - 1;  // first sequence with upto > begin
     while (lo < hi) {
@@ -180,7 +181,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
     const int tiles = (s.rows + BM - 1) / BM;
     for (int t0 = 0; t0 < tiles; t0 += 32) {  // every warp for itself
       const int t = t0 + lane;
-      const int64_t w = t < tiles ? (int64_t)attn_slices<S>(attn_tile_range<BM>(p, s, kv, t)) * p.kv_heads : 0;
+      const int64_t w = t < tiles ? (int64_t)(OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, t))) * p.kv_heads : 0;
       int64_t y = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -194,7 +195,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
         left -= __shfl_sync(0xFFFFFFFFu, y - w, src);
         const int n = (int)(__shfl_sync(0xFFFFFFFFu, w, src) / p.kv_heads);
         r.head = (int)(left / n);
-        r.slice = (int)(left - (int64_t)r.head * n);
+        r.at = (int)(left - (int64_t)r.head * n);
         break;
       }
       left -= __shfl_sync(0xFFFFFFFFu, y, 31);
@@ -211,22 +212,22 @@ struct AttnUnit {
   int row0, rows;  // the tile's first row of the sequence, and its rows
   int2 range;      // keys that any of them sees
   int n, s0, s1;   // slices of the tile, and those of this unit
-  int64_t first;   // the tile's first slice among the call's
+  int64_t first;   // slice 0's place among the call's costs
 };
 // The units of a run, one after the other.
 struct AttnWalk {
   int64_t x;
-  int b, tile, head, slice;
+  int b, tile, head, at;
   __device__ __forceinline__ explicit AttnWalk(const AttnRun& r)
-      : x(r.begin), b(r.seq), tile(r.tile), head(r.head), slice(r.slice) {}
-  template <int BM, int S>
+      : x(r.begin), b(r.seq), tile(r.tile), head(r.head), at(r.at) {}
+  template <int BM, int S, int OH>
   __device__ __forceinline__ bool next(const AttnParams& p, const AttnRun& r, AttnUnit& u) {
     while (x < r.end) {
       u.kv = __ldg(p.kv_len + b);
       u.seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), u.kv);
       if (tile * BM >= u.seq.rows) {
         ++b;
-        tile = head = slice = 0;
+        tile = head = at = 0;
         continue;
       }
       u.b = b;
@@ -236,16 +237,17 @@ struct AttnWalk {
       u.rows = min(BM, u.seq.rows - u.row0);
       u.range = attn_tile_range<BM>(p, u.seq, u.kv, tile);
       u.n = attn_slices<S>(u.range);
-      u.s0 = slice;
-      u.s1 = (int)min((int64_t)u.n, slice + (r.end - x));
-      u.first = x - slice;
-      x += u.s1 - u.s0;
-      slice = 0;
+      const int take = (int)min((int64_t)(OH + u.n - at), r.end - x);
+      u.s0 = max(0, at - OH);
+      u.s1 = max(0, at + take - OH);
+      u.first = x - at + OH;
+      x += take;
+      at = 0;
       if (++head == p.kv_heads) {
         head = 0;
         ++tile;
       }
-      return true;
+      if (u.s0 < u.s1) return true;  // (a run may end in front of slice 0)
     }
     return false;
   }

@@ -24,6 +24,7 @@ namespace fp4moe {
 namespace {
 
 constexpr int AT_BM = 256, AT_KEYS = 128;
+constexpr int AT_OH = 2;           // what a unit costs, in steps, beside its steps
 constexpr int AT_THREADS = 352;    // 168 registers a thread: a row of S stays in them
 constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
 
@@ -35,7 +36,8 @@ struct TileCfg {
   static constexpr int kStages = DP == 128 ? 2 : 4;   // of k, and of v
   static constexpr int kK = 2 * kTile, kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  static constexpr int kSmem = kBars + 512 + 1024;    // and to align it
+  static constexpr int kOut = kBars + 512;            // the softmax warps' output, 32 rows x 32 dims each
+  static constexpr int kSmem = kOut + 8 * 2048 + 1024;  // and to align it
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert((FP4MOE_KV_MAX_SEQS + AT_THREADS / 32 + 1) * 8 <= kBars, "the division's sums fit");
 };
@@ -264,7 +266,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
     return true;
   };
   AttnWalk walk(run);
-  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS, AT_OH>(p, run, u); ++units) {
     const int n = u.s1 - u.s0, first = (u.range.x / AT_KEYS + u.s0) * AT_KEYS;
     const int32_t* table = p.table + (int64_t)u.b * p.columns;
     int page[4];
@@ -375,7 +377,7 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
   };
   AttnWalk walk(run);
   bool ok = true;
-  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS, AT_OH>(p, run, u); ++units) {
     const int tiles = u.rows > 128 ? 2 : 1, n = u.s1 - u.s0;
     if (!(ok = mbar_wait(bar.q_full(), units & 1, p.err))) break;
     for (int j = 0; j <= n; ++j) {
@@ -447,7 +449,7 @@ __device__ __noinline__ void row_again(const AttnParams& p, const AttnUnit& u, i
 
 template <typename T, int DP>
 __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint32_t tmem,
-                                             volatile int* odd, volatile uint32_t* arrived) {
+                                             volatile int* odd, volatile uint32_t* arrived, uint8_t* stage) {
   const int t = threadIdx.x >> 7, row = threadIdx.x & 127;
   const uint32_t lanes = (uint32_t)(row & 96) << 16;  // this warp's 32 lanes of TMEM
   const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + 256 + t * DP;
@@ -456,7 +458,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
   uint32_t sp = 0, op = 0, jp = 0;
   bool ok = true;
   AttnWalk walk(run);
-  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS>(p, run, u); ++units) {
+  for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS, AT_OH>(p, run, u); ++units) {
     if (t * 128 >= u.rows) continue;  // (as the MMAs leave the tile out)
     const int last = min(u.rows, t * 128 + 128) - 1, r = min(t * 128 + row, last);
     const bool real = t * 128 + row <= last;
@@ -536,19 +538,28 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     const int tok = (int)p.group.div(u.row0 + r), g = u.row0 + r - tok * (int)p.group.d;
     const int64_t tq = u.seq.first + tok;
     const int hq = u.head * (int)p.group.d + g;
-    T* out = static_cast<T*>(p.out) + tq * p.out_stride + (int64_t)hq * p.D;
+    const int64_t at = real ? tq * p.out_stride + (int64_t)hq * p.D : -1;
     const bool none = see.x >= see.y;  // a row without keys is 0; one whose scores are all -infinity is 0 / 0
+    // 32 dims of the warp's rows, through shared memory: four lanes write a row's 64 bytes
     auto finish = [&](float (&o)[32], int d, float inv) {
-      if (!real) return;
+      const int lane = row & 31;
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
-        if (d + c < p.D) {
-          float v[8];
+      for (int c = 0; c < 4; ++c) {
+        float v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = none ? 0.0f : o[c + e] * inv;
-          *reinterpret_cast<uint4*>(out + d + c) = pack<T>(v);
-        }
+        for (int e = 0; e < 8; ++e) v[e] = none ? 0.0f : o[c * 8 + e] * inv;
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = pack<T>(v);
       }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2), c = lane & 3;
+        const int64_t to = __shfl_sync(0xFFFFFFFFu, at, rr);
+        if (to >= 0 && d + c * 8 < p.D)
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to + d + c * 8) =
+              *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+      }
+      __syncwarp();
     };
     auto finish_lse = [&](float M, float sum) {
       if (real && p.lse != nullptr) p.lse[tq * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(sum));
@@ -567,19 +578,18 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       const int c0 = attn_owner(u.first, run.total, run.ctas), c1 = attn_owner(u.first + u.n - 1, run.total, run.ctas);
       float2* stats = reinterpret_cast<float2*>(p.ws + kAttnStats);
       float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
-      auto place = [&](int c, bool begins) { return (int64_t)(2 * c + (begins ? 1 : 0)) * AT_BM + r; };
-      const int64_t mine = place(blockIdx.x, u.s0 == 0);
-      if (real) __stcg(stats + mine, make_float2(m, l));
+      // the rows' vectors of four dims lie side by side
+      auto slot = [&](int c, bool begins) { return (int64_t)(2 * c + (begins ? 1 : 0)); };
+      auto vec = [&](int64_t s, int d) { return reinterpret_cast<float4*>(sums) + (s * (DP / 4) + d / 4) * AT_BM + t * 128 + row; };
+      const int64_t mine = slot(blockIdx.x, u.s0 == 0);
+      __stcg(stats + mine * AT_BM + t * 128 + row, make_float2(m, l));
 #pragma unroll 1
       for (int d = 0; d < dims; d += 32) {
         float o[32];
         tmem_ld32(ot + d, o);
         tmem_ld_wait();
-        if (real) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            __stcg(reinterpret_cast<float4*>(sums + mine * DP + d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
-        }
+        for (int c = 0; c < 32; c += 4) __stcg(vec(mine, d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
       }
       __threadfence();
       mbar_arrive(bar.join(t));
@@ -591,35 +601,34 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       if (arrived[t] == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
         __threadfence();
         if (row == 0) *count = 0;
-        if (real) {
-          float M = -INFINITY, sum = 0.0f;
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(stats + place(c, c == c0)).x);
-          for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(stats + place(c, c == c0));
-            sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
-          }
-          const float inv = __fdiv_rn(1.0f, sum);
-#pragma unroll 1
-          for (int d = 0; d < dims; d += 32) {
-            float o[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-            for (int c = c0; c <= c1; ++c) {
-              const int64_t at = place(c, c == c0);
-              const float f = exp2_fast((__ldcg(stats + at).x - safe_max(M)) * p.scale_log2);
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(sums + at * DP + d + e));
-                o[e] = fmaf(v.x, f, o[e]);
-                o[e + 1] = fmaf(v.y, f, o[e + 1]);
-                o[e + 2] = fmaf(v.z, f, o[e + 2]);
-                o[e + 3] = fmaf(v.w, f, o[e + 3]);
-              }
-            }
-            finish(o, d, inv);
-          }
-          finish_lse(M, sum);
+        const float2* own = stats + t * 128 + row;
+        float M = -INFINITY, sum = 0.0f;
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(own + slot(c, c == c0) * AT_BM).x);
+        for (int c = c0; c <= c1; ++c) {
+          const float2 ml = __ldcg(own + slot(c, c == c0) * AT_BM);
+          sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
         }
+        const float inv = __fdiv_rn(1.0f, sum);
+#pragma unroll 1
+        for (int d = 0; d < dims; d += 32) {
+          float o[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0.0f;
+          for (int c = c0; c <= c1; ++c) {
+            const int64_t s = slot(c, c == c0);
+            const float f = exp2_fast((__ldcg(own + s * AT_BM).x - safe_max(M)) * p.scale_log2);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 v = __ldcg(vec(s, d + e));
+              o[e] = fmaf(v.x, f, o[e]);
+              o[e + 1] = fmaf(v.y, f, o[e + 1]);
+              o[e + 2] = fmaf(v.z, f, o[e + 2]);
+              o[e + 3] = fmaf(v.w, f, o[e + 3]);
+            }
+          }
+          finish(o, d, inv);
+        }
+        finish_lse(M, sum);
       }
       __syncwarp();
     }
@@ -664,7 +673,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) skip = *(volatile uint32_t*)p.err & kAbortMask;
-  AttnRun run = attn_plan<AT_BM, AT_KEYS, AT_THREADS>(p, reinterpret_cast<int64_t*>(sm));
+  AttnRun run = attn_plan<AT_BM, AT_KEYS, AT_OH, AT_THREADS>(p, reinterpret_cast<int64_t*>(sm));
   fence_proxy_async_smem();  // the division's sums lie where loads will
   tc_fence_before();
   __syncthreads();
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   if (skip) run.end = run.begin;  // an earlier call gave up
   const uint32_t tmem = tmem_at;
   if (warp < 8) {
-    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived);
+    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived, sm + C::kOut + warp * 2048);
   } else if (warp == 8) {
     if (lane_id() == 0) mma_role<T, DP>(p, run, bar, sm32, tmem);
     __syncwarp();
