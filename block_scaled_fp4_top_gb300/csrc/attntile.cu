@@ -6,12 +6,12 @@
 //   O += P V           tcgen05.mma with P out of TMEM, V in shared memory as it lies (keys x dims: transposed B), O in TMEM
 // The tensor cores work on one tile while the other's softmax runs:
 //   warps 0-3, 4-7     softmax, rescaling and output of tile 0 and 1 (warp w: TMEM lanes 32 (w % 4) ..)
-//   warp 8             MMAs: for each step, of each tile the P V of the step before and the next Q K^T
-//   warp 9, warp 10    loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
+//   warp 8, warp 9     MMAs of tile 0 and 1: for each step the P V of the step before and the next Q K^T
+//   warp 10, warp 11   loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
 //                      swizzle atoms: a box is 64 dims of the keys that a page and a step share (gcd(page size, 128)), one
 //                      lane a box. Other page sizes by 16-byte cp.async, a lane looking a key's place up for the lanes that
 //                      copy it.
-// The MMAs of one thread run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
+// The MMAs of a tile come from one thread and run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
 // take the place of S(j). O is rescaled only where a row's maximum grew by more than 2^8; until then P and its sum are
 // under the old maximum, up to 256, which neither 16-bit type minds.
 // Scores of keys that a row does not see are -infinity; v of keys outside the tile's range is zeroed in shared memory, for 0
@@ -24,8 +24,8 @@ namespace fp4moe {
 namespace {
 
 constexpr int AT_BM = 256, AT_KEYS = 128;
-constexpr int AT_OH = 2;           // what a unit costs, in steps, beside its steps
-constexpr int AT_THREADS = 352;    // 168 registers a thread: a row of S stays in them
+constexpr int AT_OH = 4;           // what a unit costs, in steps, beside its steps
+constexpr int AT_THREADS = 384;    // 168 registers a thread: a row of S stays in them
 constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
 
 template <int DP>
@@ -57,8 +57,8 @@ struct TileBars {
   __device__ __forceinline__ uint32_t p_full(int t) const { return base + 8 * (4 * C::kStages + 4 + t); }
   __device__ __forceinline__ uint32_t o_full(int t) const { return base + 8 * (4 * C::kStages + 6 + t); }
   __device__ __forceinline__ uint32_t join(int t) const { return base + 8 * (4 * C::kStages + 8 + t); }
-  __device__ __forceinline__ uint32_t done() const { return base + 8 * (4 * C::kStages + 10); }
-  __device__ __forceinline__ uint32_t landed() const { return base + 8 * (4 * C::kStages + 11); }
+  __device__ __forceinline__ uint32_t done(int t) const { return base + 8 * (4 * C::kStages + 10 + t); }
+  __device__ __forceinline__ uint32_t landed() const { return base + 8 * (4 * C::kStages + 12); }
 };
 
 // Tensor maps: k and v as [pages][tokens][heads][dims], boxes of `rows` tokens x 64 dims; q as [T][heads][dims], boxes of
@@ -90,6 +90,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
+  return ok != 0;
+}
+// One lane of a converged warp, which the compiler knows to be one: descriptors stay in uniform registers, where the MMA
+// wants them (a lane picked by its index costs several register moves an MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
   return ok != 0;
 }
 // The whole warp waits, and goes on together.
@@ -347,7 +354,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
   if (!ok && WHICH == 0 && maps.q_box) drain_wait(bar.q_full(), units & 1);
 }
 
-// ---------------------------------------------------------------- MMAs (one thread)
+// ---------------------------------------------------------------- MMAs (one warp)
 template <typename T, int DP>
 __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint32_t sm32,
                                          uint32_t tmem) {
@@ -355,67 +362,67 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
   const int dims = (p.D + 15) / 16 * 16;
   const uint32_t is = idesc_16<T>(AT_KEYS, false), io = idesc_16<T>(dims, true);
   int ks = 0, vs = 0, units = 0;
-  uint32_t kp = 0, vp = 0, pp = 0;  // phases of the k and v stages, and of the p barriers (bit t)
+  uint32_t kp = 0, vp = 0, pp[2] = {0, 0};  // phases of the k and v stages, and of the p barriers
   // descriptors count in 16 bytes, so offsets are added to them
   const uint64_t qd = desc_sw128(sm32), kd = desc_sw128(sm32 + C::kK), vd = desc_sw128_t(sm32 + C::kV, C::kBlock);
-  auto qk = [&](int t) {
-    const uint64_t a = qd + (uint32_t)(t * (C::kTile >> 4)), b = kd + (uint32_t)(ks * (C::kTile >> 4));
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i) {
-      if (i * 16 < dims) {
-        constexpr uint32_t block = C::kBlock >> 4;
-        const uint32_t at = (i >> 2) * block + (i & 3) * 2;
-        mma_ss(tmem + t * 128, a + at, b + at, is, i > 0);
-      }
-    }
-    tc_commit(bar.s_full(t));
-  };
-  auto pv = [&](int t, bool first) {
-    const uint64_t b = vd + (uint32_t)(vs * (C::kTile >> 4));
-#pragma unroll
-    for (int i = 0; i < AT_KEYS / 16; ++i) mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, b + i * 128, io, !(first && i == 0));
-  };
   AttnWalk walk(run);
   bool ok = true;
   for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS, AT_OH>(p, run, u); ++units) {
-    const int tiles = u.rows > 128 ? 2 : 1, n = u.s1 - u.s0;
-    if (!(ok = mbar_wait(bar.q_full(), units & 1, p.err))) break;
+    const bool two = u.rows > 128;
+    const int n = u.s1 - u.s0;
+    if (!(ok = warp_wait(bar.q_full(), units & 1, p.err))) break;
     for (int j = 0; j <= n; ++j) {
-      if (j < n && !(ok = mbar_wait(bar.k_full(ks), kp, p.err))) break;
-      if (j > 0 && !(ok = mbar_wait(bar.v_full(vs), vp, p.err))) break;
-      for (int t = 0; t < tiles; ++t) {
+      if (j < n && !(ok = warp_wait(bar.k_full(ks), kp, p.err))) break;
+      if (j > 0 && !(ok = warp_wait(bar.v_full(vs), vp, p.err))) break;
+      const uint64_t kb = kd + (uint32_t)(ks * (C::kTile >> 4)), vb = vd + (uint32_t)(vs * (C::kTile >> 4));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && !two) break;
+        const uint32_t st = tmem + t * 128, ot = tmem + 256 + t * DP;
         if (j > 0) {
-          if (!(ok = mbar_wait(bar.p_full(t), (pp >> t) & 1, p.err))) break;
-          pp ^= 1u << t;
-          tc_fence_after();
-          pv(t, j == 1);
-          if (j == n) tc_commit(bar.o_full(t));
+          if (!(ok = warp_wait(bar.p_full(t), pp[t], p.err))) break;
+          pp[t] ^= 1;
         }
-        if (j < n) {
-          tc_fence_after();
-          qk(t);
+        tc_fence_after();
+        if (elect_one()) {
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < AT_KEYS / 16; ++i) mma_ts(ot, st + i * 8, vb + i * 128, io, j > 1 || i > 0);
+            if (j == n) tc_commit(bar.o_full(t));
+          }
+          if (j < n) {
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+              constexpr uint32_t block = C::kBlock >> 4;
+              const uint32_t at = (i >> 2) * block + (i & 3) * 2;
+              if (i * 16 < dims) mma_ss(st, qd + t * (C::kTile >> 4) + at, kb + at, is, i > 0);
+            }
+            tc_commit(bar.s_full(t));
+          }
         }
+        __syncwarp();
       }
       if (!ok) break;
-      if (j > 0) {
-        tc_commit(bar.v_empty(vs));
-        if (++vs == C::kStages) {
-          vs = 0;
-          vp ^= 1;
-        }
+      if (elect_one()) {
+        if (j > 0) tc_commit(bar.v_empty(vs));
+        if (j < n) tc_commit(bar.k_empty(ks));
+        if (j == n - 1) tc_commit(bar.q_empty());
       }
-      if (j < n) {
-        tc_commit(bar.k_empty(ks));
-        if (++ks == C::kStages) {
-          ks = 0;
-          kp ^= 1;
-        }
+      __syncwarp();
+      if (j > 0 && ++vs == C::kStages) {
+        vs = 0;
+        vp ^= 1;
       }
-      if (j == n - 1) tc_commit(bar.q_empty());
+      if (j < n && ++ks == C::kStages) {
+        ks = 0;
+        kp ^= 1;
+      }
     }
   }
-  tc_commit(bar.done());  // nothing may be in flight when the CTA gives its memory back
-  drain_wait(bar.done(), 0);
+  // nothing may be in flight when the CTA gives its memory back
+  if (elect_one()) tc_commit(bar.done(0));
+  drain_wait(bar.done(0), 0);
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- softmax, output
@@ -660,8 +667,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
       mbar_init(bar.p_full(t), 128);
       mbar_init(bar.o_full(t), 1);
       mbar_init(bar.join(t), 128);
+      mbar_init(bar.done(t), 1);
     }
-    mbar_init(bar.done(), 1);
     mbar_init(bar.landed(), 1);
     fence_mbar_init();
     odd[0] = odd[1] = odd[2] = 0;
@@ -683,9 +690,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   if (warp < 8) {
     softmax_role<T, DP>(p, run, bar, tmem, odd, arrived, sm + C::kOut + warp * 2048);
   } else if (warp == 8) {
-    if (lane_id() == 0) mma_role<T, DP>(p, run, bar, sm32, tmem);
-    __syncwarp();
+    mma_role<T, DP>(p, run, bar, sm32, tmem);
   } else if (warp == 9) {
+  } else if (warp == 10) {
     load_role<T, DP, BOXES, 0>(p, maps, run, bar, sm, sm32, odd);
   } else {
     load_role<T, DP, BOXES, 1>(p, maps, run, bar, sm, sm32, odd);
