@@ -12,8 +12,8 @@
 //                      lane a box. Other page sizes by 16-byte cp.async, a lane looking a key's place up for the lanes that
 //                      copy it.
 // The MMAs of a tile come from one thread and run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
-// take the place of S(j). O is rescaled only where a row's maximum grew by more than 2^8; until then P and its sum are
-// under the old maximum, up to 256, which neither 16-bit type minds.
+// take the place of S(j). P is made under the maximum of the steps before, so that finding this step's is not in its way;
+// only where that had grown by more than 2^8 is O rescaled and P made again (up to 256, which neither 16-bit type minds).
 // Scores of keys that a row does not see are -infinity; v of keys outside the tile's range is zeroed in shared memory, for 0
 // times what lies there may be NaN. Where a v that only some rows see is not finite, the unit's rows are made again one by
 // one.
@@ -135,6 +135,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
+}
+// The loads of v, and whatever was loaded before, have arrived: nothing may use v earlier.
+__device__ __forceinline__ void tmem_arrived(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]) : : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two of each in one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float f, float c) {  // (x, y) = (a, b) f + c
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmov.b64 w, {%5, %5};\n\t"
+      "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {  // (x, y) += (a, b)
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
 }
 // 8 columns in and out, times f: few registers beside a row of S.
 __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
@@ -478,50 +507,87 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       if (!(ok = warp_wait(bar.s_full(t), sp, p.err))) break;
       sp ^= 1;
       tc_fence_after();
-      float s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(st + i * 32, s[i]);
-      tmem_ld_wait();
-      if (k0 < all_lo || k0 + AT_KEYS > all_hi) {
-        const int a = see.x - k0, b = see.y - k0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+      const bool edge = k0 < all_lo || k0 + AT_KEYS > all_hi;
+      const int vis0 = see.x - k0, vis1 = see.y - k0;  // columns that the row sees
+      float a[32], b[32];
+      uint32_t w[2][32];
+      float top, sum[4];
+      // 32 columns: their maximum, and their weights under m
+      auto mask = [&](float (&s)[32], int at) {
+        if (edge) {
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (i * 32 + c < a || i * 32 + c >= b) s[i][c] = -INFINITY;
-      }
-      float nm[4];
+            if (at + c < vis0 || at + c >= vis1) s[c] = -INFINITY;
+        }
+      };
+      auto greatest = [&](const float (&s)[32]) {
+        float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        nm[i] = s[i][0];
+        for (int c = 4; c < 28; c += 8)
 #pragma unroll
-        for (int c = 1; c < 32; ++c) nm[i] = fmaxf(nm[i], s[i][c]);
-      }
-      const float top = fmaxf(m, fmaxf(fmaxf(nm[0], nm[1]), fmaxf(nm[2], nm[3])));
-      if (j == u.s0) {
+          for (int i = 0; i < 4; ++i) x[i] = max3(x[i], s[c + 2 * i], s[c + 2 * i + 1]);
+        top = max3(top, max3(x[0], x[1], s[28]), max3(x[2], x[3], s[29]));
+        top = max3(top, s[30], s[31]);
+      };
+      auto weights = [&](const float (&s)[32], uint32_t* to, float mb) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float u, v;
+          fma2(u, v, s[2 * c], s[2 * c + 1], p.scale_log2, -mb);
+          u = exp2_fast(u);
+          v = exp2_fast(v);
+          add2(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], u, v);
+          to[c] = pack2<T>(u, v);  // half a step of the cache's type, against a result of that type
+        }
+      };
+      if (j == u.s0) {  // no maximum yet
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tmem_ld32(st + i * 32, a);
+          tmem_arrived(a);
+          mask(a, i * 32);
+          greatest(a);
+        }
         m = top;
-      } else if (__any_sync(0xFFFFFFFFu, (top - safe_max(m)) * p.scale_log2 > AT_GROWTH || (m == -INFINITY && top > m))) {
+      }
+      // The weights under the maximum so far, and the step's maximum beside them; again if it had grown too much.
+      for (;;) {
+        const float mb = safe_max(m) * p.scale_log2;
+        top = m;
+        sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
+        tmem_ld32(st, a);
+        tmem_arrived(a);
+        tmem_ld32(st + 32, b);
+        mask(a, 0);
+        greatest(a);
+        weights(a, w[0], mb);
+        tmem_arrived(b);
+        tmem_ld32(st + 64, a);
+        mask(b, 32);
+        greatest(b);
+        weights(b, w[0] + 16, mb);
+        tmem_arrived(a);
+        tmem_ld32(st + 96, b);
+        mask(a, 64);
+        greatest(a);
+        weights(a, w[1], mb);
+        tmem_arrived(b);
+        mask(b, 96);
+        greatest(b);
+        weights(b, w[1] + 16, mb);
+        if (!__any_sync(0xFFFFFFFFu, (top - safe_max(m)) * p.scale_log2 > AT_GROWTH || (m == -INFINITY && top > m))) break;
         const float f = exp2_fast((m - safe_max(top)) * p.scale_log2);
         m = top;
         l *= f;
+        if (j > u.s0) {
 #pragma unroll 1
-        for (int d = 0; d < dims; d += 8) tmem_scale8(ot + d, f);
-      }
-      const float mb = safe_max(m) * p.scale_log2;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int i = 2 * h + (c >> 4), e = 2 * (c & 15);
-          const float a = exp2_fast(fmaf(s[i][e], p.scale_log2, -mb)), b = exp2_fast(fmaf(s[i][e + 1], p.scale_log2, -mb));
-          sum[c & 3] += a + b;
-          w[c] = pack2<T>(a, b);  // half a step of the cache's type, against a result of that type
+          for (int d = 0; d < dims; d += 8) tmem_scale8(ot + d, f);
         }
-        tmem_st32(st + h * 32, w);
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32(st, w[0]);
+      tmem_st32(st + 32, w[1]);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar.p_full(t));
