@@ -290,11 +290,20 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
     if (WHICH && (late.rows || late.mark)) {
       bool bad = false;
       uint8_t* tile = sm + C::kV + late.stage * C::kTile;
-      for (int i = lane; i < 128 * C::kBlocks * 8; i += 32) {  // 16 bytes each, rows in turn
-        const int row = i / (C::kBlocks * 8), c = i % (C::kBlocks * 8);
-        uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-        if (late.k0 + row < late.lo || late.k0 + row >= late.hi) *at = make_uint4(0u, 0u, 0u, 0u);
-        else if (late.mark) bad |= any_nonfinite<T>(*at);
+      constexpr int PER = C::kBlocks * 8;  // 16-byte pieces of a row
+      auto piece = [&](int i) {
+        const int row = i / PER, c = i % PER;
+        return reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+      };
+      if (late.rows) {
+        const int lo = max(late.lo - late.k0, 0) * PER, hi = min(max(late.hi - late.k0, 0), 128) * PER;
+        for (int i = lane; i < lo; i += 32) *piece(i) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = hi + lane; i < 128 * PER; i += 32) *piece(i) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
+      if (late.mark) {
+#pragma unroll 8
+        for (int i = 0; i < 128 * PER / 32; ++i) bad |= any_nonfinite<T>(*piece(i * 32 + lane));
       }
       if (bad) odd[(late.mark - 1) % 3] = late.mark;
     }
@@ -483,6 +492,94 @@ __device__ __noinline__ void row_again(const AttnParams& p, const AttnUnit& u, i
   }
 }
 
+// Of 32 scores of a row.
+template <bool EDGE>
+__device__ __forceinline__ void hide(float (&s)[32], int from, int to) {  // all but columns [from, to)
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c < from || c >= to) s[c] = -INFINITY;
+  }
+}
+__device__ __forceinline__ float greatest(const float (&s)[32], float top) {
+  float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int c = 4; c < 28; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = max3(x[i], s[c + 2 * i], s[c + 2 * i + 1]);
+  return max3(max3(top, max3(x[0], x[1], s[28]), max3(x[2], x[3], s[29])), s[30], s[31]);
+}
+template <typename T>
+__device__ __forceinline__ void weights(const float (&s)[32], uint32_t* w, float (&sum)[4], float scale, float mb) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    float u, v;
+    fma2(u, v, s[2 * c], s[2 * c + 1], scale, -mb);
+    u = exp2_fast(u);
+    v = exp2_fast(v);
+    add2(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], u, v);
+    w[c] = pack2<T>(u, v);  // half a step of the cache's type, against a result of that type
+  }
+}
+// One step of a row: S (128 columns, of which the row sees [from, to)) into P, m and l brought up to date, O rescaled.
+template <typename T, bool EDGE>
+__device__ __forceinline__ void softmax_step(uint32_t st, uint32_t ot, int dims, bool first, int from, int to, float scale, float& m,
+                                             float& l) {
+  float a[2][32], b[2][32];
+  uint32_t w[2][32];
+  float top, sum[4];
+  if (first) {  // no maximum yet
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tmem_ld32(st + i * 32, a[0]);
+      tmem_arrived(a[0]);
+      hide<EDGE>(a[0], from - i * 32, to - i * 32);
+      top = greatest(a[0], top);
+    }
+    m = top;
+  }
+  // The weights under the maximum so far, and the step's maximum beside them; again if it had grown too much.
+  for (;;) {
+    const float mb = safe_max(m) * scale;
+    top = m;
+    sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
+    tmem_ld32(st, a[0]);
+    tmem_ld32(st + 32, a[1]);
+    tmem_arrived(a[0]);
+    tmem_arrived(a[1]);
+    tmem_ld32(st + 64, b[0]);
+    tmem_ld32(st + 96, b[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hide<EDGE>(a[i], from - i * 32, to - i * 32);
+      top = greatest(a[i], top);
+      weights<T>(a[i], w[0] + 16 * i, sum, scale, mb);
+    }
+    tmem_arrived(b[0]);
+    tmem_arrived(b[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hide<EDGE>(b[i], from - 64 - i * 32, to - 64 - i * 32);
+      top = greatest(b[i], top);
+      weights<T>(b[i], w[1] + 16 * i, sum, scale, mb);
+    }
+    if (!__any_sync(0xFFFFFFFFu, (top - safe_max(m)) * scale > AT_GROWTH || (m == -INFINITY && top > m))) break;
+    const float f = exp2_fast((m - safe_max(top)) * scale);
+    m = top;
+    l *= f;
+    if (!first) {
+#pragma unroll 1
+      for (int d = 0; d < dims; d += 8) tmem_scale8(ot + d, f);
+    }
+  }
+  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  tmem_st32(st, w[0]);
+  tmem_st32(st + 32, w[1]);
+  tmem_st_wait();
+  tc_fence_before();
+}
+
 template <typename T, int DP>
 __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun& run, const TileBars<DP>& bar, uint32_t tmem,
                                              volatile int* odd, volatile uint32_t* arrived, uint8_t* stage) {
@@ -502,94 +599,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + last)).x;
     const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + t * 128)).y;
     float m = -INFINITY, l = 0.0f;
-    for (int j = u.s0; j < u.s1; ++j) {
-      const int k0 = (u.range.x / AT_KEYS + j) * AT_KEYS;
+    const int k00 = (u.range.x / AT_KEYS + u.s0) * AT_KEYS, n = u.s1 - u.s0;
+    // steps [in0, in1) are all visible to all rows
+    const int in0 = all_lo > k00 ? (all_lo - k00 + AT_KEYS - 1) / AT_KEYS : 0, in1 = all_hi > k00 ? (all_hi - k00) / AT_KEYS : 0;
+    for (int j = 0; j < n; ++j) {
       if (!(ok = warp_wait(bar.s_full(t), sp, p.err))) break;
       sp ^= 1;
       tc_fence_after();
-      const bool edge = k0 < all_lo || k0 + AT_KEYS > all_hi;
-      const int vis0 = see.x - k0, vis1 = see.y - k0;  // columns that the row sees
-      float a[32], b[32];
-      uint32_t w[2][32];
-      float top, sum[4];
-      // 32 columns: their maximum, and their weights under m
-      auto mask = [&](float (&s)[32], int at) {
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (at + c < vis0 || at + c >= vis1) s[c] = -INFINITY;
-        }
-      };
-      auto greatest = [&](const float (&s)[32]) {
-        float x[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < 28; c += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = max3(x[i], s[c + 2 * i], s[c + 2 * i + 1]);
-        top = max3(top, max3(x[0], x[1], s[28]), max3(x[2], x[3], s[29]));
-        top = max3(top, s[30], s[31]);
-      };
-      auto weights = [&](const float (&s)[32], uint32_t* to, float mb) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float u, v;
-          fma2(u, v, s[2 * c], s[2 * c + 1], p.scale_log2, -mb);
-          u = exp2_fast(u);
-          v = exp2_fast(v);
-          add2(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], u, v);
-          to[c] = pack2<T>(u, v);  // half a step of the cache's type, against a result of that type
-        }
-      };
-      if (j == u.s0) {  // no maximum yet
-        top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tmem_ld32(st + i * 32, a);
-          tmem_arrived(a);
-          mask(a, i * 32);
-          greatest(a);
-        }
-        m = top;
-      }
-      // The weights under the maximum so far, and the step's maximum beside them; again if it had grown too much.
-      for (;;) {
-        const float mb = safe_max(m) * p.scale_log2;
-        top = m;
-        sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
-        tmem_ld32(st, a);
-        tmem_arrived(a);
-        tmem_ld32(st + 32, b);
-        mask(a, 0);
-        greatest(a);
-        weights(a, w[0], mb);
-        tmem_arrived(b);
-        tmem_ld32(st + 64, a);
-        mask(b, 32);
-        greatest(b);
-        weights(b, w[0] + 16, mb);
-        tmem_arrived(a);
-        tmem_ld32(st + 96, b);
-        mask(a, 64);
-        greatest(a);
-        weights(a, w[1], mb);
-        tmem_arrived(b);
-        mask(b, 96);
-        greatest(b);
-        weights(b, w[1] + 16, mb);
-        if (!__any_sync(0xFFFFFFFFu, (top - safe_max(m)) * p.scale_log2 > AT_GROWTH || (m == -INFINITY && top > m))) break;
-        const float f = exp2_fast((m - safe_max(top)) * p.scale_log2);
-        m = top;
-        l *= f;
-        if (j > u.s0) {
-#pragma unroll 1
-          for (int d = 0; d < dims; d += 8) tmem_scale8(ot + d, f);
-        }
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32(st, w[0]);
-      tmem_st32(st + 32, w[1]);
-      tmem_st_wait();
-      tc_fence_before();
+      if (j >= in0 && j < in1)
+        softmax_step<T, false>(st, ot, dims, j == 0, 0, 0, p.scale_log2, m, l);
+      else
+        softmax_step<T, true>(st, ot, dims, j == 0, see.x - k00 - j * AT_KEYS, see.y - k00 - j * AT_KEYS, p.scale_log2, m, l);
       mbar_arrive(bar.p_full(t));
     }
     if (!ok || !(ok = warp_wait(bar.o_full(t), op, p.err))) break;
