@@ -218,13 +218,20 @@ struct AttnUnit {
 struct AttnWalk {
   int64_t x;
   int b, tile, head, at;
+  int read = -1, kv = 0;  // the sequence that `seq` is
+  AttnSeq seq{};
   __device__ __forceinline__ explicit AttnWalk(const AttnRun& r)
       : x(r.begin), b(r.seq), tile(r.tile), head(r.head), at(r.at) {}
   template <int BM, int S, int OH>
   __device__ __forceinline__ bool next(const AttnParams& p, const AttnRun& r, AttnUnit& u) {
     while (x < r.end) {
-      u.kv = __ldg(p.kv_len + b);
-      u.seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), u.kv);
+      if (read != b) {
+        kv = __ldg(p.kv_len + b);
+        seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), kv);
+        read = b;
+      }
+      u.kv = kv;
+      u.seq = seq;
       if (tile * BM >= u.seq.rows) {
         ++b;
         tile = head = at = 0;

@@ -36,8 +36,8 @@ struct TileCfg {
   static constexpr int kStages = DP == 128 ? 2 : 4;   // of k, and of v
   static constexpr int kK = 2 * kTile, kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  static constexpr int kOut = kBars + 512;            // the softmax warps' output, 32 rows x 32 dims each
-  static constexpr int kSmem = kOut + 8 * 2048 + 1024;  // and to align it
+  static constexpr int kOut = kBars + 512;            // the softmax warps' output, 32 rows x 64 dims each
+  static constexpr int kSmem = kOut + 8 * 4096 + 1024;  // and to align it
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert((FP4MOE_KV_MAX_SEQS + AT_THREADS / 32 + 1) * 8 <= kBars, "the division's sums fit");
 };
@@ -345,21 +345,20 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
     const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0)).y;
     for (int i = 0; i < n; ++i) {
       const int k0 = first + i * AT_KEYS;
-      // what is late may be what frees the stage
-      if (late.any && !mbar_test(empty(stage), phase ^ 1) && !(ok = look_after(false))) break;
-      if (!(ok = warp_wait(empty(stage), phase ^ 1, p.err))) break;
       const bool edge = k0 < u.range.x || k0 + AT_KEYS > u.range.y, some = k0 < all_lo || k0 + AT_KEYS > all_hi;
       const bool differ = some && (all_lo != u.range.x || all_hi != u.range.y);
       const bool look = !BOXES || (WHICH && (edge || differ));
-      const uint32_t tile = sm32 + tiles + stage * C::kTile;
+      const uint32_t tile = sm32 + tiles + stage * C::kTile, b = BOXES && look ? bar.landed() : full(stage);
+      const int box_tok = BOXES ? L.in_page(k0 + box_key) : 0, box_page = BOXES ? L.checked(page[0]) : 0;
+      if (BOXES && look && !(ok = look_after(false))) break;  // one at a time
+      // what is late may be what frees the stage
+      if (late.any && !mbar_test(empty(stage), phase ^ 1) && !(ok = look_after(false))) break;
+      if (!(ok = warp_wait(empty(stage), phase ^ 1, p.err))) break;
       if (BOXES) {
-        if (look && !(ok = look_after(false))) break;  // one at a time
-        const uint32_t b = look ? bar.landed() : full(stage);
         if (lane == 0) mbar_arrive_expect_tx(b, (p.D > 64 ? 2 : 1) * C::kBlock);
         __syncwarp();
         if (lane < boxes)
-          tma_load_4d(tile + box_col * C::kBlock + box_key * 128, map, b, box_col * 64, u.head, L.in_page(k0 + box_key),
-                      L.checked(page[0]));
+          tma_load_4d(tile + box_col * C::kBlock + box_key * 128, map, b, box_col * 64, u.head, box_tok, box_page);
       } else {
         L.key_rows(u, tile, base, k0, page);
       }
@@ -403,26 +402,29 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
   uint32_t kp = 0, vp = 0, pp[2] = {0, 0};  // phases of the k and v stages, and of the p barriers
   // descriptors count in 16 bytes, so offsets are added to them
   const uint64_t qd = desc_sw128(sm32), kd = desc_sw128(sm32 + C::kK), vd = desc_sw128_t(sm32 + C::kV, C::kBlock);
-  AttnWalk walk(run);
+  // A wait that gave up is only looked at once a step: what is issued until then reads and writes this CTA's own memory.
   bool ok = true;
+  auto wait = [&](uint32_t b, uint32_t parity) { ok &= mbar_wait(b, parity, p.err); };
+  const bool leader = elect_one();
+  AttnWalk walk(run);
   for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS, AT_OH>(p, run, u); ++units) {
     const bool two = u.rows > 128;
     const int n = u.s1 - u.s0;
-    if (!(ok = warp_wait(bar.q_full(), units & 1, p.err))) break;
+    wait(bar.q_full(), units & 1);
     for (int j = 0; j <= n; ++j) {
-      if (j < n && !(ok = warp_wait(bar.k_full(ks), kp, p.err))) break;
-      if (j > 0 && !(ok = warp_wait(bar.v_full(vs), vp, p.err))) break;
+      if (j < n) wait(bar.k_full(ks), kp);
+      if (j > 0) wait(bar.v_full(vs), vp);
       const uint64_t kb = kd + (uint32_t)(ks * (C::kTile >> 4)), vb = vd + (uint32_t)(vs * (C::kTile >> 4));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (t == 1 && !two) break;
         const uint32_t st = tmem + t * 128, ot = tmem + 256 + t * DP;
         if (j > 0) {
-          if (!(ok = warp_wait(bar.p_full(t), pp[t], p.err))) break;
+          wait(bar.p_full(t), pp[t]);
           pp[t] ^= 1;
         }
         tc_fence_after();
-        if (elect_one()) {
+        if (leader) {
           if (j > 0) {
 #pragma unroll
             for (int i = 0; i < AT_KEYS / 16; ++i) mma_ts(ot, st + i * 8, vb + i * 128, io, j > 1 || i > 0);
@@ -440,13 +442,12 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
         }
         __syncwarp();
       }
-      if (!ok) break;
-      if (elect_one()) {
+      if (leader) {
         if (j > 0) tc_commit(bar.v_empty(vs));
         if (j < n) tc_commit(bar.k_empty(ks));
         if (j == n - 1) tc_commit(bar.q_empty());
       }
-      __syncwarp();
+      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
       if (j > 0 && ++vs == C::kStages) {
         vs = 0;
         vp ^= 1;
@@ -458,7 +459,7 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
     }
   }
   // nothing may be in flight when the CTA gives its memory back
-  if (elect_one()) tc_commit(bar.done(0));
+  if (leader) tc_commit(bar.done(0));
   drain_wait(bar.done(0), 0);
   __syncwarp();
 }
@@ -610,7 +611,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
         softmax_step<T, false>(st, ot, dims, j == 0, 0, 0, p.scale_log2, m, l);
       else
         softmax_step<T, true>(st, ot, dims, j == 0, see.x - k00 - j * AT_KEYS, see.y - k00 - j * AT_KEYS, p.scale_log2, m, l);
-      mbar_arrive(bar.p_full(t));
+      __syncwarp();
+      if (lane_id() == 0) mbar_arrive(bar.p_full(t));
     }
     if (!ok || !(ok = warp_wait(bar.o_full(t), op, p.err))) break;
     op ^= 1;
@@ -633,24 +635,25 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     const int hq = u.head * (int)p.group.d + g;
     const int64_t at = real ? tq * p.out_stride + (int64_t)hq * p.D : -1;
     const bool none = see.x >= see.y;  // a row without keys is 0; one whose scores are all -infinity is 0 / 0
-    // 32 dims of the warp's rows, through shared memory: four lanes write a row's 64 bytes
-    auto finish = [&](float (&o)[32], int d, float inv) {
+    // 64 dims of the warp's rows, through shared memory: eight lanes write a row's 128 bytes
+    auto finish = [&](float (&o)[2][32], int d, float inv) {
       const int lane = row & 31;
+      if (none) inv = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = none ? 0.0f : o[c * 8 + e] * inv;
-        *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = pack<T>(v);
+        for (int e = 0; e < 8; ++e) v[e] = none ? 0.0f : o[c >> 2][(c & 3) * 8 + e] * inv;
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = pack<T>(v);
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = i * 8 + (lane >> 2), c = lane & 3;
+      for (int i = 0; i < 8; ++i) {
+        const int rr = i * 4 + (lane >> 3), c = lane & 7;
         const int64_t to = __shfl_sync(0xFFFFFFFFu, at, rr);
         if (to >= 0 && d + c * 8 < p.D)
           *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to + d + c * 8) =
-              *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+              *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
       }
       __syncwarp();
     };
@@ -660,10 +663,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     if (u.s0 == 0 && u.s1 == u.n) {
       const float inv = __fdiv_rn(1.0f, l);
 #pragma unroll 1
-      for (int d = 0; d < dims; d += 32) {
-        float o[32];
-        tmem_ld32(ot + d, o);
-        tmem_ld_wait();
+      for (int d = 0; d < DP; d += 64) {
+        float o[2][32];
+        tmem_ld32(ot + d, o[0]);
+        tmem_ld32(ot + d + 32, o[1]);
+        tmem_arrived(o[0]);
+        tmem_arrived(o[1]);
         finish(o, d, inv);
       }
       finish_lse(m, l);
@@ -677,10 +682,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       const int64_t mine = slot(blockIdx.x, u.s0 == 0);
       __stcg(stats + mine * AT_BM + t * 128 + row, make_float2(m, l));
 #pragma unroll 1
-      for (int d = 0; d < dims; d += 32) {
+      for (int d = 0; d < DP; d += 32) {
         float o[32];
         tmem_ld32(ot + d, o);
-        tmem_ld_wait();
+        tmem_arrived(o);
 #pragma unroll
         for (int c = 0; c < 32; c += 4) __stcg(vec(mine, d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
       }
@@ -703,20 +708,23 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
         }
         const float inv = __fdiv_rn(1.0f, sum);
 #pragma unroll 1
-        for (int d = 0; d < dims; d += 32) {
-          float o[32];
+        for (int d = 0; d < DP; d += 64) {
+          float o[2][32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const int64_t s = slot(c, c == c0);
-            const float f = exp2_fast((__ldcg(own + s * AT_BM).x - safe_max(M)) * p.scale_log2);
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 v = __ldcg(vec(s, d + e));
-              o[e] = fmaf(v.x, f, o[e]);
-              o[e + 1] = fmaf(v.y, f, o[e + 1]);
-              o[e + 2] = fmaf(v.z, f, o[e + 2]);
-              o[e + 3] = fmaf(v.w, f, o[e + 3]);
+            for (int c = 0; c < 32; ++c) o[h][c] = 0.0f;
+            for (int c = c0; c <= c1; ++c) {
+              const int64_t s = slot(c, c == c0);
+              const float f = exp2_fast((__ldcg(own + s * AT_BM).x - safe_max(M)) * p.scale_log2);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 v = __ldcg(vec(s, d + 32 * h + e));
+                o[h][e] = fmaf(v.x, f, o[h][e]);
+                o[h][e + 1] = fmaf(v.y, f, o[h][e + 1]);
+                o[h][e + 2] = fmaf(v.z, f, o[h][e + 2]);
+                o[h][e + 3] = fmaf(v.w, f, o[h][e + 3]);
+              }
             }
           }
           finish(o, d, inv);
@@ -750,7 +758,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
     mbar_init(bar.q_empty(), 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar.s_full(t), 1);
-      mbar_init(bar.p_full(t), 128);
+      mbar_init(bar.p_full(t), 4);
       mbar_init(bar.o_full(t), 1);
       mbar_init(bar.join(t), 128);
       mbar_init(bar.done(t), 1);
@@ -774,7 +782,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   if (skip) run.end = run.begin;  // an earlier call gave up
   const uint32_t tmem = tmem_at;
   if (warp < 8) {
-    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived, sm + C::kOut + warp * 2048);
+    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived, sm + C::kOut + warp * 4096);
   } else if (warp == 8) {
     mma_role<T, DP>(p, run, bar, sm32, tmem);
   } else if (warp == 9) {
