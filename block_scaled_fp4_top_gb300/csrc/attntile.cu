@@ -36,8 +36,8 @@ struct TileCfg {
   static constexpr int kStages = DP == 128 ? 2 : 4;   // of k, and of v
   static constexpr int kK = 2 * kTile, kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  static constexpr int kOut = kBars + 512;            // the softmax warps' output, 32 rows x 64 dims each
-  static constexpr int kSmem = kOut + 8 * 4096 + 1024;  // and to align it
+  static constexpr int kOut = kBars + 512;            // the softmax warps' output, 32 rows x 32 dims each
+  static constexpr int kSmem = kOut + 8 * 2048 + 1024;  // and to align it
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert((FP4MOE_KV_MAX_SEQS + AT_THREADS / 32 + 1) * 8 <= kBars, "the division's sums fit");
 };
@@ -271,8 +271,8 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
   bool ok = true;
   // The load that is looked after once it has landed: a step of v that is not all visible to all rows, or one by cp.async.
   struct {
-    bool any, rows;  // rows: zero those outside [lo, hi); mark: unit + 1 if those inside are looked through
-    int stage, k0, lo, hi, mark;
+    bool any, rows;  // rows: zero those outside [lo, hi); mark: unit + 1 if those that not all rows see are looked through
+    int stage, k0, lo, hi, all_lo, all_hi, mark;
     int64_t n;
   } late{};
   uint32_t landed = 0;
@@ -302,8 +302,18 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
         __syncwarp();
       }
       if (late.mark) {
-#pragma unroll 8
-        for (int i = 0; i < 128 * PER / 32; ++i) bad |= any_nonfinite<T>(*piece(i * 32 + lane));
+        auto look = [&](int from, int to) {
+          from = max(from - late.k0, 0) * PER;
+          to = min(to - late.k0, 128) * PER;
+#pragma unroll 4
+          for (int i = from + lane; i < to; i += 32) bad |= any_nonfinite<T>(*piece(i));
+        };
+        if (late.all_lo < late.all_hi) {
+          look(late.lo, late.all_lo);
+          look(late.all_hi, late.hi);
+        } else {
+          look(late.lo, late.hi);
+        }
       }
       if (bad) odd[(late.mark - 1) % 3] = late.mark;
     }
@@ -371,6 +381,8 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
         late.k0 = k0;
         late.lo = u.range.x;
         late.hi = u.range.y;
+        late.all_lo = all_lo;
+        late.all_hi = all_hi;
         late.mark = differ ? units + 1 : 0;
         late.n = issued;
       }
@@ -634,26 +646,25 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     const int64_t tq = u.seq.first + tok;
     const int hq = u.head * (int)p.group.d + g;
     const int64_t at = real ? tq * p.out_stride + (int64_t)hq * p.D : -1;
-    const bool none = see.x >= see.y;  // a row without keys is 0; one whose scores are all -infinity is 0 / 0
-    // 64 dims of the warp's rows, through shared memory: eight lanes write a row's 128 bytes
-    auto finish = [&](float (&o)[2][32], int d, float inv) {
+    const bool none = see.x >= see.y;  // a row without keys is 0 (its sums are); one whose scores are all -infinity is 0 / 0
+    // 32 dims of the warp's rows, through shared memory: four lanes write a row's 64 bytes
+    auto finish = [&](float (&o)[32], int d, float inv) {
       const int lane = row & 31;
-      if (none) inv = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = none ? 0.0f : o[c >> 2][(c & 3) * 8 + e] * inv;
-        *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = pack<T>(v);
+        for (int e = 0; e < 8; ++e) v[e] = o[c * 8 + e] * inv;
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = pack<T>(v);
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = i * 4 + (lane >> 3), c = lane & 7;
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2), c = lane & 3;
         const int64_t to = __shfl_sync(0xFFFFFFFFu, at, rr);
         if (to >= 0 && d + c * 8 < p.D)
           *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to + d + c * 8) =
-              *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+              *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
       }
       __syncwarp();
     };
@@ -661,14 +672,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       if (real && p.lse != nullptr) p.lse[tq * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(sum));
     };
     if (u.s0 == 0 && u.s1 == u.n) {
-      const float inv = __fdiv_rn(1.0f, l);
+      const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll 1
-      for (int d = 0; d < DP; d += 64) {
-        float o[2][32];
-        tmem_ld32(ot + d, o[0]);
-        tmem_ld32(ot + d + 32, o[1]);
-        tmem_arrived(o[0]);
-        tmem_arrived(o[1]);
+      for (int d = 0; d < dims; d += 32) {
+        float o[32];
+        tmem_ld32(ot + d, o);
+        tmem_arrived(o);
         finish(o, d, inv);
       }
       finish_lse(m, l);
@@ -682,7 +691,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       const int64_t mine = slot(blockIdx.x, u.s0 == 0);
       __stcg(stats + mine * AT_BM + t * 128 + row, make_float2(m, l));
 #pragma unroll 1
-      for (int d = 0; d < DP; d += 32) {
+      for (int d = 0; d < dims; d += 32) {
         float o[32];
         tmem_ld32(ot + d, o);
         tmem_arrived(o);
@@ -706,25 +715,24 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
           const float2 ml = __ldcg(own + slot(c, c == c0) * AT_BM);
           sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
         }
-        const float inv = __fdiv_rn(1.0f, sum);
+        const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll 1
-        for (int d = 0; d < DP; d += 64) {
-          float o[2][32];
+        for (int d = 0; d < dims; d += 32) {
+          float o[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int c = 0; c < 32; ++c) o[c] = 0.0f;
+          for (int c = c0; c <= c1; ++c) {
+            const int64_t s = slot(c, c == c0);
+            const float f = exp2_fast((__ldcg(own + s * AT_BM).x - safe_max(M)) * p.scale_log2);
+            float4 v[8];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[h][c] = 0.0f;
-            for (int c = c0; c <= c1; ++c) {
-              const int64_t s = slot(c, c == c0);
-              const float f = exp2_fast((__ldcg(own + s * AT_BM).x - safe_max(M)) * p.scale_log2);
+            for (int e = 0; e < 8; ++e) v[e] = __ldcg(vec(s, d + 4 * e));
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 v = __ldcg(vec(s, d + 32 * h + e));
-                o[h][e] = fmaf(v.x, f, o[h][e]);
-                o[h][e + 1] = fmaf(v.y, f, o[h][e + 1]);
-                o[h][e + 2] = fmaf(v.z, f, o[h][e + 2]);
-                o[h][e + 3] = fmaf(v.w, f, o[h][e + 3]);
-              }
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = fmaf(v[e].x, f, o[4 * e]);
+              o[4 * e + 1] = fmaf(v[e].y, f, o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(v[e].z, f, o[4 * e + 2]);
+              o[4 * e + 3] = fmaf(v[e].w, f, o[4 * e + 3]);
             }
           }
           finish(o, d, inv);
@@ -782,7 +790,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   if (skip) run.end = run.begin;  // an earlier call gave up
   const uint32_t tmem = tmem_at;
   if (warp < 8) {
-    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived, sm + C::kOut + warp * 4096);
+    softmax_role<T, DP>(p, run, bar, tmem, odd, arrived, sm + C::kOut + warp * 2048);
   } else if (warp == 8) {
     mma_role<T, DP>(p, run, bar, sm32, tmem);
   } else if (warp == 9) {
