@@ -465,11 +465,14 @@ def _kv_cache(k_cache, v_cache, dev):
         raise Fp4MoeError(f"v_cache: expected {tuple(shape)} of {dt}, got {tuple(v_cache.shape)} of {v_cache.dtype}")
     if k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise Fp4MoeError("k_cache, v_cache: expected CUDA tensors on the current device")
+    P, S, H, D = shape
+    if k_cache.is_contiguous() and v_cache.is_contiguous():
+        return _lib.KvCache(d, H, D, S, P, S * H * D, H * D, D), k_cache.data_ptr(), v_cache.data_ptr()
     # (the stride of a dimension of one element says nothing)
     st = [0 if n == 1 else s for n, s in zip(shape, k_cache.stride())]
     if st != [0 if n == 1 else s for n, s in zip(shape, v_cache.stride())] or st[3] != 1 or any(s % 8 for s in st[:3]):
         raise Fp4MoeError("k_cache, v_cache: expected the same strides, head dim contiguous, the others multiples of 8")
-    return _lib.KvCache(d, shape[2], shape[3], shape[1], shape[0], st[0], st[1], st[2]), k_cache.data_ptr(), v_cache.data_ptr()
+    return _lib.KvCache(d, H, D, S, P, st[0], st[1], st[2]), k_cache.data_ptr(), v_cache.data_ptr()
 
 
 def _arg_heads(name, t, T, D, dt, dev):
