@@ -15,6 +15,7 @@ namespace fp4moe {
 namespace {
 
 constexpr int AD_ROWS = 16, AD_KEYS = 16;  // of a tile, of a warp's group
+constexpr int AD_MIN = 1;                    // least cost of a CTA's run
 constexpr int AD_OH = 1;                     // what a tile costs, in slices, beside its slices
 
 template <int DP>
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const AttnRun run = attn_plan<AD_ROWS, C::S, AD_OH, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
+  const AttnRun run = attn_plan<AD_ROWS, C::S, AD_OH, AD_MIN, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
   uint8_t* ring = sm + warp * C::kRing;
   const uint32_t ring32 = smem_u32(ring);
   const T* kbase = static_cast<const T*>(p.k);
@@ -333,7 +334,9 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (r < rows) {
+#pragma unroll 8
           for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(st + (int64_t)(2 * c + (c == c0)) * AD_ROWS + r).x);
+#pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
             const int64_t at = (int64_t)(2 * c + (c == c0)) * AD_ROWS + r;
             const float2 ml = __ldcg(st + at);
@@ -432,7 +435,13 @@ fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cac
   int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
   if (nsm > kAttnMaxCtas) nsm = kAttnMaxCtas;
-  if (c.head_dim <= 128 && (int64_t)T * p.group.d > (int64_t)32 * num_seqs) return attn_tile_launch(c.dtype, p, nsm, st);
+  // Sequences of more than 16 rows a kv head, on the average, are for the larger tiles, which read k and v once for 256
+  // rows (us, 32 / 8 heads of 128 dims, 16 sequences of 8192 keys: 16 rows 93 here and 106 there, 32 rows 175 and 108),
+  // unless all of them are a few tiles of 16, which a part of the SMs works on (32 rows of one sequence 23 and 28, of four
+  // sequences of 4096 keys 32 and 27).
+  const int64_t tiles = ((int64_t)T * p.group.d + AD_ROWS - 1) / AD_ROWS * c.kv_heads;
+  if (c.head_dim <= 128 && (int64_t)T * p.group.d > (int64_t)AD_ROWS * num_seqs && tiles > 48)
+    return attn_tile_launch(c.dtype, p, nsm, st);
   return c.dtype == FP4MOE_BF16 ? attn_rows_typed<__nv_bfloat16>(p, nsm, st) : attn_rows_typed<__half>(p, nsm, st);
 }
 

@@ -83,7 +83,7 @@ __device__ __forceinline__ int attn_slices(int2 r) {
 // Where a CTA's run of costs lies, and where it starts.
 struct AttnRun {
   int64_t total, begin, end;  // of the call, and the CTA's own
-  int ctas;                   // CTAs that have a run: no more than the total, so that none of these is empty
+  int ctas;                   // CTAs that have a run, of a cost of MIN at least where there is that much
   int seq, tile, head;        // of `begin`
   int at;                     // its place in its tile and head: the first OH are before slice 0
 };
@@ -98,7 +98,7 @@ __device__ __forceinline__ int attn_owner(int64_t x, int64_t total, int ctas) {
 }
 
 // All threads of the CTA call this. sums: (B + THREADS / 32 + 2) * 8 bytes of shared memory, free again afterwards.
-template <int BM, int S, int OH, int THREADS>
+template <int BM, int S, int OH, int MIN, int THREADS>
 __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int WARPS = THREADS / 32;
@@ -163,7 +163,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
   __syncthreads();
   AttnRun r;
   r.total = total;
-  r.ctas = (int)min(total, (int64_t)gridDim.x);
+  r.ctas = (int)max((int64_t)1, min(total / MIN, (int64_t)gridDim.x));
   r.begin = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x, r.ctas) : 0;
   r.end = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x + 1, r.ctas) : 0;
   r.seq = r.tile = r.head = r.at = 0;

@@ -24,6 +24,8 @@ namespace fp4moe {
 namespace {
 
 constexpr int AT_BM = 256, AT_KEYS = 128;
+constexpr int AT_FEW = 32;         // rows of a tile whose parts are joined a few lanes a row
+constexpr int AT_MIN = 4;          // least cost of a CTA's run
 constexpr int AT_OH = 4;           // what a unit costs, in steps, beside its steps
 constexpr int AT_THREADS = 384;    // 168 registers a thread: a row of S stays in them
 constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
@@ -607,7 +609,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
   for (AttnUnit u; ok && walk.next<AT_BM, AT_KEYS, AT_OH>(p, run, u); ++units) {
     if (t * 128 >= u.rows) continue;  // (as the MMAs leave the tile out)
     const int last = min(u.rows, t * 128 + 128) - 1, r = min(t * 128 + row, last);
-    const bool real = t * 128 + row <= last;
+    const bool real = t * 128 + row <= last, idle = t * 128 + (row & 96) > last;  // idle: a warp without rows
     const int2 see = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + r));
     const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + last)).x;
     const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + t * 128)).y;
@@ -619,7 +621,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       if (!(ok = warp_wait(bar.s_full(t), sp, p.err))) break;
       sp ^= 1;
       tc_fence_after();
-      if (j >= in0 && j < in1)
+      if (idle) {  // (what P holds of rows that there are not reaches only rows of O that there are not)
+      } else if (j >= in0 && j < in1)
         softmax_step<T, false>(st, ot, dims, j == 0, 0, 0, p.scale_log2, m, l);
       else
         softmax_step<T, true>(st, ot, dims, j == 0, see.x - k00 - j * AT_KEYS, see.y - k00 - j * AT_KEYS, p.scale_log2, m, l);
@@ -629,7 +632,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     if (!ok || !(ok = warp_wait(bar.o_full(t), op, p.err))) break;
     op ^= 1;
     tc_fence_after();
-    if (odd[units % 3] == units + 1) {
+    if (!idle && odd[units % 3] == units + 1) {
       const int k0 = (u.range.x / AT_KEYS + u.s0) * AT_KEYS, k1 = (u.range.x / AT_KEYS + u.s1) * AT_KEYS;
       for (int d = 0; d < dims; d += 32) {
         float o[32];
@@ -674,7 +677,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     if (u.s0 == 0 && u.s1 == u.n) {
       const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll 1
-      for (int d = 0; d < dims; d += 32) {
+      for (int d = 0; d < dims && !idle; d += 32) {
         float o[32];
         tmem_ld32(ot + d, o);
         tmem_arrived(o);
@@ -685,18 +688,41 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       const int c0 = attn_owner(u.first, run.total, run.ctas), c1 = attn_owner(u.first + u.n - 1, run.total, run.ctas);
       float2* stats = reinterpret_cast<float2*>(p.ws + kAttnStats);
       float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
-      // the rows' vectors of four dims lie side by side
-      auto slot = [&](int c, bool begins) { return (int64_t)(2 * c + (begins ? 1 : 0)); };
-      auto vec = [&](int64_t s, int d) { return reinterpret_cast<float4*>(sums) + (s * (DP / 4) + d / 4) * AT_BM + t * 128 + row; };
-      const int64_t mine = slot(blockIdx.x, u.s0 == 0);
-      __stcg(stats + mine * AT_BM + t * 128 + row, make_float2(m, l));
+      const int lane = row & 31, rows_t = last + 1 - t * 128;
+      auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)) * AT_BM + t * 128; };  // of CTA c: this tile's rows
+      // Few rows lie one after the other, a warp's lanes across them; of many, vectors of four dims of all rows lie side by
+      // side, a lane a row.
+      const bool few = rows_t <= AT_FEW;
+      auto vec = [&](int64_t s, int d) { return reinterpret_cast<float4*>(sums + s * DP) + (d / 4) * 128 + row; };
+      const int64_t mine = slot(blockIdx.x);
+      if (!idle) {
+        __stcg(stats + mine + row, make_float2(m, l));
 #pragma unroll 1
-      for (int d = 0; d < dims; d += 32) {
-        float o[32];
-        tmem_ld32(ot + d, o);
-        tmem_arrived(o);
+        for (int d = 0; d < dims; d += 32) {  // few: through shared memory, 16 dims at a time, four lanes to a row's 64 bytes
+          float o[32];
+          tmem_ld32(ot + d, o);
+          tmem_arrived(o);
+          if (!few) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) __stcg(vec(mine, d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+            for (int c = 0; c < 32; c += 4) __stcg(vec(mine, d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+            continue;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<float4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                  make_float4(o[h * 16 + c * 4], o[h * 16 + c * 4 + 1], o[h * 16 + c * 4 + 2], o[h * 16 + c * 4 + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = i * 8 + (lane >> 2), c = lane & 3;
+              __stcg(reinterpret_cast<float4*>(sums + (mine + (row & 96) + rr) * DP + d + h * 16 + c * 4),
+                     *reinterpret_cast<const float4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)));
+            }
+            __syncwarp();
+          }
+        }
       }
       __threadfence();
       mbar_arrive(bar.join(t));
@@ -708,36 +734,95 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       if (arrived[t] == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
         __threadfence();
         if (row == 0) *count = 0;
-        const float2* own = stats + t * 128 + row;
-        float M = -INFINITY, sum = 0.0f;
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(own + slot(c, c == c0) * AT_BM).x);
-        for (int c = c0; c <= c1; ++c) {
-          const float2 ml = __ldcg(own + slot(c, c == c0) * AT_BM);
-          sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
-        }
-        const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
-#pragma unroll 1
-        for (int d = 0; d < dims; d += 32) {
-          float o[32];
+        // Few: a warp takes four rows at a time, eight lanes a row; a lane four dims of every 32, and the weight of every eighth
+        // part.
+        const int sub = lane & 7;
+        for (int r0 = (row >> 5) * 4; few && r0 < rows_t; r0 += 16) {
+          const int rr = min(r0 + (lane >> 3), rows_t - 1);
+          float M = -INFINITY, sum = 0.0f;
+          for (int c = c0 + sub; c <= c1; c += 8) M = fmaxf(M, __ldcg(stats + slot(c) + rr).x);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-          for (int c = c0; c <= c1; ++c) {
-            const int64_t s = slot(c, c == c0);
-            const float f = exp2_fast((__ldcg(own + s * AT_BM).x - safe_max(M)) * p.scale_log2);
-            float4 v[8];
+          for (int d = 4; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+          constexpr int NV = DP / 32;
+          float4 o[NV];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __ldcg(vec(s, d + 4 * e));
+          for (int d = 0; d < NV; ++d) o[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int cb = c0; cb <= c1; cb += 8) {
+            const int n = min(8, c1 + 1 - cb);
+            float f = 0.0f, w = 0.0f;
+            if (sub < n) {
+              const float2 ml = __ldcg(stats + slot(cb + sub) + rr);
+              f = exp2_fast((ml.x - safe_max(M)) * p.scale_log2);
+              w = ml.y * f;
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o[4 * e] = fmaf(v[e].x, f, o[4 * e]);
-              o[4 * e + 1] = fmaf(v[e].y, f, o[4 * e + 1]);
-              o[4 * e + 2] = fmaf(v[e].z, f, o[4 * e + 2]);
-              o[4 * e + 3] = fmaf(v[e].w, f, o[4 * e + 3]);
+            for (int d = 4; d; d >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
+            sum += w;
+#pragma unroll 4
+            for (int c = 0; c < n; ++c) {
+              const float fc = __shfl_sync(0xFFFFFFFFu, f, (lane & 24) + c);
+              const float4* part = reinterpret_cast<const float4*>(sums + (slot(cb + c) + rr) * DP) + sub;
+#pragma unroll
+              for (int d = 0; d < NV; ++d) {
+                if (d * 32 < dims) {
+                  const float4 v = __ldcg(part + d * 8);
+                  o[d].x = fmaf(v.x, fc, o[d].x);
+                  o[d].y = fmaf(v.y, fc, o[d].y);
+                  o[d].z = fmaf(v.z, fc, o[d].z);
+                  o[d].w = fmaf(v.w, fc, o[d].w);
+                }
+              }
             }
           }
-          finish(o, d, inv);
+          if (r0 + (lane >> 3) < rows_t) {
+            const int gr = u.row0 + t * 128 + rr, rtok = (int)p.group.div(gr), rhq = u.head * (int)p.group.d + gr - rtok * (int)p.group.d;
+            const int2 sees = attn_range(p, u.seq, u.kv, rtok);
+            const bool nothing = sees.x >= sees.y;
+            const float inv = nothing ? 0.0f : __fdiv_rn(1.0f, sum);
+            const int64_t rt = u.seq.first + rtok;
+            T* to = static_cast<T*>(p.out) + rt * p.out_stride + (int64_t)rhq * p.D;
+#pragma unroll
+            for (int d = 0; d < NV; ++d)
+              if (d * 32 + sub * 4 < p.D)
+                *reinterpret_cast<uint2*>(to + d * 32 + sub * 4) =
+                    make_uint2(pack2<T>(o[d].x * inv, o[d].y * inv), pack2<T>(o[d].z * inv, o[d].w * inv));
+            if (sub == 0 && p.lse != nullptr) p.lse[rt * p.q_heads + rhq] = nothing ? -INFINITY : fmaf(M, p.scale, logf(sum));
+          }
         }
-        finish_lse(M, sum);
+        if (!few && !idle) {
+          const float2* own = stats + row;
+          float M = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(own + slot(c)).x);
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) {
+            const float2 ml = __ldcg(own + slot(c));
+            sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
+          }
+          const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
+#pragma unroll 1
+          for (int d = 0; d < dims; d += 32) {
+            float o[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0.0f;
+#pragma unroll 2
+            for (int c = c0; c <= c1; ++c) {
+              const float f = exp2_fast((__ldcg(own + slot(c)).x - safe_max(M)) * p.scale_log2);
+              float4 v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __ldcg(vec(slot(c), d + 4 * e));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                o[4 * e] = fmaf(v[e].x, f, o[4 * e]);
+                o[4 * e + 1] = fmaf(v[e].y, f, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(v[e].z, f, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(v[e].w, f, o[4 * e + 3]);
+              }
+            }
+            finish(o, d, inv);
+          }
+          finish_lse(M, sum);
+        }
       }
       __syncwarp();
     }
@@ -782,7 +867,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) skip = *(volatile uint32_t*)p.err & kAbortMask;
-  AttnRun run = attn_plan<AT_BM, AT_KEYS, AT_OH, AT_THREADS>(p, reinterpret_cast<int64_t*>(sm));
+  AttnRun run = attn_plan<AT_BM, AT_KEYS, AT_OH, AT_MIN, AT_THREADS>(p, reinterpret_cast<int64_t*>(sm));
   fence_proxy_async_smem();  // the division's sums lie where loads will
   tc_fence_before();
   __syncthreads();
