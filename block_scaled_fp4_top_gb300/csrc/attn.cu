@@ -64,11 +64,13 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   constexpr int RPI = 32 / CH;                           // keys that one copy instruction of the warp covers
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ float stats[C::kWarps][AD_ROWS][2];
-  __shared__ uint32_t arrived;
+  __shared__ uint32_t arrived, skip;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
+  if (tid == 0) skip = *(volatile uint32_t*)p.err & kAbortMask;
   const AttnRun run = attn_plan<AD_ROWS, C::S, AD_OH, AD_MIN, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
+  if (skip) return;  // an earlier call gave up
   uint8_t* ring = sm + warp * C::kRing;
   const uint32_t ring32 = smem_u32(ring);
   const T* kbase = static_cast<const T*>(p.k);
