@@ -90,6 +90,7 @@ SIGNATURES = {
                           [c_vp, c_f32, c_vp, c_i64] + [c_vp] * 4),
     "fp4moe_paged_attention": (c_i32, [KVP, c_vp, c_vp] + [c_i32] * 3 + [c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_f32,
                                                                      c_i32, c_i32, c_vp, c_i64] + [c_vp] * 4),
+    "fp4moe_paged_attention_plan": (c_i32, [KVP, c_i32, c_i32, c_i32, ctypes.POINTER(c_i32)]),
 }
 
 _lib = None

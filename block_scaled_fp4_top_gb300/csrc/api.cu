@@ -852,6 +852,13 @@ fp4moe_status check_kv_cache(const fp4moe_kv_cache* c) {
     if (s < 0 || s >= ((int64_t)1 << 40) || s % 8 != 0) return FP4MOE_INVALID_ARG;
   return FP4MOE_OK;
 }
+fp4moe_status check_attention(const fp4moe_kv_cache* c, int32_t num_seqs, int32_t T, int32_t q_heads) {
+  FP4_TRY(check_kv_cache(c));
+  if (num_seqs < 0 || T < 0) return FP4MOE_INVALID_ARG;
+  if (num_seqs > FP4MOE_KV_MAX_SEQS) return FP4MOE_UNSUPPORTED;
+  if (q_heads < 1 || q_heads % c->kv_heads != 0 || (int64_t)T * q_heads > INT32_MAX) return FP4MOE_INVALID_ARG;
+  return FP4MOE_OK;
+}
 // The distance between the rows of T tokens of `width` elements each.
 bool row_stride_ok(int32_t T, int64_t stride, int64_t width) {
   return stride % 8 == 0 && (T <= 1 || stride >= width) && stride >= 0 && stride < ((int64_t)1 << 40);
@@ -909,10 +916,8 @@ fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k
                                      const int32_t* page_table, int32_t table_columns, const int32_t* kv_len,
                                      const int32_t* q_offset, float scale, int32_t causal, int32_t window, void* out,
                                      int64_t out_stride, float* lse, void* ws, uint32_t* err, fp4moe_stream_t stream) {
-  FP4_TRY(check_kv_cache(cache));
-  if (num_seqs < 0 || T < 0 || table_columns < 0 || window < 0) return FP4MOE_INVALID_ARG;
-  if (num_seqs > FP4MOE_KV_MAX_SEQS) return FP4MOE_UNSUPPORTED;
-  if (q_heads < 1 || q_heads % cache->kv_heads != 0 || (int64_t)T * q_heads > INT32_MAX) return FP4MOE_INVALID_ARG;
+  FP4_TRY(check_attention(cache, num_seqs, T, q_heads));
+  if (table_columns < 0 || window < 0) return FP4MOE_INVALID_ARG;
   if (!(scale > 0.0f) || std::isinf(scale) || (window > 0 && !causal)) return FP4MOE_INVALID_ARG;
   const int64_t width = (int64_t)q_heads * cache->head_dim;
   if (!row_stride_ok(T, q_stride, width) || !row_stride_ok(T, out_stride, width)) return FP4MOE_INVALID_ARG;
@@ -924,6 +929,13 @@ fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k
   return paged_attention_launch(*cache, k_cache, v_cache, num_seqs, T, q_heads, q, q_stride, page_table, table_columns,
                                 kv_len, q_offset, scale, causal != 0, window, out, out_stride, lse, ws, err,
                                 (cudaStream_t)stream);
+}
+
+fp4moe_status fp4moe_paged_attention_plan(const fp4moe_kv_cache* cache, int32_t num_seqs, int32_t T, int32_t q_heads,
+                                          int32_t* tile_rows) {
+  FP4_TRY(check_attention(cache, num_seqs, T, q_heads));
+  if (tile_rows) *tile_rows = paged_attention_tile(*cache, num_seqs, T, q_heads);
+  return FP4MOE_OK;
 }
 
 }  // extern "C"

@@ -404,6 +404,15 @@ fp4moe_status attn_rows_typed(const AttnParams& p, int nsm, cudaStream_t st) {
 
 }  // namespace
 
+// Sequences of more than 16 rows a kv head, on the average, are for the larger tiles, which read k and v once for 256
+// rows (us, 32 / 8 heads of 128 dims, 16 sequences of 8192 keys: 16 rows 93 with tiles of 16 and 106 with the others, 32
+// rows 175 and 108), unless all of them are a few tiles of 16, which a part of the SMs works on (32 rows of one sequence
+// 23 and 28, of four sequences of 4096 keys 32 and 27).
+int paged_attention_tile(const fp4moe_kv_cache& c, int32_t num_seqs, int32_t T, int32_t q_heads) {
+  const int64_t rows = (int64_t)T * (q_heads / c.kv_heads), tiles = (rows + AD_ROWS - 1) / AD_ROWS * c.kv_heads;
+  return c.head_dim <= 128 && rows > (int64_t)AD_ROWS * num_seqs && tiles > 48 ? kAttnTileRows : AD_ROWS;
+}
+
 fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cache, const void* v_cache, int32_t num_seqs,
                                      int32_t T, int32_t q_heads, const void* q, int64_t q_stride,
                                      const int32_t* page_table, int32_t table_columns, const int32_t* kv_len,
@@ -437,13 +446,7 @@ fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cac
   int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
   if (nsm > kAttnMaxCtas) nsm = kAttnMaxCtas;
-  // Sequences of more than 16 rows a kv head, on the average, are for the larger tiles, which read k and v once for 256
-  // rows (us, 32 / 8 heads of 128 dims, 16 sequences of 8192 keys: 16 rows 93 here and 106 there, 32 rows 175 and 108),
-  // unless all of them are a few tiles of 16, which a part of the SMs works on (32 rows of one sequence 23 and 28, of four
-  // sequences of 4096 keys 32 and 27).
-  const int64_t tiles = ((int64_t)T * p.group.d + AD_ROWS - 1) / AD_ROWS * c.kv_heads;
-  if (c.head_dim <= 128 && (int64_t)T * p.group.d > (int64_t)AD_ROWS * num_seqs && tiles > 48)
-    return attn_tile_launch(c.dtype, p, nsm, st);
+  if (paged_attention_tile(c, num_seqs, T, q_heads) == kAttnTileRows) return attn_tile_launch(c.dtype, p, nsm, st);
   return c.dtype == FP4MOE_BF16 ? attn_rows_typed<__nv_bfloat16>(p, nsm, st) : attn_rows_typed<__half>(p, nsm, st);
 }
 

@@ -170,6 +170,8 @@ fp4moe_status rope_cache_launch(const fp4moe_kv_cache& c, int32_t T, int32_t q_h
                                 const int32_t* position, const int32_t* slot, int32_t rot_first, int32_t rot_dim,
                                 bool interleaved, const double* inv_freq, float amplitude, void* q_out,
                                 int64_t q_out_stride, void* k_cache, void* v_cache, uint32_t* err, cudaStream_t st);
+// attn.cu: rows of a tile of the kernel that takes these sizes
+int paged_attention_tile(const fp4moe_kv_cache& c, int32_t num_seqs, int32_t T, int32_t q_heads);
 // attn.cu: attention over the pages
 fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cache, const void* v_cache, int32_t num_seqs,
                                      int32_t T, int32_t q_heads, const void* q, int64_t q_stride,

@@ -748,6 +748,16 @@ fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k
                                      const int32_t* q_offset, float scale, int32_t causal, int32_t window, void* out,
                                      int64_t out_stride, float* lse, void* ws, uint32_t* err, fp4moe_stream_t stream);
 
+/*
+ * fp4moe_paged_attention_plan: rows of a tile of the kernel that a call of these
+ * sizes takes (host arithmetic): 16, or 256 (two of 128) on the tensor cores of
+ * one CTA. A row is a token and one of the query heads of a kv head. Results differ
+ * between the two by the order of fp32 additions and by where weights are rounded.
+ * Errors as in fp4moe_paged_attention; num_seqs or T 0: 16.
+ */
+fp4moe_status fp4moe_paged_attention_plan(const fp4moe_kv_cache* cache, int32_t num_seqs, int32_t T, int32_t q_heads,
+                                          int32_t* tile_rows);
+
 /* ------------------------------------------------------------------ prep --
  * Load-time helpers. They run outside the timed hot path and may use
  * cudaMemsetAsync. They still never synchronise.

@@ -371,7 +371,10 @@ def run_attention(q, kc, vc, table, kv, first, scale, causal, window, with_lse=T
     return got
 
 
-def check_attention(new, kv, H, Hk, D, dtype="bfloat16", page=16, causal=True, window=0, scale=None, **kw):
+def check_attention(new, kv, H, Hk, D, dtype="bfloat16", page=16, causal=True, window=0, scale=None, tile=None, **kw):
+    if tile:
+        from block_scaled_fp4_top_gb300 import api
+        assert api.fp4moe_paged_attention_plan(len(new), sum(new), H, Hk, D) == tile
     q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D, dtype, page, **kw)
     scale = D ** -0.5 if scale is None else scale
     first = [sum(new[:b]) for b in range(len(new) + 1)]
@@ -431,6 +434,127 @@ def test_attention_of_every_key(new, kv, D):
 @pytest.mark.parametrize("new", [[1, 1], [40, 3]])
 def test_attention_spread_of_the_scores(dtype, spread, scale, new):
     check_attention(new, [900, 77], 4, 2, 128, dtype, spread=spread, scale=scale)
+
+
+# The same for the larger tiles, which these sizes take.
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [8, 16, 24, 48, 64, 72, 80, 96, 112, 120, 128])
+@pytest.mark.parametrize("page", [5, 16])
+def test_tiles_head_dims(D, dtype, page):
+    check_attention([70, 1, 30], [70, 150, 401], 16, 8, D, dtype, page, tile=256)
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 8), (24, 8), (20, 4), (56, 8), (16, 1), (17, 1), (33, 1), (128, 1), (130, 1), (256, 2), (600, 2)])
+@pytest.mark.parametrize("new", [[129, 3], [64, 64, 65], [0, 1000, 0]])
+def test_tiles_head_groups(H, Hk, new):
+    new = [n if H // Hk < 60 else n // 4 for n in new]
+    check_attention(new, [n + 77 for n in new], H, Hk, 64, tile=256)
+
+
+@pytest.mark.parametrize("page", [1, 2, 3, 8, 16, 24, 48, 64, 100, 128, 136, 256, 1000])
+@pytest.mark.parametrize("order", ["tokens", "heads"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiles_pages(page, order, D):
+    check_attention([100, 20, 3], [733, 257, 128], 16, 4, D, page=page, order=order, tile=256)
+
+
+@pytest.mark.parametrize("new,kv", [([128], [128]), ([129], [129]), ([300], [300]), ([65], [1000]), ([257], [5000]), ([90, 1, 0, 90], [90, 5000, 50, 91]),
+                                    ([200, 7], [3, 0]), ([60, 60, 60], [1, 20000, 59]), ([40] * 40, list(range(40, 80))), ([1] * 30 + [500], [100] * 30 + [500])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiles_lengths(new, kv, D):
+    out = check_attention(new, kv, 32, 8, D, tile=256)
+    first = np.cumsum([0] + new)
+    for b, (n, L) in enumerate(zip(new, kv)):
+        if L < n:
+            assert (out[first[b]:first[b] + n - L] == 0).all()
+
+
+@pytest.mark.parametrize("window", [1, 2, 64, 100, 128, 129, 300, 5000])
+@pytest.mark.parametrize("new,kv", [([60, 200], [700, 200]), ([1, 300], [3000, 1500])])
+def test_tiles_window(window, new, kv):
+    check_attention(new, kv, 16, 8, 64, window=window, tile=256)
+
+
+@pytest.mark.parametrize("new,kv", [([100, 64], [700, 0]), ([60, 300], [130, 17]), ([130], [4000])])
+@pytest.mark.parametrize("D,page", [(80, 16), (128, 7)])
+def test_tiles_of_every_key(new, kv, D, page):
+    check_attention(new, kv, 16, 8, D, "float16", page, causal=False, tile=256)
+
+
+@pytest.mark.parametrize("dtype,spread,scale", [("bfloat16", 30.0, None), ("float16", 8.0, None), ("bfloat16", 1.0, 1e-4),
+                                                ("bfloat16", 1.0, 3.0), ("float16", 0.0, None)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiles_spread_of_the_scores(dtype, spread, scale, D):
+    check_attention([140, 3], [1900, 77], 16, 8, D, dtype, spread=spread, scale=scale, tile=256)
+
+
+def test_tiles_scores_that_rise():
+    """Every step's maximum far above the steps' before: the sums so far are rescaled each time, in every row."""
+    import torch
+    for D in (64, 128):
+        new, kv = [130], [1500]
+        q, kc, vc, flat, table, slots = attention_case(new, kv, 16, 8, D)
+        q.copy_(torch.ones_like(q) + 0.1 * q)
+        rise = torch.linspace(-4.0, 4.0, 1500, device="cuda")[:, None, None]
+        for b, f in ((kc, flat[0]),):
+            s = slots[0]
+            b[s // 16, s % 16] = (rise + 0.05 * f[s].float()).bfloat16()
+        flat = [c.reshape(-1, 8, D) for c in (kc, vc)]
+        out, lse = run_attention(q, kc, vc, table, kv, [0, 130], 1.0, True, 0)
+        want = ref.attention(q, *flat, slots, [0], new, kv, 1.0, True, 0)
+        compare(out, lse, want, kv, D, "bfloat16")
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 7)])
+@pytest.mark.parametrize("new", [[130], [200, 31]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_tiles_keep_hidden_keys_out(D, page, new, bad):
+    import torch
+    kv, H, Hk = [380, 300][:len(new)], 16, 8
+    first = [0] + np.cumsum(new).tolist()
+    for where, window in (("v", 0), ("v", 70), ("k", 0)):
+        q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D, page=page)
+        j = kv[0] - 1 - new[0] // 2                     # a middle new token's own key
+        s = int(slots[0][j])
+        (vc if where == "v" else kc)[s // page, s % page, 1, 3] = bad
+        flat = [c.reshape(-1, Hk, D) for c in (kc, vc)]
+        out, lse = run_attention(q, kc, vc, table, kv, first, D ** -0.5, True, window)
+        want = ref.attention(q, *flat, slots, first[:-1], new, kv, D ** -0.5, True, window)
+        i = torch.arange(sum(new), device="cuda")
+        pos = i + kv[0] - new[0]
+        sees = (i < new[0]) & (pos >= j) & ((pos - window < j) if window else True)
+        clean = [0, 1] + list(range(4, H))
+        assert torch.isfinite(out[~sees]).all() and torch.isfinite(out[:, clean]).all()
+        if where == "v":
+            assert not torch.isfinite(out[sees][:, 2:4, 3]).any()
+            compare(out, lse, want, kv, D, "bfloat16")
+        else:
+            compare(out[~sees], lse[~sees], [t[~sees] for t in want], kv, D, "bfloat16")
+            compare(out[:, clean], lse[:, clean], [t[:, clean] for t in want], kv, D, "bfloat16")
+
+
+@pytest.mark.parametrize("page", [16, 7])
+def test_tiles_pages_out_of_the_cache(page):
+    check_attention([100, 30, 2], [300, 60, 40], 16, 8, 64, page=page, hole=[(0, 2), (1, 0), (2, 1)], tile=256)
+
+
+@pytest.mark.parametrize("H,Hk,D", [(32, 8, 128), (24, 8, 64), (12, 4, 80)])
+def test_tiles_strides(H, Hk, D):
+    """q as a slice of a projection's rows, out into a wider matrix; rows past the last sequence stay as they were."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    new, kv = [130, 70], [290, 140]
+    q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D)
+    wide = torch.randn(210, (H + 4) * D, device="cuda").bfloat16()
+    wide[:200, D:(H + 1) * D] = q.flatten(1)
+    out = torch.full((210, H + 2, D), 9.0, device="cuda", dtype=torch.bfloat16)
+    ws, err = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda"), ints([0])
+    api.fp4moe_paged_attention(wide[:, D:(H + 1) * D].unflatten(1, (H, D)), kc, vc, table, ints(kv), ints([0, 130, 200]), D ** -0.5,
+                               out[:, 1:H + 1], None, ws, err)
+    torch.cuda.synchronize()
+    want = ref.attention(q, *flat, slots, [0, 130], new, kv, D ** -0.5, True, 0)
+    compare(out[:200, 1:H + 1], None, want, kv, D, "bfloat16")
+    assert (out[:, 0] == 9.0).all() and (out[:, H + 1] == 9.0).all() and (out[200:] == 9.0).all() and err.tolist() == [0]
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -521,7 +645,7 @@ def test_attention_strides():
     assert (out[:, 0] == 9.0).all() and (out[:, 5] == 9.0).all()
 
 
-@pytest.mark.parametrize("new", [[1, 1], [100, 1]])
+@pytest.mark.parametrize("new", [[1, 1], [100, 100]])
 def test_attention_offsets_past_32_bits(new):
     """Pages whose elements lie past 2^31 and 2^32 of the cache's."""
     import torch

@@ -108,6 +108,22 @@ def test_attention_refusals(lib):
     assert f(T=0, q=None, out=None) == _lib.OK and f(B=0, table=None) == _lib.OK
 
 
+def test_attention_plan(lib):
+    """Which kernel takes what: the sizes that the GPU tests use for each do take it."""
+    from block_scaled_fp4_top_gb300 import _lib, api
+    plan = api.fp4moe_paged_attention_plan
+    for B, T, H, Hk, D, want in ((1, 1, 32, 8, 128, 16), (64, 64, 32, 8, 128, 16), (16, 64, 64, 8, 64, 256), (8, 2048, 32, 8, 128, 256),
+                                 (1, 8, 32, 8, 128, 16), (4, 32, 32, 8, 128, 256), (1, 8192, 32, 8, 136, 16), (1, 8192, 32, 8, 256, 16),
+                                 (0, 0, 8, 8, 64, 16), (1, 2**31 // 64 - 1, 64, 1, 64, 256), (8192, 8192, 1, 1, 8, 16)):
+        assert plan(B, T, H, Hk, D) == want, (B, T, H, Hk, D)
+    p = lib.fp4moe_paged_attention_plan
+    assert p(kv(), 1, 1, 3, None) == _lib.INVALID_ARG and p(kv(), -1, 1, 2, None) == _lib.INVALID_ARG
+    assert p(kv(), 1, -1, 2, None) == _lib.INVALID_ARG and p(kv(), 8193, 1, 2, None) == _lib.UNSUPPORTED
+    assert p(None, 1, 1, 2, None) == _lib.INVALID_ARG and p(kv(), 1, 1, 2, None) == _lib.OK      # outputs optional
+    for c, want in BAD_CACHES:
+        assert p(kv(**c), 1, 1, 2, None) == getattr(_lib, want), c
+
+
 def test_binding_refuses_wrong_shapes_and_types():
     """The C calls see pointers only, so the binding holds every tensor to its shape and type; and every tensor here is on
     the host, which is refused before any call too."""
