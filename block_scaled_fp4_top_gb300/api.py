@@ -425,12 +425,14 @@ def fp4moe_mx_gemm(fmt, K, a_codes, a_sf, b_codes, b_sf, alpha, out, err, stream
 
 # ------------------------------------------------- the paged key-value cache
 _I32, _F64 = torch.int32, torch.float64
+_KvCache = _lib.KvCache
 _KV_DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16}
 
 
 def _arg_ints(name, t, n, dev):
     """The pointer of n int32 values (n None: any number of them)."""
-    if t.dtype is not _I32 or t.dim() != 1 or (n is not None and t.shape[0] != n):
+    shape = t.shape
+    if t.dtype is not _I32 or len(shape) != 1 or (n is not None and shape[0] != n):
         raise Fp4MoeError(f"{name}: expected {'a vector' if n is None else n} of {_I32}, got {tuple(t.shape)} of {t.dtype}")
     if t.get_device() != dev or not t.is_contiguous():
         _place(name, t, dev)
@@ -447,9 +449,10 @@ def _arg_table(name, t, B, dev):
 
 
 def _arg_err(err, dev):
-    if err.element_size() * err.numel() < 4:
+    if err.nbytes < 4:
         raise Fp4MoeError("err: expected a device word of 4 bytes")
-    _place("err", err, dev)
+    if err.get_device() != dev or not err.is_contiguous():
+        _place("err", err, dev)
     return err.data_ptr()
 
 
@@ -467,7 +470,8 @@ def _kv_cache(k_cache, v_cache, dev):
         raise Fp4MoeError("k_cache, v_cache: expected CUDA tensors on the current device")
     P, S, H, D = shape
     if k_cache.is_contiguous() and v_cache.is_contiguous():
-        return _lib.KvCache(d, H, D, S, P, S * H * D, H * D, D), k_cache.data_ptr(), v_cache.data_ptr()
+        row = H * D
+        return _KvCache(d, H, D, S, P, S * row, row, D), k_cache.data_ptr(), v_cache.data_ptr()
     # (the stride of a dimension of one element says nothing)
     st = [0 if n == 1 else s for n, s in zip(shape, k_cache.stride())]
     if st != [0 if n == 1 else s for n, s in zip(shape, v_cache.stride())] or st[3] != 1 or any(s % 8 for s in st[:3]):
@@ -537,9 +541,11 @@ def fp4moe_rope_cache(q, k, v, position, slot, inv_freq, q_out, k_cache, v_cache
     c, pk, pv = _kv_cache(k_cache, v_cache, dev)
     dt, D = k_cache.dtype, c.head_dim
     T = slot.shape[0]
-    if inv_freq.dtype is not _F64 or inv_freq.dim() != 1:
-        raise Fp4MoeError(f"inv_freq: expected a vector of {_F64}, got {tuple(inv_freq.shape)} of {inv_freq.dtype}")
-    _place("inv_freq", inv_freq, dev)
+    pairs = inv_freq.shape
+    if inv_freq.dtype is not _F64 or len(pairs) != 1:
+        raise Fp4MoeError(f"inv_freq: expected a vector of {_F64}, got {tuple(pairs)} of {inv_freq.dtype}")
+    if inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+        _place("inv_freq", inv_freq, dev)
     Hq = q_stride = q_out_stride = k_stride = v_stride = 0
     ptr_q = ptr_qo = ptr_k = ptr_v = None
     if (q is None) != (q_out is None) or (k is None) != (v is None):
@@ -560,7 +566,7 @@ def fp4moe_rope_cache(q, k, v, position, slot, inv_freq, q_out, k_cache, v_cache
         pk = pv = None
     _check(_lib.load().fp4moe_rope_cache(c, T, Hq, ptr_q, q_stride, ptr_k, k_stride, ptr_v, v_stride,
                                          _arg_ints("position", position, T, dev), _arg_ints("slot", slot, T, dev), first,
-                                         2 * inv_freq.shape[0], interleaved, inv_freq.data_ptr(), amplitude, ptr_qo,
+                                         2 * pairs[0], interleaved, inv_freq.data_ptr(), amplitude, ptr_qo,
                                          q_out_stride, pk, pv, _arg_err(err, dev), _s(stream)), "fp4moe_rope_cache")
 
 
@@ -587,9 +593,10 @@ def fp4moe_paged_attention(q, k_cache, v_cache, page_table, kv_len, q_offset, sc
         raise Fp4MoeError(f"out: expected {H} heads, got {Ho}")
     B = kv_len.shape[0]
     columns, pt = _arg_table("page_table", page_table, B, dev)
-    if ws.element_size() * ws.numel() < _lib.ATTENTION_WORKSPACE_BYTES:
+    if ws.nbytes < _lib.ATTENTION_WORKSPACE_BYTES:
         raise Fp4MoeError(f"ws: expected {_lib.ATTENTION_WORKSPACE_BYTES} bytes")
-    _place("ws", ws, dev)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _place("ws", ws, dev)
     _check(_lib.load().fp4moe_paged_attention(c, pk, pv, B, T, H, ptr_q, q_stride, pt, columns,
                                               _arg_ints("kv_len", kv_len, B, dev),
                                               _arg_ints("q_offset", q_offset, B + 1, dev), scale, causal, window, ptr_o,

@@ -177,24 +177,54 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(KvPlanParams p) {
   auto stack_page = [&](int32_t v) { return v < F ? p.free_pages[v] : given_page(v - F); };
   err = 0;
   const int step = (int)ctas * KP_THREADS, i0 = (int)rank * KP_THREADS + tid;
-  // ---- tokens
-  for (int64_t t = i0; t < p.rows; t += step) {
-    int32_t pos = 0, slot = -1;
-    if (t < total) {
-      const int b = last_at_most(first, B, (int32_t)t);
-      const int32_t c = from[b], i = (int32_t)t - first[b];
+  // ---- tokens. Where there are more than threads, a thread takes four neighbours: one search, and mostly one page, for
+  // them (512 sequences, 50000 tokens: 16.8 -> 14.4 us); else one each, so that the reads of all are under way at once.
+  auto take = [&](int64_t t, int n, int32_t (&pos)[4], int32_t (&slot)[4]) {
+    int b = t < total ? last_at_most(first, B, (int32_t)t) : 0;
+    int32_t page = -1, page_at = -1, page_of = -1;  // the last page read: entry page_at of sequence page_of
+#pragma unroll
+    for (int i = 0; i < 4; ++i, ++t) {
+      pos[i] = 0;
+      slot[i] = -1;
+      if (i >= n || t >= total) continue;
+      while (t >= first[b + 1]) ++b;
+      const int32_t c = from[b], k = (int32_t)t - first[b];
       if (c < 0) {
-        pos = clamp32((int64_t)~c + i, INT32_MAX);
+        pos[i] = clamp32((int64_t)~c + k, INT32_MAX);
+        continue;
+      }
+      pos[i] = c + k;
+      const int32_t j = (int32_t)p.page.div((uint32_t)pos[i]);
+      if (j != page_at || b != page_of) {
+        const int32_t old = pages(c);
+        page = j < old ? p.table[(int64_t)b * p.columns + j] : stack_page(top - 1 - (taken[b] + j - old));
+        page_at = j;
+        page_of = b;
+      }
+      if (page >= 0 && page < p.num_pages) slot[i] = page * (int32_t)p.page.d + (pos[i] - j * (int32_t)p.page.d);
+      else err |= FP4MOE_ERR_PAGE;
+    }
+  };
+  if (p.rows > step) {
+    for (int64_t t = (int64_t)i0 * 4; t < p.rows; t += (int64_t)step * 4) {
+      int32_t pos[4], slot[4];
+      const int n = (int)min((int64_t)4, p.rows - t);
+      take(t, n, pos, slot);
+      if (n == 4) {
+        *reinterpret_cast<int4*>(p.position + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(p.slot + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
       } else {
-        pos = c + i;
-        const int32_t j = (int32_t)p.page.div((uint32_t)pos), old = pages(c);
-        const int32_t page = j < old ? p.table[(int64_t)b * p.columns + j] : stack_page(top - 1 - (taken[b] + j - old));
-        if (page >= 0 && page < p.num_pages) slot = page * (int32_t)p.page.d + (pos - j * (int32_t)p.page.d);
-        else err |= FP4MOE_ERR_PAGE;
+        for (int i = 0; i < n; ++i) {
+          p.position[t + i] = pos[i];
+          p.slot[t + i] = slot[i];
+        }
       }
     }
-    p.position[t] = pos;
-    p.slot[t] = slot;
+  } else if (i0 < p.rows) {
+    int32_t pos[4], slot[4];
+    take(i0, 1, pos, slot);
+    p.position[i0] = pos[0];
+    p.slot[i0] = slot[0];
   }
   // ---- pages taken, and those given back that stay on the stack
   for (int64_t k = i0; k < Q; k += step) {
