@@ -425,14 +425,21 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
     const bool two = u.rows > 128;
     const int n = u.s1 - u.s0;
     wait(bar.q_full(), units & 1);
+    bool k_there = false, v_there = false;  // the next step's, known already
     for (int j = 0; j <= n; ++j) {
-      if (j < n) wait(bar.k_full(ks), kp);
-      if (j > 0) wait(bar.v_full(vs), vp);
+      if (!k_there && j < n) wait(bar.k_full(ks), kp);
+      if (!v_there && j > 0) wait(bar.v_full(vs), vp);
+      k_there = v_there = false;
       const uint64_t kb = kd + (uint32_t)(ks * (C::kTile >> 4)), vb = vd + (uint32_t)(vs * (C::kTile >> 4));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (t == 1 && !two) break;
         const uint32_t st = tmem + t * 128, ot = tmem + 256 + t * DP;
+        if (t == 1) {  // while the first tile's MMAs run, and this one's weights are made
+          const int k1 = ks + 1 == C::kStages ? 0 : ks + 1, v1 = j == 0 ? vs : vs + 1 == C::kStages ? 0 : vs + 1;
+          k_there = j + 1 < n && mbar_test(bar.k_full(k1), k1 == 0 ? kp ^ 1 : kp);
+          v_there = mbar_test(bar.v_full(v1), j > 0 && v1 == 0 ? vp ^ 1 : vp);
+        }
         if (j > 0) {
           wait(bar.p_full(t), pp[t]);
           pp[t] ^= 1;
@@ -695,43 +702,59 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       const bool few = rows_t <= AT_FEW;
       auto vec = [&](int64_t s, int d) { return reinterpret_cast<float4*>(sums + s * DP) + (d / 4) * 128 + row; };
       const int64_t mine = slot(blockIdx.x);
-      if (!idle) {
-        __stcg(stats + mine + row, make_float2(m, l));
+      auto meet = [&] {  // the tile's four warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.join(t));
+        ok = warp_wait(bar.join(t), jp, p.err);
+        jp ^= 1;
+        return ok;
+      };
+      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0 + t;
+      const uint32_t others = (uint32_t)(c1 - c0);
+      // Where all others have left their parts, this one's need not be written: it is added out of TMEM, in its turn.
+      if (row == 0) arrived[t] = *(volatile uint32_t*)count;
+      if (!meet()) break;
+      bool last_one = arrived[t] == others;
+      const bool kept = last_one && !few;
+      if (!kept) {
+        if (!idle) {
+          __stcg(stats + mine + row, make_float2(m, l));
 #pragma unroll 1
-        for (int d = 0; d < dims; d += 32) {  // few: through shared memory, 16 dims at a time, four lanes to a row's 64 bytes
-          float o[32];
-          tmem_ld32(ot + d, o);
-          tmem_arrived(o);
-          if (!few) {
+          for (int d = 0; d < dims; d += 32) {  // few: through shared memory, 16 dims at a time, four lanes to a row's 64 bytes
+            float o[32];
+            tmem_ld32(ot + d, o);
+            tmem_arrived(o);
+            if (!few) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) __stcg(vec(mine, d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
-            continue;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<float4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-                  make_float4(o[h * 16 + c * 4], o[h * 16 + c * 4 + 1], o[h * 16 + c * 4 + 2], o[h * 16 + c * 4 + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = i * 8 + (lane >> 2), c = lane & 3;
-              __stcg(reinterpret_cast<float4*>(sums + (mine + (row & 96) + rr) * DP + d + h * 16 + c * 4),
-                     *reinterpret_cast<const float4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)));
+              for (int c = 0; c < 32; c += 4) __stcg(vec(mine, d + c), make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+              continue;
             }
-            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<float4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                    make_float4(o[h * 16 + c * 4], o[h * 16 + c * 4 + 1], o[h * 16 + c * 4 + 2], o[h * 16 + c * 4 + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int rr = i * 8 + (lane >> 2), c = lane & 3;
+                __stcg(reinterpret_cast<float4*>(sums + (mine + (row & 96) + rr) * DP + d + h * 16 + c * 4),
+                       *reinterpret_cast<const float4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)));
+              }
+              __syncwarp();
+            }
           }
         }
+        __threadfence();
+        if (!meet()) break;
+        if (!last_one) {
+          if (row == 0) arrived[t] = atomicAdd(count, 1u);
+          if (!meet()) break;
+          last_one = arrived[t] == others;
+        }
       }
-      __threadfence();
-      mbar_arrive(bar.join(t));
-      if (!(ok = warp_wait(bar.join(t), jp, p.err))) break;
-      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0 + t;
-      if (row == 0) arrived[t] = atomicAdd(count, 1u);
-      mbar_arrive(bar.join(t));
-      if (!(ok = warp_wait(bar.join(t), jp ^ 1, p.err))) break;
-      if (arrived[t] == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
+      if (last_one) {  // adds all parts in order
         __threadfence();
         if (row == 0) *count = 0;
         // Few: a warp takes four rows at a time, eight lanes a row; a lane four dims of every 32, and the weight of every eighth
@@ -790,24 +813,31 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
           }
         }
         if (!few && !idle) {
-          const float2* own = stats + row;
+          auto stat = [&](int c) { return c == (int)blockIdx.x ? make_float2(m, l) : __ldcg(stats + slot(c) + row); };
           float M = -INFINITY, sum = 0.0f;
 #pragma unroll 4
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(own + slot(c)).x);
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, stat(c).x);
 #pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(own + slot(c));
+            const float2 ml = stat(c);
             sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
           }
           const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll 1
           for (int d = 0; d < dims; d += 32) {
-            float o[32];
+            float o[32], own[32];
+            tmem_ld32(ot + d, own);
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-#pragma unroll 2
+            tmem_arrived(own);
+#pragma unroll 1
             for (int c = c0; c <= c1; ++c) {
-              const float f = exp2_fast((__ldcg(own + slot(c)).x - safe_max(M)) * p.scale_log2);
+              const float f = exp2_fast((stat(c).x - safe_max(M)) * p.scale_log2);
+              if (c == (int)blockIdx.x) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = fmaf(own[e], f, o[e]);
+                continue;
+              }
               float4 v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = __ldcg(vec(slot(c), d + 4 * e));
@@ -853,12 +883,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
       mbar_init(bar.s_full(t), 1);
       mbar_init(bar.p_full(t), 4);
       mbar_init(bar.o_full(t), 1);
-      mbar_init(bar.join(t), 128);
+      mbar_init(bar.join(t), 4);
       mbar_init(bar.done(t), 1);
     }
     mbar_init(bar.landed(), 1);
     fence_mbar_init();
     odd[0] = odd[1] = odd[2] = 0;
+  }
+  if (threadIdx.x == 32) {
+    for (const CUtensorMap* m : {&maps.k, &maps.v, &maps.q})
+      asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory");
   }
   if (warp == 8) {
     tmem_alloc(smem_u32(&tmem_at), 512);
