@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     }
     bool whole = s0 == 0 && s1 == n;
     if (!whole) {
-      const int c0 = attn_owner(u.first, run.total, run.ctas), c1 = attn_owner(u.first + n - 1, run.total, run.ctas);
+      const int c0 = attn_owner(run, u.first), c1 = attn_owner(run, u.first + n - 1);
       float2* st = reinterpret_cast<float2*>(p.ws + kAttnStats);
       float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
       const int64_t slot = 2 * blockIdx.x + (s0 == 0);

@@ -84,16 +84,21 @@ __device__ __forceinline__ int attn_slices(int2 r) {
 struct AttnRun {
   int64_t total, begin, end;  // of the call, and the CTA's own
   int ctas;                   // CTAs that have a run, of a cost of MIN at least where there is that much
+  int64_t each;               // total / ctas,
+  int rest;                   // and what that leaves
   int seq, tile, head;        // of `begin`
   int at;                     // its place in its tile and head: the first OH are before slice 0
 };
 
-__device__ __forceinline__ int64_t attn_begin(int64_t total, int cta, int ctas) { return total * cta / ctas; }
-// The CTA whose run holds x.
-__device__ __forceinline__ int attn_owner(int64_t x, int64_t total, int ctas) {
-  int c = (int)(x * ctas / total);
-  while (c + 1 < ctas && attn_begin(total, c + 1, ctas) <= x) ++c;
-  while (c > 0 && attn_begin(total, c, ctas) > x) --c;
+// Where the run of a CTA begins: total * cta / ctas.
+__device__ __forceinline__ int64_t attn_begin(const AttnRun& r, int cta) {
+  return r.each * cta + (uint32_t)(r.rest * cta) / (uint32_t)r.ctas;
+}
+// The CTA whose run holds x: about where x / total is, then exactly.
+__device__ __forceinline__ int attn_owner(const AttnRun& r, int64_t x) {
+  int c = min((int)((float)x / (float)r.total * (float)r.ctas), r.ctas - 1);
+  while (c + 1 < r.ctas && attn_begin(r, c + 1) <= x) ++c;
+  while (c > 0 && attn_begin(r, c) > x) --c;
   return c;
 }
 
@@ -164,8 +169,10 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
   AttnRun r;
   r.total = total;
   r.ctas = (int)max((int64_t)1, min(total / MIN, (int64_t)gridDim.x));
-  r.begin = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x, r.ctas) : 0;
-  r.end = (int)blockIdx.x < r.ctas ? attn_begin(total, blockIdx.x + 1, r.ctas) : 0;
+  r.each = total / r.ctas;
+  r.rest = (int)(total - r.each * r.ctas);
+  r.begin = (int)blockIdx.x < r.ctas ? attn_begin(r, blockIdx.x) : 0;
+  r.end = (int)blockIdx.x < r.ctas ? attn_begin(r, blockIdx.x + 1) : 0;
   r.seq = r.tile = r.head = r.at = 0;
   if (r.begin < r.end) {
     int lo = 0, hi = p.B - 1;  // first sequence with upto > begin

@@ -692,7 +692,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       }
       finish_lse(m, l);
     } else {
-      const int c0 = attn_owner(u.first, run.total, run.ctas), c1 = attn_owner(u.first + u.n - 1, run.total, run.ctas);
+      const int c0 = attn_owner(run, u.first), c1 = attn_owner(run, u.first + u.n - 1);
       float2* stats = reinterpret_cast<float2*>(p.ws + kAttnStats);
       float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
       const int lane = row & 31, rows_t = last + 1 - t * 128;
@@ -815,12 +815,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
         if (!few && !idle) {
           auto stat = [&](int c) { return c == (int)blockIdx.x ? make_float2(m, l) : __ldcg(stats + slot(c) + row); };
           float M = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, stat(c).x);
-#pragma unroll 4
+#pragma unroll 1
           for (int c = c0; c <= c1; ++c) {
             const float2 ml = stat(c);
-            sum = fmaf(ml.y, exp2_fast((ml.x - safe_max(M)) * p.scale_log2), sum);
+            const float nm = fmaxf(M, ml.x);
+            sum = fmaf(sum, exp2_fast((M - safe_max(nm)) * p.scale_log2), ml.y * exp2_fast((ml.x - safe_max(nm)) * p.scale_log2));
+            M = nm;
           }
           const float inv = none ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll 1
