@@ -20,14 +20,21 @@ constexpr int AD_OH = 1;                     // what a tile costs, in slices, be
 
 template <int DP>
 struct AttnCfg {
-  static constexpr int kWarps = DP == 256 ? 4 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int S = AD_KEYS * kWarps;       // keys of a slice: one group a warp
-  static constexpr int kStage = 2 * AD_KEYS * DP * 2;  // k and v of a group
-  static constexpr int kStages = 196608 / (kWarps * kStage);
-  static constexpr int kRing = kStages * kStage;   // of a warp
-  static constexpr int kSmem = kWarps * kRing;
-  static constexpr int kPitch = DP + 8;            // floats between rows of a warp's sums: no bank conflicts
+  static constexpr int S = AD_KEYS * kWarps;           // keys of a slice: one group a warp
+  static constexpr int kTile = AD_KEYS * DP * 2;       // k, or v, of a group
+  // A load is both of them (64 dims: 104 us, one at a time 121; 32 sequences of 8192 keys), or one where three of both do
+  // not fit (256 dims: 343 us, both with half the warps 500).
+  static constexpr int kParts = DP == 256 ? 1 : 2;
+  static constexpr int kLoad = kParts * kTile;
+  static constexpr int kLoads = 196608 / (kWarps * kLoad);
+  static constexpr int kRing = kLoads * kLoad;         // of a warp
+  static constexpr int kRings = kWarps * kRing;
+  static constexpr bool kSharedQ = DP == 256;          // its 64 registers a thread are not there
+  static constexpr int kSmem = kRings + (kSharedQ ? AD_ROWS * DP * 2 : 0);
+  static constexpr int kPitch = DP + 8;                // floats between rows of a warp's sums: no bank conflicts
+  static_assert(kLoads >= 3, "two loads under way while one is used");
   static_assert(AD_ROWS * kPitch * 4 <= kRing, "sums fit the ring");
   static_assert((FP4MOE_KV_MAX_SEQS + kWarps + 1) * 8 <= kSmem, "the division's sums fit");
 };
@@ -83,7 +90,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     const int kv = u.kv, head = u.head, row0 = u.row0, rows = u.rows, n = u.n, s0 = u.s0, s1 = u.s1;
     const int2 range = u.range;
     // ---- this lane's two rows: q as the MMA's A, and the keys they see
-    uint32_t qa[KS][4];
+    uint32_t qa[C::kSharedQ ? 1 : KS][4];
     int2 see[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -92,13 +99,25 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       see[i] = attn_range(p, seq, kv, tok);
       const T* q = static_cast<const T*>(p.q) + (int64_t)(seq.first + tok) * p.q_stride +
                    (int64_t)(head * (int)p.group.d + g) * p.D + qc;
+      if constexpr (!C::kSharedQ) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int d = ks * 16 + 8 * j;
-          qa[ks][i + 2 * j] = d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
-        }
+          for (int j = 0; j < 2; ++j) {
+            const int d = ks * 16 + 8 * j;
+            qa[ks][i + 2 * j] = d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
+          }
+      }
+    }
+    if constexpr (C::kSharedQ) {  // (free since the end of the unit before)
+      for (int i = tid; i < AD_ROWS * CH; i += C::kThreads) {
+        const int r = row0 + min(i / CH, rows - 1), c = i % CH, tok = (int)p.group.div(r), g = r - tok * (int)p.group.d;
+        const T* q = static_cast<const T*>(p.q) + (int64_t)(seq.first + tok) * p.q_stride +
+                     (int64_t)(head * (int)p.group.d + g) * p.D + c * 8;
+        *reinterpret_cast<uint4*>(sm + C::kRings + (i / CH) * (DP * 2) + ((c ^ ((i / CH) & 7)) << 4)) =
+            c * 8 < p.D ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncthreads();
     }
     // keys that every row of the tile sees
     const int all_lo = attn_range(p, seq, kv, (int)p.group.div(row0 + rows - 1)).x;
@@ -114,20 +133,28 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       const int key = base + s * C::S + (lane & 15);
       return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
     };
-    auto issue = [&](int s, int page, int stage) {
+    // Loads in order: of slice s0 + i for the i-th, or k, v, k, v ..
+    int64_t off = -1;  // of this lane's key, in the slice whose k was issued last
+    int page = page_of(s0), issued = 0, fill = 0;
+    auto issue = [&] {
+      const int s = C::kParts == 2 ? s0 + issued : s0 + issued / 2;
       if (s < s1) {
-        const int key = base + s * C::S + (lane & 15);
-        int64_t off = -1;
-        if (page != -2) {
-          if ((uint32_t)page < (uint32_t)p.map.num_pages) {
-            off = page * p.map.page_stride +
-                  (int64_t)(key - (int)p.map.page.div(key) * (int)p.map.page.d) * p.map.token_stride + head_off;
-          } else {
-            raise_error(p.err, FP4MOE_ERR_PAGE);
+        if (C::kParts == 2 || issued % 2 == 0) {
+          const int key = base + s * C::S + (lane & 15);
+          off = -1;
+          if (page != -2) {
+            if ((uint32_t)page < (uint32_t)p.map.num_pages) {
+              off = page * p.map.page_stride +
+                    (int64_t)(key - (int)p.map.page.div(key) * (int)p.map.page.d) * p.map.token_stride + head_off;
+            } else {
+              raise_error(p.err, FP4MOE_ERR_PAGE);
+            }
           }
+          page = page_of(s + 1);  // a group ahead
         }
+        const T* from = C::kParts == 1 && issued % 2 ? vbase : kbase;
         const int c = lane % CH;
-        const uint32_t dst0 = ring32 + stage * C::kStage;
+        const uint32_t dst0 = ring32 + fill * C::kLoad;
 #pragma unroll
         for (int it = 0; it < AD_KEYS / RPI; ++it) {
           const int r = it * RPI + lane / CH;
@@ -136,29 +163,27 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
           const int64_t src = use ? ro + c * 8 : 0;
           const uint32_t dst = dst0 + r * (DP * 2) + ((c ^ (r & 7)) << 4);
           if (c * 8 < dims) {
-            cp_async16(dst, kbase + src, use);
-            cp_async16(dst + AD_KEYS * DP * 2, vbase + src, use);
+            cp_async16(dst, from + src, use);
+            if (C::kParts == 2) cp_async16(dst + C::kTile, vbase + src, use);
           }
         }
       }
       cp_async_commit();
+      ++issued;
+      fill = fill + 1 == C::kLoads ? 0 : fill + 1;
     };
-    int next = page_of(s0);
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-      const int page = next;
-      next = page_of(s0 + i + 1);
-      issue(s0 + i, page, i);
-    }
-    int stage = 0, fill = C::kStages - 1;
+    for (int i = 0; i < C::kLoads - 1; ++i) issue();
+    int stage = 0;
+    auto step = [&] { stage = stage + 1 == C::kLoads ? 0 : stage + 1; };
     for (int s = s0; s < s1; ++s) {
-      const int page = next;
-      next = page_of(s + C::kStages);
-      cp_async_wait<C::kStages - 2>();
+      cp_async_wait<C::kLoads - 2>();
       __syncwarp();
       const int k0 = base + s * C::S;
-      const uint32_t kst = ring32 + stage * C::kStage, vst = kst + AD_KEYS * DP * 2;
-      if (k0 < range.y && k0 + AD_KEYS > range.x) {
+      const bool any = k0 < range.y && k0 + AD_KEYS > range.x;
+      float pr[2][4];
+      const bool edge = k0 < all_lo || k0 + AD_KEYS > all_hi;
+      if (any) {
+        const uint32_t kst = ring32 + stage * C::kLoad;
         float sc[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -166,11 +191,14 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
             uint32_t f[4];
             const int key = (lane >> 4) * 8 + (lane & 7), c = ks * 2 + ((lane >> 3) & 1);
             ldsm4(f, kst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
-            mma16816<T>(sc[0], qa[ks], f[0], f[1]);
-            mma16816<T>(sc[1], qa[ks], f[2], f[3]);
+            if constexpr (C::kSharedQ) {
+              const int r = lane & 15, qc16 = ks * 2 + (lane >> 4);
+              ldsm4(qa[0], smem_u32(sm) + C::kRings + r * (DP * 2) + ((qc16 ^ (r & 7)) << 4));
+            }
+            mma16816<T>(sc[0], qa[C::kSharedQ ? 0 : ks], f[0], f[1]);
+            mma16816<T>(sc[1], qa[C::kSharedQ ? 0 : ks], f[2], f[3]);
           }
         }
-        const bool edge = k0 < all_lo || k0 + AD_KEYS > all_hi;
         if (edge) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
@@ -201,7 +229,6 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
             m[i] = nm[i];
           }
         }
-        float pr[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float mb = safe_max(m[i]) * p.scale_log2;
@@ -213,13 +240,24 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
               l[i] += pr[t][2 * i + e];
             }
         }
+      }
+      if constexpr (C::kParts == 1) {
+        __syncwarp();
+        issue();
+        step();
+        cp_async_wait<C::kLoads - 2>();
+        __syncwarp();
+      }
+      if (any) {
+        const uint8_t* vt = ring + stage * C::kLoad + (C::kParts - 1) * C::kTile;
+        const uint32_t vst = ring32 + stage * C::kLoad + (C::kParts - 1) * C::kTile;
         bool odd = false;  // a v that some rows must not touch even with weight 0
         if (edge && (all_lo != range.x || all_hi != range.y)) {
           for (int it = 0; it < AD_KEYS / RPI; ++it) {
             const int r = it * RPI + lane / CH, c = lane % CH;
             if (c * 8 < dims)
               odd |= any_nonfinite<T>(
-                  *reinterpret_cast<const uint4*>(ring + stage * C::kStage + AD_KEYS * DP * 2 + r * (DP * 2) + ((c ^ (r & 7)) << 4)));
+                  *reinterpret_cast<const uint4*>(vt + r * (DP * 2) + ((c ^ (r & 7)) << 4)));
           }
           odd = __any_sync(0xFFFFFFFFu, odd);
         }
@@ -250,8 +288,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if (t * 8 < dims) {
-                const T* v = reinterpret_cast<const T*>(ring + stage * C::kStage + AD_KEYS * DP * 2 + c * (DP * 2) +
-                                                        ((t ^ (c & 7)) << 4)) + qc;
+                const T* v = reinterpret_cast<const T*>(vt + c * (DP * 2) + ((t ^ (c & 7)) << 4)) + qc;
                 const float v0 = to_f32(v[0]), v1 = to_f32(v[1]);
                 if (in0) {
                   o[t][0] = fmaf(w[0], v0, o[t][0]);
@@ -267,9 +304,8 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
         }
       }
       __syncwarp();
-      issue(s + C::kStages - 1, page, fill);
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
-      fill = fill + 1 == C::kStages ? 0 : fill + 1;
+      issue();
+      step();
     }
     cp_async_wait<0>();
     __syncwarp();

@@ -9,8 +9,8 @@
 //   warp 8, warp 9     MMAs of tile 0 and 1: for each step the P V of the step before and the next Q K^T
 //   warp 10, warp 11   loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
 //                      swizzle atoms: a box is 64 dims of the keys that a page and a step share (gcd(page size, 128)), one
-//                      lane a box. Other page sizes by 16-byte cp.async, a lane looking a key's place up for the lanes that
-//                      copy it.
+//                      lane a box. Other page sizes by gathers of four rows where all slots lie evenly apart, one lane a
+//                      gather, else by 16-byte cp.async, a lane looking a key's place up for the lanes that copy it.
 // The MMAs of a tile come from one thread and run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
 // take the place of S(j). P is made under the maximum of the steps before, so that finding this step's is not in its way;
 // only where that had grown by more than 2^8 is O rescaled and P made again (up to 256, which neither 16-bit type minds).
@@ -67,7 +67,7 @@ struct TileBars {
 // 128 rows x 64 dims where the heads of a group divide 128.
 struct TileMaps {
   CUtensorMap k, v, q;
-  int rows;   // 0: no boxes, by cp.async
+  int rows;   // of a box; 1: four rows at a time, wherever they lie (k and v as [slots][heads and dims]); 0: no boxes, by cp.async
   int q_box;  // whether q has boxes
 };
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
@@ -75,6 +75,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
           dst),
       "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int (&row)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, "
+      "%7}], [%2];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3])
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -253,8 +260,10 @@ struct Loader {
   }
 };
 
+// How k and v are brought: by cp.async, by boxes of a page's keys, or by gathers of four keys a lane.
+enum LoadMode { kCopies = 0, kBoxes = 1, kGathers = 2 };
 // One of the two streams: WHICH = 0 k (and q), 1 v. Stages go round; load n is told on full(n % kStages).
-template <typename T, int DP, bool BOXES, int WHICH>
+template <typename T, int DP, int MODE, int WHICH>
 __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& maps, const AttnRun& run, const TileBars<DP>& bar,
                                           uint8_t* sm, uint32_t sm32, volatile int* odd) {
   using C = TileCfg<DP>;
@@ -265,7 +274,8 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
   const uint32_t tiles = WHICH ? C::kV : C::kK;
   auto full = [&](int s) { return WHICH ? bar.v_full(s) : bar.k_full(s); };
   auto empty = [&](int s) { return WHICH ? bar.v_empty(s) : bar.k_empty(s); };
-  const int per = BOXES ? 128 / maps.rows : 1, boxes = per * (p.D > 64 ? 2 : 1);  // of a step: one lane each
+  constexpr bool BOXES = MODE != kCopies, gather = MODE == kGathers;
+  const int per = !BOXES ? 1 : gather ? 32 : 128 / maps.rows, boxes = per * (p.D > 64 ? 2 : 1);  // of a step: one lane each
   const int box_key = lane % per * maps.rows, box_col = lane / per;
   int stage = 0, units = 0;
   uint32_t phase = 0;
@@ -329,7 +339,10 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
     int page[4];
     auto look_up = [&](int i) {
       const int k0 = first + i * AT_KEYS;
-      if (BOXES) {
+      if constexpr (gather) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) page[h] = L.page_of(u, table, k0 + lane * 4 + h, i < n);
+      } else if constexpr (BOXES) {
         page[0] = L.page_of(u, table, max(k0 + box_key, u.range.x), i < n && lane < boxes && k0 + box_key + maps.rows > u.range.x);
       } else {
 #pragma unroll
@@ -361,7 +374,15 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
       const bool differ = some && (all_lo != u.range.x || all_hi != u.range.y);
       const bool look = !BOXES || (WHICH && (edge || differ));
       const uint32_t tile = sm32 + tiles + stage * C::kTile, b = BOXES && look ? bar.landed() : full(stage);
-      const int box_tok = BOXES ? L.in_page(k0 + box_key) : 0, box_page = BOXES ? L.checked(page[0]) : 0;
+      int box_tok = 0, box_page = 0, slot[4];
+      if constexpr (gather) {  // (a row past the last reads as zeros)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          slot[h] = L.checked(page[h]) * (int)p.map.page.d + (page[h] == -2 ? 0 : L.in_page(k0 + lane * 4 + h));
+      } else if constexpr (BOXES) {
+        box_tok = L.in_page(k0 + box_key);
+        box_page = L.checked(page[0]);
+      }
       if (BOXES && look && !(ok = look_after(false))) break;  // one at a time
       // what is late may be what frees the stage
       if (late.any && !mbar_test(empty(stage), phase ^ 1) && !(ok = look_after(false))) break;
@@ -369,8 +390,12 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
       if (BOXES) {
         if (lane == 0) mbar_arrive_expect_tx(b, (p.D > 64 ? 2 : 1) * C::kBlock);
         __syncwarp();
-        if (lane < boxes)
+        if constexpr (gather) {
+          const int x = u.head * (int)p.map.head_stride;
+          for (int c = 0; c < (p.D > 64 ? 2 : 1); ++c) tma_gather4(tile + c * C::kBlock + lane * 512, map, b, x + c * 64, slot);
+        } else if (lane < boxes) {
           tma_load_4d(tile + box_col * C::kBlock + box_key * 128, map, b, box_col * 64, u.head, box_tok, box_page);
+        }
       } else {
         L.key_rows(u, tile, base, k0, page);
       }
@@ -860,7 +885,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
   }
 }
 
-template <typename T, int DP, bool BOXES>
+template <typename T, int DP, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, const __grid_constant__ TileMaps maps) {
   using C = TileCfg<DP>;
   extern __shared__ uint8_t raw[];
@@ -914,9 +939,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
     mma_role<T, DP>(p, run, bar, sm32, tmem);
   } else if (warp == 9) {
   } else if (warp == 10) {
-    load_role<T, DP, BOXES, 0>(p, maps, run, bar, sm, sm32, odd);
+    load_role<T, DP, MODE, 0>(p, maps, run, bar, sm, sm32, odd);
   } else {
-    load_role<T, DP, BOXES, 1>(p, maps, run, bar, sm, sm32, odd);
+    load_role<T, DP, MODE, 1>(p, maps, run, bar, sm, sm32, odd);
   }
   tc_fence_before();
   __syncthreads();
@@ -924,20 +949,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int DP, bool BOXES>
+template <typename T, int DP, int MODE>
 fp4moe_status attn_tile_run(const AttnParams& p, const TileMaps& maps, int nsm, cudaStream_t st) {
   using C = TileCfg<DP>;
   static PerDevice done;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP4MOE_CUDA_ERROR;
   if (done.get(dev, [] {
-        return cudaFuncSetAttribute(attn_tile_kernel<T, DP, BOXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+        return cudaFuncSetAttribute(attn_tile_kernel<T, DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
                        cudaSuccess
                    ? 1
                    : 0;
       }) <= 0)
     return FP4MOE_CUDA_ERROR;
-  return launch_pdl(attn_tile_kernel<T, DP, BOXES>, dim3((unsigned)nsm), dim3(AT_THREADS), C::kSmem, st, p, maps) == cudaSuccess
+  return launch_pdl(attn_tile_kernel<T, DP, MODE>, dim3((unsigned)nsm), dim3(AT_THREADS), C::kSmem, st, p, maps) == cudaSuccess
              ? FP4MOE_OK
              : FP4MOE_CUDA_ERROR;
 }
@@ -973,10 +998,15 @@ bool encode_boxes(CUtensorMap* m, int32_t dtype, const void* base, int rank, con
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <typename T, int DP>
+fp4moe_status attn_tile_mode(const AttnParams& p, const TileMaps& maps, int nsm, cudaStream_t st) {
+  return maps.rows > 1    ? attn_tile_run<T, DP, kBoxes>(p, maps, nsm, st)
+         : maps.rows == 1 ? attn_tile_run<T, DP, kGathers>(p, maps, nsm, st)
+                          : attn_tile_run<T, DP, kCopies>(p, maps, nsm, st);
+}
 template <typename T>
 fp4moe_status attn_tile_typed(const AttnParams& p, const TileMaps& maps, int nsm, cudaStream_t st) {
-  if (maps.rows) return p.D <= 64 ? attn_tile_run<T, 64, true>(p, maps, nsm, st) : attn_tile_run<T, 128, true>(p, maps, nsm, st);
-  return p.D <= 64 ? attn_tile_run<T, 64, false>(p, maps, nsm, st) : attn_tile_run<T, 128, false>(p, maps, nsm, st);
+  return p.D <= 64 ? attn_tile_mode<T, 64>(p, maps, nsm, st) : attn_tile_mode<T, 128>(p, maps, nsm, st);
 }
 
 }  // namespace
@@ -990,6 +1020,16 @@ fp4moe_status attn_tile_launch(int32_t dtype, const AttnParams& p, int nsm, cuda
   const uint32_t kb[4] = {64, 1, (uint32_t)rows, 1};
   if (rows >= 8 && encode_boxes(&maps.k, dtype, p.k, 4, kd, ks, kb) && encode_boxes(&maps.v, dtype, p.v, 4, kd, ks, kb))
     maps.rows = rows;
+  if (maps.rows == 0) {  // a token's heads as one row, where the slots lie evenly
+    const int64_t slots = (int64_t)p.map.num_pages * p.map.page.d, width = (p.kv_heads - 1) * p.map.head_stride + p.D;
+    const int64_t apart = p.map.page.d == 1 ? p.map.page_stride : p.map.token_stride;
+    const bool even = p.map.page.d == 1 || p.map.num_pages == 1 || p.map.page_stride == p.map.page.d * p.map.token_stride;
+    const int64_t gd[2] = {width, slots}, gs[1] = {apart};
+    const uint32_t gb[2] = {64, 1};
+    if (even && width <= INT32_MAX && encode_boxes(&maps.k, dtype, p.k, 2, gd, gs, gb) &&
+        encode_boxes(&maps.v, dtype, p.v, 2, gd, gs, gb))
+      maps.rows = 1;
+  }
   if (128 % p.group.d == 0) {
     const int64_t qd[3] = {p.D, p.q_heads, p.T}, qs[2] = {p.D, p.q_stride};
     const uint32_t qb[3] = {64, p.group.d, 128 / p.group.d};
