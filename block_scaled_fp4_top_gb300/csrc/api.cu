@@ -838,6 +838,7 @@ fp4moe_status fp4moe_mx_gemm(int32_t format, int32_t dtype, int32_t M, int32_t N
 // ------------------------------------------------- the paged key-value cache
 namespace {
 constexpr int32_t kMaxHeads = 65535;  // grid rows
+constexpr int32_t kMaxKeys = INT32_MAX - 1023;  // of a sequence: key indices are 32-bit, and kernels step past the last by a tile
 fp4moe_status check_kv_pages(int32_t page_size, int32_t num_pages) {
   if (page_size < 1 || num_pages < 1 || (int64_t)page_size * num_pages > INT32_MAX) return FP4MOE_INVALID_ARG;
   return FP4MOE_OK;
@@ -918,7 +919,8 @@ fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k
                                      int64_t out_stride, float* lse, void* ws, uint32_t* err, fp4moe_stream_t stream) {
   FP4_TRY(check_attention(cache, num_seqs, T, q_heads));
   if (table_columns < 0 || window < 0) return FP4MOE_INVALID_ARG;
-  if (!(scale > 0.0f) || std::isinf(scale) || (window > 0 && !causal)) return FP4MOE_INVALID_ARG;
+  if (!(scale > 0.0f) || std::isinf(scale * 1.5f) || (window > 0 && !causal)) return FP4MOE_INVALID_ARG;
+  if ((int64_t)table_columns * cache->page_size > kMaxKeys) return FP4MOE_UNSUPPORTED;
   const int64_t width = (int64_t)q_heads * cache->head_dim;
   if (!row_stride_ok(T, q_stride, width) || !row_stride_ok(T, out_stride, width)) return FP4MOE_INVALID_ARG;
   if (T == 0 || num_seqs == 0) return FP4MOE_OK;

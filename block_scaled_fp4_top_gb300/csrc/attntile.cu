@@ -24,6 +24,7 @@ namespace fp4moe {
 namespace {
 
 constexpr int AT_BM = 256, AT_KEYS = 128;
+constexpr int AT_ODD = 8;          // units whose flags are kept: loads run ahead by a unit for each stage at most
 constexpr int AT_FEW = 32;         // rows of a tile whose parts are joined a few lanes a row
 constexpr int AT_MIN = 4;          // least cost of a CTA's run
 constexpr int AT_OH = 4;           // what a unit costs, in steps, beside its steps
@@ -41,6 +42,7 @@ struct TileCfg {
   static constexpr int kOut = kBars + 512;            // the softmax warps' output, 32 rows x 32 dims each
   static constexpr int kSmem = kOut + 8 * 2048 + 1024;  // and to align it
   static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(AT_ODD > kStages + 1, "a unit's flag is read before it is another's");
   static_assert((FP4MOE_KV_MAX_SEQS + AT_THREADS / 32 + 1) * 8 <= kBars, "the division's sums fit");
 };
 
@@ -327,7 +329,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
           look(late.lo, late.hi);
         }
       }
-      if (bad) odd[(late.mark - 1) % 3] = late.mark;
+      if (bad) odd[(late.mark - 1) % AT_ODD] = late.mark;
     }
     L.told(full(late.stage));
     return true;
@@ -664,7 +666,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     if (!ok || !(ok = warp_wait(bar.o_full(t), op, p.err))) break;
     op ^= 1;
     tc_fence_after();
-    if (!idle && odd[units % 3] == units + 1) {
+    if (!idle && odd[units % AT_ODD] == units + 1) {
       const int k0 = (u.range.x / AT_KEYS + u.s0) * AT_KEYS, k1 = (u.range.x / AT_KEYS + u.s1) * AT_KEYS;
       for (int d = 0; d < dims; d += 32) {
         float o[32];
@@ -890,7 +892,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   using C = TileCfg<DP>;
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t tmem_at, arrived[2], skip;
-  __shared__ int odd[3];
+  __shared__ int odd[AT_ODD];  // [unit % AT_ODD]: unit + 1 if a v that only some of its rows see is not finite
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const uint32_t sm32 = smem_u32(sm);
   const TileBars<DP> bar{sm32 + C::kBars};
@@ -913,7 +915,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
     }
     mbar_init(bar.landed(), 1);
     fence_mbar_init();
-    odd[0] = odd[1] = odd[2] = 0;
+    for (int i = 0; i < AT_ODD; ++i) odd[i] = 0;
   }
   if (threadIdx.x == 32) {
     for (const CUtensorMap* m : {&maps.k, &maps.v, &maps.q})

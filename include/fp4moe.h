@@ -720,8 +720,10 @@ fp4moe_status fp4moe_rope_cache(const fp4moe_kv_cache* cache, int32_t T, int32_t
  *   s_j = scale * q . k_j; out = RN(sum e^(s_j - m) v_j / sum e^(s_j - m)), m = max s
  *   lse = m + ln(sum e^(s_j - m)) in fp32
  * A row that sees no key gets out = 0 and lse = -infinity. Keys that a row does not
- * see do not reach it, whatever they hold. Sums and statistics are fp32; e^(s - m)
- * is rounded to the cache's type in front of the product with v.
+ * see do not reach it, whatever they hold; infinities and NaN in those that it sees
+ * do, as the formulas have it (a row whose scores are all -infinity is NaN). Sums
+ * and statistics are fp32; e^(s - m) is rounded to the cache's type in front of the
+ * product with v.
  *   q, out [T][q_heads][head_dim] of the cache's type, rows q_stride and
  *     out_stride elements apart (multiples of 8, at least a row long where T > 1);
  *     out must not overlap q. lse [T][q_heads] fp32 or NULL.
@@ -730,10 +732,12 @@ fp4moe_status fp4moe_rope_cache(const fp4moe_kv_cache* cache, int32_t T, int32_t
  *   page_table [num_seqs][table_columns], kv_len [num_seqs], q_offset
  *     [num_seqs + 1] int32 on the device, as fp4moe_kv_plan writes them. Rows past
  *     q_offset[num_seqs] are left as they were.
- *   scale: finite, > 0. window: >= 0; 0 where causal = 0.
+ *   scale: > 0 and at most 2^127. window: >= 0; 0 where causal = 0. table_columns *
+ *     page_size at most 2^31 - 1024 (else FP4MOE_UNSUPPORTED).
  *   ws: FP4MOE_ATTENTION_WORKSPACE_BYTES of device memory, zeroed once before
- *     first use; a call leaves its counters at zero again. Calls (and graphs) that
- *     share one must be ordered.
+ *     first use; a call leaves its counters at zero again (after a
+ *     FP4MOE_ERR_TIMEOUT zero it anew). Calls (and graphs) that share one must be
+ *     ordered.
  * Offsets out of order or past T count as the nearest in range. Of a length that is
  * negative or longer than the table's columns, only keys that have a column count,
  * and a page outside [0, num_pages) reads as zeros: all with FP4MOE_ERR_PAGE in

@@ -533,6 +533,23 @@ def test_tiles_keep_hidden_keys_out(D, page, new, bad):
             compare(out[:, clean], lse[:, clean], [t[:, clean] for t in want], kv, D, "bfloat16")
 
 
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 5), (128, 16)])
+def test_tiles_keep_hidden_keys_out_of_many_short_sequences(D, page):
+    """Units of one step each, so that loads run several units ahead of the rows that are made again."""
+    import torch
+    B, n, H, Hk = 300, 40, 16, 8
+    new = kv = [n] * B
+    q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D, page=page)
+    for b in range(B):
+        s = int(slots[b][20 + b % 19])
+        vc[s // page, s % page, b % Hk, 5] = (float("nan"), float("inf"))[b % 2]
+    flat = [c.reshape(-1, Hk, D) for c in (kc, vc)]
+    first = [n * b for b in range(B + 1)]
+    out, lse = run_attention(q, kc, vc, table, kv, first, D ** -0.5, True, 0)
+    want = ref.attention(q, *flat, slots, first[:-1], new, kv, D ** -0.5, True, 0)
+    compare(out, lse, want, [n], D, "bfloat16")
+
+
 @pytest.mark.parametrize("page", [16, 7])
 def test_tiles_pages_out_of_the_cache(page):
     check_attention([100, 30, 2], [300, 60, 40], 16, 8, 64, page=page, hole=[(0, 2), (1, 0), (2, 1)], tile=256)

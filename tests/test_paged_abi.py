@@ -100,7 +100,8 @@ def test_attention_refusals(lib):
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=0, window=3), dict(qs=380),
                 dict(qs=376), dict(os=376), dict(os=2 ** 40), dict(out=P)):
         assert f(**bad) == _lib.INVALID_ARG, bad
-    assert f(B=8193) == _lib.UNSUPPORTED
+    assert f(scale=3.4e38) == _lib.INVALID_ARG
+    assert f(B=8193) == _lib.UNSUPPORTED and f(columns=2 ** 27 - 63) == _lib.UNSUPPORTED
     for n in ptrs:
         assert f(**{n: None}) == _lib.INVALID_ARG, n
         assert f(**{n: BAD}) == _lib.MISALIGNED, n
