@@ -89,6 +89,14 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     const AttnSeq& seq = u.seq;
     const int kv = u.kv, head = u.head, row0 = u.row0, rows = u.rows, n = u.n, s0 = u.s0, s1 = u.s1;
     const int2 range = u.range;
+    const int base = range.x / C::S * C::S + warp * AD_KEYS;  // first key of this warp's group of slice 0
+    const int32_t* table = p.table + (int64_t)u.b * p.columns;
+    const int64_t head_off = (int64_t)head * p.map.head_stride;
+    auto page_of = [&](int s) {  // page of the key that this lane looks up in slice s; -2: none
+      const int key = base + s * C::S + (lane & 15);
+      return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
+    };
+    int page = page_of(s0);  // on its way while q is fetched
     // ---- this lane's two rows: q as the MMA's A, and the keys they see
     uint32_t qa[C::kSharedQ ? 1 : KS][4];
     int2 see[2];
@@ -126,16 +134,9 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-    const int base = range.x / C::S * C::S + warp * AD_KEYS;  // first key of this warp's group of slice 0
-    const int32_t* table = p.table + (int64_t)u.b * p.columns;
-    const int64_t head_off = (int64_t)head * p.map.head_stride;
-    auto page_of = [&](int s) {  // page of the key that this lane looks up in slice s; -2: none
-      const int key = base + s * C::S + (lane & 15);
-      return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
-    };
     // Loads in order: of slice s0 + i for the i-th, or k, v, k, v ..
     int64_t off = -1;  // of this lane's key, in the slice whose k was issued last
-    int page = page_of(s0), issued = 0, fill = 0;
+    int issued = 0, fill = 0;
     auto issue = [&] {
       const int s = C::kParts == 2 ? s0 + issued : s0 + issued / 2;
       if (s < s1) {
@@ -358,14 +359,16 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
         for (int j = 0; j < NJ; ++j)
           __stcg(reinterpret_cast<float4*>(sums + (slot * AD_ROWS + r) * DP + dv + j * 4 * TPR), acc[j]);
       }
-      __threadfence();
       __syncthreads();
-      uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0;
-      if (tid == 0) arrived = atomicAdd(count, 1u);
+      if (tid == 0) {  // its fences stand for the CTA's writes before the barrier, and for its reads after the next
+        uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0;
+        __threadfence();
+        arrived = atomicAdd(count, 1u);
+        __threadfence();
+        if (arrived == (uint32_t)(c1 - c0)) *count = 0;
+      }
       __syncthreads();
       if (arrived == (uint32_t)(c1 - c0)) {  // the last: adds all parts in order
-        __threadfence();
-        if (tid == 0) *count = 0;
         whole = true;
         M = -INFINITY;
         L = 0.0f;

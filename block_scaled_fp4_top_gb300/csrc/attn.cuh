@@ -102,107 +102,130 @@ __device__ __forceinline__ int attn_owner(const AttnRun& r, int64_t x) {
   return c;
 }
 
+// a / b of non-negative values, which mostly fit 32 bits.
+__device__ __forceinline__ int64_t attn_div(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Cost of sequence b, by all lanes of a warp, each with a sequence of its own (or none: b >= B); short sequences by their
+// lane, those of several tiles by the warp. bad: whether a length is out of range.
+template <int BM, int S, int OH>
+__device__ __forceinline__ int64_t attn_cost(const AttnParams& p, int b, uint32_t& bad) {
+  const int lane = lane_id();
+  int64_t w = 0;
+  int big = 0, kv = 0;
+  AttnSeq s{};
+  if (b < p.B) {
+    const int q0 = __ldg(p.q_offset + b), q1 = __ldg(p.q_offset + b + 1);
+    kv = __ldg(p.kv_len + b);
+    s = attn_seq(p, q0, q1, kv);
+    if (s.keys != kv && s.rows > 0) bad = 1;
+    if (s.rows > BM) big = 1;
+    else if (s.rows > 0) w = (int64_t)(OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, 0))) * p.kv_heads;
+  }
+  for (uint32_t m = __ballot_sync(0xFFFFFFFFu, big); m; m &= m - 1) {
+    const int src = __ffs(m) - 1;
+    AttnSeq o;
+    o.first = __shfl_sync(0xFFFFFFFFu, s.first, src);
+    o.rows = __shfl_sync(0xFFFFFFFFu, s.rows, src);
+    o.keys = __shfl_sync(0xFFFFFFFFu, s.keys, src);
+    o.tokens = __shfl_sync(0xFFFFFFFFu, s.tokens, src);
+    const int okv = __shfl_sync(0xFFFFFFFFu, kv, src);
+    int64_t sum = 0;
+    for (int t = lane; t < (o.rows + BM - 1) / BM; t += 32) sum += OH + attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == src) w = sum * p.kv_heads;
+  }
+  return w;
+}
+__device__ __forceinline__ int64_t attn_warp_sum(int64_t x) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if ((int)lane_id() >= o) x += y;
+  }
+  return x;
+}
+
 // All threads of the CTA call this. sums: (B + THREADS / 32 + 2) * 8 bytes of shared memory, free again afterwards.
 template <int BM, int S, int OH, int MIN, int THREADS>
 __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int WARPS = THREADS / 32;
-  int64_t* part = sums;         // [WARPS + 1]
+  int64_t* part = sums;              // [WARPS + 1]
   int64_t* upto = sums + WARPS + 1;  // [B] costs of the sequences up to and with b
-  const int per = (p.B + THREADS - 1) / THREADS;
   uint32_t bad = 0;
-  // short sequences by their thread, those of several tiles by a warp
-  for (int i = 0; i < per; ++i) {
-    const int b = i * THREADS + tid;
-    int64_t w = 0;
-    int big = 0;
-    AttnSeq s{};
-    int kv = 0;
-    if (b < p.B) {
-      const int q0 = __ldg(p.q_offset + b), q1 = __ldg(p.q_offset + b + 1);
-      kv = __ldg(p.kv_len + b);
-      s = attn_seq(p, q0, q1, kv);
-      if (s.keys != kv && s.rows > 0) bad = 1;
-      if (s.rows > BM) big = 1;
-      else if (s.rows > 0) w = (int64_t)(OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, 0))) * p.kv_heads;
+  const bool few = p.B <= 32;  // every warp for itself: no shared memory, and no barrier but the last
+  int64_t before = 0, total = 0, mine = 0;
+  if (few) {
+    mine = attn_warp_sum(attn_cost<BM, S, OH>(p, lane, bad));
+    total = __shfl_sync(0xFFFFFFFFu, mine, 31);
+  } else {
+    const int per = (p.B + THREADS - 1) / THREADS;
+    for (int i = 0; i < per; ++i) {
+      const int b = i * THREADS + tid;
+      const int64_t w = attn_cost<BM, S, OH>(p, b, bad);
+      if (b < p.B) upto[b] = w;
     }
-    for (uint32_t m = __ballot_sync(0xFFFFFFFFu, big); m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      AttnSeq o;
-      o.first = __shfl_sync(0xFFFFFFFFu, s.first, src);
-      o.rows = __shfl_sync(0xFFFFFFFFu, s.rows, src);
-      o.keys = __shfl_sync(0xFFFFFFFFu, s.keys, src);
-      o.tokens = __shfl_sync(0xFFFFFFFFu, s.tokens, src);
-      const int okv = __shfl_sync(0xFFFFFFFFu, kv, src);
-      int64_t sum = 0;
-      for (int t = lane; t < (o.rows + BM - 1) / BM; t += 32) sum += OH + attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      if (lane == src) w = sum * p.kv_heads;
+    __syncthreads();
+    // running sum: a thread's stretch of sequences, then the threads
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    for (int b = b0; b < b1; ++b) mine += upto[b];
+    const int64_t x = attn_warp_sum(mine);
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    before = x - mine;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += part[w];
+      total += part[w];
     }
-    if (b < p.B) upto[b] = w;
+    for (int b = b0; b < b1; ++b) {
+      before += upto[b];
+      upto[b] = before;
+    }
+    __syncthreads();
   }
   if (bad) raise_error(p.err, FP4MOE_ERR_PAGE);
-  __syncthreads();
-  // running sum: a thread's stretch of sequences, then the threads
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += upto[b];
-  int64_t x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  int64_t before = x - mine, total = 0;
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += part[w];
-    total += part[w];
-  }
-  for (int b = b0; b < b1; ++b) {
-    before += upto[b];
-    upto[b] = before;
-  }
-  __syncthreads();
   AttnRun r;
   r.total = total;
-  r.ctas = (int)max((int64_t)1, min(total / MIN, (int64_t)gridDim.x));
-  r.each = total / r.ctas;
+  r.ctas = (int)max((int64_t)1, min(attn_div(total, MIN), (int64_t)gridDim.x));
+  r.each = attn_div(total, r.ctas);
   r.rest = (int)(total - r.each * r.ctas);
   r.begin = (int)blockIdx.x < r.ctas ? attn_begin(r, blockIdx.x) : 0;
   r.end = (int)blockIdx.x < r.ctas ? attn_begin(r, blockIdx.x + 1) : 0;
   r.seq = r.tile = r.head = r.at = 0;
   if (r.begin < r.end) {
-    int lo = 0, hi = p.B - 1;  // first sequence with upto > begin
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (upto[mid] > r.begin) hi = mid;
-      else lo = mid + 1;
+    int64_t left;
+    if (few) {
+      r.seq = __ffs(__ballot_sync(0xFFFFFFFFu, mine > r.begin)) - 1;
+      const int64_t y = __shfl_sync(0xFFFFFFFFu, mine, max(r.seq - 1, 0));
+      left = r.begin - (r.seq ? y : 0);
+    } else {
+      int lo = 0, hi = p.B - 1;  // first sequence with upto > begin
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (upto[mid] > r.begin) hi = mid;
+        else lo = mid + 1;
+      }
+      r.seq = lo;
+      left = r.begin - (lo ? upto[lo - 1] : 0);
     }
-    r.seq = lo;
-    int64_t left = r.begin - (lo ? upto[lo - 1] : 0);
-    const int kv = __ldg(p.kv_len + lo);
-    const AttnSeq s = attn_seq(p, __ldg(p.q_offset + lo), __ldg(p.q_offset + lo + 1), kv);
+    const int kv = __ldg(p.kv_len + r.seq);
+    const AttnSeq s = attn_seq(p, __ldg(p.q_offset + r.seq), __ldg(p.q_offset + r.seq + 1), kv);
     const int tiles = (s.rows + BM - 1) / BM;
     for (int t0 = 0; t0 < tiles; t0 += 32) {  // every warp for itself
       const int t = t0 + lane;
-      const int64_t w = t < tiles ? (int64_t)(OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, t))) * p.kv_heads : 0;
-      int64_t y = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t z = __shfl_up_sync(0xFFFFFFFFu, y, o);
-        if (lane >= o) y += z;
-      }
+      const int n = t < tiles ? OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, t)) : 0;
+      const int64_t w = (int64_t)n * p.kv_heads, y = attn_warp_sum(w);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, t < tiles && y > left);
       if (hit) {
         const int src = __ffs(hit) - 1;
         r.tile = t0 + src;
         left -= __shfl_sync(0xFFFFFFFFu, y - w, src);
-        const int n = (int)(__shfl_sync(0xFFFFFFFFu, w, src) / p.kv_heads);
-        r.head = (int)(left / n);
-        r.at = (int)(left - (int64_t)r.head * n);
+        const int cost = __shfl_sync(0xFFFFFFFFu, n, src);
+        r.head = (int)attn_div(left, cost);
+        r.at = (int)(left - (int64_t)r.head * cost);
         break;
       }
       left -= __shfl_sync(0xFFFFFFFFu, y, 31);

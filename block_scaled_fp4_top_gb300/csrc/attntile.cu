@@ -739,7 +739,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       uint32_t* count = reinterpret_cast<uint32_t*>(p.ws + kAttnCounters) + 2 * c0 + t;
       const uint32_t others = (uint32_t)(c1 - c0);
       // Where all others have left their parts, this one's need not be written: it is added out of TMEM, in its turn.
-      if (row == 0) arrived[t] = *(volatile uint32_t*)count;
+      if (row == 0) {
+        arrived[t] = *(volatile uint32_t*)count;
+        __threadfence();
+      }
       if (!meet()) break;
       bool last_one = arrived[t] == others;
       const bool kept = last_one && !few;
@@ -773,16 +776,18 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
             }
           }
         }
-        __threadfence();
         if (!meet()) break;
         if (!last_one) {
-          if (row == 0) arrived[t] = atomicAdd(count, 1u);
+          if (row == 0) {  // its fences stand for the tile's writes before this, and for its reads after the next meeting
+            __threadfence();
+            arrived[t] = atomicAdd(count, 1u);
+            __threadfence();
+          }
           if (!meet()) break;
           last_one = arrived[t] == others;
         }
       }
       if (last_one) {  // adds all parts in order
-        __threadfence();
         if (row == 0) *count = 0;
         // Few: a warp takes four rows at a time, eight lanes a row; a lane four dims of every 32, and the weight of every eighth
         // part.
