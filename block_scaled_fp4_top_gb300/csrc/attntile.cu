@@ -9,8 +9,8 @@
 //   warp 8, warp 9     MMAs of tile 0 and 1: for each step the P V of the step before and the next Q K^T
 //   warp 10, warp 11   loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
 //                      swizzle atoms: a box is 64 dims of the keys that a page and a step share (gcd(page size, 128)), one
-//                      lane a box. Other page sizes by gathers of four rows where all slots lie evenly apart, one lane a
-//                      gather, else by 16-byte cp.async, a lane looking a key's place up for the lanes that copy it.
+//                      lane a box. Other page sizes by gathers of four rows where all slots lie evenly apart and heads
+//                      are whole MMA steps, one lane a gather, else by 16-byte cp.async, a lane looking a key's place up for the lanes that copy it.
 // The MMAs of a tile come from one thread and run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
 // take the place of S(j). P is made under the maximum of the steps before, so that finding this step's is not in its way;
 // only where that had grown by more than 2^8 is O rescaled and P made again (up to 256, which neither 16-bit type minds).
@@ -320,7 +320,8 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
           from = max(from - late.k0, 0) * PER;
           to = min(to - late.k0, 128) * PER;
 #pragma unroll 4
-          for (int i = from + lane; i < to; i += 32) bad |= any_nonfinite<T>(*piece(i));
+          for (int i = from + lane; i < to; i += 32)
+            if (i % PER * 8 < p.D) bad |= any_nonfinite<T>(*piece(i));  // (past the head's dims lies anything)
         };
         if (late.all_lo < late.all_hi) {
           look(late.lo, late.all_lo);
@@ -379,8 +380,10 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
       int box_tok = 0, box_page = 0, slot[4];
       if constexpr (gather) {  // (a row past the last reads as zeros)
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          slot[h] = L.checked(page[h]) * (int)p.map.page.d + (page[h] == -2 ? 0 : L.in_page(k0 + lane * 4 + h));
+        for (int h = 0; h < 4; ++h) {
+          const int pg = L.checked(page[h]);
+          slot[h] = pg * (int)p.map.page.d + (pg == p.map.num_pages ? 0 : L.in_page(k0 + lane * 4 + h));
+        }
       } else if constexpr (BOXES) {
         box_tok = L.in_page(k0 + box_key);
         box_page = L.checked(page[0]);
@@ -1027,7 +1030,9 @@ fp4moe_status attn_tile_launch(int32_t dtype, const AttnParams& p, int nsm, cuda
   const uint32_t kb[4] = {64, 1, (uint32_t)rows, 1};
   if (rows >= 8 && encode_boxes(&maps.k, dtype, p.k, 4, kd, ks, kb) && encode_boxes(&maps.v, dtype, p.v, 4, kd, ks, kb))
     maps.rows = rows;
-  if (maps.rows == 0) {  // a token's heads as one row, where the slots lie evenly
+  // A token's heads as one row, where the slots lie evenly and an MMA step's dims are all of one head: what lies behind a
+  // head is brought with it, and 0 (q's) times that may be NaN.
+  if (maps.rows == 0 && p.D % 16 == 0) {
     const int64_t slots = (int64_t)p.map.num_pages * p.map.page.d, width = (p.kv_heads - 1) * p.map.head_stride + p.D;
     const int64_t apart = p.map.page.d == 1 ? p.map.page_stride : p.map.token_stride;
     const bool even = p.map.page.d == 1 || p.map.num_pages == 1 || p.map.page_stride == p.map.page.d * p.map.token_stride;

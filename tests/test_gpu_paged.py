@@ -683,3 +683,53 @@ def test_attention_offsets_past_32_bits(new):
     out, lse = run_attention(q, kc, vc, table, kv, first, D ** -0.5, True, 0)
     want = ref.attention(q, kc.view(-1, Hk, D), vc.view(-1, Hk, D), slots, first, new, kv, D ** -0.5, True, 0)
     compare(out, lse, want, kv, D, "bfloat16")
+
+
+def in_gaps(c, order, filler):
+    """The same cache with `filler` between its heads."""
+    import torch
+    wide = torch.full((*c.shape[:3], c.shape[3] + 8), filler, device="cuda", dtype=c.dtype)
+    if order == "heads":
+        wide = torch.full((c.shape[0], c.shape[2], c.shape[1], c.shape[3] + 8), filler, device="cuda", dtype=c.dtype).transpose(1, 2)
+    wide[..., :c.shape[3]] = c
+    return wide[..., :c.shape[3]]
+
+
+@pytest.mark.parametrize("D", [8, 24, 64, 72, 80, 120])
+@pytest.mark.parametrize("page", [1, 5, 16])
+@pytest.mark.parametrize("order", ["tokens", "heads"])
+@pytest.mark.parametrize("new", [[1, 1], [140, 31]])
+def test_attention_of_heads_apart(D, page, order, new):
+    """What lies between a cache's heads is no part of any: NaN there reach no result. Nor does one head's reach another's."""
+    import torch
+    H, Hk, kv = 16, 8, [300, 140]
+    q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D, page=page, order=order)
+    first = [0, new[0], sum(new)]
+    want = ref.attention(q, *flat, slots, first, new, kv, D ** -0.5, True, 0)
+    kc, vc = (in_gaps(c, order, float("nan")) for c in (kc, vc))
+    out, lse = run_attention(q, kc, vc, table, kv, first, D ** -0.5, True, 0)
+    compare(out, lse, want, kv, D, "bfloat16")
+    kc[:, :, 3] = float("nan")
+    out, lse = run_attention(q, kc, vc, table, kv, first, D ** -0.5, True, 0)
+    clean = [h for h in range(H) if h // 2 != 3]
+    compare(out[:, clean], lse[:, clean], [t[:, clean] for t in want], kv, D, "bfloat16")
+
+
+@pytest.mark.parametrize("D", [48, 80])
+@pytest.mark.parametrize("page,order", [(16, "tokens"), (5, "tokens"), (5, "heads")])
+def test_attention_after_another_call(D, page, order):
+    """A call's bits do not depend on what the one before it, of values that are not finite, left behind."""
+    import torch
+    new, kv, H, Hk = [140, 31], [300, 140], 16, 8
+    case = attention_case(new, kv, H, Hk, D, page=page, order=order)
+    other = attention_case(new, kv, H, Hk, 64 if D < 64 else 128, page=page, order=order)
+    got = []
+    for left in (0.0, float("nan")):
+        q, kc, vc, flat, table, slots = other
+        vc[:] = left
+        run_attention(q, kc, vc, table, kv, [0, 140, 171], 0.1, True, 0)
+        q, kc, vc, flat, table, slots = case
+        got.append(run_attention(q, kc, vc, table, kv, [0, 140, 171], D ** -0.5, True, 0)[0])
+    want = ref.attention(case[0], *case[3], case[5], [0, 140], new, kv, D ** -0.5, True, 0)
+    compare(got[0], None, want, kv, D, "bfloat16")
+    assert torch.equal(got[0].view(torch.int16), got[1].view(torch.int16))
