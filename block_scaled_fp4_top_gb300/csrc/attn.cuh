@@ -68,10 +68,15 @@ __device__ __forceinline__ int2 attn_range(const AttnParams& p, const AttnSeq& s
   lo = lo < 0 ? 0 : lo > hi ? hi : lo;
   return make_int2((int)lo, (int)hi);
 }
+// Tiles of a sequence. (rows may be 2^31 - 1: no sum here passes it)
+template <int BM>
+__device__ __forceinline__ int attn_tiles(int rows) {
+  return rows / BM + (rows % BM != 0);
+}
 // Keys that any row of tile `i` sees; a superset with the same ends.
 template <int BM>
 __device__ __forceinline__ int2 attn_tile_range(const AttnParams& p, const AttnSeq& s, int kv, int i) {
-  const int r0 = i * BM, r1 = min(r0 + BM, s.rows) - 1;
+  const int r0 = i * BM, r1 = r0 + min(BM, s.rows - r0) - 1;
   const int lo = attn_range(p, s, kv, (int)p.group.div(r0)).x, hi = attn_range(p, s, kv, (int)p.group.div(r1)).y;
   return make_int2(min(lo, hi), hi);
 }
@@ -132,7 +137,7 @@ __device__ __forceinline__ int64_t attn_cost(const AttnParams& p, int b, uint32_
     o.tokens = __shfl_sync(0xFFFFFFFFu, s.tokens, src);
     const int okv = __shfl_sync(0xFFFFFFFFu, kv, src);
     int64_t sum = 0;
-    for (int t = lane; t < (o.rows + BM - 1) / BM; t += 32) sum += OH + attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
+    for (int t = lane; t < attn_tiles<BM>(o.rows); t += 32) sum += OH + attn_slices<S>(attn_tile_range<BM>(p, o, okv, t));
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     if (lane == src) w = sum * p.kv_heads;
@@ -213,7 +218,7 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
     }
     const int kv = __ldg(p.kv_len + r.seq);
     const AttnSeq s = attn_seq(p, __ldg(p.q_offset + r.seq), __ldg(p.q_offset + r.seq + 1), kv);
-    const int tiles = (s.rows + BM - 1) / BM;
+    const int tiles = attn_tiles<BM>(s.rows);
     for (int t0 = 0; t0 < tiles; t0 += 32) {  // every warp for itself
       const int t = t0 + lane;
       const int n = t < tiles ? OH + attn_slices<S>(attn_tile_range<BM>(p, s, kv, t)) : 0;
@@ -262,7 +267,7 @@ struct AttnWalk {
       }
       u.kv = kv;
       u.seq = seq;
-      if (tile * BM >= u.seq.rows) {
+      if (tile >= attn_tiles<BM>(seq.rows)) {
         ++b;
         tile = head = at = 0;
         continue;

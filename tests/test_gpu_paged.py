@@ -733,3 +733,22 @@ def test_attention_after_another_call(D, page, order):
     want = ref.attention(case[0], *case[3], case[5], [0, 140], new, kv, D ** -0.5, True, 0)
     compare(got[0], None, want, kv, D, "bfloat16")
     assert torch.equal(got[0].view(torch.int16), got[1].view(torch.int16))
+
+
+def test_attention_of_as_many_rows_as_32_bits_count():
+    """One sequence of nearly 2^31 rows, of which the last ten see keys."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    T, D, L = 2 ** 31 - 64, 8, 10
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("100 GB of memory")
+    q, kc, vc, flat, table, slots = attention_case([L], [L], 1, 1, D)
+    big = torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    big[T - L:] = q
+    out = torch.full_like(big, 9.0)
+    ws, err = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda"), ints([0])
+    api.fp4moe_paged_attention(big, kc, vc, table, ints([L]), ints([0, T]), D ** -0.5, out, None, ws, err)
+    torch.cuda.synchronize()
+    want = ref.attention(q, *flat, slots, [0], [L], [L], D ** -0.5, True, 0)
+    compare(out[T - L:], None, want, [L], D, "bfloat16")
+    assert not any(c.any() for c in out[:T - L].view(-1).split(2 ** 30)) and err.tolist() == [0]
