@@ -571,7 +571,7 @@ def fp4moe_rope_cache(q, k, v, position, slot, inv_freq, q_out, k_cache, v_cache
 
 
 def fp4moe_paged_attention_plan(num_seqs: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
-    """Rows of a tile (16 or 256) of the kernel that fp4moe_paged_attention takes for these sizes (host arithmetic)."""
+    """Rows of a tile (16, 32 or 256) of the kernel that fp4moe_paged_attention takes for these sizes (host arithmetic)."""
     v = ctypes.c_int32()
     c = _lib.KvCache(_lib.BF16, kv_heads, head_dim, 1, 1, 0, 0, 0)
     _check(_lib.load().fp4moe_paged_attention_plan(c, num_seqs, T, heads, ctypes.byref(v)), "fp4moe_paged_attention_plan")

@@ -1,10 +1,15 @@
 // Attention over the paged cache for few rows a sequence and kv head (fp4moe_paged_attention): decoding, proposed tokens.
 //
 // One pass over the keys: with the running maximum m and sum l of a row, each group of 16 keys adds
-//   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), O' = O 2^(m - m') + sum 2^(s - m') v    (s in powers of two).
+//   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), O' = O 2^(m - m') + sum 2^(s - m') v    (s in powers of two),
+// where m' stays m until a score passes it by more than 2^8, so that the rows' maxima need not be made for every group.
 // The bytes of k and v bound it: 16 rows of a tile cost 64 KFLOP for 8 KB of a group (head_dim 128), far below what
 // mma.sync gives, so the tile's M = 16 is that of mma.sync, and a warp works alone: it brings its own groups of 16 keys by
 // cp.async through a ring of its own, without any barrier between warps, and joins the others at the end of a tile only.
+// 64 sequences of up to 8192 keys, 8 kv heads of 128 dims: 1367 MB in 214 us, 6.4 TB/s, 94 % of a plain copy's rate; four of
+// 131072 keys 321 us, 98 %. One row of 4096 keys is 13 us of latency: the division 2, page and keys 2, the joins 4.
+// Tiles of 32 rows (64 dims) use what is read twice: 16 x 32 rows of up to 8192 keys, 8 kv heads, in 49 us, which tiles of
+// 16 take 58 for and the larger ones 56. There instructions bind it, as more warps show: 16 of them take 52.
 // Any page size and stride: a lane works out its key's place and hands it to the lanes that copy the key's 16-byte
 // pieces; the page of the next group is looked up a group ahead.
 // Keys outside the tile's range are zeros in shared memory. Keys that only some rows of a tile see have score -infinity
@@ -14,12 +19,14 @@
 namespace fp4moe {
 namespace {
 
-constexpr int AD_ROWS = 16, AD_KEYS = 16;  // of a tile, of a warp's group
-constexpr int AD_MIN = 1;                    // least cost of a CTA's run
-constexpr int AD_OH = 1;                     // what a tile costs, in slices, beside its slices
+constexpr int AD_KEYS = 16;  // of a warp's group
+constexpr float AD_GROWTH = 8.0f;  // powers of two that a maximum may lag behind: weights up to 256, which neither 16-bit type minds
+constexpr int AD_MIN = 1;    // least cost of a CTA's run
+constexpr int AD_OH = 1;     // what a tile costs, in slices, beside its slices
 
-template <int DP>
+template <int DP, int RT>  // RT: 16-row MMA tiles of a tile
 struct AttnCfg {
+  static constexpr int kRows = 16 * RT;
   static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int S = AD_KEYS * kWarps;           // keys of a slice: one group a warp
@@ -31,11 +38,11 @@ struct AttnCfg {
   static constexpr int kLoads = 196608 / (kWarps * kLoad);
   static constexpr int kRing = kLoads * kLoad;         // of a warp
   static constexpr int kRings = kWarps * kRing;
-  static constexpr bool kSharedQ = DP == 256;          // its 64 registers a thread are not there
-  static constexpr int kSmem = kRings + (kSharedQ ? AD_ROWS * DP * 2 : 0);
+  static constexpr bool kSharedQ = DP * RT >= 256;     // its 64 registers a thread are not there
+  static constexpr int kSmem = kRings + (kSharedQ ? kRows * DP * 2 : 0);
   static constexpr int kPitch = DP + 8;                // floats between rows of a warp's sums: no bank conflicts
   static_assert(kLoads >= 3, "two loads under way while one is used");
-  static_assert(AD_ROWS * kPitch * 4 <= kRing, "sums fit the ring");
+  static_assert(kRows * kPitch * 4 <= kRing, "sums fit the ring");
   static_assert((FP4MOE_KV_MAX_SEQS + kWarps + 1) * 8 <= kSmem, "the division's sums fit");
 };
 
@@ -64,19 +71,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <typename T, int DP>
-__global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(AttnParams p) {
-  using C = AttnCfg<DP>;
+template <typename T, int DP, int RT>
+__global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel(AttnParams p) {
+  using C = AttnCfg<DP, RT>;
+  constexpr int ROWS = C::kRows, RL = 2 * RT;            // rows of a tile, and of a lane: qr + 8 i
   constexpr int CH = DP / 8, KS = DP / 16, NT = DP / 8;  // 16-byte pieces of a key, MMA steps, output columns of 8
   constexpr int RPI = 32 / CH;                           // keys that one copy instruction of the warp covers
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ float stats[C::kWarps][AD_ROWS][2];
+  __shared__ float stats[C::kWarps][ROWS][2];
   __shared__ uint32_t arrived, skip;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
   if (tid == 0) skip = *(volatile uint32_t*)p.err & kAbortMask;
-  const AttnRun run = attn_plan<AD_ROWS, C::S, AD_OH, AD_MIN, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
+  const AttnRun run = attn_plan<ROWS, C::S, AD_OH, AD_MIN, C::kThreads>(p, reinterpret_cast<int64_t*>(sm));
   if (skip) return;  // an earlier call gave up
   uint8_t* ring = sm + warp * C::kRing;
   const uint32_t ring32 = smem_u32(ring);
@@ -85,7 +93,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   const int dims = (p.D + 15) / 16 * 16;  // MMA steps past the head's own dims are left out
   const int qr = lane >> 2, qc = (lane & 3) * 2;
   AttnWalk walk(run);
-  for (AttnUnit u; walk.next<AD_ROWS, C::S, AD_OH>(p, run, u);) {
+  for (AttnUnit u; walk.next<ROWS, C::S, AD_OH>(p, run, u);) {
     const AttnSeq& seq = u.seq;
     const int kv = u.kv, head = u.head, row0 = u.row0, rows = u.rows, n = u.n, s0 = u.s0, s1 = u.s1;
     const int2 range = u.range;
@@ -97,11 +105,11 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
     };
     int page = page_of(s0);  // on its way while q is fetched
-    // ---- this lane's two rows: q as the MMA's A, and the keys they see
-    uint32_t qa[C::kSharedQ ? 1 : KS][4];
-    int2 see[2];
+    // ---- this lane's rows: q as the MMA's A, and the keys they see
+    uint32_t qa[RT][C::kSharedQ ? 1 : KS][4];
+    int2 see[RL];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RL; ++i) {
       const int r = row0 + min(qr + 8 * i, rows - 1);  // rows past the last are computed with it, and dropped
       const int tok = (int)p.group.div(r), g = r - tok * (int)p.group.d;
       see[i] = attn_range(p, seq, kv, tok);
@@ -113,12 +121,12 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int d = ks * 16 + 8 * j;
-            qa[ks][i + 2 * j] = d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
+            qa[i / 2][ks][i % 2 + 2 * j] = d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
           }
       }
     }
     if constexpr (C::kSharedQ) {  // (free since the end of the unit before)
-      for (int i = tid; i < AD_ROWS * CH; i += C::kThreads) {
+      for (int i = tid; i < ROWS * CH; i += C::kThreads) {
         const int r = row0 + min(i / CH, rows - 1), c = i % CH, tok = (int)p.group.div(r), g = r - tok * (int)p.group.d;
         const T* q = static_cast<const T*>(p.q) + (int64_t)(seq.first + tok) * p.q_stride +
                      (int64_t)(head * (int)p.group.d + g) * p.D + c * 8;
@@ -130,9 +138,12 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     // keys that every row of the tile sees
     const int all_lo = attn_range(p, seq, kv, (int)p.group.div(row0 + rows - 1)).x;
     const int all_hi = attn_range(p, seq, kv, (int)p.group.div(row0)).y;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[NT][4];
+    float m[RL], l[RL], o[RT][NT][4] = {};
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    for (int i = 0; i < RL; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+    }
 
     // Loads in order: of slice s0 + i for the i-th, or k, v, k, v ..
     int64_t off = -1;  // of this lane's key, in the slice whose k was issued last
@@ -181,64 +192,71 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       __syncwarp();
       const int k0 = base + s * C::S;
       const bool any = k0 < range.y && k0 + AD_KEYS > range.x;
-      float pr[2][4];
+      float pr[RT][2][4];
       const bool edge = k0 < all_lo || k0 + AD_KEYS > all_hi;
       if (any) {
         const uint32_t kst = ring32 + stage * C::kLoad;
-        float sc[2][4] = {};
+        float sc[RT][2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           if (ks * 16 < dims) {
             uint32_t f[4];
             const int key = (lane >> 4) * 8 + (lane & 7), c = ks * 2 + ((lane >> 3) & 1);
             ldsm4(f, kst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
-            if constexpr (C::kSharedQ) {
-              const int r = lane & 15, qc16 = ks * 2 + (lane >> 4);
-              ldsm4(qa[0], smem_u32(sm) + C::kRings + r * (DP * 2) + ((qc16 ^ (r & 7)) << 4));
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              if constexpr (C::kSharedQ) {
+                const int r = lane & 15, qc16 = ks * 2 + (lane >> 4);
+                ldsm4(qa[rt][0], smem_u32(sm) + C::kRings + (rt * 16 + r) * (DP * 2) + ((qc16 ^ (r & 7)) << 4));
+              }
+              mma16816<T>(sc[rt][0], qa[rt][C::kSharedQ ? 0 : ks], f[0], f[1]);
+              mma16816<T>(sc[rt][1], qa[rt][C::kSharedQ ? 0 : ks], f[2], f[3]);
             }
-            mma16816<T>(sc[0], qa[C::kSharedQ ? 0 : ks], f[0], f[1]);
-            mma16816<T>(sc[1], qa[C::kSharedQ ? 0 : ks], f[2], f[3]);
           }
         }
         if (edge) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int i = 0; i < RL; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = k0 + t * 8 + qc + (e & 1);
-              if (key < see[e >> 1].x || key >= see[e >> 1].y) sc[t][e] = -INFINITY;
+              const int key = k0 + (e >> 1) * 8 + qc + (e & 1);
+              if (key < see[i].x || key >= see[i].y) sc[i / 2][e >> 1][2 * (i % 2) + (e & 1)] = -INFINITY;
             }
         }
-        float nm[2];
+        float nm[RL];
+        bool grown = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float v = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-          nm[i] = fmaxf(m[i], v);
+        for (int i = 0; i < RL; ++i) {
+          const float(&s4)[2][4] = sc[i / 2];
+          const int a = 2 * (i % 2);
+          nm[i] = fmaxf(fmaxf(s4[0][a], s4[0][a + 1]), fmaxf(s4[1][a], s4[1][a + 1]));  // of this lane's keys
+          grown |= (nm[i] - m[i]) * p.scale_log2 > AD_GROWTH;
         }
-        if (__any_sync(0xFFFFFFFFu, nm[0] != m[0] || nm[1] != m[1])) {
+        if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < RL; ++i) {
+            nm[i] = fmaxf(nm[i], __shfl_xor_sync(0xFFFFFFFFu, nm[i], 1));
+            nm[i] = fmaxf(nm[i], __shfl_xor_sync(0xFFFFFFFFu, nm[i], 2));
+            nm[i] = fmaxf(m[i], nm[i]);
             const float f = exp2_fast((m[i] - safe_max(nm[i])) * p.scale_log2);
             l[i] *= f;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              o[t][2 * i] *= f;
-              o[t][2 * i + 1] *= f;
+              o[i / 2][t][2 * (i % 2)] *= f;
+              o[i / 2][t][2 * (i % 2) + 1] *= f;
             }
             m[i] = nm[i];
           }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < RL; ++i) {
           const float mb = safe_max(m[i]) * p.scale_log2;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              pr[t][2 * i + e] = exp2_fast(fmaf(sc[t][2 * i + e], p.scale_log2, -mb));
-              l[i] += pr[t][2 * i + e];
+            for (int e = 2 * (i % 2); e < 2 * (i % 2) + 2; ++e) {
+              pr[i / 2][t][e] = exp2_fast(fmaf(sc[i / 2][t][e], p.scale_log2, -mb));
+              l[i] += pr[i / 2][t][e];
             }
         }
       }
@@ -264,40 +282,46 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
         }
         if (!odd) {
           // the weights are rounded to the cache's type for the MMA: half a step each, against a result of that type
-          const uint32_t pa[4] = {pack2<T>(pr[0][0], pr[0][1]), pack2<T>(pr[0][2], pr[0][3]), pack2<T>(pr[1][0], pr[1][1]),
-                                  pack2<T>(pr[1][2], pr[1][3])};
+          uint32_t pa[RT][4];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pa[rt][e] = pack2<T>(pr[rt][e >> 1][2 * (e & 1)], pr[rt][e >> 1][2 * (e & 1) + 1]);
 #pragma unroll
           for (int t = 0; t < NT; t += 2) {
             if (t * 8 < dims) {
               uint32_t f[4];
               const int key = ((lane >> 3) & 1) * 8 + (lane & 7), c = t + (lane >> 4);
               ldsm4_t(f, vst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
-              mma16816<T>(o[t], pa, f[0], f[1]);
-              mma16816<T>(o[t + 1], pa, f[2], f[3]);
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) {
+                mma16816<T>(o[rt][t], pa[rt], f[0], f[1]);
+                mma16816<T>(o[rt][t + 1], pa[rt], f[2], f[3]);
+              }
             }
           }
         } else {
 #pragma unroll 1
           for (int c = 0; c < AD_KEYS; ++c) {
-            float w[2];
+            float w[RL];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float a = (c & 1) ? pr[0][2 * i + 1] : pr[0][2 * i], d = (c & 1) ? pr[1][2 * i + 1] : pr[1][2 * i];
+            for (int i = 0; i < RL; ++i) {
+              const float(&p4)[2][4] = pr[i / 2];
+              const int at = 2 * (i % 2);
+              const float a = (c & 1) ? p4[0][at + 1] : p4[0][at], d = (c & 1) ? p4[1][at + 1] : p4[1][at];
               w[i] = __shfl_sync(0xFFFFFFFFu, c < 8 ? a : d, (lane & ~3) + ((c & 7) >> 1));
             }
-            const bool in0 = k0 + c >= see[0].x && k0 + c < see[0].y, in1 = k0 + c >= see[1].x && k0 + c < see[1].y;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if (t * 8 < dims) {
                 const T* v = reinterpret_cast<const T*>(vt + c * (DP * 2) + ((t ^ (c & 7)) << 4)) + qc;
                 const float v0 = to_f32(v[0]), v1 = to_f32(v[1]);
-                if (in0) {
-                  o[t][0] = fmaf(w[0], v0, o[t][0]);
-                  o[t][1] = fmaf(w[0], v1, o[t][1]);
-                }
-                if (in1) {
-                  o[t][2] = fmaf(w[1], v0, o[t][2]);
-                  o[t][3] = fmaf(w[1], v1, o[t][3]);
+#pragma unroll
+                for (int i = 0; i < RL; ++i) {
+                  if (k0 + c < see[i].x || k0 + c >= see[i].y) continue;
+                  float(&o4)[4] = o[i / 2][t];
+                  o4[2 * (i % 2)] = fmaf(w[i], v0, o4[2 * (i % 2)]);
+                  o4[2 * (i % 2) + 1] = fmaf(w[i], v1, o4[2 * (i % 2) + 1]);
                 }
               }
             }
@@ -313,7 +337,7 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
     // ---- the warps' sums, in their rings
     float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RL; ++i) {
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
       l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
       if ((lane & 3) == 0) {
@@ -322,10 +346,10 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        *reinterpret_cast<float2*>(mine + (qr + 8 * i) * C::kPitch + t * 8 + qc) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
+        *reinterpret_cast<float2*>(mine + (qr + 8 * i) * C::kPitch + t * 8 + qc) = make_float2(o[i / 2][t][2 * (i % 2)], o[i / 2][t][2 * (i % 2) + 1]);
     }
     __syncthreads();
-    constexpr int TPR = C::kThreads / AD_ROWS, NJ = DP / (4 * TPR);  // threads of a row, vectors of a thread
+    constexpr int TPR = C::kThreads / ROWS, NJ = DP / (4 * TPR);  // threads of a row, vectors of a thread
     const int r = tid / TPR, dv = (tid % TPR) * 4;
     float M = -INFINITY, L = 0.0f;
     float4 acc[NJ];
@@ -354,10 +378,10 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
       float* sums = reinterpret_cast<float*>(p.ws + kAttnSums);
       const int64_t slot = 2 * blockIdx.x + (s0 == 0);
       if (r < rows) {
-        if (dv == 0) __stcg(st + slot * AD_ROWS + r, make_float2(M, L));
+        if (dv == 0) __stcg(st + slot * ROWS + r, make_float2(M, L));
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-          __stcg(reinterpret_cast<float4*>(sums + (slot * AD_ROWS + r) * DP + dv + j * 4 * TPR), acc[j]);
+          __stcg(reinterpret_cast<float4*>(sums + (slot * ROWS + r) * DP + dv + j * 4 * TPR), acc[j]);
       }
       __syncthreads();
       if (tid == 0) {  // its fences stand for the CTA's writes before the barrier, and for its reads after the next
@@ -376,10 +400,10 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
         for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (r < rows) {
 #pragma unroll 8
-          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(st + (int64_t)(2 * c + (c == c0)) * AD_ROWS + r).x);
+          for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(st + (int64_t)(2 * c + (c == c0)) * ROWS + r).x);
 #pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
-            const int64_t at = (int64_t)(2 * c + (c == c0)) * AD_ROWS + r;
+            const int64_t at = (int64_t)(2 * c + (c == c0)) * ROWS + r;
             const float2 ml = __ldcg(st + at);
             const float f = exp2_fast((ml.x - safe_max(M)) * p.scale_log2);
             L = fmaf(ml.y, f, L);
@@ -419,37 +443,44 @@ __global__ void __launch_bounds__(AttnCfg<DP>::kThreads, 1) attn_rows_kernel(Att
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int RT>
 fp4moe_status attn_rows_run(const AttnParams& p, int nsm, cudaStream_t st) {
-  using C = AttnCfg<DP>;
+  using C = AttnCfg<DP, RT>;
   static PerDevice done;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP4MOE_CUDA_ERROR;
   if (done.get(dev, [] {
-        return cudaFuncSetAttribute(attn_rows_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+        return cudaFuncSetAttribute(attn_rows_kernel<T, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
                        cudaSuccess
                    ? 1
                    : 0;
       }) <= 0)
     return FP4MOE_CUDA_ERROR;
-  return launch_pdl(attn_rows_kernel<T, DP>, dim3((unsigned)nsm), dim3(C::kThreads), C::kSmem, st, p) == cudaSuccess
+  return launch_pdl(attn_rows_kernel<T, DP, RT>, dim3((unsigned)nsm), dim3(C::kThreads), C::kSmem, st, p) == cudaSuccess
              ? FP4MOE_OK
              : FP4MOE_CUDA_ERROR;
 }
 template <typename T>
-fp4moe_status attn_rows_typed(const AttnParams& p, int nsm, cudaStream_t st) {
-  return p.D <= 64 ? attn_rows_run<T, 64>(p, nsm, st) : p.D <= 128 ? attn_rows_run<T, 128>(p, nsm, st) : attn_rows_run<T, 256>(p, nsm, st);
+fp4moe_status attn_rows_typed(const AttnParams& p, int tile, int nsm, cudaStream_t st) {
+  return tile == 32   ? attn_rows_run<T, 64, 2>(p, nsm, st)
+         : p.D <= 64  ? attn_rows_run<T, 64, 1>(p, nsm, st)
+         : p.D <= 128 ? attn_rows_run<T, 128, 1>(p, nsm, st)
+                      : attn_rows_run<T, 256, 1>(p, nsm, st);
 }
 
 }  // namespace
 
-// Sequences of more than 16 rows a kv head, on the average, are for the larger tiles, which read k and v once for 256
-// rows (us, 32 / 8 heads of 128 dims, 16 sequences of 8192 keys: 16 rows 93 with tiles of 16 and 106 with the others, 32
-// rows 175 and 108), unless all of them are a few tiles of 16, which a part of the SMs works on (32 rows of one sequence
-// 23 and 28, of four sequences of 4096 keys 32 and 27).
+// Sequences of more than 16 rows a kv head, on the average, are for larger tiles, which read k and v once for more rows,
+// unless all of them are a few tiles of 16, which a part of the SMs works on. Heads of 32 / 8, us with tiles of 16, 32, 256:
+//   128 dims, 16 sequences of up to 8192 keys: 16 rows 62, 78, 71; 32 rows 91, 80, 72; one sequence of 8192: 32 rows 22, 21,
+//   28, 48 rows 26, 27, 56. Tiles of 32 gain too little there to be kept.
+//   64 dims, 16 sequences of up to 8192 keys: 16 rows 41, 47, 55; 32 rows 62, 48, 56; 48 rows 94, 74, 56; one sequence of
+//   8192: 32 rows 17, 16, 25, 64 rows 24, 21, 36.
 int paged_attention_tile(const fp4moe_kv_cache& c, int32_t num_seqs, int32_t T, int32_t q_heads) {
-  const int64_t rows = (int64_t)T * (q_heads / c.kv_heads), tiles = (rows + AD_ROWS - 1) / AD_ROWS * c.kv_heads;
-  return c.head_dim <= 128 && rows > (int64_t)AD_ROWS * num_seqs && tiles > 48 ? kAttnTileRows : AD_ROWS;
+  const int64_t rows = (int64_t)T * (q_heads / c.kv_heads), tiles = (rows + 15) / 16 * c.kv_heads;
+  if (c.head_dim > 128 || rows <= (int64_t)16 * num_seqs) return 16;
+  if (c.head_dim > 64) return tiles > 48 ? kAttnTileRows : 16;
+  return tiles > 48 && rows > (int64_t)32 * num_seqs ? kAttnTileRows : 32;
 }
 
 fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cache, const void* v_cache, int32_t num_seqs,
@@ -485,8 +516,9 @@ fp4moe_status paged_attention_launch(const fp4moe_kv_cache& c, const void* k_cac
   int nsm = sm_count();
   if (nsm <= 0) return FP4MOE_CUDA_ERROR;
   if (nsm > kAttnMaxCtas) nsm = kAttnMaxCtas;
-  if (paged_attention_tile(c, num_seqs, T, q_heads) == kAttnTileRows) return attn_tile_launch(c.dtype, p, nsm, st);
-  return c.dtype == FP4MOE_BF16 ? attn_rows_typed<__nv_bfloat16>(p, nsm, st) : attn_rows_typed<__half>(p, nsm, st);
+  const int tile = paged_attention_tile(c, num_seqs, T, q_heads);
+  if (tile == kAttnTileRows) return attn_tile_launch(c.dtype, p, nsm, st);
+  return c.dtype == FP4MOE_BF16 ? attn_rows_typed<__nv_bfloat16>(p, tile, nsm, st) : attn_rows_typed<__half>(p, tile, nsm, st);
 }
 
 }  // namespace fp4moe

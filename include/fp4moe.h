@@ -754,9 +754,9 @@ fp4moe_status fp4moe_paged_attention(const fp4moe_kv_cache* cache, const void* k
 
 /*
  * fp4moe_paged_attention_plan: rows of a tile of the kernel that a call of these
- * sizes takes (host arithmetic): 16, or 256 (two of 128) on the tensor cores of
- * one CTA. A row is a token and one of the query heads of a kv head. Results differ
- * between the two by the order of fp32 additions and by where weights are rounded.
+ * sizes takes (host arithmetic): 16 or 32, or 256 (two of 128) on the tensor cores
+ * of one CTA. A row is a token and one of the query heads of a kv head. Results differ
+ * between them by the order of fp32 additions and by where weights are rounded.
  * Errors as in fp4moe_paged_attention; num_seqs or T 0: 16.
  */
 fp4moe_status fp4moe_paged_attention_plan(const fp4moe_kv_cache* cache, int32_t num_seqs, int32_t T, int32_t q_heads,

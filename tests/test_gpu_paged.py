@@ -752,3 +752,47 @@ def test_attention_of_as_many_rows_as_32_bits_count():
     want = ref.attention(q, *flat, slots, [0], [L], [L], D ** -0.5, True, 0)
     compare(out[T - L:], None, want, [L], D, "bfloat16")
     assert not any(c.any() for c in out[:T - L].view(-1).split(2 ** 30)) and err.tolist() == [0]
+
+
+# The same for tiles of 32 rows, which these sizes take.
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [8, 16, 24, 48, 56, 64])
+@pytest.mark.parametrize("page", [5, 16])
+def test_tiles_of_32_head_dims(D, dtype, page):
+    check_attention([7, 1, 9], [7, 150, 401], 16, 4, D, dtype, page, tile=32)
+
+
+@pytest.mark.parametrize("H,Hk,new", [(1, 1, [17, 18]), (6, 2, [10, 7]), (7, 1, [3, 4]), (17, 1, [1, 1]), (31, 1, [1, 1]), (32, 1, [1, 1]),
+                                      (33, 1, [1, 0, 1]), (71, 1, [2, 0]), (8, 1, [4] * 40), (16, 8, [16] * 30 + [5]), (600, 1, [1, 0])])
+def test_tiles_of_32_head_groups(H, Hk, new):
+    check_attention(new, [200 + 43 * b for b in range(len(new))], H, Hk, 64, tile=32)
+
+
+@pytest.mark.parametrize("new,kv", [([5], [5]), ([5], [4]), ([8], [1]), ([8], [128]), ([8], [129]), ([8], [20000]), ([0, 20, 0], [0, 37, 9]),
+                                    ([8] * 50, list(range(8, 58))), ([6, 8, 7, 8], [1, 9000, 3, 8])])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 3), (True, 100), (False, 0)])
+def test_tiles_of_32_lengths(new, kv, causal, window):
+    check_attention(new, kv, 32, 8, 64, causal=causal, window=window, tile=32)
+
+
+@pytest.mark.parametrize("dtype,spread,scale", [("bfloat16", 30.0, None), ("float16", 8.0, None), ("bfloat16", 1.0, 1e-4),
+                                                ("bfloat16", 1.0, 3.0), ("float16", 0.0, None)])
+def test_tiles_of_32_spread_of_the_scores(dtype, spread, scale):
+    check_attention([8, 7], [1900, 77], 32, 8, 64, dtype, spread=spread, scale=scale, tile=32)
+
+
+@pytest.mark.parametrize("D,new", [(64, [3]), (64, [9]), (128, [3]), (256, [3])])
+def test_attention_scores_that_rise(D, new):
+    """Every group's maximum above the groups' before, by little and by much: a maximum that lags loses nothing."""
+    import torch
+    for top in (0.25, 4.0):
+        kv = [1500]
+        q, kc, vc, flat, table, slots = attention_case(new, kv, 8, 2, D)
+        q.copy_(torch.ones_like(q) + 0.1 * q)
+        rise = torch.linspace(-top, top, 1500, device="cuda")[:, None, None]
+        s = slots[0]
+        kc[s // 16, s % 16] = (rise + 0.05 * flat[0][s].float()).bfloat16()
+        flat = [c.reshape(-1, 2, D) for c in (kc, vc)]
+        out, lse = run_attention(q, kc, vc, table, kv, [0, new[0]], 1.0, True, 0)
+        want = ref.attention(q, *flat, slots, [0], new, kv, 1.0, True, 0)
+        compare(out, lse, want, kv, D, "bfloat16")

@@ -113,7 +113,8 @@ def test_attention_plan(lib):
     """Which kernel takes what: the sizes that the GPU tests use for each do take it."""
     from block_scaled_fp4_top_gb300 import _lib, api
     plan = api.fp4moe_paged_attention_plan
-    for B, T, H, Hk, D, want in ((1, 1, 32, 8, 128, 16), (64, 64, 32, 8, 128, 16), (16, 64, 64, 8, 64, 256), (8, 2048, 32, 8, 128, 256),
+    for B, T, H, Hk, D, want in ((1, 1, 32, 8, 128, 16), (64, 64, 32, 8, 128, 16), (16, 64, 64, 8, 64, 32), (16, 65, 64, 8, 64, 256), (16, 32, 64, 8, 64, 16),
+                                 (1, 8, 32, 8, 64, 32), (1, 24, 32, 8, 64, 32), (1, 25, 32, 8, 64, 256), (8, 2048, 32, 8, 128, 256),
                                  (1, 8, 32, 8, 128, 16), (4, 32, 32, 8, 128, 256), (1, 8192, 32, 8, 136, 16), (1, 8192, 32, 8, 256, 16),
                                  (0, 0, 8, 8, 64, 16), (1, 2**31 // 64 - 1, 64, 1, 64, 256), (8192, 8192, 1, 1, 8, 16)):
         assert plan(B, T, H, Hk, D) == want, (B, T, H, Hk, D)
