@@ -1,15 +1,17 @@
 // Attention over the paged cache for few rows a sequence and kv head (fp4moe_paged_attention): decoding, proposed tokens.
 //
-// One pass over the keys: with the running maximum m and sum l of a row, each group of 16 keys adds
+// One pass over the keys: with the running maximum m and sum l of a row, each group of 16 keys (32 with 64 dims) adds
 //   m' = max(m, max s), l' = l 2^(m - m') + sum 2^(s - m'), O' = O 2^(m - m') + sum 2^(s - m') v    (s in powers of two),
 // where m' stays m until a score passes it by more than 2^8, so that the rows' maxima need not be made for every group.
 // The bytes of k and v bound it: 16 rows of a tile cost 64 KFLOP for 8 KB of a group (head_dim 128), far below what
-// mma.sync gives, so the tile's M = 16 is that of mma.sync, and a warp works alone: it brings its own groups of 16 keys by
+// mma.sync gives, so the tile's M = 16 is that of mma.sync, and a warp works alone: it brings its own groups of keys by
 // cp.async through a ring of its own, without any barrier between warps, and joins the others at the end of a tile only.
 // 64 sequences of up to 8192 keys, 8 kv heads of 128 dims: 1367 MB in 214 us, 6.4 TB/s, 94 % of a plain copy's rate; four of
 // 131072 keys 321 us, 98 %. One row of 4096 keys is 13 us of latency: the division 2, page and keys 2, the joins 4.
-// Tiles of 32 rows (64 dims) use what is read twice: 16 x 32 rows of up to 8192 keys, 8 kv heads, in 49 us, which tiles of
-// 16 take 58 for and the larger ones 56. There instructions bind it, as more warps show: 16 of them take 52.
+// Tiles of 32 rows (64 dims) use what is read twice: 16 x 32 rows of up to 8192 keys, 8 kv heads, in 42 us, which tiles of
+// 16 take 50 for and the larger ones 55. There the chain of a group binds it, scores to weights to sums, with two warps a
+// scheduler to hide it: groups of 32 keys, twice as many products side by side, took it from 49 to 42 us, and decoding from
+// 125 to 123; twice as many warps instead, with less of the ring and of the registers each, 52 and 128.
 // Any page size and stride: a lane works out its key's place and hands it to the lanes that copy the key's 16-byte
 // pieces; the page of the next group is looked up a group ahead.
 // Keys outside the tile's range are zeros in shared memory. Keys that only some rows of a tile see have score -infinity
@@ -19,7 +21,6 @@
 namespace fp4moe {
 namespace {
 
-constexpr int AD_KEYS = 16;  // of a warp's group
 constexpr float AD_GROWTH = 8.0f;  // powers of two that a maximum may lag behind: weights up to 256, which neither 16-bit type minds
 constexpr int AD_MIN = 1;    // least cost of a CTA's run
 constexpr int AD_OH = 1;     // what a tile costs, in slices, beside its slices
@@ -27,10 +28,11 @@ constexpr int AD_OH = 1;     // what a tile costs, in slices, beside its slices
 template <int DP, int RT>  // RT: 16-row MMA tiles of a tile
 struct AttnCfg {
   static constexpr int kRows = 16 * RT;
+  static constexpr int KT = DP == 64 ? 2 : 1, kKeys = 16 * KT;  // keys of a warp's group: 8 KB of k and v
   static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int S = AD_KEYS * kWarps;           // keys of a slice: one group a warp
-  static constexpr int kTile = AD_KEYS * DP * 2;       // k, or v, of a group
+  static constexpr int S = kKeys * kWarps;           // keys of a slice: one group a warp
+  static constexpr int kTile = kKeys * DP * 2;       // k, or v, of a group
   // A load is both of them (64 dims: 104 us, one at a time 121; 32 sequences of 8192 keys), or one where three of both do
   // not fit (256 dims: 343 us, both with half the warps 500).
   static constexpr int kParts = DP == 256 ? 1 : 2;
@@ -74,7 +76,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <typename T, int DP, int RT>
 __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel(AttnParams p) {
   using C = AttnCfg<DP, RT>;
-  constexpr int ROWS = C::kRows, RL = 2 * RT;            // rows of a tile, and of a lane: qr + 8 i
+  constexpr int ROWS = C::kRows, KEYS = C::kKeys, KT = C::KT, RL = 2 * RT;  // rows of a tile, and of a lane: qr + 8 i
   constexpr int CH = DP / 8, KS = DP / 16, NT = DP / 8;  // 16-byte pieces of a key, MMA steps, output columns of 8
   constexpr int RPI = 32 / CH;                           // keys that one copy instruction of the warp covers
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -97,11 +99,11 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
     const AttnSeq& seq = u.seq;
     const int kv = u.kv, head = u.head, row0 = u.row0, rows = u.rows, n = u.n, s0 = u.s0, s1 = u.s1;
     const int2 range = u.range;
-    const int base = range.x / C::S * C::S + warp * AD_KEYS;  // first key of this warp's group of slice 0
+    const int base = range.x / C::S * C::S + warp * KEYS;  // first key of this warp's group of slice 0
     const int32_t* table = p.table + (int64_t)u.b * p.columns;
     const int64_t head_off = (int64_t)head * p.map.head_stride;
     auto page_of = [&](int s) {  // page of the key that this lane looks up in slice s; -2: none
-      const int key = base + s * C::S + (lane & 15);
+      const int key = base + s * C::S + (lane & (KEYS - 1));
       return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
     };
     int page = page_of(s0);  // on its way while q is fetched
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
       const int s = C::kParts == 2 ? s0 + issued : s0 + issued / 2;
       if (s < s1) {
         if (C::kParts == 2 || issued % 2 == 0) {
-          const int key = base + s * C::S + (lane & 15);
+          const int key = base + s * C::S + (lane & (KEYS - 1));
           off = -1;
           if (page != -2) {
             if ((uint32_t)page < (uint32_t)p.map.num_pages) {
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         const int c = lane % CH;
         const uint32_t dst0 = ring32 + fill * C::kLoad;
 #pragma unroll
-        for (int it = 0; it < AD_KEYS / RPI; ++it) {
+        for (int it = 0; it < KEYS / RPI; ++it) {
           const int r = it * RPI + lane / CH;
           const int64_t ro = __shfl_sync(0xFFFFFFFFu, off, r);
           const bool use = ro >= 0 && c * 8 < p.D;
@@ -191,26 +193,29 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
       cp_async_wait<C::kLoads - 2>();
       __syncwarp();
       const int k0 = base + s * C::S;
-      const bool any = k0 < range.y && k0 + AD_KEYS > range.x;
-      float pr[RT][2][4];
-      const bool edge = k0 < all_lo || k0 + AD_KEYS > all_hi;
+      const bool any = k0 < range.y && k0 + KEYS > range.x;
+      float pr[RT][2 * KT][4];
+      const bool edge = k0 < all_lo || k0 + KEYS > all_hi;
       if (any) {
         const uint32_t kst = ring32 + stage * C::kLoad;
-        float sc[RT][2][4] = {};
+        float sc[RT][2 * KT][4] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           if (ks * 16 < dims) {
-            uint32_t f[4];
-            const int key = (lane >> 4) * 8 + (lane & 7), c = ks * 2 + ((lane >> 3) & 1);
-            ldsm4(f, kst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              if constexpr (C::kSharedQ) {
-                const int r = lane & 15, qc16 = ks * 2 + (lane >> 4);
-                ldsm4(qa[rt][0], smem_u32(sm) + C::kRings + (rt * 16 + r) * (DP * 2) + ((qc16 ^ (r & 7)) << 4));
+            for (int kt = 0; kt < KT; ++kt) {
+              uint32_t f[4];
+              const int key = kt * 16 + (lane >> 4) * 8 + (lane & 7), c = ks * 2 + ((lane >> 3) & 1);
+              ldsm4(f, kst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (C::kSharedQ) {
+                  const int r = lane & 15, qc16 = ks * 2 + (lane >> 4);
+                  ldsm4(qa[rt][0], smem_u32(sm) + C::kRings + (rt * 16 + r) * (DP * 2) + ((qc16 ^ (r & 7)) << 4));
+                }
+                mma16816<T>(sc[rt][2 * kt], qa[rt][C::kSharedQ ? 0 : ks], f[0], f[1]);
+                mma16816<T>(sc[rt][2 * kt + 1], qa[rt][C::kSharedQ ? 0 : ks], f[2], f[3]);
               }
-              mma16816<T>(sc[rt][0], qa[rt][C::kSharedQ ? 0 : ks], f[0], f[1]);
-              mma16816<T>(sc[rt][1], qa[rt][C::kSharedQ ? 0 : ks], f[2], f[3]);
             }
           }
         }
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
 #pragma unroll
           for (int i = 0; i < RL; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4 * KT; ++e) {
               const int key = k0 + (e >> 1) * 8 + qc + (e & 1);
               if (key < see[i].x || key >= see[i].y) sc[i / 2][e >> 1][2 * (i % 2) + (e & 1)] = -INFINITY;
             }
@@ -227,9 +232,9 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         bool grown = false;
 #pragma unroll
         for (int i = 0; i < RL; ++i) {
-          const float(&s4)[2][4] = sc[i / 2];
-          const int a = 2 * (i % 2);
-          nm[i] = fmaxf(fmaxf(s4[0][a], s4[0][a + 1]), fmaxf(s4[1][a], s4[1][a + 1]));  // of this lane's keys
+          nm[i] = -INFINITY;  // of this lane's keys
+#pragma unroll
+          for (int t = 0; t < 2 * KT; ++t) nm[i] = fmaxf(nm[i], fmaxf(sc[i / 2][t][2 * (i % 2)], sc[i / 2][t][2 * (i % 2) + 1]));
           grown |= (nm[i] - m[i]) * p.scale_log2 > AD_GROWTH;
         }
         if (__any_sync(0xFFFFFFFFu, grown)) {
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         for (int i = 0; i < RL; ++i) {
           const float mb = safe_max(m[i]) * p.scale_log2;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2 * KT; ++t)
 #pragma unroll
             for (int e = 2 * (i % 2); e < 2 * (i % 2) + 2; ++e) {
               pr[i / 2][t][e] = exp2_fast(fmaf(sc[i / 2][t][e], p.scale_log2, -mb));
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         const uint32_t vst = ring32 + stage * C::kLoad + (C::kParts - 1) * C::kTile;
         bool odd = false;  // a v that some rows must not touch even with weight 0
         if (edge && (all_lo != range.x || all_hi != range.y)) {
-          for (int it = 0; it < AD_KEYS / RPI; ++it) {
+          for (int it = 0; it < KEYS / RPI; ++it) {
             const int r = it * RPI + lane / CH, c = lane % CH;
             if (c * 8 < dims)
               odd |= any_nonfinite<T>(
@@ -282,34 +287,43 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         }
         if (!odd) {
           // the weights are rounded to the cache's type for the MMA: half a step each, against a result of that type
-          uint32_t pa[RT][4];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+          for (int kt = 0; kt < KT; ++kt) {
+            uint32_t pa[RT][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pa[rt][e] = pack2<T>(pr[rt][e >> 1][2 * (e & 1)], pr[rt][e >> 1][2 * (e & 1) + 1]);
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int t = 0; t < NT; t += 2) {
-            if (t * 8 < dims) {
-              uint32_t f[4];
-              const int key = ((lane >> 3) & 1) * 8 + (lane & 7), c = t + (lane >> 4);
-              ldsm4_t(f, vst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
+              for (int e = 0; e < 4; ++e) {
+                const float(&w)[4] = pr[rt][2 * kt + (e >> 1)];
+                pa[rt][e] = pack2<T>(w[2 * (e & 1)], w[2 * (e & 1) + 1]);
+              }
 #pragma unroll
-              for (int rt = 0; rt < RT; ++rt) {
-                mma16816<T>(o[rt][t], pa[rt], f[0], f[1]);
-                mma16816<T>(o[rt][t + 1], pa[rt], f[2], f[3]);
+            for (int t = 0; t < NT; t += 2) {
+              if (t * 8 < dims) {
+                uint32_t f[4];
+                const int key = kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), c = t + (lane >> 4);
+                ldsm4_t(f, vst + key * (DP * 2) + ((c ^ (key & 7)) << 4));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                  mma16816<T>(o[rt][t], pa[rt], f[0], f[1]);
+                  mma16816<T>(o[rt][t + 1], pa[rt], f[2], f[3]);
+                }
               }
             }
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < AD_KEYS; ++c) {
+          for (int c = 0; c < KEYS; ++c) {
             float w[RL];
 #pragma unroll
             for (int i = 0; i < RL; ++i) {
-              const float(&p4)[2][4] = pr[i / 2];
               const int at = 2 * (i % 2);
-              const float a = (c & 1) ? p4[0][at + 1] : p4[0][at], d = (c & 1) ? p4[1][at + 1] : p4[1][at];
-              w[i] = __shfl_sync(0xFFFFFFFFu, c < 8 ? a : d, (lane & ~3) + ((c & 7) >> 1));
+              w[i] = 0.0f;
+#pragma unroll
+              for (int t = 0; t < 2 * KT; ++t) {  // (all eights of keys are asked for, so that the weights stay in registers)
+                const float x = __shfl_sync(0xFFFFFFFFu, (c & 1) ? pr[i / 2][t][at + 1] : pr[i / 2][t][at], (lane & ~3) + ((c & 7) >> 1));
+                if (t == c >> 3) w[i] = x;
+              }
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -474,8 +488,8 @@ fp4moe_status attn_rows_typed(const AttnParams& p, int tile, int nsm, cudaStream
 // unless all of them are a few tiles of 16, which a part of the SMs works on. Heads of 32 / 8, us with tiles of 16, 32, 256:
 //   128 dims, 16 sequences of up to 8192 keys: 16 rows 62, 78, 71; 32 rows 91, 80, 72; one sequence of 8192: 32 rows 22, 21,
 //   28, 48 rows 26, 27, 56. Tiles of 32 gain too little there to be kept.
-//   64 dims, 16 sequences of up to 8192 keys: 16 rows 41, 47, 55; 32 rows 62, 48, 56; 48 rows 94, 74, 56; one sequence of
-//   8192: 32 rows 17, 16, 25, 64 rows 24, 21, 36.
+//   64 dims, 16 sequences of up to 8192 keys: 16 rows 38, 41, 54; 32 rows 53, 43, 56; 48 rows 75, 60, 56; one sequence of
+//   8192: 32 rows 14, 15, 25, 64 rows 20, 16, 36.
 int paged_attention_tile(const fp4moe_kv_cache& c, int32_t num_seqs, int32_t T, int32_t q_heads) {
   const int64_t rows = (int64_t)T * (q_heads / c.kv_heads), tiles = (rows + 15) / 16 * c.kv_heads;
   if (c.head_dim > 128 || rows <= (int64_t)16 * num_seqs) return 16;
