@@ -873,4 +873,9 @@ class PagedKvCache:
                                lse, self.ws, self.err, True, window, stream)
 
     def read_error(self, clear=True) -> int:
-        return fp4moe_read_error(self.err, clear)
+        """The error word. A call that gave up leaves the workspace's counters as they were, and the next call would take
+        them for arrivals of its own: with a timeout that is cleared, the workspace is zeroed (on the current stream)."""
+        bits = fp4moe_read_error(self.err, clear)
+        if clear and bits & _lib.ERR_TIMEOUT:
+            self.ws.zero_()
+        return bits
