@@ -26,6 +26,7 @@
 // step); weights under the maximum so far 448 and under the new one 483; one lane of a converged warp issues MMAs 483 and a
 // lane picked by index 573; boxes 1056 and cp.async 1206. Chunks over pages of one token: gathers 207, cp.async 438.
 #include "attn.cuh"
+#include "inflight.h"
 
 namespace fp4moe {
 namespace {
@@ -287,6 +288,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
   int stage = 0, units = 0;
   uint32_t phase = 0;
   int64_t issued = 0;
+  InFlight q_boxes;  // loads of q on q_full
   bool ok = true;
   // The load that is looked after once it has landed: a step of v that is not all visible to all rows, or one by cp.async.
   struct {
@@ -367,6 +369,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
         const int blocks = p.D > 64 ? 2 : 1;
         if (lane == 0) mbar_arrive_expect_tx(bar.q_full(), qt * blocks * C::kBlock);
         __syncwarp();
+        q_boxes.issue();
         if (lane < qt * blocks) {
           const int t = lane / blocks, b = lane % blocks;
           tma_load_3d(sm32 + t * C::kTile + b * C::kBlock, &maps.q, bar.q_full(), b * 64, u.head * (int)p.group.d,
@@ -437,7 +440,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
     for (int64_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
       if (!late.any || i != late.n) drain_wait(full(i % C::kStages), (i / C::kStages) & 1);
   }
-  if (!ok && WHICH == 0 && maps.q_box) drain_wait(bar.q_full(), units & 1);
+  if (!ok && q_boxes.any()) drain_wait(bar.q_full(), q_boxes.last());
 }
 
 // ---------------------------------------------------------------- MMAs (one warp)
