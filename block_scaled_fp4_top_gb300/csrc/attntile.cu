@@ -15,8 +15,8 @@
 // take the place of S(j). P is made under the maximum of the steps before, so that finding this step's is not in its way;
 // only where that had grown by more than 2^8 is O rescaled and P made again (up to 256, which neither 16-bit type minds).
 // Scores of keys that a row does not see are -infinity; v of keys outside the tile's range is zeroed in shared memory, for 0
-// times what lies there may be NaN. Where a v that only some rows see is not finite, the unit's rows are made again one by
-// one.
+// times what lies there may be NaN. So does what is not finite of a v that only some rows of the unit see: those add weight
+// times it in the end. Such keys lie at the ends of a unit's range, at most 2 x 255 of them, however long it is.
 // Every wait is bounded, as in the layer's GEMMs.
 //
 // What bounds it: a tile's round from its scores to its weights to the next scores, 3000 cycles, in which the MMAs of both
@@ -268,6 +268,26 @@ struct Loader {
   }
 };
 
+// Zeros for what is not finite in rows [lo, hi) of a tile of v but [all_lo, all_hi), by a warp. (rare: kept out of the loads)
+template <typename T, int DP>
+__device__ __noinline__ void keep_finite(uint8_t* tile, int lo, int all_lo, int all_hi, int hi) {
+  using C = TileCfg<DP>;
+  constexpr int PER = C::kBlocks * 8;  // 16-byte pieces of a row
+  constexpr uint32_t E = std::is_same_v<T, __nv_bfloat16> ? 0x7F80u : 0x7C00u;
+  for (int i = max(lo, 0) * PER + (int)lane_id(); i < min(hi, 128) * PER; i += 32) {
+    const int row = i / PER, c = i % PER;
+    if (row >= all_lo && row < all_hi) continue;
+    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * C::kBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    uint32_t w[4] = {at->x, at->y, at->z, at->w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((w[e] & E) == E) w[e] &= 0xFFFF0000u;
+      if (((w[e] >> 16) & E) == E) w[e] &= 0xFFFFu;
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // How k and v are brought: by cp.async, by boxes of a page's keys, or by gathers of four keys a lane.
 enum LoadMode { kCopies = 0, kBoxes = 1, kGathers = 2 };
 // One of the two streams: WHICH = 0 k (and q), 1 v. Stages go round; load n is told on full(n % kStages).
@@ -337,7 +357,10 @@ __device__ __forceinline__ void load_role(const AttnParams& p, const TileMaps& m
           look(late.lo, late.hi);
         }
       }
-      if (bad) odd[(late.mark - 1) % AT_ODD] = late.mark;
+      if (__any_sync(0xFFFFFFFFu, bad)) {
+        keep_finite<T, DP>(tile, late.lo - late.k0, late.all_lo - late.k0, late.all_hi - late.k0, late.hi - late.k0);
+        odd[(late.mark - 1) % AT_ODD] = late.mark;
+      }
     }
     L.told(full(late.stage));
     return true;
@@ -524,31 +547,72 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, const AttnRun& run
 }
 
 // ---------------------------------------------------------------- softmax, output
-// A row again, key by key: m, l, and the sums of 32 dims from d0 on.
-template <typename T>
-__device__ __noinline__ void row_again(const AttnParams& p, const AttnUnit& u, int row, int lo, int hi, int d0, float& m, float& l,
-                                       float (&o)[32]) {
+// What is called out of line finds in shared memory: where the CTA's TMEM begins, and the maximum and sum of a row.
+__device__ __forceinline__ uint32_t& tmem_base() {
+  __shared__ uint32_t at;
+  return at;
+}
+__device__ __forceinline__ float2& row_stats() {
+  __shared__ float2 of[AT_BM];
+  return of[threadIdx.x];
+}
+
+// What the loads took out of v where only some rows of the unit see it: weight times value, infinite or NaN, is added to the 32
+// dims from d0 on of O, which hold the finite values already, for the keys [lo, hi) that a row sees. All keys that a unit can
+// have of that kind, with values like that in every one, cost its rows some milliseconds, far from the waits' limit.
+// Everything but the row's place comes out of memory and m, l and o are only written, so that the caller's loop over the
+// steps has no registers to keep for this: with m handed over and O handed in, a prompt of 8192 tokens took 395 us for 387,
+// one with a window of 1024 205 for 180.
+template <typename T, int DP>
+__device__ __noinline__ void add_odd(const AttnParams& p, const AttnUnit& u, int row, int lo, int hi, int d0, float& m, float& l,
+                                     float (&o)[32]) {
+  __syncwarp();
+  tmem_ld32(tmem_base() + ((uint32_t)(threadIdx.x & 96) << 16) + 256 + (threadIdx.x >> 7) * DP + d0, o);
+  tmem_arrived(o);
+  m = row_stats().x;
+  l = row_stats().y;
   const int tok = (int)p.group.div(u.row0 + row), g = u.row0 + row - tok * (int)p.group.d;
   const T* q = static_cast<const T*>(p.q) + (int64_t)(u.seq.first + tok) * p.q_stride +
                (int64_t)(u.head * (int)p.group.d + g) * p.D;
-  m = -INFINITY;
-  l = 0.0f;
-  for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-  for (int key = lo; key < hi; ++key) {
+  // keys that all rows of the unit see, as the loads have it
+  const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + u.rows - 1)).x;
+  const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0)).y;
+  const int end = min(u.range.y, (u.range.x / AT_KEYS + u.s1) * AT_KEYS);
+#pragma unroll 1
+  for (int key = max(u.range.x, (u.range.x / AT_KEYS + u.s0) * AT_KEYS); key < end; ++key) {  // the same for all lanes
+    if (key >= all_lo && key < all_hi) {
+      key = all_hi - 1;
+      continue;
+    }
     const int j = (int)p.map.page.div(key), page = __ldg(p.table + (int64_t)u.b * p.columns + j);
-    const bool there = (uint32_t)page < (uint32_t)p.map.num_pages;
-    const int64_t off = there ? page * p.map.page_stride + (int64_t)(key - j * (int)p.map.page.d) * p.map.token_stride +
-                                    (int64_t)u.head * p.map.head_stride
-                              : 0;
+    if ((uint32_t)page >= (uint32_t)p.map.num_pages) continue;  // (reads as zeros)
+    const int64_t off = page * p.map.page_stride + (int64_t)(key - j * (int)p.map.page.d) * p.map.token_stride +
+                        (int64_t)u.head * p.map.head_stride;
     const T *k = static_cast<const T*>(p.k) + off, *v = static_cast<const T*>(p.v) + off;
-    float s = 0.0f;
-    if (there)
-      for (int d = 0; d < p.D; ++d) s = fmaf(to_f32(q[d]), to_f32(k[d]), s);
-    const float nm = fmaxf(m, s), f = exp2_fast((m - safe_max(nm)) * p.scale_log2);
-    const float w = exp2_fast(fmaf(s, p.scale_log2, -safe_max(nm) * p.scale_log2));
-    m = nm;
-    l = fmaf(l, f, w);
-    for (int i = 0; i < 32; ++i) o[i] = fmaf(o[i], f, there && d0 + i < p.D ? w * to_f32(v[d0 + i]) : 0.0f);
+    float w = -1.0f;  // not made yet
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (d0 + c * 8 >= p.D) break;
+      const uint4 piece = *reinterpret_cast<const uint4*>(v + d0 + c * 8);
+      if (!any_nonfinite<T>(piece) || key < lo || key >= hi) continue;
+      if (w == -1.0f) {
+        float s = 0.0f;
+#pragma unroll 1
+        for (int d = 0; d < p.D; d += 8) {
+          float a[8], b[8];
+          unpack<T>(*reinterpret_cast<const uint4*>(q + d), a);
+          unpack<T>(*reinterpret_cast<const uint4*>(k + d), b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+        }
+        w = exp2_fast(fmaf(s, p.scale_log2, -safe_max(m) * p.scale_log2));
+      }
+      float x[8];
+      unpack<T>(piece, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!isfinite(x[e])) o[c * 8 + e] = fmaf(w, x[e], o[c * 8 + e]);
+    }
   }
 }
 
@@ -679,10 +743,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
     tc_fence_after();
     if (!idle && odd[units % AT_ODD] == units + 1) {
       const int k0 = (u.range.x / AT_KEYS + u.s0) * AT_KEYS, k1 = (u.range.x / AT_KEYS + u.s1) * AT_KEYS;
+      row_stats() = make_float2(m, l);
       for (int d = 0; d < dims; d += 32) {
         float o[32];
         uint32_t w[32];
-        row_again<T>(p, u, r, max(see.x, k0), min(see.y, k1), d, m, l, o);
+        add_odd<T, DP>(p, u, r, max(see.x, k0), min(see.y, k1), d, m, l, o);
 #pragma unroll
         for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(o[c]);
         __syncwarp();
@@ -907,7 +972,8 @@ template <typename T, int DP, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_tile_kernel(AttnParams p, const __grid_constant__ TileMaps maps) {
   using C = TileCfg<DP>;
   extern __shared__ uint8_t raw[];
-  __shared__ uint32_t tmem_at, arrived[2], skip;
+  __shared__ uint32_t arrived[2], skip;
+  uint32_t& tmem_at = tmem_base();
   __shared__ int odd[AT_ODD];  // [unit % AT_ODD]: unit + 1 if a v that only some of its rows see is not finite
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const uint32_t sm32 = smem_u32(sm);

@@ -53,3 +53,52 @@ def test_a_cache_after_a_call_that_gave_up(D, new):
     for _ in range(3):
         assert torch.equal(attend(-q, out).view(torch.int16), want.view(torch.int16))
         assert cache.read_error() == 0 and not cache.ws[:4096].any()
+
+
+# ------------------------------------------------------------------------- values that are not finite
+def put(cache, slots, page, key, head, dims, value):
+    s = int(slots[key])
+    for d in dims:
+        cache[s // page, s % page, head, d] = value
+
+
+def check_values(new, kv, H, Hk, D, bad, dtype="bfloat16", page=16, window=0, order="tokens"):
+    """bad: (sequence, key, kv head, dims, value) of v. Infinite or NaN for the rows that see them, and for no others; the
+    call does not give up (run_attention holds the error word to 0)."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    assert api.fp4moe_paged_attention_plan(len(new), sum(new), H, Hk, D) == 256
+    q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D, dtype, page, order=order)
+    for b, key, head, dims, value in bad:
+        put(vc, slots[b], page, key, head, dims, value)
+    flat = [c.reshape(-1, Hk, D) for c in (kc, vc)]
+    first = [sum(new[:b]) for b in range(len(new) + 1)]
+    out, lse = run_attention(q, kc, vc, table, kv, first, D ** -0.5, True, window)
+    want = ref.attention(q, *flat, slots, first[:-1], new, kv, D ** -0.5, True, window)
+    assert torch.isinf(want[0]).any() or torch.isnan(want[0]).any()
+    compare(out, lse, want, kv, D, dtype)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+def test_one_value_late_in_a_long_prompt():
+    """The rows of its unit see up to 16384 keys; the other sequences are served as well."""
+    check_values([16384, 40, 1], [16384, 900, 50], 1, 1, 128, [(0, 16384 - 77, 0, (3, 90), INF), (0, 9000, 0, (4,), NAN)])
+
+
+@pytest.mark.parametrize("D,prefix", [(128, 131072), (64, 32768)])
+def test_new_values_behind_a_long_prefix(D, prefix):
+    """Every new key has some: as many as a unit can have that only some of its rows see."""
+    bad = [(0, prefix + i, i % 2, (i % D, (7 * i + 1) % D), (NAN, INF, -INF)[i % 3]) for i in range(0, 300)]
+    check_values([300, 5], [prefix + 300, 70], 4, 2, D, bad)
+
+
+@pytest.mark.parametrize("page,order", [(16, "tokens"), (7, "tokens"), (7, "heads")])
+@pytest.mark.parametrize("D,dtype", [(128, "bfloat16"), (64, "float16"), (72, "bfloat16")])
+def test_values_at_both_ends_of_a_window(D, dtype, page, order):
+    """Keys that enter and that leave the window within a unit, one that all its rows see, both signs of one dim, whole rows."""
+    bad = [(0, 3000, 0, (0,), INF), (0, 3100, 0, (0, 5), -INF), (0, 3499, 1, range(D), NAN), (0, 2400, 1, (D - 1,), INF),
+           (0, 2010, 1, (1,), -INF), (0, 2700, 0, (9,), NAN), (1, 0, 0, (2,), INF), (1, 449, 1, (3,), INF), (1, 300, 1, range(8), -INF)]
+    check_values([600, 450], [3500, 450], 6, 2, D, bad, dtype, page, 1000, order)
+    check_values([600, 450], [3500, 450], 6, 2, D, bad, dtype, page, 40, order)
