@@ -21,7 +21,7 @@
 namespace fp4moe {
 namespace {
 
-constexpr float AD_GROWTH = 8.0f;  // powers of two that a maximum may lag behind: weights up to 256, which neither 16-bit type minds
+constexpr float AD_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
 constexpr int AD_MIN = 1;    // least cost of a CTA's run
 constexpr int AD_OH = 1;     // what a tile costs, in slices, beside its slices
 
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         }
 #pragma unroll
         for (int i = 0; i < RL; ++i) {
-          const float mb = safe_max(m[i]) * p.scale_log2;
+          const float mb = weight_base<T>(m[i], p.scale_log2);
 #pragma unroll
           for (int t = 0; t < 2 * KT; ++t)
 #pragma unroll
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
           *reinterpret_cast<uint2*>(out + d) = v;
         }
       }
-      if (p.lse != nullptr && dv == 0) p.lse[t * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(L));
+      if (p.lse != nullptr && dv == 0) p.lse[t * p.q_heads + hq] = none ? -INFINITY : weights_lse<T>(M, p.scale, L);
     }
     __syncthreads();
   }

@@ -319,6 +319,23 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 // The exponent's base: a row without a finite score so far has maximum -infinity, and exponentials of 0.
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
+// Weights are 2^(score - base). fp16 has them 2^7 times as large, which the division by their sum takes back: with a maximum
+// that may lag by 2^8 they stay at or below 2^15 (fp16 ends at 65504), and down to 2^-21 of the largest they are normal numbers.
+// Smaller ones are off by at most 2^-32 of the largest each, n keys together by n 2^-32 of the greatest |v|. bf16 has fp32's
+// exponents and needs none.
+template <typename T>
+constexpr float kWeightShift = std::is_same_v<T, __half> ? 7.0f : 0.0f;
+template <typename T>
+__device__ __forceinline__ float weight_base(float m, float scale_log2) {
+  if constexpr (kWeightShift<T> == 0.0f) return safe_max(m) * scale_log2;
+  else return fmaf(safe_max(m), scale_log2, -kWeightShift<T>);
+}
+// m scale + ln of the sum of e^(score - m): `sum` is that of the weights.
+template <typename T>
+__device__ __forceinline__ float weights_lse(float m, float scale, float sum) {
+  if constexpr (kWeightShift<T> != 0.0f) sum *= 0x1p-7f;
+  return fmaf(m, scale, logf(sum));
+}
 
 // attntile.cu: 256-row units on the tensor cores, head_dim up to 128, on nsm CTAs
 fp4moe_status attn_tile_launch(int32_t dtype, const AttnParams& p, int nsm, cudaStream_t st);

@@ -13,7 +13,7 @@
 //                      are whole MMA steps, one lane a gather, else by 16-byte cp.async, a lane looking a key's place up for the lanes that copy it.
 // The MMAs of a tile come from one thread and run in order, so a finished S(j) means a finished P V(j - 1): O may be rescaled then, and P(j) may
 // take the place of S(j). P is made under the maximum of the steps before, so that finding this step's is not in its way;
-// only where that had grown by more than 2^8 is O rescaled and P made again (up to 256, which neither 16-bit type minds).
+// only where that had grown by more than 2^8 is O rescaled and P made again (weights up to 2^8, in fp16 2^15: attn.cuh).
 // Scores of keys that a row does not see are -infinity; v of keys outside the tile's range is zeroed in shared memory, for 0
 // times what lies there may be NaN. So does what is not finite of a v that only some rows of the unit see: those add weight
 // times it in the end. Such keys lie at the ends of a unit's range, at most 2 x 255 of them, however long it is.
@@ -605,7 +605,7 @@ __device__ __noinline__ void add_odd(const AttnParams& p, const AttnUnit& u, int
 #pragma unroll
           for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
         }
-        w = exp2_fast(fmaf(s, p.scale_log2, -safe_max(m) * p.scale_log2));
+        w = exp2_fast(fmaf(s, p.scale_log2, -weight_base<T>(m, p.scale_log2)));
       }
       float x[8];
       unpack<T>(piece, x);
@@ -665,7 +665,7 @@ __device__ __forceinline__ void softmax_step(uint32_t st, uint32_t ot, int dims,
   }
   // The weights under the maximum so far, and the step's maximum beside them; again if it had grown too much.
   for (;;) {
-    const float mb = safe_max(m) * scale;
+    const float mb = weight_base<T>(m, scale);
     top = m;
     sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
     tmem_ld32(st, a[0]);
@@ -782,7 +782,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
       __syncwarp();
     };
     auto finish_lse = [&](float M, float sum) {
-      if (real && p.lse != nullptr) p.lse[tq * p.q_heads + hq] = none ? -INFINITY : fmaf(M, p.scale, logf(sum));
+      if (real && p.lse != nullptr) p.lse[tq * p.q_heads + hq] = none ? -INFINITY : weights_lse<T>(M, p.scale, sum);
     };
     if (u.s0 == 0 && u.s1 == u.n) {
       const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
@@ -917,7 +917,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, const AttnRun&
               if (d * 32 + sub * 4 < p.D)
                 *reinterpret_cast<uint2*>(to + d * 32 + sub * 4) =
                     make_uint2(pack2<T>(o[d].x * inv, o[d].y * inv), pack2<T>(o[d].z * inv, o[d].w * inv));
-            if (sub == 0 && p.lse != nullptr) p.lse[rt * p.q_heads + rhq] = nothing ? -INFINITY : fmaf(M, p.scale, logf(sum));
+            if (sub == 0 && p.lse != nullptr) p.lse[rt * p.q_heads + rhq] = nothing ? -INFINITY : weights_lse<T>(M, p.scale, sum);
           }
         }
         if (!few && !idle) {

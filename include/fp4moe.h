@@ -723,7 +723,8 @@ fp4moe_status fp4moe_rope_cache(const fp4moe_kv_cache* cache, int32_t T, int32_t
  * see do not reach it, whatever they hold; infinities and NaN in those that it sees
  * do, as the formulas have it (a row whose scores are all -infinity is NaN). Sums
  * and statistics are fp32; e^(s - m) is rounded to the cache's type in front of the
- * product with v.
+ * product with v, by half a step of itself; in fp16, where it is below 2^-21 of the
+ * row's largest, by at most 2^-32 of that.
  *   q, out [T][q_heads][head_dim] of the cache's type, rows q_stride and
  *     out_stride elements apart (multiples of 8, at least a row long where T > 1);
  *     out must not overlap q. lse [T][q_heads] fp32 or NULL.

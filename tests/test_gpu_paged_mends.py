@@ -102,3 +102,33 @@ def test_values_at_both_ends_of_a_window(D, dtype, page, order):
            (0, 2010, 1, (1,), -INF), (0, 2700, 0, (9,), NAN), (1, 0, 0, (2,), INF), (1, 449, 1, (3,), INF), (1, 300, 1, range(8), -INF)]
     check_values([600, 450], [3500, 450], 6, 2, D, bad, dtype, page, 1000, order)
     check_values([600, 450], [3500, 450], 6, 2, D, bad, dtype, page, 40, order)
+
+
+# ------------------------------------------------------------------------- weights across fp16's range
+@pytest.mark.parametrize("gap", [10.0, 14.0, 18.0])
+@pytest.mark.parametrize("D,new,tile", [(64, 1, 16), (128, 2, 16), (256, 1, 16), (64, 20, 32), (64, 40, 256), (128, 33, 256)])
+@pytest.mark.parametrize("where", ["first", "late"])
+def test_one_key_above_very_many(D, new, tile, gap, where):
+    """A key e^gap times as heavy as each of 131071 others, whose value is 0: the result is the others' share, from 0.86 down
+    to 0.002. A weight is rounded by half a step of fp16, or, where it is below 2^-21 of the row's largest, by 2^-32 of that: n
+    keys by n 2^-32 max|v| / sum of weights (at least 1) beside the tolerance of compare. The sequences share their pages,
+    and there are as many as the GPU has work for, so that no row's keys are divided and every one meets the heavy key."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    n, page, H, B = 131072, 64, 8, 20
+    q, kc, vc, flat, table, slots = attention_case([new], [n], H, H, D, "float16", page, spread=0.02)
+    q = (0.02 * torch.randn(B * new, H, D, device="cuda", generator=torch.Generator("cuda").manual_seed(3))).half()
+    assert api.fp4moe_paged_attention_plan(B, B * new, H, H, D) == tile
+    s = slots[0]
+    q[..., 0] = 1.0
+    kc[s // page, s % page, :, 0] = 0.0
+    vc[s // page, s % page] = (1.0 + vc[s // page, s % page] / 8).clamp(0.25, 1.75)
+    at = 0 if where == "first" else n - new - 5
+    put(kc, s, page, at, slice(None), [0], gap)
+    put(vc, s, page, at, slice(None), [slice(None)], 0.0)
+    flat = [c.reshape(-1, H, D) for c in (kc, vc)]
+    first, kv, new = [new * b for b in range(B + 1)], [n] * B, [new] * B
+    out, lse = run_attention(q, kc, vc, table.expand(B, -1).contiguous(), kv, first, 1.0, True, 0)
+    o, z, mag, top = ref.attention(q, *flat, slots * B, first[:-1], new, kv, 1.0, True, 0)
+    small = n * 2.0 ** -32 * 1.75 / ref.HALF_STEP["float16"]     # (compare takes half a step of mag)
+    compare(out, lse, (o, z, mag + small, top), kv, D, "float16")
