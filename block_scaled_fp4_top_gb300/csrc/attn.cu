@@ -492,7 +492,7 @@ fp4moe_status attn_rows_typed(const AttnParams& p, int tile, int nsm, cudaStream
 //   8192: 32 rows 14, 15, 25, 64 rows 20, 16, 36.
 int paged_attention_tile(const fp4moe_kv_cache& c, int32_t num_seqs, int32_t T, int32_t q_heads) {
   const int64_t rows = (int64_t)T * (q_heads / c.kv_heads), tiles = (rows + 15) / 16 * c.kv_heads;
-  if (c.head_dim > 128 || rows <= (int64_t)16 * num_seqs) return 16;
+  if (num_seqs == 0 || c.head_dim > 128 || rows <= (int64_t)16 * num_seqs) return 16;
   if (c.head_dim > 64) return tiles > 48 ? kAttnTileRows : 16;
   return tiles > 48 && rows > (int64_t)32 * num_seqs ? kAttnTileRows : 32;
 }
