@@ -855,10 +855,14 @@ class PagedKvCache:
         self.ws = torch.zeros(_lib.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
         self.err = torch.zeros(4, **i32)
 
-    def plan(self, new_len: torch.Tensor, stream=None):
-        """new_len [max_seqs] int32 on the device: tokens that each sequence adds (negative: gives back)."""
+    def plan(self, new_len: torch.Tensor, stream=None, rows: int | None = None):
+        """new_len [max_seqs] int32 on the device: tokens that each sequence adds (negative: gives back). rows: the rows of
+        the step's q, k and v (max_rows if None): a sequence whose tokens pass them takes nothing, and the error word says so
+        (ERR_CAPACITY). Rows beyond those that append and attend are given are not noticed there: their keys would be missing,
+        and the last sequence's positions be counted from the rows that are left."""
+        position, slot = (self.position, self.slot) if rows is None else (self.position[:rows], self.slot[:rows])
         fp4moe_kv_plan(self.page_size, self.kv_len, new_len, self.page_table, self.free_pages, self.free_count,
-                       self.kv_len, self.free_count, self.q_offset, self.position, self.slot, self.err, stream)
+                       self.kv_len, self.free_count, self.q_offset, position, slot, self.err, stream)
 
     def append(self, q, k, v, inv_freq, q_out, first: int = 0, interleaved: bool = False, amplitude: float = 1.0,
                layer: int = 0, stream=None):

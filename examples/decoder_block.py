@@ -182,13 +182,13 @@ def decode(wl: sg.Workload, block: DecoderBlock, prompt: int, steps: int = 50):
     for b in range(T):  # (the experts of the block are sized for T rows, so prompts run through its attention half)
         new.zero_()
         new[b] = prompt - b % 7
-        cache.plan(new)
+        cache.plan(new, rows=prompt - b % 7)
         attn.forward(torch.randn(prompt - b % 7, wl.H, device="cuda", generator=gen).to(torch.bfloat16))
     new.fill_(1)
     h = torch.randn(T, wl.H, device="cuda", generator=gen).to(torch.bfloat16)
 
     def step():
-        cache.plan(new)
+        cache.plan(new, rows=T)
         return block.forward(attn.forward(h), h)
 
     step()

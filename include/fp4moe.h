@@ -739,10 +739,12 @@ fp4moe_status fp4moe_rope_cache(const fp4moe_kv_cache* cache, int32_t T, int32_t
  *     first use; a call leaves its counters at zero again (after a
  *     FP4MOE_ERR_TIMEOUT zero it anew). Calls (and graphs) that share one must be
  *     ordered.
- * Offsets out of order or past T count as the nearest in range. Of a length that is
- * negative or longer than the table's columns, only keys that have a column count,
- * and a page outside [0, num_pages) reads as zeros: all with FP4MOE_ERR_PAGE in
- * *err. err also receives FP4MOE_ERR_TIMEOUT, as in fp4moe_mx_gemm.
+ * Of a length that is negative or longer than the table's columns, only keys that
+ * have a column count, and a page outside [0, num_pages) reads as zeros: both with
+ * FP4MOE_ERR_PAGE in *err. Offsets out of order or past T count as the nearest in
+ * range, and n with them, without an error: give fp4moe_kv_plan the step's T as its
+ * `rows`, so that no offset passes it. err also receives FP4MOE_ERR_TIMEOUT, as in
+ * fp4moe_mx_gemm.
  * Deterministic: equal inputs give equal bits. Other arguments out of range:
  * FP4MOE_INVALID_ARG.
  */

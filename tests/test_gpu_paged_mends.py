@@ -132,3 +132,33 @@ def test_one_key_above_very_many(D, new, tile, gap, where):
     o, z, mag, top = ref.attention(q, *flat, slots * B, first[:-1], new, kv, 1.0, True, 0)
     small = n * 2.0 ** -32 * 1.75 / ref.HALF_STEP["float16"]     # (compare takes half a step of mag)
     compare(out, lse, (o, z, mag + small, top), kv, D, "float16")
+
+
+# ------------------------------------------------------------------------- steps of fewer rows, and of some of the tensors
+def test_a_step_of_fewer_rows_than_tokens():
+    """A plan that knows the step's rows leaves out the sequence that does not fit, and says so; the others are served."""
+    import torch
+    from block_scaled_fp4_top_gb300 import _lib, api
+    H, Hk, D = 4, 2, 64
+    cache = api.PagedKvCache(40, 16, Hk, D, 3, 200, 100)
+    inv = api.rope_inv_freq(D)
+    gen = torch.Generator("cuda").manual_seed(1)
+    q, k, v = (torch.randn(24, h, D, device="cuda", generator=gen).bfloat16() for h in (H, Hk, Hk))
+    cache.plan(ints([20, 6, 0]), rows=24)
+    cache.append(q, k, v, inv, q)
+    assert cache.read_error() == _lib.ERR_CAPACITY
+    assert cache.kv_len.tolist() == [20, 0, 0] and cache.q_offset.tolist() == [0, 20, 24, 24]
+    assert (cache.slot[:20] >= 0).all() and (cache.slot[20:] == -1).all()
+    out = torch.empty_like(q)
+    cache.attend(q, 0.125, out)
+    torch.cuda.synchronize()
+    assert cache.read_error() == 0
+    slots = [torch.tensor([int(cache.page_table[0, j // 16]) * 16 + j % 16 for j in range(20)], device="cuda")]
+    flat = [c[0].flatten(0, 1) for c in (cache.k, cache.v)]
+    want = ref.attention(q[:20], *flat, slots, [0], [20], [20], 0.125, True, 0)
+    compare(out[:20], None, want, [20], D, "bfloat16")
+    assert (out[20:] == 0).all()                              # rows of a sequence without keys
+    cache.plan(ints([1, 6, 0]), rows=7)                       # its tokens again, where there is room
+    cache.append(q[:7], k[:7], v[:7], inv, q[:7])
+    torch.cuda.synchronize()
+    assert cache.read_error() == 0 and cache.kv_len.tolist() == [21, 6, 0]
