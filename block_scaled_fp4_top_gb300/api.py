@@ -866,15 +866,19 @@ class PagedKvCache:
 
     def append(self, q, k, v, inv_freq, q_out, first: int = 0, interleaved: bool = False, amplitude: float = 1.0,
                layer: int = 0, stream=None):
-        """The step's q [T, heads, D] turned into q_out (may be q), its k and v [T, kv heads, D] into the cache."""
-        T = k.shape[0]
+        """The step's q [T, heads, D] turned into q_out (may be q), its k and v [T, kv heads, D] into the cache. q and q_out, or
+        k and v (of layers that read another one's keys), may be None."""
+        if q is None and k is None:
+            raise Fp4MoeError("append: q, or k and v, must be given")
+        T = (q if k is None else k).shape[0]
         fp4moe_rope_cache(q, k, v, self.position[:T], self.slot[:T], inv_freq, q_out, self.k[layer], self.v[layer],
                           self.err, first, interleaved, amplitude, stream)
 
-    def attend(self, q, scale: float, out, lse=None, window: int = 0, layer: int = 0, stream=None):
-        """out [T, heads, D] of the step's turned q over the sequences' pages."""
+    def attend(self, q, scale: float, out, lse=None, window: int = 0, layer: int = 0, stream=None, causal: bool = True):
+        """out [T, heads, D] of the step's turned q over the sequences' pages: each row over the keys up to its own (window > 0:
+        the last `window` of them), or, not causal, over all keys of its sequence."""
         fp4moe_paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.kv_len, self.q_offset, scale, out,
-                               lse, self.ws, self.err, True, window, stream)
+                               lse, self.ws, self.err, causal, window, stream)
 
     def read_error(self, clear=True) -> int:
         """The error word. A call that gave up leaves the workspace's counters as they were, and the next call would take

@@ -162,3 +162,40 @@ def test_a_step_of_fewer_rows_than_tokens():
     cache.append(q[:7], k[:7], v[:7], inv, q[:7])
     torch.cuda.synchronize()
     assert cache.read_error() == 0 and cache.kv_len.tolist() == [21, 6, 0]
+
+
+def test_q_and_k_of_a_step_apart():
+    """The forms of the calls that take q alone, or k and v alone, and attention to every key, through the class."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    H, Hk, D, new = 4, 2, 64, [30, 9]
+    T = sum(new)
+    gen = torch.Generator("cuda").manual_seed(2)
+    q, k, v = (torch.randn(T, h, D, device="cuda", generator=gen).bfloat16() for h in (H, Hk, Hk))
+    inv = api.rope_inv_freq(D)
+    caches, turned = [], []
+    for apart in (False, True):
+        cache = api.PagedKvCache(20, 16, Hk, D, 2, 64, 64)
+        cache.plan(ints(new), rows=T)
+        qt = torch.empty_like(q)
+        if apart:
+            cache.append(None, k, v, inv, None)
+            cache.append(q, None, None, inv, qt)
+        else:
+            cache.append(q, k, v, inv, qt)
+        caches.append(cache)
+        turned.append(qt)
+    assert torch.equal(turned[0], turned[1])
+    for a, b in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v)):
+        assert torch.equal(a[0], b[0])
+    cache, out, lse = caches[1], torch.empty_like(q), torch.empty(T, H, device="cuda")
+    cache.attend(turned[1], 0.125, out, lse, causal=False)
+    torch.cuda.synchronize()
+    assert cache.read_error() == 0
+    slots = [torch.tensor([int(cache.page_table[b, j // 16]) * 16 + j % 16 for j in range(n)], device="cuda") for b, n in enumerate(new)]
+    flat = [c[0].flatten(0, 1) for c in (cache.k, cache.v)]
+    compare(out, lse, ref.attention(turned[1], *flat, slots, [0, 30], new, new, 0.125, False, 0), new, D, "bfloat16")
+    with pytest.raises(api.Fp4MoeError):
+        cache.append(None, None, None, inv, None)
+    with pytest.raises(api.Fp4MoeError):
+        cache.append(q, k, None, inv, q)
