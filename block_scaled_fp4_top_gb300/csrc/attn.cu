@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
     const int64_t head_off = (int64_t)head * p.map.head_stride;
     auto page_of = [&](int s) {  // page of the key that this lane looks up in slice s; -2: none
       const int key = base + s * C::S + (lane & (KEYS - 1));
-      return s < s1 && key >= range.x && key < range.y ? __ldg(table + p.map.page.div(key)) : -2;
+      return s < s1 && key >= range.x && key < range.y ? table[p.map.page.div(key)] : -2;
     };
     int page = page_of(s0);  // on its way while q is fetched
     // ---- this lane's rows: q as the MMA's A, and the keys they see
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int d = ks * 16 + 8 * j;
-            qa[i / 2][ks][i % 2 + 2 * j] = d < p.D ? __ldg(reinterpret_cast<const uint32_t*>(q + d)) : 0u;
+            qa[i / 2][ks][i % 2 + 2 * j] = d < p.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
           }
       }
     }
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(AttnCfg<DP, RT>::kThreads, 1) attn_rows_kernel
         const T* q = static_cast<const T*>(p.q) + (int64_t)(seq.first + tok) * p.q_stride +
                      (int64_t)(head * (int)p.group.d + g) * p.D + c * 8;
         *reinterpret_cast<uint4*>(sm + C::kRings + (i / CH) * (DP * 2) + ((c ^ ((i / CH) & 7)) << 4)) =
-            c * 8 < p.D ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0u, 0u, 0u, 0u);
+            c * 8 < p.D ? *reinterpret_cast<const uint4*>(q) : make_uint4(0u, 0u, 0u, 0u);
       }
       __syncthreads();
     }

@@ -121,8 +121,8 @@ __device__ __forceinline__ int64_t attn_cost(const AttnParams& p, int b, uint32_
   int big = 0, kv = 0;
   AttnSeq s{};
   if (b < p.B) {
-    const int q0 = __ldg(p.q_offset + b), q1 = __ldg(p.q_offset + b + 1);
-    kv = __ldg(p.kv_len + b);
+    const int q0 = p.q_offset[b], q1 = p.q_offset[b + 1];
+    kv = p.kv_len[b];
     s = attn_seq(p, q0, q1, kv);
     if (s.keys != kv && s.rows > 0) bad = 1;
     if (s.rows > BM) big = 1;
@@ -216,8 +216,8 @@ __device__ __forceinline__ AttnRun attn_plan(const AttnParams& p, int64_t* sums)
       r.seq = lo;
       left = r.begin - (lo ? upto[lo - 1] : 0);
     }
-    const int kv = __ldg(p.kv_len + r.seq);
-    const AttnSeq s = attn_seq(p, __ldg(p.q_offset + r.seq), __ldg(p.q_offset + r.seq + 1), kv);
+    const int kv = p.kv_len[r.seq];
+    const AttnSeq s = attn_seq(p, p.q_offset[r.seq], p.q_offset[r.seq + 1], kv);
     const int tiles = attn_tiles<BM>(s.rows);
     for (int t0 = 0; t0 < tiles; t0 += 32) {  // every warp for itself
       const int t = t0 + lane;
@@ -261,8 +261,8 @@ struct AttnWalk {
   __device__ __forceinline__ bool next(const AttnParams& p, const AttnRun& r, AttnUnit& u) {
     while (x < r.end) {
       if (read != b) {
-        kv = __ldg(p.kv_len + b);
-        seq = attn_seq(p, __ldg(p.q_offset + b), __ldg(p.q_offset + b + 1), kv);
+        kv = p.kv_len[b];
+        seq = attn_seq(p, p.q_offset[b], p.q_offset[b + 1], kv);
         read = b;
       }
       u.kv = kv;

@@ -246,7 +246,7 @@ struct Loader {
   }
   // Where a key of the unit lies: its page, or num_pages (zeros) if it has none or a bad one.
   __device__ __forceinline__ int page_of(const AttnUnit& u, const int32_t* table, int key, bool there) {
-    return there && key >= u.range.x && key < u.range.y ? __ldg(table + p.map.page.div(key)) : -2;
+    return there && key >= u.range.x && key < u.range.y ? table[p.map.page.div(key)] : -2;
   }
   __device__ __forceinline__ int checked(int page) {
     if ((uint32_t)page < (uint32_t)p.map.num_pages) return page;
@@ -584,7 +584,7 @@ __device__ __noinline__ void add_odd(const AttnParams& p, const AttnUnit& u, int
       key = all_hi - 1;
       continue;
     }
-    const int j = (int)p.map.page.div(key), page = __ldg(p.table + (int64_t)u.b * p.columns + j);
+    const int j = (int)p.map.page.div(key), page = p.table[(int64_t)u.b * p.columns + j];
     if ((uint32_t)page >= (uint32_t)p.map.num_pages) continue;  // (reads as zeros)
     const int64_t off = page * p.map.page_stride + (int64_t)(key - j * (int)p.map.page.d) * p.map.token_stride +
                         (int64_t)u.head * p.map.head_stride;

@@ -98,12 +98,13 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(KvPlanParams p) {
   // ---- lengths, first rows and pages given back
   const int per = (B + KP_THREADS - 1) / KP_THREADS, b0 = tid * per;
   int64_t tokens = 0, back = 0;
+  int32_t fresh[KP_ITEMS];
 #pragma unroll
   for (int i = 0; i < KP_ITEMS; ++i) {
     const int b = b0 + i;
     if (i >= per || b >= B) break;
-    int64_t c = __ldg(p.cached + b);
-    const int64_t n = __ldg(p.fresh + b);
+    int64_t c = p.cached[b];
+    const int64_t n = fresh[i] = p.fresh[b];
     if (c < 0 || c > limit) {
       err |= FP4MOE_ERR_PAGE;
       c = c < 0 ? 0 : limit;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(KvPlanParams p) {
     const int b = b0 + i;
     if (i >= per || b >= B) break;
     const int32_t c = from[b];
-    const int64_t n = __ldg(p.fresh + b);
+    const int64_t n = fresh[i];
     first[b] = clamp32(at, p.rows);
     given[b] = clamp32(ab, INT32_MAX);
     if (n > 0) at += n;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(KP_THREADS) kv_plan_kernel(KvPlanParams p) {
   }
   int64_t an = block_sum(need, part, all_need);
   // ---- the stack
-  int32_t F = __ldg(p.free_count);
+  int32_t F = *p.free_count;
   if (F < 0 || F > p.num_pages) {
     err |= FP4MOE_ERR_PAGE;
     F = F < 0 ? 0 : p.num_pages;

@@ -1,4 +1,6 @@
 // The paged key-value cache as its kernels see it (kvplan.cu, rope.cu, attn.cu, attntile.cu).
+// They start before the kernel in front of them has ended, and lengths may be outputs too: what the calls write is read with
+// plain loads, behind pdl_wait, since read-only loads (__ldg) are for memory that does not change while a kernel lives.
 #pragma once
 
 #include "dense.cuh"

@@ -73,7 +73,7 @@ __device__ __forceinline__ void rope_tokens(const RopeParams& p, int t0, int n, 
   const int half = p.rot / 2;
   for (int f = threadIdx.x; f < half; f += blockDim.x) s.step[f] = turn_step(__ldg(p.inv_freq + f));
   if (threadIdx.x < n) {
-    const int32_t slot = __ldg(p.slot + t0 + threadIdx.x);
+    const int32_t slot = p.slot[t0 + threadIdx.x];
     int64_t a = -1;
     if (slot != -1) {
       const uint32_t page = slot < 0 ? (uint32_t)p.map.num_pages : p.map.page.div((uint32_t)slot);
@@ -89,7 +89,7 @@ __device__ __forceinline__ void rope_tokens(const RopeParams& p, int t0, int n, 
   __syncthreads();
   for (int i = threadIdx.x; i < n * half; i += blockDim.x) {
     const int t = i / half, f = i - t * half;
-    s.turns[i] = turn(__ldg(p.position + t0 + t), s.step[f], p.amplitude);
+    s.turns[i] = turn(p.position[t0 + t], s.step[f], p.amplitude);
   }
   __syncthreads();
 }

@@ -15,3 +15,17 @@ def test_plan_of_no_sequences(T, H, Hk, D):
     """The header: num_seqs or T 0: 16."""
     from block_scaled_fp4_top_gb300 import api
     assert api.fp4moe_paged_attention_plan(0, T, H, Hk, D) == 16
+
+
+def test_no_read_only_loads_of_what_the_calls_write():
+    """A kernel may start before the one in front of it has ended, and one output may be an input: what these calls write
+    (lengths, tables, offsets, positions, slots, q, the caches) is memory that changes while a kernel lives, which loads of the
+    read-only kind are not defined for and which a compiler may move in front of the wait for the kernel before."""
+    import os
+    import re
+    from helpers import ROOT
+    for name in ("kvplan.cu", "rope.cu", "attn.cu", "attn.cuh", "attntile.cu", "paged.cuh"):
+        with open(os.path.join(ROOT, "block_scaled_fp4_top_gb300", "csrc", name)) as f:
+            text = f.read()
+        assert [m for m in re.findall(r"__ldg\(([^)]*)\)", text) if not m.startswith("p.inv_freq")] == [], name
+        assert "ld.global.nc" not in text and "__restrict__" not in text, name
