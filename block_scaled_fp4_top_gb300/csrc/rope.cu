@@ -6,8 +6,9 @@
 //
 // Angles. turns = position * inv_freq / (2 pi) matters modulo 1 only, and a product of 64-bit integers is a product
 // modulo 2^64: with step = inv_freq / (2 pi) as a fraction of 2^64, position * step is the fraction of a turn, off by
-// position * 2^-53 of it at most (the rounding of step). Its upper 32 bits go to sincospif. An fp32 product would be a
-// whole radian off past 2^24 radians; an fp64 sine costs a hundred fp64 operations.
+// position * |inv_freq| * 2^-55 turns at most: 1 / (2 pi) is off by 2^-53.8 of itself and the product by 2^-53, over 2 pi.
+// Its upper 32 bits go to sincospif as fp32, whose 24 bits are 2^-26 turns at most of half a turn. An fp32 product would be
+// a whole radian off past 2^24 radians; an fp64 sine costs a hundred fp64 operations.
 //
 // rope_vec_kernel: a thread keeps one item of a token's row (a 16-byte vector, or the two vectors that hold eight pairs of
 // the half layout) and goes through the CTA's tokens with it, the next two on their way, so places are worked out once. It takes

@@ -694,8 +694,9 @@ fp4moe_status fp4moe_kv_plan(int32_t num_seqs, int32_t page_size, int32_t num_pa
  *     for it. A slot outside the cache leaves the cache as it was (q_out is
  *     written) and sets FP4MOE_ERR_PAGE in *err. Of two rows with one slot
  *     either may be left in the cache.
- *   inv_freq [rot_dim / 2] fp64 radians per position, finite. The angle is exact
- *     to 2^-31 turns at any position (a product modulo one turn in 64 bits).
+ *   inv_freq [rot_dim / 2] fp64 radians per position, finite. The angle, a product
+ *     modulo one turn in 64 bits, is off by at most 2^-25 turns (its rounding to
+ *     fp32) + position * |inv_freq| * 2^-55 turns (the rounding of inv_freq / 2 pi).
  *   amplitude: finite fp32.
  * Row strides are multiples of 8 and at least a row long where T > 1. 0 <= rot_first,
  * rot_dim even, >= 0, rot_first + rot_dim <= head_dim (rot_dim = 0: inv_freq may be

@@ -2,6 +2,7 @@
 weights across the range of fp16, with lengths and positions at their limits. Against the 64-bit references of paged_ref.py,
 with the tolerances that test_gpu_paged.py derives."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -199,3 +200,46 @@ def test_q_and_k_of_a_step_apart():
         cache.append(None, None, None, inv, None)
     with pytest.raises(api.Fp4MoeError):
         cache.append(q, k, None, inv, q)
+
+
+# ------------------------------------------------------------------------- angles of far positions
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494")
+
+
+@pytest.mark.parametrize("position", [2 ** 31 - 1, 2 ** 31 - 12345, 2 ** 28 + 3, 2 ** 24 + 1, 1000003, -7])
+@pytest.mark.parametrize("quarter", [0, 1, 2, 3])
+@pytest.mark.parametrize("near", [1.0, 1e-3, 500.0])
+def test_rope_angles(position, quarter, near):
+    """Angles next to a multiple of a quarter turn, where a cosine or sine is as small as the angle's own error and a bf16
+    value shows it: off by at most 2^-25 turns + position |inv_freq| 2^-55. Beside that the sine of an fp32 angle is off by
+    2^-22 of itself, and half a step of bf16. Next to whole turns fp32 holds the fraction of a turn to 2^-24 of itself, and
+    what is left of 2^-25 is the cut to 32 bits, 2^-32, and that of the step, position 2^-63."""
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    half = 64
+    rng = np.random.default_rng(quarter)
+    turns = abs(position) * near / (2 * math.pi)
+    freq = np.array([2 * math.pi * (math.floor(turns * (1 + i / half)) + quarter / 4 + rng.normal() * 2.0 ** -27) / abs(position)
+                     for i in range(half)])
+    x = torch.zeros(1, 1, 2 * half, device="cuda", dtype=torch.bfloat16)
+    x[..., :half] = 1.0                                                     # (1, 0) -> (cos, sin)
+    out = torch.empty_like(x)
+    cache = torch.zeros(1, 1, 1, 2 * half, device="cuda", dtype=torch.bfloat16)
+    err = ints([0])
+    api.fp4moe_rope_cache(x, None, None, ints([position]), ints([0]), torch.from_numpy(freq).cuda(), out, cache, cache.clone(), err)
+    torch.cuda.synchronize()
+    assert err.tolist() == [0]
+    got = out.double().cpu().numpy().reshape(2, half)
+    for i in range(half):
+        angle = position * Fraction(float(freq[i])) / (2 * PI)              # in turns
+        nearest = round(angle * 4)
+        a = float((angle - Fraction(nearest, 4)) * 2 * PI)                  # from the quarter, in radians
+        s, c = math.sin(a), math.cos(a)
+        want = [(c, s), (-s, c), (-c, -s), (s, -c)][nearest % 4]
+        step = abs(position) * freq[i] * 2.0 ** -55
+        for part in range(2):
+            w = want[part]
+            left = 2.0 ** -32 + abs(position) * 2.0 ** -63 if nearest % 4 == 0 and part == 1 else 2.0 ** -25
+            # (a cosine next to 1 is off by the square of the angle's error)
+            tol = 2 * math.pi * (left + step) + abs(w) * (2.0 ** -22 + ref.HALF_STEP["bfloat16"])
+            assert abs(got[part][i] - w) <= tol, (i, part, got[part][i], w, tol, freq[i])
