@@ -558,26 +558,27 @@ __device__ __forceinline__ float2& row_stats() {
 }
 
 // What the loads took out of v where only some rows of the unit see it: weight times value, infinite or NaN, is added to the 32
-// dims from d0 on of O, which hold the finite values already, for the keys [lo, hi) that a row sees. All keys that a unit can
-// have of that kind, with values like that in every one, cost its rows some milliseconds, far from the waits' limit.
+// dims from d0 on of O, which hold the finite values already, for the keys [lo, hi) that a row sees. 256 tokens of one head of
+// 128 dims, whose 255 keys of that kind hold nothing else, take 4 ms, far from the 200 that the other warps wait.
 // Everything but the row's place comes out of memory and m, l and o are only written, so that the caller's loop over the
 // steps has no registers to keep for this: with m handed over and O handed in, a prompt of 8192 tokens took 395 us for 387,
 // one with a window of 1024 205 for 180.
 template <typename T, int DP>
 __device__ __noinline__ void add_odd(const AttnParams& p, const AttnUnit& u, int row, int lo, int hi, int d0, float& m, float& l,
                                      float (&o)[32]) {
+  float sum[32];  // (o itself is the caller's, in memory)
   __syncwarp();
-  tmem_ld32(tmem_base() + ((uint32_t)(threadIdx.x & 96) << 16) + 256 + (threadIdx.x >> 7) * DP + d0, o);
-  tmem_arrived(o);
+  tmem_ld32(tmem_base() + ((uint32_t)(threadIdx.x & 96) << 16) + 256 + (threadIdx.x >> 7) * DP + d0, sum);
+  tmem_arrived(sum);
   m = row_stats().x;
   l = row_stats().y;
   const int tok = (int)p.group.div(u.row0 + row), g = u.row0 + row - tok * (int)p.group.d;
-  const T* q = static_cast<const T*>(p.q) + (int64_t)(u.seq.first + tok) * p.q_stride +
-               (int64_t)(u.head * (int)p.group.d + g) * p.D;
+  const int64_t q_at = (int64_t)(u.seq.first + tok) * p.q_stride + (int64_t)(u.head * (int)p.group.d + g) * p.D;
   // keys that all rows of the unit see, as the loads have it
   const int all_lo = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0 + u.rows - 1)).x;
   const int all_hi = attn_range(p, u.seq, u.kv, (int)p.group.div(u.row0)).y;
   const int end = min(u.range.y, (u.range.x / AT_KEYS + u.s1) * AT_KEYS);
+  const int lane = lane_id(), c16 = (lane & 15) * 8;
 #pragma unroll 1
   for (int key = max(u.range.x, (u.range.x / AT_KEYS + u.s0) * AT_KEYS); key < end; ++key) {  // the same for all lanes
     if (key >= all_lo && key < all_hi) {
@@ -588,32 +589,48 @@ __device__ __noinline__ void add_odd(const AttnParams& p, const AttnUnit& u, int
     if ((uint32_t)page >= (uint32_t)p.map.num_pages) continue;  // (reads as zeros)
     const int64_t off = page * p.map.page_stride + (int64_t)(key - j * (int)p.map.page.d) * p.map.token_stride +
                         (int64_t)u.head * p.map.head_stride;
-    const T *k = static_cast<const T*>(p.k) + off, *v = static_cast<const T*>(p.v) + off;
-    float w = -1.0f;  // not made yet
+    const T* v = static_cast<const T*>(p.v) + off + d0;
+    const bool bad = lane < 4 && d0 + lane * 8 < p.D && any_nonfinite<T>(reinterpret_cast<const uint4*>(v)[lane & 3]);
+    uint32_t pieces = __ballot_sync(0xFFFFFFFFu, bad);
+    if (pieces == 0) continue;
+    // the key's scores with the warp's rows: 16 lanes a row, a lane 8 dims
+    float k8[8], s = 0.0f;
+    unpack<T>(c16 < p.D ? *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + off + c16) : make_uint4(0u, 0u, 0u, 0u), k8);
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+      uint4 raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, q_at, i0 + 2 * i + (lane >> 4));
+        raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at + (c16 < p.D ? c16 : 0));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float q8[8], dot = 0.0f;
+        unpack<T>(raw[i], q8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot = fmaf(q8[e], k8[e], dot);
+        if (c16 >= p.D) dot = 0.0f;
+#pragma unroll
+        for (int d = 8; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+        dot = __shfl_sync(0xFFFFFFFFu, dot, (lane & 1) * 16);  // of the first row to even lanes, of the second to odd ones
+        if ((lane & ~1) == i0 + 2 * i) s = dot;
+      }
+    }
+    if (key < lo || key >= hi) continue;
+    const float w = exp2_fast(fmaf(s, p.scale_log2, -weight_base<T>(m, p.scale_log2)));
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      if (d0 + c * 8 >= p.D) break;
-      const uint4 piece = *reinterpret_cast<const uint4*>(v + d0 + c * 8);
-      if (!any_nonfinite<T>(piece) || key < lo || key >= hi) continue;
-      if (w == -1.0f) {
-        float s = 0.0f;
-#pragma unroll 1
-        for (int d = 0; d < p.D; d += 8) {
-          float a[8], b[8];
-          unpack<T>(*reinterpret_cast<const uint4*>(q + d), a);
-          unpack<T>(*reinterpret_cast<const uint4*>(k + d), b);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
-        }
-        w = exp2_fast(fmaf(s, p.scale_log2, -weight_base<T>(m, p.scale_log2)));
-      }
+      if ((pieces >> c & 1) == 0) continue;
       float x[8];
-      unpack<T>(piece, x);
+      unpack<T>(reinterpret_cast<const uint4*>(v)[c], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (!isfinite(x[e])) o[c * 8 + e] = fmaf(w, x[e], o[c * 8 + e]);
+        if (!isfinite(x[e])) sum[c * 8 + e] = fmaf(w, x[e], sum[c * 8 + e]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) o[i] = sum[i];
 }
 
 // Of 32 scores of a row.

@@ -95,6 +95,13 @@ def test_new_values_behind_a_long_prefix(D, prefix):
     check_values([300, 5], [prefix + 300, 70], 4, 2, D, bad)
 
 
+@pytest.mark.parametrize("window", [0, 300])
+def test_no_value_is_finite(window):
+    """Every key of every unit, one query head a kv head, so that most keys of a unit are seen by some of its rows only."""
+    bad = [(0, j, h, [slice(None)], -INF if j % 97 == 0 else INF) for j in range(900) for h in range(2)]
+    check_values([600, 5], [900, 70], 2, 2, 128, bad, window=window)
+
+
 @pytest.mark.parametrize("page,order", [(16, "tokens"), (7, "tokens"), (7, "heads")])
 @pytest.mark.parametrize("D,dtype", [(128, "bfloat16"), (64, "float16"), (72, "bfloat16")])
 def test_values_at_both_ends_of_a_window(D, dtype, page, order):
