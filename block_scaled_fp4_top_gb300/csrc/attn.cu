@@ -6,8 +6,8 @@
 // The bytes of k and v bound it: 16 rows of a tile cost 64 KFLOP for 8 KB of a group (head_dim 128), far below what
 // mma.sync gives, so the tile's M = 16 is that of mma.sync, and a warp works alone: it brings its own groups of keys by
 // cp.async through a ring of its own, without any barrier between warps, and joins the others at the end of a tile only.
-// 64 sequences of up to 8192 keys, 8 kv heads of 128 dims: 1367 MB in 214 us, 6.4 TB/s, 94 % of a plain copy's rate; four of
-// 131072 keys 321 us, 98 %. One row of 4096 keys is 13 us of latency: the division 2, page and keys 2, the joins 4.
+// 64 sequences of up to 8192 keys, 8 kv heads of 128 dims: 1367 MB in 213 us, 6.4 TB/s, 95 % of a plain copy's rate; four of
+// 131072 keys 321 us, 99 %. One row of 4096 keys is 13 us of latency: the division 2, page and keys 2, the joins 4.
 // Tiles of 32 rows (64 dims) use what is read twice: 16 x 32 rows of up to 8192 keys, 8 kv heads, in 42 us, which tiles of
 // 16 take 50 for and the larger ones 55. There the chain of a group binds it, scores to weights to sums, with two warps a
 // scheduler to hide it: groups of 32 keys, twice as many products side by side, took it from 49 to 42 us, and decoding from
@@ -490,6 +490,9 @@ fp4moe_status attn_rows_typed(const AttnParams& p, int tile, int nsm, cudaStream
 //   28, 48 rows 26, 27, 56. Tiles of 32 gain too little there to be kept.
 //   64 dims, 16 sequences of up to 8192 keys: 16 rows 38, 41, 54; 32 rows 53, 43, 56; 48 rows 75, 60, 56; one sequence of
 //   8192: 32 rows 14, 15, 25, 64 rows 20, 16, 36.
+// Those are sequences of one length. The average decides for unequal ones too: 512 decodes beside one chunk of 1500 tokens,
+// 5000 keys each, 128 dims, go through tiles of 16 in 2006 us, 64 beside a chunk of 1024 through the larger ones in 314. Decodes
+// and chunks in calls of their own take 1507 + 90 and 202 + 73.
 int paged_attention_tile(const fp4moe_kv_cache& c, int32_t num_seqs, int32_t T, int32_t q_heads) {
   const int64_t rows = (int64_t)T * (q_heads / c.kv_heads), tiles = (rows + 15) / 16 * c.kv_heads;
   if (num_seqs == 0 || c.head_dim > 128 || rows <= (int64_t)16 * num_seqs) return 16;

@@ -20,9 +20,10 @@
 // Every wait is bounded, as in the layer's GEMMs.
 //
 // What bounds it: a tile's round from its scores to its weights to the next scores, 3000 cycles, in which the MMAs of both
-// tiles take 2064 (128 dims); a third tile has no room in TMEM. A causal prompt of 8192 tokens, 32 / 8 heads of 128 dims: 387
-// us, 1420 TFLOP/s; chunks of 512 tokens behind up to 3584, eight sequences: 134 us, 1010 TFLOP/s, of which 5 us begin and
-// end a CTA's run. Measured on the prompt: one warp for the MMAs of both tiles 406 and one each 489 (the tiles fall into
+// tiles take 2064 (128 dims); a third tile has no room in TMEM. A causal prompt of 8192 tokens, 32 / 8 heads of 128 dims: 388
+// us, 1417 TFLOP/s, for twenty calls one after the other, 406 over seconds, plain or in a graph, when the power limit takes the
+// clock from 2070 to 1970 MHz; chunks of 512 tokens behind up to 3584, eight sequences: 132 us, 1010 TFLOP/s, of which 5 us begin
+// and end a CTA's run. Measured on the prompt: one warp for the MMAs of both tiles 406 and one each 489 (the tiles fall into
 // step); weights under the maximum so far 448 and under the new one 483; one lane of a converged warp issues MMAs 483 and a
 // lane picked by index 573; boxes 1056 and cp.async 1206. Chunks over pages of one token: gathers 207, cp.async 438.
 #include "attn.cuh"
@@ -36,7 +37,7 @@ constexpr int AT_ODD = 8;          // units whose flags are kept: loads run ahea
 constexpr int AT_FEW = 32;         // rows of a tile whose parts are joined a few lanes a row
 constexpr int AT_MIN = 4;          // least cost of a CTA's run
 constexpr int AT_OH = 4;           // what a unit costs, in steps, beside its steps
-constexpr int AT_THREADS = 352;    // 168 registers a thread: a row of S stays in them
+constexpr int AT_THREADS = 352;    // 168 registers a thread, for a row of S; 80 to 88 bytes beside it are spilled
 constexpr float AT_GROWTH = 8.0f;  // powers of two that a maximum may lag behind
 
 template <int DP>

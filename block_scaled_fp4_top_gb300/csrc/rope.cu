@@ -1,7 +1,7 @@
 // Rotary positions of q and k, and k and v into the paged cache (fp4moe_rope_cache).
 //
 // The pass moves (q_heads + 2 kv_heads) head_dim elements a token in and out and is bound by memory: 8192 tokens of 32 + 8 + 8
-// heads of 128 dims, 201 MB in and out, in 34.9 us, 5.8 TB/s. The angle's cosine and sine are one for all heads of a token: a
+// heads of 128 dims, 201 MB in and out, in 34.4 us, 5.9 TB/s. The angle's cosine and sine are one for all heads of a token: a
 // CTA makes those of its tokens once, in shared memory, and a token's row has CTAs of its own where there are few.
 //
 // Angles. turns = position * inv_freq / (2 pi) matters modulo 1 only, and a product of 64-bit integers is a product
@@ -13,7 +13,8 @@
 // rope_vec_kernel: a thread keeps one item of a token's row (a 16-byte vector, or the two vectors that hold eight pairs of
 // the half layout) and goes through the CTA's tokens with it, the next two on their way, so places are worked out once. It takes
 // parts of the head that consist of whole vectors. rope_any_kernel takes the others: a warp has whole heads in shared
-// memory, and each turned element picks its partner there.
+// memory, and each turned element picks its partner there, one token after the other with no load under way: 8192 tokens
+// as above take 72 us with 38 dims turned and 81 with 126 in neighbouring pairs, 2.5 to 2.8 TB/s.
 #include <algorithm>
 
 #include "paged.cuh"

@@ -85,7 +85,7 @@ NAN, INF = float("nan"), float("inf")
 
 def test_one_value_late_in_a_long_prompt():
     """The rows of its unit see up to 16384 keys; the other sequences are served as well."""
-    check_values([16384, 40, 1], [16384, 900, 50], 1, 1, 128, [(0, 16384 - 77, 0, (3, 90), INF), (0, 9000, 0, (4,), NAN)])
+    check_values([4096, 40, 1], [16384, 900, 50], 1, 1, 128, [(0, 16384 - 77, 0, (3, 90), INF), (0, 13000, 0, (4,), NAN)])
 
 
 @pytest.mark.parametrize("D,prefix", [(128, 131072), (64, 32768)])
