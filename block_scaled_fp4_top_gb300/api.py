@@ -860,7 +860,11 @@ class PagedKvCache:
         the step's q, k and v (max_rows if None): a sequence whose tokens pass them takes nothing, and the error word says so
         (ERR_CAPACITY). Rows beyond those that append and attend are given are not noticed there: their keys would be missing,
         and the last sequence's positions be counted from the rows that are left."""
-        position, slot = (self.position, self.slot) if rows is None else (self.position[:rows], self.slot[:rows])
+        position, slot = self.position, self.slot
+        if rows is not None:
+            if not 0 <= rows <= slot.shape[0]:
+                raise Fp4MoeError(f"rows: expected 0 to {slot.shape[0]}, got {rows}")
+            position, slot = position[:rows], slot[:rows]
         fp4moe_kv_plan(self.page_size, self.kv_len, new_len, self.page_table, self.free_pages, self.free_count,
                        self.kv_len, self.free_count, self.q_offset, position, slot, self.err, stream)
 

@@ -17,6 +17,19 @@ def test_plan_of_no_sequences(T, H, Hk, D):
     assert api.fp4moe_paged_attention_plan(0, T, H, Hk, D) == 16
 
 
+@pytest.mark.parametrize("rows", [-1, 101])
+def test_rows_of_a_step_that_the_cache_was_not_made_for(rows):
+    import torch
+    from block_scaled_fp4_top_gb300 import api
+    ws, api._lib.ATTENTION_WORKSPACE_BYTES = api._lib.ATTENTION_WORKSPACE_BYTES, 64
+    try:
+        cache = api.PagedKvCache(4, 16, 1, 8, 2, 64, 100, device="cpu")
+    finally:
+        api._lib.ATTENTION_WORKSPACE_BYTES = ws
+    with pytest.raises(api.Fp4MoeError, match="rows"):
+        cache.plan(torch.zeros(2, dtype=torch.int32), rows=rows)
+
+
 def test_no_read_only_loads_of_what_the_calls_write():
     """A kernel may start before the one in front of it has ended, and one output may be an input: what these calls write
     (lengths, tables, offsets, positions, slots, q, the caches) is memory that changes while a kernel lives, which loads of the
