@@ -103,13 +103,34 @@ def test_no_value_is_finite(window):
 
 
 @pytest.mark.parametrize("page,order", [(16, "tokens"), (7, "tokens"), (7, "heads")])
-@pytest.mark.parametrize("D,dtype", [(128, "bfloat16"), (64, "float16"), (72, "bfloat16")])
+@pytest.mark.parametrize("D,dtype", [(128, "bfloat16"), (64, "float16"), (72, "bfloat16"), (8, "bfloat16"), (40, "float16"), (120, "bfloat16")])
 def test_values_at_both_ends_of_a_window(D, dtype, page, order):
     """Keys that enter and that leave the window within a unit, one that all its rows see, both signs of one dim, whole rows."""
     bad = [(0, 3000, 0, (0,), INF), (0, 3100, 0, (0, 5), -INF), (0, 3499, 1, range(D), NAN), (0, 2400, 1, (D - 1,), INF),
-           (0, 2010, 1, (1,), -INF), (0, 2700, 0, (9,), NAN), (1, 0, 0, (2,), INF), (1, 449, 1, (3,), INF), (1, 300, 1, range(8), -INF)]
+           (0, 2010, 1, (1,), -INF), (0, 2700, 0, (9 % D,), NAN), (1, 0, 0, (2,), INF), (1, 449, 1, (3,), INF), (1, 300, 1, range(8), -INF)]
     check_values([600, 450], [3500, 450], 6, 2, D, bad, dtype, page, 1000, order)
     check_values([600, 450], [3500, 450], 6, 2, D, bad, dtype, page, 40, order)
+
+
+@pytest.mark.parametrize("D", [128, 24])
+def test_infinite_keys_with_infinite_values(D):
+    """A score of -infinity has weight 0, and 0 times infinity is NaN in its dims only; one of infinity makes the row NaN."""
+    import torch
+    new, kv, H, Hk, page = [300], [700], 4, 2, 16
+    q, kc, vc, flat, table, slots = attention_case(new, kv, H, Hk, D, "bfloat16", page)
+    for key in (450, 690):
+        put(kc, slots[0], page, key, 0, [0], INF)
+        put(vc, slots[0], page, key, 0, [1, 2], -INF)
+    put(vc, slots[0], page, 600, 1, [5], NAN)
+    flat = [c.reshape(-1, Hk, D) for c in (kc, vc)]
+    out, lse = run_attention(q, kc, vc, table, kv, [0, 300], D ** -0.5, True, 0)
+    with np.errstate(invalid="ignore"):
+        want = ref.attention(q, *flat, slots, [0], new, kv, D ** -0.5, True, 0)
+        nan = torch.isnan(want[0])
+        assert (nan.all(2).sum() > 0) and (nan.any(2) & ~nan.all(2)).sum() > 0
+        compare(out, lse, want, kv, D, "bfloat16")
+    clean = torch.isfinite(want[3])                             # rows whose scores are finite: their tolerances are too
+    compare(out[clean][:, None], lse[clean][:, None], [t[clean][:, None] for t in want], kv, D, "bfloat16")
 
 
 # ------------------------------------------------------------------------- weights across fp16's range
